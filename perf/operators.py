@@ -297,9 +297,10 @@ def _norm_rope(x, w, cos_sin, pos, interleaved, eps=1e-6):
 
 
 def _plain_rows(s, w, page, at):
-    """Page values in fp32 as the attention takes them: rounded to the queries' type."""
+    """Page values in fp32 as the attention takes them: 16-bit rows as they are, the others rounded to fp16."""
     c = s["case"]
-    return _load(c, s["pool"], s["n_pages"], w, page, at).to(DT[c["dtype"]]).float()
+    x = _load(c, s["pool"], s["n_pages"], w, page, at)
+    return x if c["v_fmt" if w else "k_fmt"] in DT else x.half().float()
 
 
 def _attention(s):
@@ -498,7 +499,9 @@ def exact(case, seed):
     lse = torch.full(s["lse"].shape, -math.inf, dtype=torch.float64, device=o.device)
     for b, n in enumerate(s["lens_host"]):
         pages = s["table"][b, :-(-n // ps)]
-        k, v = (_exact_rows(s, w, pages, ps, n).to(DT[case["dtype"]]).double() for w in range(2))
+        k, v = (_exact_rows(s, w, pages, ps, n) for w in range(2))
+        if case["k_fmt"] not in DT:                        # quantised rows enter the attention as fp16 values
+            k, v = k.half().double(), v.half().double()
         pos = torch.arange(n - (cu[b + 1] - cu[b]), n, device=o.device)
         gap = pos[:, None] - torch.arange(n, device=o.device)
         hide = gap < 0
