@@ -3,14 +3,23 @@
 The work is done by ``lib/libkvq.so`` (hand-written CUDA behind the C ABI of
 ``include/kvq.h``); this package only marshals arguments (``_lib``), names the measured
 workloads (``configs``), draws seeded synthetic inputs (``synth``) and wraps device memory
-owned by PyTorch (``KVCache``). There is no CPU fallback: without the shared library every
-call raises.
+owned by PyTorch (``KVCache``; the paged cache and what goes with it: ``PagedKVCache``,
+``paged_config``, ``qk_norm_rope``). There is no CPU fallback: without the shared library every call
+raises.
 """
 
 from . import _lib, configs, synth  # noqa: F401
 from ._lib import (KVQError, kvq_config, kv_bytes_per_token, kv_required_bytes, kv_create,  # noqa: F401
                    kv_destroy, kv_reset, kv_append, kv_prefill, kv_seal, kv_decode_attn, kv_state, kv_get_status,
                    kv_dequant, kv_region_ptr, kv_format_tables, kvq_synth_fill)
+
+
+def __getattr__(name):
+    # .paged imports torch, which importing this package does not
+    if name in ("PagedKVCache", "paged_config", "qk_norm_rope"):
+        from . import paged
+        return getattr(paged, name)
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 class KVCache:

@@ -23,6 +23,9 @@ KVARN_BALANCE = {"final16": 0, "best8": 1}
 # regions
 REGION_SINK, REGION_JOURNAL, REGION_JOURNAL_SCALE, REGION_TAIL, REGION_BODY = range(5)
 ENOSPC = 2
+# dtype of kv_paged_read beside F16 and BF16; bits of the paged status word
+PAGED_F32 = 100
+PAGED_NONFINITE, PAGED_TIMEOUT, PAGED_BAD_INDEX, PAGED_BAD_LENGTH = 1, 2, 4, 8
 STATUS = {0: "KVQ_OK", 1: "KVQ_EINVAL", 2: "KVQ_ENOSPC", 3: "KVQ_EUNSUPPORTED", 4: "KVQ_ECUDA", 5: "KVQ_EDEVICE"}
 
 
@@ -45,6 +48,26 @@ class kvq_bytes(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int64) for n in ("body_bytes_per_token", "f16_bytes_per_token",
                                                "journal_bytes_per_slot", "tail_bytes_per_slot", "sink_bytes",
                                                "fixed_bytes_per_seq", "pool_bytes")]
+
+
+class kvq_paged_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_layers", "n_kv_heads", "head_dim", "n_q_heads", "page_size", "n_pages",
+                                               "k_fmt", "v_fmt")] + [("softmax_scale", ctypes.c_float),
+                                                                     ("reserved", ctypes.c_int32)]
+
+
+class kvq_attn_opts(ctypes.Structure):
+    _fields_ = [("softcap", ctypes.c_float), ("window", ctypes.c_int32), ("slopes", ctypes.c_void_p),
+                ("prefix", ctypes.c_void_p), ("lse", ctypes.c_void_p)]
+
+
+class kvq_norm_rope_args(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("dtype", "n_tok", "n_q_heads", "n_k_heads", "head_dim", "rot_dim",
+                                                "interleaved", "max_pos")] +
+                [("eps", ctypes.c_float), ("reserved", ctypes.c_int32)] +
+                [(n, ctypes.c_void_p) for n in ("q", "k", "q_weight", "k_weight", "cos_sin", "positions", "q_out",
+                                                "k_out")] +
+                [(n, ctypes.c_int64) for n in ("q_stride", "k_stride", "q_out_stride", "k_out_stride")])
 
 
 _lib = None
@@ -85,6 +108,16 @@ _SIGS = {
     "kv_snapshot": [P, P, SZ],
     "kv_restore": [P, P, SZ],
     "kv_test_wait_timeout": [P, ctypes.c_uint64, P],
+    "kv_paged_required_bytes": [ctypes.POINTER(kvq_paged_config), I32, I64, ctypes.POINTER(SZ), ctypes.POINTER(SZ)],
+    "kv_paged_create": [ctypes.POINTER(kvq_paged_config), P, SZ, ctypes.c_int, ctypes.POINTER(P)],
+    "kv_paged_destroy": [P],
+    "kv_paged_get_status": [P, ctypes.POINTER(ctypes.c_uint32)],
+    "kv_paged_write": [P, I32, I32, I32, P, I64, P, I64, P, P],
+    "kv_paged_read": [P, I32, I32, I32, P, I32, I64, P, P, I32, P, P, P],
+    "kv_paged_decode_attn": [P, I32, I32, I32, P, I64, P, I32, I64, P, P, ctypes.POINTER(kvq_attn_opts), P, SZ, P],
+    "kv_paged_prefill_attn": [P, I32, I32, I32, I32, I32, P, I64, P, P, I32, I64, P, P, ctypes.POINTER(kvq_attn_opts), P,
+                              SZ, P],
+    "kv_qk_norm_rope": [ctypes.POINTER(kvq_norm_rope_args), P],
     "kvq_synth_fill": [P, I64, ctypes.c_int, ctypes.c_int, ctypes.POINTER(ctypes.c_uint64), I64, P, P, P],
 }
 
@@ -282,3 +315,61 @@ def kvq_synth_fill(out_ptr, n_pos, n_heads, head_dim, head_keys, pos0, factor_pt
     keys = (ctypes.c_uint64 * len(head_keys))(*[int(k) for k in head_keys])
     _check("kvq_synth_fill", load().kvq_synth_fill(P(out_ptr), n_pos, n_heads, head_dim, keys, pos0,
                                                    P(factor_ptr or 0), P(table_ptr), P(stream)))
+
+
+def kv_paged_required_bytes(cfg, max_seqs, max_tokens=0):
+    pool, ws = SZ(), SZ()
+    _check("kv_paged_required_bytes", load().kv_paged_required_bytes(ctypes.byref(cfg), max_seqs, max_tokens,
+                                                                     ctypes.byref(pool), ctypes.byref(ws)))
+    return pool.value, ws.value
+
+
+def kv_paged_create(cfg, pool_ptr, pool_bytes, device):
+    h = P()
+    _check("kv_paged_create", load().kv_paged_create(ctypes.byref(cfg), P(pool_ptr), pool_bytes, device,
+                                                     ctypes.byref(h)))
+    return h
+
+
+def kv_paged_destroy(h):
+    _check("kv_paged_destroy", load().kv_paged_destroy(h))
+
+
+def kv_paged_get_status(h):
+    w = ctypes.c_uint32()
+    code = load().kv_paged_get_status(h, ctypes.byref(w))
+    if code not in (0, 5):
+        raise KVQError("kv_paged_get_status", code)
+    return w.value
+
+
+def kv_paged_write(h, layer, dtype, n_tok, k_ptr, k_stride, v_ptr, v_stride, slots_ptr, stream=0):
+    _check("kv_paged_write", load().kv_paged_write(h, layer, dtype, n_tok, k_ptr, k_stride, v_ptr, v_stride, slots_ptr,
+                                                   stream))
+
+
+def kv_paged_read(h, layer, dtype, n_seq, table_ptr, max_pages, table_stride, cu_ptr, start_ptr, n_rows, k_ptr, v_ptr,
+                  stream=0):
+    _check("kv_paged_read", load().kv_paged_read(h, layer, dtype, n_seq, table_ptr, max_pages, table_stride, cu_ptr,
+                                                 start_ptr, n_rows, k_ptr, v_ptr, stream))
+
+
+def kv_paged_decode_attn(h, layer, dtype, n_seq, q_ptr, q_stride, table_ptr, max_pages, table_stride, lens_ptr, out_ptr,
+                         opts, ws_ptr, ws_bytes, stream=0):
+    """opts: a kvq_attn_opts or None."""
+    _check("kv_paged_decode_attn", load().kv_paged_decode_attn(h, layer, dtype, n_seq, q_ptr, q_stride, table_ptr,
+                                                               max_pages, table_stride, lens_ptr, out_ptr, opts, ws_ptr,
+                                                               ws_bytes, stream))
+
+
+def kv_paged_prefill_attn(h, layer, dtype, n_seq, n_rows, max_q, q_ptr, q_stride, cu_ptr, table_ptr, max_pages,
+                          table_stride, lens_ptr, out_ptr, opts, ws_ptr, ws_bytes, stream=0):
+    """opts: a kvq_attn_opts or None."""
+    _check("kv_paged_prefill_attn", load().kv_paged_prefill_attn(h, layer, dtype, n_seq, n_rows, max_q, q_ptr, q_stride,
+                                                                 cu_ptr, table_ptr, max_pages, table_stride, lens_ptr,
+                                                                 out_ptr, opts, ws_ptr, ws_bytes, stream))
+
+
+def kv_qk_norm_rope(args, stream=0):
+    """args: a kvq_norm_rope_args."""
+    _check("kv_qk_norm_rope", load().kv_qk_norm_rope(args, stream))

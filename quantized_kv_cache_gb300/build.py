@@ -29,6 +29,10 @@ UNITS = {
     "kernels_attn.cu": [],
     "kernels_body.cu": [],
     "synth.cu": [],
+    "paged_api.cpp": [],
+    "kernels_paged_rows.cu": [],
+    "kernels_paged_decode.cu": [],
+    "kernels_paged_prefill.cu": [],
 }
 
 

@@ -1,0 +1,333 @@
+// Decode attention over pages: one query per sequence, split over positions and joined.
+//
+// The work is one line of 16-position tiles: sequences in order, in each its KV heads in order, in
+// each head the tiles that hold a visible position. The line is cut into equal runs, one per CTA, on
+// the device (lengths are device arrays), so ragged batches balance and a captured call follows new
+// lengths. A CTA's four warps take the tiles of a run in turn, each with its own running maximum, sum
+// and output (fp32, registers); at the end of a head they join through shared memory. A head that lies
+// in one run is written out at once; others leave (m, l, o) per run, which the merge kernel joins.
+#include "paged_frag.cuh"
+
+namespace kvq {
+namespace {
+
+constexpr int kDW = 4;                    // warps of a CTA
+constexpr int kDT = kDW * 32;
+constexpr int kMinTiles = 4;              // smallest run: one tile per warp
+
+// Visible tiles of a sequence: [0, n0) (the prefix) and [t1, t1 + n1) (the window, or everything).
+struct SeqTiles {
+    int len, lo, pre, n0, t1, n;          // n: tiles in all
+    __device__ __forceinline__ int tile(int i) const { return i < n0 ? i : t1 + i - n0; }
+    __device__ __forceinline__ bool sees(int pos) const { return pos < len && (pos >= lo || pos < pre); }
+};
+__device__ __forceinline__ SeqTiles seq_tiles(const PagedAttnParams& p, int b) {
+    SeqTiles s;
+    const int64_t cap = (int64_t)p.max_pages << p.v.ps_shift;
+    const int n = p.lens[b];
+    s.len = n < 0 ? 0 : (n > cap ? (int)cap : n);
+    s.lo = p.window > 0 && s.len > p.window ? s.len - p.window : 0;
+    const int x = p.prefix ? p.prefix[b] : 0;
+    s.pre = min(max(x, 0), s.len);
+    const int end = (s.len + kTile - 1) / kTile;
+    s.t1 = s.lo / kTile;
+    s.n0 = min((s.pre + kTile - 1) / kTile, s.t1);
+    s.n = s.n0 + end - s.t1;
+    return s;
+}
+
+// Tiles of all sequences before b0 and of all, by the whole block (`b0` any, `red` shared scratch).
+template <int T>
+__device__ __forceinline__ int64_t block_sum(int64_t x, int64_t* red) {
+#pragma unroll
+    for (int s = 16; s >= 1; s >>= 1) x += __shfl_xor_sync(kAll, x, s);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
+    __syncthreads();
+    int64_t y = 0;
+#pragma unroll
+    for (int i = 0; i < T / 32; ++i) y += red[i];
+    __syncthreads();
+    return y;
+}
+
+__device__ __forceinline__ int64_t run_tiles(int64_t total, int n_cta) {
+    const int64_t u = (total + n_cta - 1) / n_cta;
+    return u < kMinTiles ? kMinTiles : u;
+}
+
+KVQ_HD int64_t partial_floats(int G, int D) { return 32 + (int64_t)G * D; }
+
+template <int D, int KF, int VF, typename T, typename TQ>
+__global__ void __launch_bounds__(kDT) decode_kernel(PagedAttnParams p) {
+    constexpr bool LO = std::is_same<T, __nv_bfloat16>::value;   // P in two bf16 parts: 16 bits of it
+    extern __shared__ __align__(16) float smem[];                // [kDW][G][D] outputs, joined per head
+    __shared__ float s_m[kDW][16], s_l[kDW][16];
+    __shared__ int64_t red[kDW];
+    __shared__ int s_b, s_h, s_i;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int H = p.v.H, G = p.G;
+
+    // this CTA's run of the line, and the head where it starts
+    int64_t mine = 0;
+    const int per = (p.n_seq + kDT - 1) / kDT;
+    for (int b = threadIdx.x * per; b < min(p.n_seq, (int)(threadIdx.x + 1) * per); ++b) {
+        mine += (int64_t)seq_tiles(p, b).n * H;
+        const int n = p.lens[b];
+        if (blockIdx.x == 0 && (n < 0 || n > ((int64_t)p.max_pages << p.v.ps_shift))) raise_status(p.v.status, KVQ_PAGED_BAD_LENGTH);
+    }
+    int64_t before = mine;                                       // inclusive scan over the warp
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) {
+        const int64_t y = __shfl_up_sync(kAll, before, s);
+        if (lane >= s) before += y;
+    }
+    if (lane == 31) red[warp] = before;
+    __syncthreads();
+    int64_t total = 0;
+    for (int i = 0; i < kDW; ++i) {
+        if (i < warp) before += red[i];
+        total += red[i];
+    }
+    before -= mine;
+    const int64_t U = run_tiles(total, p.n_cta), first = blockIdx.x * U;
+    int64_t left = min(U, total - first);
+    if (left <= 0) return;
+    if (first >= before && first < before + mine) {
+        int64_t at = first - before;
+        for (int b = threadIdx.x * per;; ++b) {
+            const int64_t n = seq_tiles(p, b).n;
+            if (at < n * H) {
+                s_b = b;
+                s_h = (int)(at / n);
+                s_i = (int)(at % n);
+                break;
+            }
+            at -= n * H;
+        }
+    }
+    __syncthreads();
+    int b = s_b, h = s_h, i0 = s_i;
+    ScoreRule rule;
+    rule.scale = p.scale;
+    rule.cap = p.softcap;
+    rule.cap_l2 = p.softcap * kL2e;
+
+    for (; left > 0; ++h, i0 = 0) {
+        if (h == H) { h = 0; ++b; }
+        const SeqTiles st = seq_tiles(p, b);
+        if (st.n == 0) { h = H - 1; continue; }
+        const int i1 = (int)min((int64_t)st.n, i0 + left);
+        left -= i1 - i0;
+        const TQ* q = (const TQ*)p.q + b * p.q_stride + (int64_t)h * G * D;
+        uint32_t qf[D / 16][4];
+        float back[2], slope[2], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[D / 8][4] = {};
+        load_queries<D, KF, T, TQ>([&](int r) { return r < G ? q + r * D : (const TQ*)nullptr; }, g, t, qf, back);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) slope[k] = p.slopes && g + 8 * k < G ? p.slopes[h * G + g + 8 * k] * kL2e : 0.f;
+
+        for (int i = i0 + warp; i < i1; i += kDW) {
+            const int p0 = st.tile(i) * kTile, e = p0 >> p.v.ps_shift, off = p0 & (p.v.ps - 1);
+            int page = p.table[b * p.table_stride + e];
+            const unsigned see = __ballot_sync(kAll, lane < 16 && st.sees(p0 + lane));
+            unsigned live = see;
+            if (page < 0 || page >= p.v.n_pages) {
+                if (lane == 0) raise_status(p.v.status, KVQ_PAGED_BAD_INDEX);
+                page = 0;
+                live = 0;
+            }
+            float s[2][4] = {};
+            tile_scores<D, KF, T>(global_tile<KGeo<D, KF>::RB>(p.v, 0, page, h, off, live), g, t, qf, s);
+            float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const int pos = 8 * n + 2 * t + (c & 1);
+                    const float x = rule(s[n][c], back[c >> 1], (float)(st.len - 1 - p0 - pos), slope[c >> 1]);
+                    s[n][c] = (see >> pos) & 1 ? x : -INFINITY;
+                    mx[c >> 1] = fmaxf(mx[c >> 1], s[n][c]);
+                }
+            float base[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                mx[k] = fmaxf(mx[k], __shfl_xor_sync(kAll, mx[k], 1));
+                mx[k] = fmaxf(mx[k], __shfl_xor_sync(kAll, mx[k], 2));
+                const float mn = fmaxf(m[k], mx[k]);
+                base[k] = mn == -INFINITY ? 0.f : mn;
+                const float a = ex2(m[k] - base[k]);
+                m[k] = mn;
+                l[k] *= a;
+#pragma unroll
+                for (int d = 0; d < D / 8; ++d) {
+                    o[d][2 * k] *= a;
+                    o[d][2 * k + 1] *= a;
+                }
+            }
+            uint32_t pa[4], pl[4] = {};
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float x = ex2(s[n][2 * k] - base[k]), y = ex2(s[n][2 * k + 1] - base[k]);
+                    l[k] += x + y;
+                    pa[2 * n + k] = Two<T>::pack(x, y);
+                    if constexpr (LO) {
+                        const float2 hi = Two<T>::unpack(pa[2 * n + k]);
+                        pl[2 * n + k] = Two<T>::pack(x - hi.x, y - hi.y);
+                    }
+                }
+            tile_values<D, VF, T, LO>(global_tile<VGeo<D, VF>::RB>(p.v, 1, page, h, off, live), g, t, pa, pl, o);
+        }
+
+        // join the warps: rows' maxima and sums, then the outputs rescaled to the common maximum
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            l[k] += __shfl_xor_sync(kAll, l[k], 1);
+            l[k] += __shfl_xor_sync(kAll, l[k], 2);
+            if (t == 0) {
+                s_m[warp][g + 8 * k] = m[k];
+                s_l[warp][g + 8 * k] = l[k];
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int r = g + 8 * k;
+            if (r >= G) continue;
+            float mm = -INFINITY;
+            for (int w = 0; w < kDW; ++w) mm = fmaxf(mm, s_m[w][r]);
+            const float a = mm == -INFINITY ? 0.f : ex2(m[k] - mm);
+            float* dst = smem + ((int64_t)warp * G + r) * D;
+            using V = VGeo<D, VF>;
+#pragma unroll
+            for (int j = 0; j < V::NJ; ++j)
+#pragma unroll
+                for (int c = 0; c < V::CH; ++c) {
+                    dst[ochan<D, VF>(j, 2 * t) + c] = o[V::CH * j + c][2 * k] * a;
+                    dst[ochan<D, VF>(j, 2 * t + 1) + c] = o[V::CH * j + c][2 * k + 1] * a;
+                }
+        }
+        __syncthreads();
+        const bool whole = i0 == 0 && i1 == st.n;
+        float* part = p.ws + ((int64_t)blockIdx.x + (int64_t)b * H + h) * partial_floats(G, D);
+        for (int e = threadIdx.x; e < G * D / 2; e += kDT) {
+            const int r = 2 * e / D;
+            float x = 0.f, y = 0.f;
+            for (int w = 0; w < kDW; ++w) {
+                const float2 f = *reinterpret_cast<const float2*>(smem + (int64_t)w * G * D + 2 * e);
+                x += f.x;
+                y += f.y;
+            }
+            if (whole) {
+                float mm = -INFINITY, ll = 0.f;
+                for (int w = 0; w < kDW; ++w) mm = fmaxf(mm, s_m[w][r]);
+                for (int w = 0; w < kDW; ++w) ll += mm == -INFINITY ? 0.f : s_l[w][r] * ex2(s_m[w][r] - mm);
+                const float inv = ll > 0.f ? 1.f / ll : 0.f;
+                reinterpret_cast<uint32_t*>((TQ*)p.out + ((int64_t)b * p.Hq + h * G) * D)[e] = Two<TQ>::pack(x * inv, y * inv);
+            } else {
+                *reinterpret_cast<float2*>(part + 32 + 2 * e) = make_float2(x, y);
+            }
+        }
+        if (threadIdx.x < G) {
+            const int r = threadIdx.x;
+            float mm = -INFINITY, ll = 0.f;
+            for (int w = 0; w < kDW; ++w) mm = fmaxf(mm, s_m[w][r]);
+            for (int w = 0; w < kDW; ++w) ll += mm == -INFINITY ? 0.f : s_l[w][r] * ex2(s_m[w][r] - mm);
+            if (!whole) {
+                part[r] = mm;
+                part[16 + r] = ll;
+            } else if (p.lse) {
+                p.lse[(int64_t)b * p.Hq + h * G + r] = ll > 0.f ? (mm + log2f(ll)) * kLn2 : -INFINITY;
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// One CTA per (sequence, KV head): joins the runs' partials, and writes zeros for a head without tiles.
+constexpr int kMT = 128;
+template <int D, typename TQ>
+__global__ void __launch_bounds__(kMT) merge_kernel(PagedAttnParams p) {
+    __shared__ int64_t red[kMT / 32];
+    const int b = blockIdx.x / p.v.H, h = blockIdx.x % p.v.H, H = p.v.H, G = p.G;
+    int64_t all = 0, before = 0;
+    for (int i = threadIdx.x; i < p.n_seq; i += kMT) {
+        const int64_t n = (int64_t)seq_tiles(p, i).n * H;
+        all += n;
+        if (i < b) before += n;
+    }
+    all = block_sum<kMT>(all, red);
+    before = block_sum<kMT>(before, red);
+    const int n = seq_tiles(p, b).n;
+    TQ* out = (TQ*)p.out + ((int64_t)b * p.Hq + h * G) * D;
+    if (n == 0) {
+        for (int e = threadIdx.x; e < G * D / 2; e += kMT) reinterpret_cast<uint32_t*>(out)[e] = 0;
+        if (p.lse && threadIdx.x < G) p.lse[(int64_t)b * p.Hq + h * G + threadIdx.x] = -INFINITY;
+        return;
+    }
+    const int64_t U = run_tiles(all, p.n_cta), s0 = before + (int64_t)h * n;
+    const int c0 = (int)(s0 / U), c1 = (int)((s0 + n - 1) / U);
+    if (c0 == c1) return;
+    const int64_t pf = partial_floats(G, D);
+    const float* part = p.ws + ((int64_t)b * H + h) * pf;
+    for (int e = threadIdx.x; e < G * D / 2; e += kMT) {
+        const int r = 2 * e / D;
+        float m = -INFINITY;
+        for (int c = c0; c <= c1; ++c) m = fmaxf(m, part[c * pf + r]);
+        float l = 0.f, x = 0.f, y = 0.f;
+        for (int c = c0; c <= c1; ++c) {
+            const float a = m == -INFINITY ? 0.f : ex2(part[c * pf + r] - m);
+            const float2 f = *reinterpret_cast<const float2*>(part + c * pf + 32 + 2 * e);
+            l += part[c * pf + 16 + r] * a;
+            x += f.x * a;
+            y += f.y * a;
+        }
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        reinterpret_cast<uint32_t*>(out)[e] = Two<TQ>::pack(x * inv, y * inv);
+        if (p.lse && (2 * e) % D == 0) p.lse[(int64_t)b * p.Hq + h * G + r] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    }
+}
+
+template <int D, int KF, int VF, typename T, typename TQ>
+int decode_run(const PagedAttnParams& p, int sm_count, cudaStream_t s) {
+    PagedAttnParams a = p;
+    const size_t smem = (size_t)kDW * p.G * D * 4;
+    auto k = decode_kernel<D, KF, VF, T, TQ>;
+    if (smem > 48 * 1024 && cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+        return (int)cudaGetLastError();
+    int res = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&res, k, kDT, smem) != cudaSuccess) return (int)cudaGetLastError();
+    a.n_cta = min(kMaxDecodeCtas, sm_count * (res > 0 ? res : 1));
+    k<<<a.n_cta, kDT, smem, s>>>(a);
+    merge_kernel<D, TQ><<<p.n_seq * p.v.H, kMT, 0, s>>>(a);
+    return (int)cudaGetLastError();
+}
+
+template <int D> int decode_d(const PagedAttnParams& p, int sms, cudaStream_t s) {
+    const int kf = p.v.fmt[0], vf = p.v.fmt[1];
+    if (kf == KVQ_F16) return decode_run<D, PF_16, PF_16, __half, __half>(p, sms, s);
+    if (kf == KVQ_BF16) return decode_run<D, PF_16, PF_16, __nv_bfloat16, __nv_bfloat16>(p, sms, s);
+    if (p.dtype == KVQ_F16) {
+        if (kf == KVQ_Q4_0) return decode_run<D, PF_Q4, PF_Q4, __half, __half>(p, sms, s);
+        if (vf == KVQ_Q4_0) return decode_run<D, PF_Q8, PF_Q4, __half, __half>(p, sms, s);
+        return decode_run<D, PF_Q8, PF_Q8, __half, __half>(p, sms, s);
+    }
+    if (kf == KVQ_Q4_0) return decode_run<D, PF_Q4, PF_Q4, __half, __nv_bfloat16>(p, sms, s);
+    if (vf == KVQ_Q4_0) return decode_run<D, PF_Q8, PF_Q4, __half, __nv_bfloat16>(p, sms, s);
+    return decode_run<D, PF_Q8, PF_Q8, __half, __nv_bfloat16>(p, sms, s);
+}
+
+}  // namespace
+
+size_t paged_decode_ws_floats(int G, int D, int64_t segments) {
+    return (size_t)((kMaxDecodeCtas + segments) * partial_floats(G, D));
+}
+
+int launch_paged_decode(PagedAttnParams p, int sm_count, void* stream) {
+    cudaStream_t s = (cudaStream_t)stream;
+    if (p.v.D == 64) return decode_d<64>(p, sm_count, s);
+    if (p.v.D == 128) return decode_d<128>(p, sm_count, s);
+    return decode_d<256>(p, sm_count, s);
+}
+
+}  // namespace kvq

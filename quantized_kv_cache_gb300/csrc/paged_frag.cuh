@@ -1,0 +1,303 @@
+// Warp-level pieces of the paged attention kernels: page rows turned into mma.sync operands.
+//
+// One warp holds 16 query rows (M of m16n8k16) against a tile of 16 positions of one page. Both
+// products take their operands from 16-byte pieces of the rows, in whatever order the lanes read
+// them: the channel order of the score product is free (the query fragments follow it), and so is
+// the channel order of the output tiles. With g = lane / 4, t = lane % 4:
+//  - scores, S[16 x 8 positions] = Q K^T: lane (g, t) reads pieces t, t + 4, .. of row g; each piece
+//    feeds k-steps whose channels qchan() names;
+//  - values, O[16 x 8 channels] = P V: lane (g, t) reads pieces g, g + 8, .. of rows 2t, 2t+1, 2t+8,
+//    2t+9 and pairs the rows channel by channel (byte permutes); a piece's i-th channel is the
+//    lane's column of output tile i, so a lane ends with runs of consecutive output channels.
+// The accumulator layout of S is the A-operand layout of P, so no data crosses lanes but the row
+// maxima. Codes become exact fp16 integers (an exponent placed around the code bits, one subtract),
+// then code x scale is rounded to fp16 once.
+#pragma once
+#include <type_traits>
+#include "paged_common.cuh"
+
+namespace kvq {
+namespace {
+
+enum { PF_16 = 0, PF_Q8 = 1, PF_Q4 = 2 };   // row encodings: 16-bit values, int8 codes, nibbles
+
+__device__ __forceinline__ void mma_t(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, __half) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_t(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, __nv_bfloat16) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ __half2 h2(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
+__device__ __forceinline__ uint32_t u32(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+// raw halves (1024 + u), u = code + off, times the scale pair d: fp16(code x scale), one rounding.
+__device__ __forceinline__ uint32_t deq(uint32_t raw, float off1024, uint32_t d) {
+    return u32(__hmul2(__hsub2(h2(raw), __float2half2_rn(off1024)), h2(d)));
+}
+// (r & 0x000f000f) | 0x64006400 and (r & 0x00ff00ff) ^ 0x64806480: one logic operation each.
+__device__ __forceinline__ uint32_t nib_raw(uint32_t r) { return (r & 0x000f000fu) | 0x64006400u; }
+// nibbles at bits 4-7 of each half: 1024 + 16 n
+__device__ __forceinline__ uint32_t nib_raw_hi(uint32_t r) { return (r & 0x00f000f0u) | 0x64006400u; }
+__device__ __forceinline__ uint32_t deq_hi(uint32_t raw, uint32_t d) {
+    // (1024 + 16 n) / 16 - 72 = n - 8, exact
+    return u32(__hmul2(__hfma2(h2(raw), __float2half2_rn(0.0625f), __float2half2_rn(-72.f)), h2(d)));
+}
+__device__ __forceinline__ uint32_t byte_raw(uint32_t r) { return (r & 0x00ff00ffu) ^ 0x64806480u; }
+// four nibbles of each half of r (two rows' halfwords): operand registers of nibble positions 0..3
+__device__ __forceinline__ void nib_pairs(uint32_t r, uint32_t d, uint32_t (&o)[4]) {
+    o[0] = deq(nib_raw(r), 1032.f, d);
+    o[1] = deq_hi(nib_raw_hi(r), d);
+    const uint32_t s = r >> 8;
+    o[2] = deq(nib_raw(s), 1032.f, d);
+    o[3] = deq_hi(nib_raw_hi(s), d);
+}
+// two signed bytes of each half of r
+__device__ __forceinline__ void byte_pairs(uint32_t r, uint32_t d, uint32_t& o0, uint32_t& o1) {
+    o0 = deq(byte_raw(r), 1152.f, d);
+    o1 = deq(byte_raw(r >> 8), 1152.f, d);
+}
+
+template <int N> struct Words { uint32_t w[N]; };
+
+template <int D, int PF> struct KGeo {
+    static constexpr int RB = PF == PF_16 ? 2 * D : (PF == PF_Q8 ? D : D / 2);   // row bytes
+    static constexpr int CB = RB / 4 < 16 ? RB / 4 : 16;                          // piece bytes
+    static constexpr int NJ = RB / 4 / CB, NW = CB / 4;                           // pieces, words of one
+    static constexpr int CH = PF == PF_16 ? CB / 2 : (PF == PF_Q8 ? CB : CB * 2); // channels of one
+};
+template <int D, int PF> struct VGeo {
+    static constexpr int RB = KGeo<D, PF>::RB;
+    static constexpr int CB = RB / 8 < 16 ? RB / 8 : 16;
+    static constexpr int NJ = RB / 8 / CB, NW = CB / 4;
+    static constexpr int CH = PF == PF_16 ? CB / 2 : (PF == PF_Q8 ? CB : CB * 2);
+};
+
+// Channel of element e (0, 1: the low k pair, 2, 3: the high pair) of k-step ks of lane t.
+template <int D, int PF> __device__ __forceinline__ int qchan(int ks, int t, int e) {
+    constexpr int CH = KGeo<D, PF>::CH, KS = CH / 4;            // k-steps of a piece
+    const int base = CH * (t + 4 * (ks / KS)), r = ks % KS;
+    if (PF != PF_Q4) return base + 4 * r + e;
+    return base + 8 * (r / 2) + 2 * (r & 1) + (e >> 1) + 4 * (e & 1);
+}
+
+// First of the CH consecutive output channels that column `col` (0..7) has in piece j's tiles.
+template <int D, int PF> __device__ __forceinline__ int ochan(int j, int col) { return VGeo<D, PF>::CH * (col + 8 * j); }
+
+// s[n] += q K^T of positions 8n .. 8n+7. `src` gives piece(row, byte) and scale(row, block) of the tile.
+template <int D, int PF, typename T, typename SRC>
+__device__ __forceinline__ void tile_scores(const SRC& src, int g, int t, const uint32_t (&qf)[D / 16][4], float (&s)[2][4]) {
+    using K = KGeo<D, PF>;
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+        const int row = g + 8 * n;
+#pragma unroll
+        for (int j = 0; j < K::NJ; ++j) {
+            const Words<K::NW> p = src.template piece<K::NW>(row, K::CB * (t + 4 * j));
+            constexpr int KS = K::CH / 4;
+            if constexpr (PF == PF_16) {
+                mma_t(s[n], qf[KS * j], p.w[0], p.w[1], T());
+                mma_t(s[n], qf[KS * j + 1], p.w[2], p.w[3], T());
+            } else {
+                const uint32_t d1 = src.scale(row, K::CH * (t + 4 * j) / 32), d = d1 | (d1 << 16);
+#pragma unroll
+                for (int i = 0; i < K::NW; ++i) {
+                    if constexpr (PF == PF_Q8) {
+                        const uint32_t x = __byte_perm(p.w[i], 0, 0x3120);    // bytes 0,2 | 1,3: halves (b0 b2), (b1 b3)
+                        uint32_t a, b;
+                        byte_pairs(x, d, a, b);                                // (b0, b1), (b2, b3)
+                        mma_t(s[n], qf[KS * j + i], a, b, T());
+                    } else {
+                        uint32_t o[4];
+                        nib_pairs(p.w[i], d, o);                               // (n0, n4), (n1, n5), (n2, n6), (n3, n7)
+                        mma_t(s[n], qf[KS * j + 2 * i], o[0], o[1], T());
+                        mma_t(s[n], qf[KS * j + 2 * i + 1], o[2], o[3], T());
+                    }
+                }
+            }
+        }
+    }
+}
+
+// o += P V of the tile's 16 positions. With LO, P = pa + pl (two bf16 parts).
+template <int D, int PF, typename T, bool LO, typename SRC>
+__device__ __forceinline__ void tile_values(const SRC& src, int g, int t, const uint32_t (&pa)[4], const uint32_t (&pl)[4],
+                                            float (&o)[D / 8][4]) {
+    using V = VGeo<D, PF>;
+#pragma unroll
+    for (int j = 0; j < V::NJ; ++j) {
+        const int at = V::CB * (g + 8 * j);
+        const Words<V::NW> r0 = src.template piece<V::NW>(2 * t, at), r1 = src.template piece<V::NW>(2 * t + 1, at);
+        const Words<V::NW> r2 = src.template piece<V::NW>(2 * t + 8, at), r3 = src.template piece<V::NW>(2 * t + 9, at);
+        uint32_t d01 = 0, d23 = 0;
+        if constexpr (PF != PF_16) {
+            const int blk = V::CH * (g + 8 * j) / 32;
+            d01 = src.scale(2 * t, blk) | (src.scale(2 * t + 1, blk) << 16);
+            d23 = src.scale(2 * t + 8, blk) | (src.scale(2 * t + 9, blk) << 16);
+        }
+#pragma unroll
+        for (int i = 0; i < V::NW; ++i) {
+            const uint32_t xl = __byte_perm(r0.w[i], r1.w[i], 0x5410), xh = __byte_perm(r0.w[i], r1.w[i], 0x7632);
+            const uint32_t yl = __byte_perm(r2.w[i], r3.w[i], 0x5410), yh = __byte_perm(r2.w[i], r3.w[i], 0x7632);
+            constexpr int N = V::CH / V::NW;      // channels of a word: 2, 4, 8
+            uint32_t b0[N], b1[N];
+            if constexpr (PF == PF_16) {
+                b0[0] = xl; b0[1] = xh; b1[0] = yl; b1[1] = yh;
+            } else if constexpr (PF == PF_Q8) {
+                byte_pairs(xl, d01, b0[0], b0[1]);
+                byte_pairs(xh, d01, b0[2], b0[3]);
+                byte_pairs(yl, d23, b1[0], b1[1]);
+                byte_pairs(yh, d23, b1[2], b1[3]);
+            } else {
+                nib_pairs(xl, d01, *(uint32_t(*)[4])&b0[0]);
+                nib_pairs(xh, d01, *(uint32_t(*)[4])&b0[4]);
+                nib_pairs(yl, d23, *(uint32_t(*)[4])&b1[0]);
+                nib_pairs(yh, d23, *(uint32_t(*)[4])&b1[4]);
+            }
+#pragma unroll
+            for (int c = 0; c < N; ++c) {
+                float (&acc)[4] = o[V::CH * j + N * i + c];
+                mma_t(acc, pa, b0[c], b1[c], T());
+                if constexpr (LO) mma_t(acc, pl, b0[c], b1[c], T());
+            }
+        }
+    }
+}
+
+// Whether the tile holds an infinity or NaN among its values (16-bit values or scales of type T).
+template <int D, int PF, typename T, typename SRC>
+__device__ __forceinline__ bool tile_nonfinite(const SRC& src, int lane) {
+    constexpr uint32_t top = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
+    bool bad = false;
+    if constexpr (PF == PF_16) {
+        for (int i = lane; i < 16 * D / 8; i += 32) {
+            const Words<4> w = src.template piece<4>(i / (D / 8), i % (D / 8) * 16);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) bad |= (w.w[e] & top) == top || ((w.w[e] >> 16) & top) == top;
+        }
+    } else {
+        for (int i = lane; i < 16 * D / 32; i += 32) bad |= (src.scale(i / (D / 32), i % (D / 32)) & top) == top;
+    }
+    return __any_sync(kAll, bad);
+}
+
+// One value of the tile as the products see it.
+template <int D, int PF, typename T, typename SRC>
+__device__ __forceinline__ float tile_value(const SRC& src, int row, int ch) {
+    if constexpr (PF == PF_16) {
+        const uint32_t w = src.template piece<1>(row, ch / 2 * 4).w[0];
+        const float2 f = Two<T>::unpack(w);
+        return ch & 1 ? f.y : f.x;
+    } else {
+        const float d = __half2float(__ushort_as_half((uint16_t)src.scale(row, ch / 32)));
+        const uint32_t w = src.template piece<1>(row, (PF == PF_Q8 ? ch : ch / 2) / 4 * 4).w[0];
+        const int c = PF == PF_Q8 ? (int)(int8_t)(w >> (8 * (ch & 3))) : (int)((w >> (4 * (ch & 7))) & 15u) - 8;
+        return __half2float(__float2half_rn((float)c * d));
+    }
+}
+
+// Query fragments of the 16 rows of a warp; row r is at base + rows(r) (null: a row of zeros), of
+// type TQ. fp16 operands of bf16 queries are scaled by a power of two per row so that no exponent
+// is out of range; back[] undoes it (rows g, g + 8).
+template <int D, int PF, typename T, typename TQ, typename ROW>
+__device__ __forceinline__ void load_queries(const ROW& rows, int g, int t, uint32_t (&qf)[D / 16][4], float (&back)[2]) {
+    constexpr bool same = std::is_same<T, TQ>::value;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        const TQ* p = rows(g + 8 * half);
+        float up = 1.f;
+        back[half] = 1.f;
+        if constexpr (!same) {
+            float a = 0.f;
+            if (p) {
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) {
+                    float f[8];
+                    unpack8<TQ>(*reinterpret_cast<const uint4*>(p + (D / 4) * t + 8 * i), f);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) a = fmaxf(a, fabsf(f[e]));
+                }
+            }
+            a = fmaxf(a, __shfl_xor_sync(kAll, a, 1));
+            a = fmaxf(a, __shfl_xor_sync(kAll, a, 2));
+            const int ex = (int)((__float_as_uint(a) >> 23) & 255) - 127;
+            if (a > 0.f && ex < 128) {
+                const int sh = min(max(14 - ex, -100), 100);         // the largest magnitude to [2^14, 2^15)
+                up = __uint_as_float((uint32_t)(127 + sh) << 23);
+                back[half] = __uint_as_float((uint32_t)(127 - sh) << 23);
+            }
+        }
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+            for (int hi = 0; hi < 2; ++hi) {
+                uint32_t u = 0;
+                if (p) {
+                    const uint32_t a = *reinterpret_cast<const uint16_t*>(p + qchan<D, PF>(ks, t, 2 * hi));
+                    const uint32_t b = *reinterpret_cast<const uint16_t*>(p + qchan<D, PF>(ks, t, 2 * hi + 1));
+                    u = a | (b << 16);
+                    if constexpr (!same) {
+                        const float2 f = Two<TQ>::unpack(u);
+                        u = Two<T>::pack(f.x * up, f.y * up);
+                    }
+                }
+                qf[ks][2 * hi + half] = u;
+            }
+    }
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+    return y;
+}
+
+constexpr float kL2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+// The score options, in units of log2: apply(q.k, row factor, |distance|, slope).
+struct ScoreRule {
+    float scale, cap, cap_l2;      // softmax scale; softcap (0: none); softcap * log2(e)
+    __device__ __forceinline__ float operator()(float dot, float back, float dist, float slope_l2) const {
+        float x = dot * (back * scale);
+        x = cap > 0.f ? cap_l2 * tanhf(x / cap) : x * kL2e;
+        return x - slope_l2 * dist;
+    }
+};
+
+// A tile's rows in global memory; rows that no query of the call sees read as zeros.
+template <int RB> struct GlobalTile {
+    const uint8_t* codes;      // row 0 of the tile (null: the page number was out of range)
+    const uint8_t* scales;
+    int scale_row;             // bytes of a row's scales
+    uint32_t live;             // bit r: row r is visible
+    template <int N> __device__ __forceinline__ Words<N> piece(int row, int byte) const {
+        Words<N> w = {};
+        if ((live >> row) & 1) {
+            const uint8_t* a = codes + row * RB + byte;
+            if constexpr (N == 4) *reinterpret_cast<uint4*>(w.w) = *reinterpret_cast<const uint4*>(a);
+            else if constexpr (N == 2) *reinterpret_cast<uint2*>(w.w) = *reinterpret_cast<const uint2*>(a);
+            else w.w[0] = *reinterpret_cast<const uint32_t*>(a);
+        }
+        return w;
+    }
+    __device__ __forceinline__ uint32_t scale(int row, int blk) const {
+        return (live >> row) & 1 ? *reinterpret_cast<const uint16_t*>(scales + row * scale_row + 2 * blk) : 0u;
+    }
+};
+
+template <int RB>
+__device__ __forceinline__ GlobalTile<RB> global_tile(const PagedView& v, int w, int page, int head, int off, uint32_t live) {
+    GlobalTile<RB> s;
+    const uint8_t* u = unit_at(v, w, page, head);
+    s.codes = u + (int64_t)off * RB;
+    s.scale_row = v.D / 16;
+    s.scales = u + (int64_t)v.ps * RB + off * s.scale_row;
+    s.live = live;
+    return s;
+}
+
+}  // namespace
+}  // namespace kvq

@@ -1,0 +1,73 @@
+// Internal definitions of the paged cache shared by its host side and its kernels: the pool's
+// geometry, row encodings and the launch parameter blocks. Not part of the public C ABI.
+#pragma once
+#include "kvq_internal.h"
+#include "../../include/kvq_paged.h"
+
+namespace kvq {
+
+constexpr int kTile = 16;            // positions per attention tile: every page size is a multiple
+constexpr int kMaxDecodeCtas = 1024; // bound of a decode launch's CTAs (sizes the workspace)
+
+// Bytes of one code row (D values) and of a row's scales.
+KVQ_HD int paged_row_bytes(int fmt, int D) { return fmt == KVQ_Q8_0 ? D : (fmt == KVQ_Q4_0 ? D / 2 : 2 * D); }
+KVQ_HD int paged_scale_bytes(int fmt, int D) { return (fmt == KVQ_Q8_0 || fmt == KVQ_Q4_0) ? D / 16 : 0; }
+KVQ_HD int64_t paged_unit_bytes(int fmt, int D, int ps) {
+    return (int64_t)ps * (paged_row_bytes(fmt, D) + paged_scale_bytes(fmt, D));
+}
+
+// One layer of the pool as the kernels see it.
+struct PagedView {
+    uint8_t* base[2];        // first unit of the K, V area
+    int64_t unit[2];         // bytes of a unit
+    uint32_t* status;
+    int32_t fmt[2];
+    int32_t H, D, ps, ps_shift, n_pages;
+};
+
+struct WriteParams {
+    PagedView v;
+    const void* src[2];
+    int64_t stride[2];       // elements
+    const int32_t* slots;
+    int32_t n_tok, dtype;
+};
+
+struct ReadParams {
+    PagedView v;
+    const int32_t* table;
+    const int32_t* cu;
+    const int32_t* start;
+    void* out[2];
+    int64_t table_stride;
+    int32_t n_seq, max_pages, n_rows, dtype;
+};
+
+struct PagedAttnParams {
+    PagedView v;
+    const void* q;
+    void* out;
+    float* lse;
+    const int32_t* table;
+    const int32_t* lens;
+    const int32_t* cu;       // prefill only
+    const int32_t* prefix;
+    const float* slopes;
+    float* ws;
+    int64_t q_stride, table_stride;
+    int32_t n_seq, max_pages, Hq, G, dtype;
+    int32_t n_rows, max_q;   // prefill only
+    int32_t window;
+    int32_t n_cta;           // decode: CTAs of the split launch; prefill: splits of a sequence
+    float scale, softcap;
+};
+
+int launch_norm_rope(const kvq_norm_rope_args& a, int sm_count, void* stream);
+int launch_paged_write(const WriteParams& p, void* stream);
+int launch_paged_read(const ReadParams& p, void* stream);
+int launch_paged_decode(PagedAttnParams p, int sm_count, void* stream);
+int launch_paged_prefill(PagedAttnParams p, int sm_count, void* stream);
+size_t paged_decode_ws_floats(int G, int D, int64_t segments);
+size_t paged_prefill_ws_floats(int G, int D, int H, int64_t rows);
+
+}  // namespace kvq
