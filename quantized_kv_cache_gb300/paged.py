@@ -32,43 +32,48 @@ def paged_config(n_layers, n_kv_heads, head_dim, n_q_heads, page_size, n_pages, 
     return c
 
 
-def _need(ok, what):
-    if not ok:
-        raise ValueError(what)
+# The checks run on every call of a decode step, so they build no message unless they fail.
+def _bad(what):
+    raise ValueError(what)
 
 
-def _ints(x, name, shape, dev):
-    _need(x.dtype is torch.int32 and x.device == dev, f"{name}: an int32 tensor on {dev} is wanted")
-    _need(tuple(x.shape) == shape and x.is_contiguous(), f"{name}: contiguous, of shape {shape}")
+def _ints(x, name, n, dev):
+    """Address of a contiguous int32 vector of n elements on device `dev`."""
+    if x.dtype is not torch.int32 or x.get_device() != dev or x.shape != (n,) or not x.is_contiguous():
+        _bad(f"{name}: a contiguous int32 tensor of shape ({n},) on cuda:{dev} is wanted")
     return x.data_ptr()
 
 
-def _rows(x, name, heads, D, dev, dtype=None):
-    """Token stride of [tokens, heads, D] rows whose heads lie behind one another."""
-    _need(x.device == dev and x.dim() == 3 and x.shape[1] == heads and x.shape[2] == D,
-          f"{name}: [tokens, {heads}, {D}] on {dev} is wanted, not {tuple(x.shape)} on {x.device}")
-    _need(dtype is None or x.dtype is dtype, f"{name}: {dtype} is wanted, not {x.dtype}")
-    st = x.stride()
-    _need(x.numel() == 0 or (st[2] == 1 and (heads == 1 or st[1] == D)), f"{name}: a token's heads must be contiguous")
-    if x.shape[0] <= 1:
-        return max(st[0], heads * D) // 8 * 8
-    return st[0]
+def _rows(x, name, heads, D, dev, dtype):
+    """(tokens, token stride) of [tokens, heads, D] rows whose heads lie behind one another."""
+    shape = x.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != D or x.get_device() != dev or x.dtype is not dtype:
+        _bad(f"{name}: {dtype} [tokens, {heads}, {D}] on cuda:{dev} is wanted, not {x.dtype} {tuple(shape)} on {x.device}")
+    n, (st, sh, sd) = shape[0], x.stride()
+    if n and (sd != 1 or (sh != D and heads != 1)):
+        _bad(f"{name}: a token's heads must be contiguous")
+    return n, (st if n > 1 else heads * D)
 
 
-def _on(dev):
-    """Makes `dev` current for a call where it is not."""
-    return torch.cuda.device(dev) if torch.cuda.current_device() != dev.index else _Here
+def _out_rows(x, name, n, heads, D, dev, dtype):
+    if x.shape != (n, heads, D) or x.get_device() != dev or x.dtype is not dtype or not x.is_contiguous():
+        _bad(f"{name}: contiguous {dtype} of shape ({n}, {heads}, {D}) on cuda:{dev} is wanted")
+    return x.data_ptr()
 
 
-class _HereType:
-    def __enter__(self):
-        return self
+def _type_of(x, name, types):
+    t = types.get(x.dtype)
+    if t is None:
+        _bad(f"{name}: one of {', '.join(map(str, types))} is wanted, not {x.dtype}")
+    return t
 
-    def __exit__(self, *a):
-        return False
 
-
-_Here = _HereType()
+def _guarded(dev, call, *args):
+    """call(*args) with device `dev` current."""
+    if torch.cuda.current_device() == dev:
+        return call(*args)
+    with torch.cuda.device(dev):
+        return call(*args)
 
 
 class PagedKVCache:
@@ -85,13 +90,14 @@ class PagedKVCache:
         self.pool_bytes, self.ws_bytes = _lib.kv_paged_required_bytes(cfg, max_seqs, max_tokens)
         if pool is None:
             pool = torch.zeros(self.pool_bytes, dtype=torch.uint8, device=self.device)
-        _need(pool.device == self.device and pool.dtype is torch.uint8 and pool.is_contiguous() and
-              pool.numel() >= self.pool_bytes, f"pool: {self.pool_bytes} contiguous bytes on {self.device} are wanted")
+        if (pool.device != self.device or pool.dtype is not torch.uint8 or not pool.is_contiguous() or
+                pool.numel() < self.pool_bytes):
+            _bad(f"pool: {self.pool_bytes} contiguous bytes on {self.device} are wanted")
         self.pool = pool
         self.ws = self.new_workspace()
-        with _on(self.device):
-            torch.cuda.current_stream().synchronize()      # the pool's contents, before the status word is set
-            self.h = _lib.kv_paged_create(cfg, pool.data_ptr(), pool.numel(), device)
+        self._dev, self._H, self._Hq, self._D = device, cfg.n_kv_heads, cfg.n_q_heads, cfg.head_dim
+        torch.cuda.current_stream(self.device).synchronize()      # the pool's contents, before the status word is set
+        self.h = _guarded(device, _lib.kv_paged_create, cfg, pool.data_ptr(), pool.numel(), device)
 
     def new_workspace(self):
         return torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.device)
@@ -109,87 +115,94 @@ class PagedKVCache:
 
     def status(self):
         """The device status word (bits PAGED_* of ``_lib``), read synchronously and cleared."""
-        with _on(self.device):
-            return _lib.kv_paged_get_status(self.h)
+        return _guarded(self._dev, _lib.kv_paged_get_status, self.h)
 
     def write(self, layer, k, v, slots, stream=0):
         """k, v: [tokens, H, D] fp16 or bf16, token stride free; slots: int32 [tokens], page * page_size + row,
         negative to skip. Slots of one call must differ from one another."""
-        c = self.cfg
-        _need(k.dtype in _DT, f"k: fp16 or bf16 is wanted, not {k.dtype}")
-        ks = _rows(k, "k", c.n_kv_heads, c.head_dim, self.device)
-        vs = _rows(v, "v", c.n_kv_heads, c.head_dim, self.device, k.dtype)
-        n = k.shape[0]
-        _need(v.shape[0] == n, "k and v: the same number of tokens")
-        sp = _ints(slots, "slots", (n,), self.device)
-        with _on(self.device):
-            _lib.kv_paged_write(self.h, layer, _DT[k.dtype], n, k.data_ptr(), ks, v.data_ptr(), vs, sp, stream)
+        dt = _type_of(k, "k", _DT)
+        n, ks = _rows(k, "k", self._H, self._D, self._dev, k.dtype)
+        nv, vs = _rows(v, "v", self._H, self._D, self._dev, k.dtype)
+        if nv != n:
+            _bad("k and v: the same number of tokens is wanted")
+        sp = _ints(slots, "slots", n, self._dev)
+        _guarded(self._dev, _lib.kv_paged_write, self.h, layer, dt, n, k.data_ptr(), ks, v.data_ptr(), vs, sp, stream)
 
     def _table(self, table):
-        _need(table.dtype is torch.int32 and table.device == self.device and table.dim() == 2 and
-              (table.stride(1) == 1 or table.shape[1] == 1),
-              f"page_table: int32 [sequences, pages] on {self.device}, rows contiguous")
-        n, w = table.shape
-        return table.data_ptr(), n, w, max(table.stride(0), w) if n <= 1 else table.stride(0)
+        """(address, sequences, entries of a row, row stride) of a page table."""
+        if table.dtype is not torch.int32 or table.get_device() != self._dev or table.dim() != 2:
+            _bad(f"page_table: int32 [sequences, pages] on {self.device} is wanted")
+        (n, w), (st, se) = table.shape, table.stride()
+        if se != 1 and w > 1:
+            _bad("page_table: a sequence's entries must be contiguous")
+        return table.data_ptr(), n, w, st if n > 1 else w
 
     def read(self, layer, page_table, cu_rows, k_out=None, v_out=None, start=None, stream=0):
         """Rows cu_rows[b].. of k_out / v_out ([rows, H, D] contiguous fp16, bf16 or fp32; either may be
         None) receive positions start[b].. of sequence b. cu_rows: int32 [sequences + 1]."""
-        c = self.cfg
         tp, n, w, ts = self._table(page_table)
-        outs = [x for x in (k_out, v_out) if x is not None]
-        _need(outs, "read: k_out or v_out is wanted")
-        _need(outs[0].dtype in _DT_READ, f"read: fp16, bf16 or fp32 rows are wanted, not {outs[0].dtype}")
-        for x in outs:
-            _rows(x, "out", c.n_kv_heads, c.head_dim, self.device, outs[0].dtype)
-            _need(x.is_contiguous() and x.shape == outs[0].shape, "k_out, v_out: contiguous, of one shape")
-        cp = _ints(cu_rows, "cu_rows", (n + 1,), self.device)
-        sp = None if start is None else _ints(start, "start", (n,), self.device)
-        with _on(self.device):
-            _lib.kv_paged_read(self.h, layer, _DT_READ[outs[0].dtype], n, tp, w, ts, cp, sp, outs[0].shape[0],
-                               None if k_out is None else k_out.data_ptr(), None if v_out is None else v_out.data_ptr(),
-                               stream)
+        x = k_out if k_out is not None else v_out
+        if x is None:
+            _bad("read: k_out or v_out is wanted")
+        dt, rows = _type_of(x, "k_out, v_out", _DT_READ), x.shape[0]
+        kp = None if k_out is None else _out_rows(k_out, "k_out", rows, self._H, self._D, self._dev, x.dtype)
+        vp = None if v_out is None else _out_rows(v_out, "v_out", rows, self._H, self._D, self._dev, x.dtype)
+        cp = _ints(cu_rows, "cu_rows", n + 1, self._dev)
+        sp = None if start is None else _ints(start, "start", n, self._dev)
+        _guarded(self._dev, _lib.kv_paged_read, self.h, layer, dt, n, tp, w, ts, cp, sp, rows, kp, vp, stream)
 
-    def _attn(self, q, page_table, lens, out, lse, softcap, window, slopes, prefix, ws):
-        c = self.cfg
-        _need(q.dtype in _DT, f"q: fp16 or bf16 is wanted, not {q.dtype}")
-        qs = _rows(q, "q", c.n_q_heads, c.head_dim, self.device)
-        tp, n, w, ts = self._table(page_table)
-        lp = _ints(lens, "lens", (n,), self.device)
-        _rows(out, "out", c.n_q_heads, c.head_dim, self.device, q.dtype)
-        _need(out.is_contiguous() and out.shape[0] == q.shape[0], "out: contiguous, of q's shape")
-        o = _lib.kvq_attn_opts()
-        o.softcap, o.window = softcap, window
-        for name, x, shape, dt in (("slopes", slopes, (c.n_q_heads,), torch.float32), ("prefix", prefix, (n,), torch.int32),
-                                   ("lse", lse, (q.shape[0], c.n_q_heads), torch.float32)):
-            if x is not None:
-                _need(x.dtype is dt and x.device == self.device and tuple(x.shape) == shape and x.is_contiguous(),
-                      f"{name}: contiguous {dt} of shape {shape} on {self.device}")
-                setattr(o, name, x.data_ptr())
-        ws = self.ws if ws is None else ws
-        _need(ws.device == self.device and ws.is_contiguous(), f"ws: contiguous, on {self.device}")
-        return qs, tp, n, w, ts, lp, ctypes.byref(o), ws.data_ptr(), ws.numel() * ws.element_size()
+    def _opts(self, n, rows, lse, softcap, window, slopes, prefix):
+        sp = pp = lp = None
+        if slopes is not None:
+            if (slopes.dtype is not torch.float32 or slopes.get_device() != self._dev or slopes.shape != (self._Hq,) or
+                    not slopes.is_contiguous()):
+                _bad(f"slopes: contiguous fp32 of shape ({self._Hq},) on {self.device} is wanted")
+            sp = slopes.data_ptr()
+        if prefix is not None:
+            pp = _ints(prefix, "prefix", n, self._dev)
+        if lse is not None:
+            if (lse.dtype is not torch.float32 or lse.get_device() != self._dev or lse.shape != (rows, self._Hq) or
+                    not lse.is_contiguous()):
+                _bad(f"lse: contiguous fp32 of shape ({rows}, {self._Hq}) on {self.device} is wanted")
+            lp = lse.data_ptr()
+        return ctypes.byref(_lib.kvq_attn_opts(softcap, window, sp, pp, lp))
+
+    def _space(self, ws):
+        if ws is None:
+            return self.ws.data_ptr(), self.ws_bytes
+        if ws.get_device() != self._dev or not ws.is_contiguous():
+            _bad(f"ws: contiguous, on {self.device}")
+        return ws.data_ptr(), ws.numel() * ws.element_size()
 
     def decode_attn(self, layer, q, page_table, lens, out, lse=None, softcap=0.0, window=0, slopes=None, prefix=None,
                     ws=None, stream=0):
         """Attention of one query per sequence. q: [sequences, Hq, D] fp16 or bf16 (token stride free), out alike
         and contiguous; lens: int32 [sequences], the new position included; lse: fp32 [sequences, Hq]."""
-        qs, tp, n, w, ts, lp, o, wp, wb = self._attn(q, page_table, lens, out, lse, softcap, window, slopes, prefix, ws)
-        _need(q.shape[0] == n, "q: one row per row of page_table")
-        with _on(self.device):
-            _lib.kv_paged_decode_attn(self.h, layer, _DT[q.dtype], n, q.data_ptr(), qs, tp, w, ts, lp, out.data_ptr(), o, wp,
-                                      wb, stream)
+        dt, dev = _type_of(q, "q", _DT), self._dev
+        tp, n, w, ts = self._table(page_table)
+        rows, qs = _rows(q, "q", self._Hq, self._D, dev, q.dtype)
+        if rows != n:
+            _bad(f"q: one row per row of page_table ({n}) is wanted, not {rows}")
+        lp = _ints(lens, "lens", n, dev)
+        op = _out_rows(out, "out", n, self._Hq, self._D, dev, q.dtype)
+        o = self._opts(n, n, lse, softcap, window, slopes, prefix)
+        wp, wb = self._space(ws)
+        _guarded(dev, _lib.kv_paged_decode_attn, self.h, layer, dt, n, q.data_ptr(), qs, tp, w, ts, lp, op, o, wp, wb, stream)
 
     def prefill_attn(self, layer, q, cu_q, max_q, page_table, lens, out, lse=None, softcap=0.0, window=0, slopes=None,
                      prefix=None, ws=None, stream=0):
         """Attention of a chunk of new tokens per sequence, whose rows are in the pages already: rows
         cu_q[b] .. cu_q[b+1]-1 of q ([rows, Hq, D]) are the last positions of the lens[b] that sequence b holds.
         max_q: at least the longest chunk."""
-        qs, tp, n, w, ts, lp, o, wp, wb = self._attn(q, page_table, lens, out, lse, softcap, window, slopes, prefix, ws)
-        cp = _ints(cu_q, "cu_q", (n + 1,), self.device)
-        with _on(self.device):
-            _lib.kv_paged_prefill_attn(self.h, layer, _DT[q.dtype], n, q.shape[0], max_q, q.data_ptr(), qs, cp, tp, w, ts, lp,
-                                       out.data_ptr(), o, wp, wb, stream)
+        dt, dev = _type_of(q, "q", _DT), self._dev
+        tp, n, w, ts = self._table(page_table)
+        rows, qs = _rows(q, "q", self._Hq, self._D, dev, q.dtype)
+        lp, cp = _ints(lens, "lens", n, dev), _ints(cu_q, "cu_q", n + 1, dev)
+        op = _out_rows(out, "out", rows, self._Hq, self._D, dev, q.dtype)
+        o = self._opts(n, rows, lse, softcap, window, slopes, prefix)
+        wp, wb = self._space(ws)
+        _guarded(dev, _lib.kv_paged_prefill_attn, self.h, layer, dt, n, rows, max_q, q.data_ptr(), qs, cp, tp, w, ts, lp, op,
+                 o, wp, wb, stream)
 
 
 def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, q_out=None, k_out=None, eps=1e-6, interleaved=False,
@@ -197,33 +210,44 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, q_out=None, k_out
     """RMS norm of every head of q [tokens, Hq, D] and k [tokens, H, D] and their rotation by position, in one
     pass; q or k may be None, a weight None leaves its side without the norm. cos_sin: fp32 [positions, rot],
     cosines then sines (None: no rotation); positions: int32 [tokens]. Outputs default to the inputs (in place)."""
-    a = _lib.kvq_norm_rope_args()
     x = q if q is not None else k
-    _need(x is not None and x.dim() == 3 and x.dtype in _DT and x.is_cuda, "q, k: [tokens, heads, D] fp16 or bf16 CUDA tensors")
-    dev, dt, n, D = x.device, x.dtype, x.shape[0], x.shape[2]
-    a.dtype, a.n_tok, a.head_dim, a.eps, a.interleaved = _DT[dt], n, D, eps, 1 if interleaved else 0
-    for name, t, wt, o in (("q", q, q_weight, q_out), ("k", k, k_weight, k_out)):
+    if x is None or x.dim() != 3 or not x.is_cuda:
+        _bad("q, k: [tokens, heads, D] CUDA tensors are wanted")
+    dt, dev, dtype, n, D = _type_of(x, "q, k", _DT), x.get_device(), x.dtype, x.shape[0], x.shape[2]
+    sides = []
+    for name, t, w, o in (("q", q, q_weight, q_out), ("k", k, k_weight, k_out)):
         if t is None:
-            _need(o is None, f"{name}_out without {name}")
+            if o is not None:
+                _bad(f"{name}_out without {name}")
+            sides.append((0, None, None, None, 0, 0))
             continue
-        o = t if o is None else o
         heads = t.shape[1] if t.dim() == 3 else -1
-        setattr(a, f"n_{name}_heads", heads)
-        setattr(a, f"{name}_stride", _rows(t, name, heads, D, dev, dt))
-        setattr(a, f"{name}_out_stride", _rows(o, name + "_out", heads, D, dev, dt))
-        _need(t.shape[0] == n and o.shape[0] == n, "q, k and outputs: the same number of tokens")
-        setattr(a, name, t.data_ptr())
-        setattr(a, name + "_out", o.data_ptr())
-        if wt is not None:
-            _need(wt.dtype is dt and wt.device == dev and tuple(wt.shape) == (D,) and wt.is_contiguous(),
-                  f"{name}_weight: contiguous {dt} of shape ({D},) on {dev}")
-            setattr(a, name + "_weight", wt.data_ptr())
+        rows, st = _rows(t, name, heads, D, dev, dtype)
+        if rows != n:
+            _bad("q and k: the same number of tokens is wanted")
+        op, ost = t.data_ptr(), st
+        if o is not None:
+            op = o.data_ptr()
+            rows, ost = _rows(o, name + "_out", heads, D, dev, dtype)
+            if rows != n:
+                _bad(f"{name}_out: as many tokens as {name} is wanted")
+        wp = None
+        if w is not None:
+            if w.dtype is not dtype or w.get_device() != dev or w.shape != (D,) or not w.is_contiguous():
+                _bad(f"{name}_weight: contiguous {dtype} of shape ({D},) on cuda:{dev} is wanted")
+            wp = w.data_ptr()
+        sides.append((heads, t.data_ptr(), wp, op, st, ost))
+    max_pos = rot = 0
+    cp = pp = None
     if cos_sin is not None:
-        _need(cos_sin.dtype is torch.float32 and cos_sin.device == dev and cos_sin.dim() == 2 and cos_sin.is_contiguous(),
-              f"cos_sin: contiguous fp32 [positions, rot] on {dev}")
-        a.max_pos, a.rot_dim = cos_sin.shape
-        a.cos_sin = cos_sin.data_ptr()
-        _need(positions is not None, "positions are wanted with cos_sin")
-        a.positions = _ints(positions, "positions", (n,), dev)
-    with _on(dev):
-        _lib.kv_qk_norm_rope(ctypes.byref(a), stream)
+        if (cos_sin.dtype is not torch.float32 or cos_sin.get_device() != dev or cos_sin.dim() != 2 or
+                not cos_sin.is_contiguous()):
+            _bad(f"cos_sin: contiguous fp32 [positions, rot] on cuda:{dev} is wanted")
+        if positions is None:
+            _bad("positions are wanted with cos_sin")
+        max_pos, rot = cos_sin.shape
+        cp, pp = cos_sin.data_ptr(), _ints(positions, "positions", n, dev)
+    (hq, qp, qw, qo, qs, qos), (hk, kp, kw, ko, ks, kos) = sides
+    a = _lib.kvq_norm_rope_args(dt, n, hq, hk, D, rot, 1 if interleaved else 0, max_pos, eps, 0, qp, kp, qw, kw, cp, pp, qo, ko,
+                                qs, ks, qos, kos)
+    _guarded(dev, _lib.kv_qk_norm_rope, ctypes.byref(a), stream)
