@@ -6,6 +6,7 @@
 // lengths. A CTA's four warps take the tiles of a run in turn, each with its own running maximum, sum
 // and output (fp32, registers); at the end of a head they join through shared memory. A head that lies
 // in one run is written out at once; others leave (m, l, o) per run, which the merge kernel joins.
+#include "device_common.cuh"
 #include "paged_frag.cuh"
 
 namespace kvq {
@@ -57,15 +58,32 @@ __device__ __forceinline__ int64_t run_tiles(int64_t total, int n_cta) {
 
 KVQ_HD int64_t partial_floats(int G, int D) { return 32 + (int64_t)G * D; }
 
+// Each warp stages its tiles through a ring of its own in shared memory, K and V tiles in turn, NS slots
+// with NS - 1 copies in flight (cp.async; no barrier but the warp's). The budget leaves three CTAs to an SM
+// (two at D = 256, where registers allow no more).
+template <int D, int KF, int VF> struct Ring {
+    static constexpr int kb = tile_bytes<D, KF>(), vb = tile_bytes<D, VF>();
+    static constexpr int slot = kb > vb ? kb : vb;
+    static constexpr int budget = (D == 256 ? 112 : 74) * 1024 / kDW;
+    static constexpr int fit = budget / slot;
+    static constexpr int NS = fit > 8 ? 8 : fit;
+    static constexpr int join = 16 * D * 4 * kDW;          // the warps' outputs at a head's end
+    static constexpr int bytes = NS * slot * kDW > join ? NS * slot * kDW : join;
+    static_assert(NS >= 3, "a tile of each kind in flight beside the one in use");
+};
+
 template <int D, int KF, int VF, typename T, typename TQ>
-__global__ void __launch_bounds__(kDT) decode_kernel(PagedAttnParams p) {
+__global__ void __launch_bounds__(kDT, D == 256 ? 2 : 3) decode_kernel(PagedAttnParams p) {
     constexpr bool LO = std::is_same<T, __nv_bfloat16>::value;   // P in two bf16 parts: 16 bits of it
-    extern __shared__ __align__(16) float smem[];                // [kDW][G][D] outputs, joined per head
+    using R = Ring<D, KF, VF>;
+    extern __shared__ __align__(128) float smem[];               // the rings; [kDW][G][D] outputs at a head's end
     __shared__ float s_m[kDW][16], s_l[kDW][16];
     __shared__ int64_t red[kDW];
     __shared__ int s_b, s_h, s_i;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int H = p.v.H, G = p.G;
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * R::NS * R::slot;
+    grid_dep_wait();
 
     // this CTA's run of the line, and the head where it starts
     int64_t mine = 0;
@@ -118,6 +136,45 @@ __global__ void __launch_bounds__(kDT) decode_kernel(PagedAttnParams p) {
         if (st.n == 0) { h = H - 1; continue; }
         const int i1 = (int)min((int64_t)st.n, i0 + left);
         left -= i1 - i0;
+        const int nt = (i1 - i0 - warp + kDW - 1) / kDW;          // this warp's tiles
+        // the copies run ahead: item 2i is K of the warp's tile i, item 2i + 1 its V
+        int pages = 0, unit_page = 0, unit_off = 0, put = 0, item = 0;
+        auto copy_next = [&]() {
+            const int i = item >> 1;
+            if (i < nt) {
+                const uint32_t dst = ring + put * R::slot;
+                if (!(item & 1)) {
+                    if ((i & 31) == 0) {                         // the next 32 tiles' page numbers, one per lane
+                        const int k = min(i + lane, nt - 1) * kDW + i0 + warp;
+                        pages = p.table[b * p.table_stride + ((st.tile(k) * kTile) >> p.v.ps_shift)];
+                        if (pages < 0 || pages >= p.v.n_pages) {
+                            raise_status(p.v.status, KVQ_PAGED_BAD_INDEX);
+                            pages = -1;
+                        }
+                    }
+                    unit_page = __shfl_sync(kAll, pages, i & 31);
+                    unit_off = (st.tile(i * kDW + i0 + warp) * kTile) & (p.v.ps - 1);
+                    copy_tile<D, KF, false>(dst, unit_page < 0 ? nullptr : unit_at(p.v, 0, unit_page, h), p.v.ps, unit_off, lane);
+                } else {
+                    copy_tile<D, VF, true>(dst, unit_page < 0 ? nullptr : unit_at(p.v, 1, unit_page, h), p.v.ps, unit_off, lane);
+                }
+            }
+            cp_commit();
+            ++item;
+            put = put + 1 == R::NS ? 0 : put + 1;
+        };
+#pragma unroll 1
+        for (int i = 0; i < R::NS - 1; ++i) copy_next();
+        int get = 0;
+        // the next item has landed, and the slot of the item before it is free for a new copy
+        auto take = [&]() -> uint32_t {
+            cp_wait<R::NS - 2>();
+            __syncwarp();
+            const uint32_t a = ring + get * R::slot;
+            get = get + 1 == R::NS ? 0 : get + 1;
+            return a;
+        };
+
         const TQ* q = (const TQ*)p.q + b * p.q_stride + (int64_t)h * G * D;
         uint32_t qf[D / 16][4];
         float back[2], slope[2], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[D / 8][4] = {};
@@ -125,49 +182,55 @@ __global__ void __launch_bounds__(kDT) decode_kernel(PagedAttnParams p) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) slope[k] = p.slopes && g + 8 * k < G ? p.slopes[h * G + g + 8 * k] * kL2e : 0.f;
 
-        for (int i = i0 + warp; i < i1; i += kDW) {
-            const int p0 = st.tile(i) * kTile, e = p0 >> p.v.ps_shift, off = p0 & (p.v.ps - 1);
-            int page = p.table[b * p.table_stride + e];
-            const unsigned see = __ballot_sync(kAll, lane < 16 && st.sees(p0 + lane));
-            unsigned live = see;
-            if (page < 0 || page >= p.v.n_pages) {
-                if (lane == 0) raise_status(p.v.status, KVQ_PAGED_BAD_INDEX);
-                page = 0;
-                live = 0;
-            }
+        for (int i = 0; i < nt; ++i) {
+            const int p0 = st.tile(i * kDW + i0 + warp) * kTile;
+            SharedTile<D, KF, false> kt;
+            kt.base = take();
+            copy_next();
             float s[2][4] = {};
-            tile_scores<D, KF, T>(global_tile<KGeo<D, KF>::RB>(p.v, 0, page, h, off, live), g, t, qf, s);
+            tile_scores<D, KF, T>(kt, g, t, qf, s);
+            const bool all = p0 + kTile <= st.len && (p0 >= st.lo || p0 + kTile <= st.pre);
+            unsigned see = 0xffffu;
+            if (!all) see = __ballot_sync(kAll, lane < 16 && st.sees(p0 + lane));
             float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
+                    if (c >= 2 && G <= 8) continue;
                     const int pos = 8 * n + 2 * t + (c & 1);
                     const float x = rule(s[n][c], back[c >> 1], (float)(st.len - 1 - p0 - pos), slope[c >> 1]);
-                    s[n][c] = (see >> pos) & 1 ? x : -INFINITY;
+                    s[n][c] = all || ((see >> pos) & 1) ? x : -INFINITY;
                     mx[c >> 1] = fmaxf(mx[c >> 1], s[n][c]);
                 }
-            float base[2];
+            float base[2] = {0.f, 0.f}, a[2] = {1.f, 1.f};
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
+                if (k == 1 && G <= 8) continue;
                 mx[k] = fmaxf(mx[k], __shfl_xor_sync(kAll, mx[k], 1));
                 mx[k] = fmaxf(mx[k], __shfl_xor_sync(kAll, mx[k], 2));
                 const float mn = fmaxf(m[k], mx[k]);
                 base[k] = mn == -INFINITY ? 0.f : mn;
-                const float a = ex2(m[k] - base[k]);
+                a[k] = m[k] == mn ? 1.f : ex2(m[k] - base[k]);
                 m[k] = mn;
-                l[k] *= a;
+            }
+            if (__any_sync(kAll, a[0] != 1.f || a[1] != 1.f)) {
+                l[0] *= a[0];
+                l[1] *= a[1];
 #pragma unroll
                 for (int d = 0; d < D / 8; ++d) {
-                    o[d][2 * k] *= a;
-                    o[d][2 * k + 1] *= a;
+                    o[d][0] *= a[0];
+                    o[d][1] *= a[0];
+                    o[d][2] *= a[1];
+                    o[d][3] *= a[1];
                 }
             }
-            uint32_t pa[4], pl[4] = {};
+            uint32_t pa[4] = {}, pl[4] = {};
 #pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
+                    if (k == 1 && G <= 8) continue;
                     const float x = ex2(s[n][2 * k] - base[k]), y = ex2(s[n][2 * k + 1] - base[k]);
                     l[k] += x + y;
                     pa[2 * n + k] = Two<T>::pack(x, y);
@@ -176,8 +239,17 @@ __global__ void __launch_bounds__(kDT) decode_kernel(PagedAttnParams p) {
                         pl[2 * n + k] = Two<T>::pack(x - hi.x, y - hi.y);
                     }
                 }
-            tile_values<D, VF, T, LO>(global_tile<VGeo<D, VF>::RB>(p.v, 1, page, h, off, live), g, t, pa, pl, o);
+            SharedTile<D, VF, true> vt;
+            vt.base = take();
+            copy_next();
+            if (!all) {
+                clear_rows<D, VF>(vt.base, see, lane);
+                __syncwarp();
+            }
+            tile_values<D, VF, T, LO>(vt, g, t, pa, pl, o);
         }
+        cp_wait<0>();
+        __syncthreads();                                          // the rings become the join's space
 
         // join the warps: rows' maxima and sums, then the outputs rescaled to the common maximum
 #pragma unroll
@@ -250,6 +322,7 @@ template <int D, typename TQ>
 __global__ void __launch_bounds__(kMT) merge_kernel(PagedAttnParams p) {
     __shared__ int64_t red[kMT / 32];
     const int b = blockIdx.x / p.v.H, h = blockIdx.x % p.v.H, H = p.v.H, G = p.G;
+    grid_dep_wait();
     int64_t all = 0, before = 0;
     for (int i = threadIdx.x; i < p.n_seq; i += kMT) {
         const int64_t n = (int64_t)seq_tiles(p, i).n * H;
@@ -291,16 +364,14 @@ __global__ void __launch_bounds__(kMT) merge_kernel(PagedAttnParams p) {
 template <int D, int KF, int VF, typename T, typename TQ>
 int decode_run(const PagedAttnParams& p, int sm_count, cudaStream_t s) {
     PagedAttnParams a = p;
-    const size_t smem = (size_t)kDW * p.G * D * 4;
-    auto k = decode_kernel<D, KF, VF, T, TQ>;
-    if (smem > 48 * 1024 && cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-        return (int)cudaGetLastError();
+    using R = Ring<D, KF, VF>;
+    const auto k = decode_kernel<D, KF, VF, T, TQ>;
     int res = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&res, k, kDT, smem) != cudaSuccess) return (int)cudaGetLastError();
-    a.n_cta = min(kMaxDecodeCtas, sm_count * (res > 0 ? res : 1));
-    k<<<a.n_cta, kDT, smem, s>>>(a);
-    merge_kernel<D, TQ><<<p.n_seq * p.v.H, kMT, 0, s>>>(a);
-    return (int)cudaGetLastError();
+    if (const int e = resident_ctas((const void*)k, kDT, R::bytes, &res)) return e;
+    a.n_cta = min(kMaxDecodeCtas, sm_count * res);
+    cudaError_t e = launch_k(k, dim3(a.n_cta), dim3(kDT), R::bytes, s, true, a);
+    if (e == cudaSuccess) e = launch_k(merge_kernel<D, TQ>, dim3(p.n_seq * p.v.H), dim3(kMT), 0, s, true, a);
+    return (int)e;
 }
 
 template <int D> int decode_d(const PagedAttnParams& p, int sms, cudaStream_t s) {

@@ -3,7 +3,10 @@
 #include <cuda_runtime.h>
 #include <cmath>
 #include <cstring>
+#include <map>
+#include <mutex>
 #include <new>
+#include <utility>
 #include "paged_internal.h"
 
 using namespace kvq;
@@ -131,6 +134,30 @@ kvq_status attn_params(kvq_paged* h, int layer, int dtype, int n_seq, int64_t ro
 }
 
 }  // namespace
+
+namespace kvq {
+
+int resident_ctas(const void* kernel, int threads, int smem, int* ctas) {
+    static std::mutex mu;
+    static std::map<std::pair<const void*, int>, int> known;
+    int d = 0;
+    cudaError_t e = cudaGetDevice(&d);
+    if (e != cudaSuccess) return (int)e;
+    std::lock_guard<std::mutex> lk(mu);
+    const auto it = known.find({kernel, d});
+    if (it != known.end()) {
+        *ctas = it->second;
+        return 0;
+    }
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas, kernel, threads, smem);
+    if (e != cudaSuccess) return (int)e;
+    if (*ctas < 1) return (int)cudaErrorInvalidConfiguration;
+    known[{kernel, d}] = *ctas;
+    return 0;
+}
+
+}  // namespace kvq
 
 extern "C" {
 

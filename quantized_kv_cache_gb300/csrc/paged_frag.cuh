@@ -299,5 +299,83 @@ __device__ __forceinline__ GlobalTile<RB> global_tile(const PagedView& v, int w,
     return s;
 }
 
+// A tile staged in shared memory: 16 code rows of RB bytes, then (block formats) the rows' scales. The
+// 16-byte pieces of a 128-byte line are permuted by row so that the eight lanes of a load phase (K:
+// two rows, four neighbouring pieces; V: rows 0, 2, 4, 6, two neighbouring pieces) hit all banks.
+template <int RB, bool VALUES> __device__ __forceinline__ uint32_t tile_swizzle(uint32_t byte) {
+    const uint32_t row = byte / RB;
+    if (VALUES) return byte ^ (RB >= 64 ? ((row >> 1) & 3) << 5 : ((row >> 2) & 1) << 5);
+    return RB >= 128 ? byte ^ ((row & 1) << 6) : byte;
+}
+
+template <int D, int PF, bool VALUES> struct SharedTile {
+    static constexpr int RB = KGeo<D, PF>::RB;
+    uint32_t base;
+    template <int N> __device__ __forceinline__ Words<N> piece(int row, int byte) const {
+        Words<N> w;
+        const uint32_t a = base + tile_swizzle<RB, VALUES>(row * RB + byte);
+        if constexpr (N == 4)
+            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n" : "=r"(w.w[0]), "=r"(w.w[1]), "=r"(w.w[2]), "=r"(w.w[3]) : "r"(a));
+        else if constexpr (N == 2)
+            asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];\n" : "=r"(w.w[0]), "=r"(w.w[1]) : "r"(a));
+        else
+            asm volatile("ld.shared.u32 %0, [%1];\n" : "=r"(w.w[0]) : "r"(a));
+        return w;
+    }
+    __device__ __forceinline__ uint32_t scale(int row, int blk) const {
+        uint16_t x;
+        asm volatile("ld.shared.u16 %0, [%1];\n" : "=h"(x) : "r"(base + 16 * RB + row * (D / 16) + 2 * blk));
+        return x;
+    }
+};
+
+template <int D, int PF> constexpr int tile_bytes() { return 16 * KGeo<D, PF>::RB + (PF == PF_16 ? 0 : D); }
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory"); }
+__device__ __forceinline__ void st_zero16(uint32_t dst) {
+    asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};\n" ::"r"(dst), "r"(0) : "memory");
+}
+
+// One warp starts the copy of a tile (16 rows from row `off` of a page's unit) to shared memory; a null
+// unit (a page number out of range) gives zeros.
+template <int D, int PF, bool VALUES>
+__device__ __forceinline__ void copy_tile(uint32_t dst, const uint8_t* unit, int ps, int off, int lane) {
+    constexpr int RB = KGeo<D, PF>::RB, N = 16 * RB / 16;
+    const uint8_t* src = unit + off * RB;
+#pragma unroll
+    for (int i = 0; i < (N + 31) / 32; ++i) {
+        const int c = i * 32 + lane;
+        if (N % 32 && c >= N) break;
+        const uint32_t d = dst + tile_swizzle<RB, VALUES>(c * 16);
+        if (unit) cp_async16(d, src + c * 16);
+        else st_zero16(d);
+    }
+    if constexpr (PF != PF_16) {
+        if (lane < D / 16) {
+            const uint32_t d = dst + 16 * RB + lane * 16;
+            if (unit) cp_async16(d, unit + (int64_t)ps * RB + off * (D / 16) + lane * 16);
+            else st_zero16(d);
+        }
+    }
+}
+
+// Zeroes what the rows outside `live` would add (the values of 16-bit rows, the scales of the others): a
+// weight of 0 does not keep an infinity or NaN of an unused row out of the product.
+template <int D, int PF> __device__ __forceinline__ void clear_rows(uint32_t base, uint32_t live, int lane) {
+    constexpr int RB = KGeo<D, PF>::RB;
+    if constexpr (PF == PF_16) {
+        for (int c = lane; c < RB; c += 32)            // 16 rows x RB / 16 pieces
+            if (!((live >> (c / (RB / 16))) & 1)) st_zero16(base + tile_swizzle<RB, true>(c * 16));
+    } else {
+        for (int c = lane; c < 16 * (D / 32); c += 32)
+            if (!((live >> (c / (D / 32))) & 1))
+                asm volatile("st.shared.u16 [%0], %1;\n" ::"r"(base + 16 * RB + 2 * c), "h"((uint16_t)0) : "memory");
+    }
+}
+
 }  // namespace
 }  // namespace kvq

@@ -62,6 +62,10 @@ struct PagedAttnParams {
     float scale, softcap;
 };
 
+// Resident CTAs per SM of a kernel on the current device; lets it use `smem` bytes of dynamic shared memory.
+// Asked once per kernel and device. Returns a cudaError_t as int.
+int resident_ctas(const void* kernel, int threads, int smem, int* ctas);
+
 int launch_norm_rope(const kvq_norm_rope_args& a, int sm_count, void* stream);
 int launch_paged_write(const WriteParams& p, void* stream);
 int launch_paged_read(const ReadParams& p, void* stream);
