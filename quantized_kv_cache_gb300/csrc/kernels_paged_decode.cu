@@ -125,10 +125,9 @@ __global__ void __launch_bounds__(kDT, D == 256 ? 2 : 3) decode_kernel(PagedAttn
     }
     __syncthreads();
     int b = s_b, h = s_h, i0 = s_i;
-    ScoreRule rule;
-    rule.scale = p.scale;
-    rule.cap = p.softcap;
-    rule.cap_l2 = p.softcap * kL2e;
+    const ScoreRule rule = score_rule(p);
+    const bool plain = rule.plain();
+    const uint32_t k_at = copy_lane<D, KF, false>(lane), v_at = copy_lane<D, VF, true>(lane);
 
     for (; left > 0; ++h, i0 = 0) {
         if (h == H) { h = 0; ++b; }
@@ -154,9 +153,9 @@ __global__ void __launch_bounds__(kDT, D == 256 ? 2 : 3) decode_kernel(PagedAttn
                     }
                     unit_page = __shfl_sync(kAll, pages, i & 31);
                     unit_off = (st.tile(i * kDW + i0 + warp) * kTile) & (p.v.ps - 1);
-                    copy_tile<D, KF, false>(dst, unit_page < 0 ? nullptr : unit_at(p.v, 0, unit_page, h), p.v.ps, unit_off, lane);
+                    copy_tile<D, KF, false>(dst, k_at, unit_page < 0 ? nullptr : unit_at(p.v, 0, unit_page, h), p.v.ps, unit_off, lane);
                 } else {
-                    copy_tile<D, VF, true>(dst, unit_page < 0 ? nullptr : unit_at(p.v, 1, unit_page, h), p.v.ps, unit_off, lane);
+                    copy_tile<D, VF, true>(dst, v_at, unit_page < 0 ? nullptr : unit_at(p.v, 1, unit_page, h), p.v.ps, unit_off, lane);
                 }
             }
             cp_commit();
@@ -180,6 +179,8 @@ __global__ void __launch_bounds__(kDT, D == 256 ? 2 : 3) decode_kernel(PagedAttn
         float back[2], slope[2], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[D / 8][4] = {};
         load_queries<D, KF, T, TQ>([&](int r) { return r < G ? q + r * D : (const TQ*)nullptr; }, g, t, qf, back);
 #pragma unroll
+        for (int k = 0; k < 2; ++k) back[k] = rule.factor(back[k]);
+#pragma unroll
         for (int k = 0; k < 2; ++k) slope[k] = p.slopes && g + 8 * k < G ? p.slopes[h * G + g + 8 * k] * kL2e : 0.f;
 
         for (int i = 0; i < nt; ++i) {
@@ -192,17 +193,27 @@ __global__ void __launch_bounds__(kDT, D == 256 ? 2 : 3) decode_kernel(PagedAttn
             const bool all = p0 + kTile <= st.len && (p0 >= st.lo || p0 + kTile <= st.pre);
             unsigned see = 0xffffu;
             if (!all) see = __ballot_sync(kAll, lane < 16 && st.sees(p0 + lane));
-            float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    if (c >= 2 && G <= 8) continue;
-                    const int pos = 8 * n + 2 * t + (c & 1);
-                    const float x = rule(s[n][c], back[c >> 1], (float)(st.len - 1 - p0 - pos), slope[c >> 1]);
-                    s[n][c] = all || ((see >> pos) & 1) ? x : -INFINITY;
-                    mx[c >> 1] = fmaxf(mx[c >> 1], s[n][c]);
-                }
+                for (int c = 0; c < 4; ++c) s[n][c] *= back[c >> 1];
+            if (!plain) {
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        if (c < 2 || G > 8) s[n][c] = rule(s[n][c], st.len - 1 - p0 - (8 * n + 2 * t + (c & 1)), slope[c >> 1]);
+            }
+            if (!all) {
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        if (!((see >> (8 * n + 2 * t + (c & 1))) & 1)) s[n][c] = -INFINITY;
+            }
+            float mx[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) mx[k] = fmaxf(fmaxf(s[0][2 * k], s[0][2 * k + 1]), fmaxf(s[1][2 * k], s[1][2 * k + 1]));
             float base[2] = {0.f, 0.f}, a[2] = {1.f, 1.f};
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
@@ -316,12 +327,16 @@ __global__ void __launch_bounds__(kDT, D == 256 ? 2 : 3) decode_kernel(PagedAttn
     }
 }
 
-// One CTA per (sequence, KV head): joins the runs' partials, and writes zeros for a head without tiles.
-constexpr int kMT = 128;
+// One CTA per (sequence, query head): joins the runs' partials, and writes zeros for a head without tiles.
+// The runs' maxima and sums give one weight per run; then the CTA's thread groups take the runs in turn.
+constexpr int kMT = 256;
 template <int D, typename TQ>
 __global__ void __launch_bounds__(kMT) merge_kernel(PagedAttnParams p) {
+    constexpr int L = D / 4, N = kMT / L;                // threads of an output row (four channels each); groups
     __shared__ int64_t red[kMT / 32];
-    const int b = blockIdx.x / p.v.H, h = blockIdx.x % p.v.H, H = p.v.H, G = p.G;
+    __shared__ float s_w[kMaxDecodeCtas + 1], s_x[kMT / 32];
+    __shared__ float4 s_o[N][L];
+    const int b = blockIdx.x / p.Hq, hq = blockIdx.x % p.Hq, h = hq / p.G, r = hq % p.G, H = p.v.H, G = p.G;
     grid_dep_wait();
     int64_t all = 0, before = 0;
     for (int i = threadIdx.x; i < p.n_seq; i += kMT) {
@@ -332,32 +347,63 @@ __global__ void __launch_bounds__(kMT) merge_kernel(PagedAttnParams p) {
     all = block_sum<kMT>(all, red);
     before = block_sum<kMT>(before, red);
     const int n = seq_tiles(p, b).n;
-    TQ* out = (TQ*)p.out + ((int64_t)b * p.Hq + h * G) * D;
+    TQ* out = (TQ*)p.out + (int64_t)blockIdx.x * D;
     if (n == 0) {
-        for (int e = threadIdx.x; e < G * D / 2; e += kMT) reinterpret_cast<uint32_t*>(out)[e] = 0;
-        if (p.lse && threadIdx.x < G) p.lse[(int64_t)b * p.Hq + h * G + threadIdx.x] = -INFINITY;
+        if (threadIdx.x < D / 2) reinterpret_cast<uint32_t*>(out)[threadIdx.x] = 0;
+        if (p.lse && threadIdx.x == 0) p.lse[blockIdx.x] = -INFINITY;
         return;
     }
     const int64_t U = run_tiles(all, p.n_cta), s0 = before + (int64_t)h * n;
-    const int c0 = (int)(s0 / U), c1 = (int)((s0 + n - 1) / U);
-    if (c0 == c1) return;
+    const int c0 = (int)(s0 / U), nc = (int)((s0 + n - 1) / U) - c0 + 1;
+    if (nc == 1) return;
     const int64_t pf = partial_floats(G, D);
-    const float* part = p.ws + ((int64_t)b * H + h) * pf;
-    for (int e = threadIdx.x; e < G * D / 2; e += kMT) {
-        const int r = 2 * e / D;
-        float m = -INFINITY;
-        for (int c = c0; c <= c1; ++c) m = fmaxf(m, part[c * pf + r]);
-        float l = 0.f, x = 0.f, y = 0.f;
-        for (int c = c0; c <= c1; ++c) {
-            const float a = m == -INFINITY ? 0.f : ex2(part[c * pf + r] - m);
-            const float2 f = *reinterpret_cast<const float2*>(part + c * pf + 32 + 2 * e);
-            l += part[c * pf + 16 + r] * a;
-            x += f.x * a;
-            y += f.y * a;
+    const float* part = p.ws + ((int64_t)b * H + h + c0) * pf;
+    float m = -INFINITY, l = 0.f;
+    for (int c = threadIdx.x; c < nc; c += kMT) m = fmaxf(m, s_w[c] = part[c * pf + r]);
+#pragma unroll
+    for (int s = 16; s >= 1; s >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, s));
+    if ((threadIdx.x & 31) == 0) s_x[threadIdx.x >> 5] = m;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kMT / 32; ++i) m = fmaxf(m, s_x[i]);
+    __syncthreads();
+    for (int c = threadIdx.x; c < nc; c += kMT) {
+        const float a = m == -INFINITY ? 0.f : ex2(s_w[c] - m);
+        s_w[c] = a;
+        l += part[c * pf + 16 + r] * a;
+    }
+#pragma unroll
+    for (int s = 16; s >= 1; s >>= 1) l += __shfl_xor_sync(kAll, l, s);
+    if ((threadIdx.x & 31) == 0) s_x[threadIdx.x >> 5] = l;
+    __syncthreads();
+    l = 0.f;
+#pragma unroll
+    for (int i = 0; i < kMT / 32; ++i) l += s_x[i];
+    const int col = threadIdx.x % L, grp = threadIdx.x / L;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int c = grp; c < nc; c += N) {
+        const float4 f = *reinterpret_cast<const float4*>(part + c * pf + 32 + (int64_t)r * D + 4 * col);
+        const float a = s_w[c];
+        o.x = fmaf(f.x, a, o.x);
+        o.y = fmaf(f.y, a, o.y);
+        o.z = fmaf(f.z, a, o.z);
+        o.w = fmaf(f.w, a, o.w);
+    }
+    s_o[grp][col] = o;
+    __syncthreads();
+    if (grp == 0) {
+#pragma unroll
+        for (int i = 1; i < N; ++i) {
+            const float4 f = s_o[i][col];
+            o.x += f.x;
+            o.y += f.y;
+            o.z += f.z;
+            o.w += f.w;
         }
         const float inv = l > 0.f ? 1.f / l : 0.f;
-        reinterpret_cast<uint32_t*>(out)[e] = Two<TQ>::pack(x * inv, y * inv);
-        if (p.lse && (2 * e) % D == 0) p.lse[(int64_t)b * p.Hq + h * G + r] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+        *reinterpret_cast<uint2*>(out + 4 * col) = make_uint2(Two<TQ>::pack(o.x * inv, o.y * inv), Two<TQ>::pack(o.z * inv, o.w * inv));
+        if (p.lse && col == 0) p.lse[blockIdx.x] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
     }
 }
 
@@ -370,7 +416,7 @@ int decode_run(const PagedAttnParams& p, int sm_count, cudaStream_t s) {
     if (const int e = resident_ctas((const void*)k, kDT, R::bytes, &res)) return e;
     a.n_cta = min(kMaxDecodeCtas, sm_count * res);
     cudaError_t e = launch_k(k, dim3(a.n_cta), dim3(kDT), R::bytes, s, true, a);
-    if (e == cudaSuccess) e = launch_k(merge_kernel<D, TQ>, dim3(p.n_seq * p.v.H), dim3(kMT), 0, s, true, a);
+    if (e == cudaSuccess) e = launch_k(merge_kernel<D, TQ>, dim3((unsigned)p.n_seq * p.Hq), dim3(kMT), 0, s, true, a);
     return (int)e;
 }
 

@@ -60,10 +60,7 @@ __global__ void __launch_bounds__(kPT) prefill_kernel(PagedAttnParams p) {
     const Chunk c = chunk_of(p, b, blockIdx.x == 0 && h == 0 && threadIdx.x == 0);
     const int rows = c.n * G, base_row = blockIdx.x * kRowsCta + warp * 16;
     if (base_row >= rows) return;
-    ScoreRule rule;
-    rule.scale = p.scale;
-    rule.cap = p.softcap;
-    rule.cap_l2 = p.softcap * kL2e;
+    const ScoreRule rule = score_rule(p);
     auto qrow = [&](int r) -> const TQ* {
         const int i = base_row + r;
         if (i >= rows) return nullptr;
@@ -106,7 +103,7 @@ __global__ void __launch_bounds__(kPT) prefill_kernel(PagedAttnParams p) {
             for (int e = 0; e < 4; ++e) {
                 const int k = e >> 1, j = p0 + 8 * n + 2 * t + (e & 1);
                 const bool see = j < c.len && ((j <= pos[k] && j >= lo[k]) || j < pre[k]);
-                const float x = rule(s[n][e], back[k], fabsf((float)(pos[k] - j)), slope[k]);
+                const float x = rule(s[n][e] * rule.factor(back[k]), abs(pos[k] - j), slope[k]);
                 s[n][e] = see ? x : -INFINITY;
                 hidden |= !see && base_row + g + 8 * k < rows;
                 mx[k] = fmaxf(mx[k], s[n][e]);

@@ -106,10 +106,9 @@ __device__ __forceinline__ void tile_scores(const SRC& src, int g, int t, const 
 #pragma unroll
                 for (int i = 0; i < K::NW; ++i) {
                     if constexpr (PF == PF_Q8) {
-                        const uint32_t x = __byte_perm(p.w[i], 0, 0x3120);    // bytes 0,2 | 1,3: halves (b0 b2), (b1 b3)
-                        uint32_t a, b;
-                        byte_pairs(x, d, a, b);                                // (b0, b1), (b2, b3)
-                        mma_t(s[n], qf[KS * j + i], a, b, T());
+                        const uint32_t x = p.w[i] ^ 0x80808080u;               // 1024 + 128 + b by an exponent byte
+                        mma_t(s[n], qf[KS * j + i], deq(__byte_perm(x, 0x64646464u, 0x4140), 1152.f, d),
+                              deq(__byte_perm(x, 0x64646464u, 0x4342), 1152.f, d), T());
                     } else {
                         uint32_t o[4];
                         nib_pairs(p.w[i], d, o);                               // (n0, n4), (n1, n5), (n2, n6), (n3, n7)
@@ -257,15 +256,27 @@ __device__ __forceinline__ float ex2(float x) {
 
 constexpr float kL2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// The score options, in units of log2: apply(q.k, row factor, |distance|, slope).
+// The score options, in units of log2. A score x = q.k * f, f = (the row's power of two) * scale * log2(e);
+// with a cap, f = .. * scale / softcap and x = softcap * log2(e) * tanh(q.k * f); then the bias.
 struct ScoreRule {
     float scale, cap, cap_l2;      // softmax scale; softcap (0: none); softcap * log2(e)
-    __device__ __forceinline__ float operator()(float dot, float back, float dist, float slope_l2) const {
-        float x = dot * (back * scale);
-        x = cap > 0.f ? cap_l2 * tanhf(x / cap) : x * kL2e;
-        return x - slope_l2 * dist;
+    bool biased;
+    __device__ __forceinline__ bool plain() const { return cap == 0.f && !biased; }
+    __device__ __forceinline__ float factor(float back) const { return back * scale * (cap > 0.f ? 1.f / cap : kL2e); }
+    // dist: |distance| in positions; slope_l2: the head's slope * log2(e)
+    __device__ __forceinline__ float operator()(float x, int dist, float slope_l2) const {
+        if (cap > 0.f) x = cap_l2 * tanhf(x);
+        return biased ? x - slope_l2 * (float)dist : x;
     }
 };
+__device__ __forceinline__ ScoreRule score_rule(const PagedAttnParams& p) {
+    ScoreRule r;
+    r.scale = p.scale;
+    r.cap = p.softcap;
+    r.cap_l2 = p.softcap * kL2e;
+    r.biased = p.slopes != nullptr;
+    return r;
+}
 
 // A tile's rows in global memory; rows that no query of the call sees read as zeros.
 template <int RB> struct GlobalTile {
@@ -340,26 +351,26 @@ __device__ __forceinline__ void st_zero16(uint32_t dst) {
     asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};\n" ::"r"(dst), "r"(0) : "memory");
 }
 
+// A lane's place in a tile's copy: piece `lane` of every 512 bytes. The permutation is a xor by bits of the
+// row, of which 512 * i and the lane set different ones: one offset per lane and a constant per i.
+template <int D, int PF, bool VALUES> __device__ __forceinline__ uint32_t copy_lane(int lane) {
+    return tile_swizzle<KGeo<D, PF>::RB, VALUES>(lane * 16);
+}
+
 // One warp starts the copy of a tile (16 rows from row `off` of a page's unit) to shared memory; a null
 // unit (a page number out of range) gives zeros.
 template <int D, int PF, bool VALUES>
-__device__ __forceinline__ void copy_tile(uint32_t dst, const uint8_t* unit, int ps, int off, int lane) {
+__device__ __forceinline__ void copy_tile(uint32_t dst, uint32_t at, const uint8_t* unit, int ps, int off, int lane) {
     constexpr int RB = KGeo<D, PF>::RB, N = 16 * RB / 16;
-    const uint8_t* src = unit + off * RB;
+    if (unit) {
+        const uint8_t* src = unit + off * RB + lane * 16;
 #pragma unroll
-    for (int i = 0; i < (N + 31) / 32; ++i) {
-        const int c = i * 32 + lane;
-        if (N % 32 && c >= N) break;
-        const uint32_t d = dst + tile_swizzle<RB, VALUES>(c * 16);
-        if (unit) cp_async16(d, src + c * 16);
-        else st_zero16(d);
-    }
-    if constexpr (PF != PF_16) {
-        if (lane < D / 16) {
-            const uint32_t d = dst + 16 * RB + lane * 16;
-            if (unit) cp_async16(d, unit + (int64_t)ps * RB + off * (D / 16) + lane * 16);
-            else st_zero16(d);
-        }
+        for (int i = 0; i < (N + 31) / 32; ++i)
+            if (N % 32 == 0 || lane < N) cp_async16(dst + 512 * i + (at ^ (tile_swizzle<RB, VALUES>(512 * i) - 512 * i)), src + 512 * i);
+        if constexpr (PF != PF_16)
+            if (lane < D / 16) cp_async16(dst + 16 * RB + lane * 16, unit + ps * RB + off * (D / 16) + lane * 16);
+    } else {
+        for (int i = lane; i < tile_bytes<D, PF>() / 16; i += 32) st_zero16(dst + i * 16);
     }
 }
 
