@@ -1,16 +1,40 @@
-// Attention of chunks of new tokens over pages.
+// Attention of chunks of new tokens over pages, on the tensor cores (tcgen05).
 //
 // The rows of a KV head are the chunk's tokens times the G query heads that read it, row r = token r / G,
-// head r % G, so the KV rows are read once for all of them. A CTA takes 64 rows of one (sequence, KV
-// head), 16 per warp, and walks the 16-position tiles that any of its rows sees.
-#include "paged_frag.cuh"
+// head r % G, so K and V tiles serve all of them. A CTA holds NT tiles of 128 rows (two up to D = 128, one
+// at D = 256, where the output takes half of the tensor memory) and walks the BN-position tiles that any of
+// its rows sees. Its warps have fixed parts:
+//  - producers bring K and V tiles into a ring of four shared-memory slots, row by row of the pages (any
+//    page size), as fp16 / bf16 in the 128-byte-swizzled layout both products read: K with the summed axis
+//    contiguous, V with its other axis contiguous. 16-bit rows are copied asynchronously, quantised rows
+//    are decoded on the way;
+//  - one thread issues the products: S = Q K^T into tensor memory, and O += P V with P read from tensor memory;
+//  - one thread per row does the softmax: S from tensor memory to registers, maximum, exponentials, P back
+//    over S. The running maximum moves only when it grows by more than 2^8, so that O is rescaled rarely.
+// With two row tiles, the products of one run while the other's softmax does; with one, S of the next
+// tile is computed meanwhile (two S buffers).
+#include "stream_common.cuh"
+#include "paged_common.cuh"
+#include "tcgen05.cuh"
 
 namespace kvq {
 namespace {
 
-constexpr int kPW = 4;
-constexpr int kPT = kPW * 32;
-constexpr int kRowsCta = kPW * 16;
+template <int D> struct Geo {
+    static constexpr int NT = D == 256 ? 1 : 2;              // row tiles of a CTA
+    static constexpr int BN = D == 256 ? 64 : 128;           // positions of a KV tile
+    static constexpr int rows = 128 * NT;
+    static constexpr int threads = 128 * NT + 128;           // softmax, then one issuing and three producing warps
+    static constexpr int q_bytes = 128 * D * 2;              // of a row tile
+    static constexpr int slot = BN * D * 2;
+    static constexpr int smem = 1024 + NT * q_bytes + 4 * slot;
+    // tensor memory columns: S (and P over it), two buffers; O
+    static constexpr int s_col(int i) { return i * BN; }
+    static constexpr int o_col(int t) { return 256 + t * D; }
+};
+constexpr int kProducers = 96;
+constexpr float kLazy = 8.f;                                  // log2 of what a weight may exceed 1 by
+constexpr int kMaxSplits = 16;
 
 // One sequence's chunk: rows of q, and the positions they sit at.
 struct Chunk {
@@ -20,180 +44,624 @@ __device__ __forceinline__ Chunk chunk_of(const PagedAttnParams& p, int b, bool 
     Chunk c;
     const int64_t cap = (int64_t)p.max_pages << p.v.ps_shift;
     const int len = p.lens[b], c0 = p.cu[b], c1 = p.cu[b + 1];
+    const bool bad = c0 < 0 || c1 > p.n_rows || c1 < c0;
     c.len = len < 0 ? 0 : (len > cap ? (int)cap : len);
     c.row0 = c0;
-    c.n = c0 < 0 || c1 > p.n_rows || c1 < c0 ? 0 : c1 - c0;
-    if (report && (len < 0 || len > cap || c0 < 0 || c1 > p.n_rows || c1 < c0 || c.n > p.max_q))
-        raise_status(p.v.status, KVQ_PAGED_BAD_LENGTH);
+    c.n = bad ? 0 : c1 - c0;
+    if (report && (len < 0 || len > cap || bad || c.n > p.max_q)) raise_status(p.v.status, KVQ_PAGED_BAD_LENGTH);
     c.pos0 = c.len - c.n;
     c.pre = p.prefix ? min(max(p.prefix[b], 0), c.len) : 0;
     return c;
 }
 
-// o += p V over the positions of the tile that each row sees (a score of -inf is one it does not see).
-template <int D, int VF, typename T, typename SRC>
-__device__ __noinline__ void add_seen(const SRC& src, int g, int t, const float (&s)[2][4], const float (&base)[2],
-                                      float (&o)[D / 8][4]) {
-    using V = VGeo<D, VF>;
-    for (int j = 0; j < 16; ++j) {
-        float x[2];
+// The KV tiles of rows whose positions span [first, last]: [0, n0) of the prefix, then [t1, t1 + n - n0).
+template <int BN> struct KvTiles {
+    int n0, t1, n;
+    __device__ __forceinline__ KvTiles(const Chunk& c, int first, int last, int window) {
+        const int end = last < 0 ? 0 : (max(last + 1, c.pre) + BN - 1) / BN;
+        t1 = min(end, window > 0 ? max(0, first - window + 1) / BN : 0);
+        n0 = last < 0 ? 0 : min((c.pre + BN - 1) / BN, t1);
+        n = n0 + end - t1;
+    }
+    __device__ __forceinline__ int at(int i) const { return (i < n0 ? i : t1 + i - n0) * BN; }
+};
+
+// Byte of the 16-byte piece holding channels ch .. ch + 7 of row r in a tile of `rows` rows.
+__device__ __forceinline__ uint32_t tile_byte(int rows, int r, int ch) {
+    return (uint32_t)((ch >> 6) * rows * 128 + r * 128 + ((((ch & 63) >> 3) ^ (r & 7)) << 4));
+}
+__device__ __forceinline__ void st_shared16(uint32_t a, const uint4& v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};\n" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared16(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+
+// Eight channels of a quantised row as fp16: code x scale, rounded once (natural channel order).
+__device__ __forceinline__ uint4 decode_q8(uint2 c, uint32_t d) {
+    uint32_t o[4];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const float a = j < 8 ? s[0][2 * k] : s[1][2 * k], b = j < 8 ? s[0][2 * k + 1] : s[1][2 * k + 1];
-            x[k] = __shfl_sync(kAll, (j & 1) ? b : a, 4 * g + (j & 7) / 2);
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t x = (i ? c.y : c.x) ^ 0x80808080u;
+        o[2 * i] = deq(__byte_perm(x, 0x64646464u, 0x4140), 1152.f, d);
+        o[2 * i + 1] = deq(__byte_perm(x, 0x64646464u, 0x4342), 1152.f, d);
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+__device__ __forceinline__ uint4 decode_q4(uint32_t c, uint32_t d) {
+    // a byte in both halves: its low nibble as 1024 + n, its high one as 1024 + 16 n; then n - 8 in one step
+    const __half2 mul = __floats2half2_rn(1.f, 0.0625f), add = __floats2half2_rn(-1032.f, -72.f);
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t r = (__byte_perm(c, 0, 0x4040 + 0x101 * i) & 0x00f0000fu) | 0x64006400u;
+        o[i] = u32(__hmul2(__hfma2(h2(r), mul, add), h2(d)));
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// What one row's thread keeps.
+struct RowState {
+    int pos, lo;             // position (rows that see nothing: -1), first position of the window
+    int hi, pre;             // last visible position; positions < pre are visible too
+    float f, slope;          // factor of a raw score; slope * log2(e)
+};
+
+// o += p V over the positions of the tile that this row sees: used where some row does not see all of the
+// tile and the tile holds an infinity or NaN, which a weight of 0 would not keep out of the product.
+template <int D, int BN, typename T>
+__device__ __noinline__ void add_seen(uint32_t v_tile, uint32_t o_addr, uint32_t p_addr, const RowState& r, int p0, bool first) {
+    // the weights come back from tensor memory (rounded as the product would take them)
+#pragma unroll 1
+    for (int d0 = 0; d0 < D; d0 += 32) {
+        uint32_t o[32];
+        if (first) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = 0;
+        } else {
+            tmem_ld32(o_addr + d0, o);
+            tmem_wait_ld();
         }
+#pragma unroll 1
+        for (int c = 0; c < BN / 64; ++c) {
+            uint32_t w[32];
+            tmem_ld32(p_addr + 32 * c, w);
+            tmem_wait_ld();
+#pragma unroll 1
+            for (int e = 0; e < 64; ++e) {
+                const int j = p0 + 64 * c + e;
+                if (!((j <= r.hi && j >= r.lo) || j < r.pre)) continue;
+                const float2 f = Two<T>::unpack(w[e / 2]);
+                const float wt = e & 1 ? f.y : f.x;
 #pragma unroll
-        for (int d = 0; d < D / 8; ++d)
+                for (int q = 0; q < 4; ++q) {
+                    float v[8];
+                    unpack8<T>(ld_shared16(v_tile + tile_byte(BN, 64 * c + e, d0 + 8 * q)), v);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const int k = c >> 1;
-                const float v = tile_value<D, VF, T>(src, j, ochan<D, VF>(d / V::CH, 2 * t + (c & 1)) + d % V::CH);
-                if (x[k] != -INFINITY) o[d][c] = fmaf(ex2(x[k] - base[k]), v, o[d][c]);
+                    for (int k = 0; k < 8; ++k)
+                        o[8 * q + k] = __float_as_uint(fmaf(wt, v[k], __uint_as_float(o[8 * q + k])));
+                }
             }
+        }
+        tmem_st32(o_addr + d0, o);
+        tmem_wait_st();
     }
 }
 
 template <int D, int KF, int VF, typename T, typename TQ>
-__global__ void __launch_bounds__(kPT) prefill_kernel(PagedAttnParams p) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+__global__ void __launch_bounds__(Geo<D>::threads, 1) prefill_kernel(PagedAttnParams p, int splits) {
+    using GE = Geo<D>;
+    constexpr int NT = GE::NT, BN = GE::BN;
+    constexpr bool BF = std::is_same<T, __nv_bfloat16>::value;
+    extern __shared__ uint8_t raw[];
+    // full / empty of the ring's slots; Q in place; S ready, P ready (by S buffer); O of a row tile up to date
+    __shared__ uint64_t bars[4 + 4 + 1 + 2 + 2 + 2];
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_abort, s_skip[2];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int h = blockIdx.x, b = blockIdx.z / splits, split = blockIdx.z % splits, G = p.G;
+    const uint32_t full = su32(bars), empty = full + 32, q_full = full + 64, s_full = full + 72, p_full = full + 88,
+                   o_done = full + 104;
+    grid_dep_wait();
+    const Chunk c = chunk_of(p, b, h == 0 && blockIdx.y == 0 && split == 0 && threadIdx.x == 0);
+    // tiles in descending order: the last rows see the most positions and start first
+    const int rows = c.n * G, row_tiles = (rows + GE::rows - 1) / GE::rows;
+    if ((int)blockIdx.y >= row_tiles) return;
+    const int r0 = (row_tiles - 1 - (int)blockIdx.y) * GE::rows, r1 = min(rows, r0 + GE::rows);
+    const KvTiles<BN> kv(c, c.pos0 + r0 / G, c.pos0 + (r1 - 1) / G, p.window);
+    const int i0 = (int)((int64_t)kv.n * split / splits), nt = (int)((int64_t)kv.n * (split + 1) / splits) - i0;
+    const int active = r1 - r0 > 128 ? 2 : 1;                  // row tiles that hold rows
+
+    const uint32_t base = (su32(raw) + 1023) & ~1023u, ring = base + NT * GE::q_bytes;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(full + 8 * i, kProducers);
+            mbar_init(empty + 8 * i, 1);
+        }
+        mbar_init(q_full, 128 * active);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(s_full + 8 * i, 1);
+            mbar_init(p_full + 8 * i, 128);
+            mbar_init(o_done + 8 * i, 1);
+        }
+        s_abort = s_skip[0] = s_skip[1] = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+    }
+    if (warp == 4 * NT) tmem_alloc512(su32(&s_tmem));
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    auto wait = [&](uint32_t bar, uint32_t parity) { mbar_wait(bar, parity, p.v.status, &s_abort); };
+
+    if (warp >= 4 * NT) {
+        if constexpr (NT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
+        if (warp == 4 * NT) {
+            // ------------------------------------------------------------------ the products
+            if (lane == 0 && nt > 0) {
+                const auto scores = [&](int t, int i) {         // S of row tile t, KV tile i
+                    const uint32_t q = base + t * GE::q_bytes, k = ring + ((2 * i) & 3) * GE::slot;
+                    const int buf = NT == 2 ? t : i & 1;
+#pragma unroll
+                    for (int s = 0; s < D / 16; ++s)
+                        mma_ss(tmem + GE::s_col(buf), smem_desc(q + (s / 4) * 128 * 128 + (s % 4) * 32, 0),
+                               smem_desc(k + (s / 4) * BN * 128 + (s % 4) * 32, 0), mma_desc(BF, false, BN), s > 0);
+                    tc_commit(s_full + 8 * buf);
+                };
+                const auto values = [&](int t, int i) {         // O of row tile t += P V of KV tile i
+                    const uint32_t v = ring + ((2 * i + 1) & 3) * GE::slot;
+                    const int buf = NT == 2 ? t : i & 1;
+                    if (!*(volatile int*)&s_skip[buf]) {
+#pragma unroll
+                        for (int s = 0; s < BN / 16; ++s)
+                            mma_ts(tmem + GE::o_col(t), tmem + GE::s_col(buf) + 8 * s, smem_desc(v + s * 2048, BN * 128),
+                                   mma_desc(BF, true, D), i > 0 || s > 0);
+                    }
+                    tc_commit(o_done + 8 * t);
+                };
+                const auto wait_item = [&](int n) {
+                    wait(full + 8 * (n & 3), (n >> 2) & 1);
+                    tc_fence_after();
+                };
+                wait(q_full, 0);
+                wait_item(0);
+                for (int t = 0; t < (NT == 2 ? active : 1); ++t) scores(t, 0);
+                tc_commit(empty);
+                for (int i = 0; i < nt; ++i) {
+                    if constexpr (NT == 2) {
+                        for (int t = 0; t < active; ++t) {
+                            wait(p_full + 8 * t, i & 1);
+                            tc_fence_after();
+                            if (t == 0) wait_item(2 * i + 1);
+                            values(t, i);
+                            if (t == active - 1) tc_commit(empty + 8 * ((2 * i + 1) & 3));
+                            if (i + 1 < nt) {
+                                if (t == 0) wait_item(2 * i + 2);
+                                scores(t, i + 1);
+                                if (t == active - 1) tc_commit(empty + 8 * ((2 * i + 2) & 3));
+                            }
+                        }
+                    } else {
+                        if (i + 1 < nt) {
+                            wait_item(2 * i + 2);
+                            scores(0, i + 1);
+                            tc_commit(empty + 8 * ((2 * i + 2) & 3));
+                        }
+                        wait(p_full + 8 * (i & 1), (i >> 1) & 1);
+                        tc_fence_after();
+                        wait_item(2 * i + 1);
+                        values(0, i);
+                        tc_commit(empty + 8 * ((2 * i + 1) & 3));
+                    }
+                }
+            }
+            __syncwarp();
+        } else {
+            // ------------------------------------------------------------------ K and V tiles
+            const int pw = warp - 4 * NT - 1;                   // 8-row blocks pw, pw + 3, ..
+            const int32_t* table = p.table + (int64_t)b * p.table_stride;
+            int posted = 0;
+            auto post = [&](int n) {                            // items before n are in place
+                fence_async_smem();
+                for (; posted < n; ++posted) mbar_arrive(full + 8 * (posted & 3));
+            };
+            for (int n = 0; n < 2 * nt; ++n) {
+                if (n >= 4) wait(empty + 8 * (n & 3), ((n >> 2) - 1) & 1);
+                const int w = n & 1, p0 = kv.at(i0 + (n >> 1));
+                const uint32_t dst = ring + (n & 3) * GE::slot;
+                // page numbers of the tile's 16-row blocks, one per lane
+                int page = -1;
+                if (lane < BN / 16 && p0 + 16 * lane < c.len) {
+                    page = table[(p0 + 16 * lane) >> p.v.ps_shift];
+                    if (page < 0 || page >= p.v.n_pages) {
+                        raise_status(p.v.status, KVQ_PAGED_BAD_INDEX);
+                        page = -1;
+                    }
+                }
+                constexpr int F[2] = {KF, VF};
+                (void)F;
+                auto block_rows = [&](int blk, int& off) -> const uint8_t* {
+                    const int pg = __shfl_sync(kAll, page, blk >> 1);
+                    off = (p0 + 8 * blk) & (p.v.ps - 1);
+                    return pg < 0 ? nullptr : unit_at(p.v, w, pg, h);
+                };
+                const int fmt = w ? VF : KF;
+                if (KF == 0) {
+                    constexpr int per = D / 8;                  // pieces of a row
+                    for (int blk = pw; blk < BN / 8; blk += 3) {
+                        int off;
+                        const uint8_t* u = block_rows(blk, off);
+#pragma unroll
+                        for (int e = 0; e < 8 * per / 32; ++e) {
+                            const int x = e * 32 + lane, r = x / per, ch = x % per * 8;
+                            const bool ok = u && p0 + 8 * blk + r < c.len;
+                            const uint8_t* src = ok ? u + (off + r) * (2 * D) + 2 * ch : p.v.base[0];
+                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(
+                                             dst + tile_byte(BN, 8 * blk + r, ch)),
+                                         "l"(src), "r"(ok ? 16 : 0)
+                                         : "memory");
+                        }
+                    }
+                    asm volatile("cp.async.commit_group;\n" ::: "memory");
+                    if (n > 0) {
+                        asm volatile("cp.async.wait_group 1;\n" ::: "memory");
+                        post(n);
+                    }
+                } else {
+                    constexpr int per = D / 16;                 // 16-channel pieces of a row
+                    constexpr int E = 8 * per / 32;             // of a lane in an 8-row block (D = 64: 1)
+                    for (int blk = pw; blk < BN / 8; blk += 3) {
+                        int off;
+                        const uint8_t* u = block_rows(blk, off);
+                        uint4 code[E] = {};
+                        uint32_t d[E] = {};
+#pragma unroll
+                        for (int e = 0; e < E; ++e) {
+                            const int x = e * 32 + lane, r = x / per, ch = x % per * 16;
+                            if (u && p0 + 8 * blk + r < c.len) {
+                                const int rb = fmt == 1 ? D : D / 2;
+                                const uint8_t* a = u + (off + r) * rb;
+                                if (fmt == 1) {
+                                    code[e] = *reinterpret_cast<const uint4*>(a + ch);
+                                } else {
+                                    const uint2 y = *reinterpret_cast<const uint2*>(a + ch / 2);
+                                    code[e].x = y.x;
+                                    code[e].y = y.y;
+                                }
+                                d[e] = *reinterpret_cast<const uint16_t*>(u + (int64_t)p.v.ps * rb + (off + r) * (D / 16) +
+                                                                          ch / 32 * 2);
+                            }
+                        }
+#pragma unroll
+                        for (int e = 0; e < E; ++e) {
+                            const int x = e * 32 + lane, r = x / per, ch = x % per * 16;
+                            const uint32_t dd = d[e] | (d[e] << 16);
+                            const uint4 lo = fmt == 1 ? decode_q8(make_uint2(code[e].x, code[e].y), dd) : decode_q4(code[e].x, dd);
+                            const uint4 hi = fmt == 1 ? decode_q8(make_uint2(code[e].z, code[e].w), dd) : decode_q4(code[e].y, dd);
+                            st_shared16(dst + tile_byte(BN, 8 * blk + r, ch), lo);
+                            st_shared16(dst + tile_byte(BN, 8 * blk + r, ch + 8), hi);
+                        }
+                    }
+                    post(n + 1);
+                }
+            }
+            if (KF == 0) {
+                asm volatile("cp.async.wait_group 0;\n" ::: "memory");
+                post(2 * nt);
+            }
+        }
+    } else {
+        // ---------------------------------------------------------------------- the softmax
+        if constexpr (NT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;\n");
+        const int t = warp >> 2, in = threadIdx.x & 127, row = r0 + 128 * t + in;
+        const bool alive = row < r1;
+        const ScoreRule rule = score_rule(p);
+        const bool plain = rule.plain();
+        RowState rs;
+        const int64_t at = (int64_t)(c.row0 + (alive ? row / G : 0)) * p.Hq + h * G + (alive ? row % G : 0);
+        rs.pos = alive ? c.pos0 + row / G : -1;
+        rs.lo = p.window > 0 ? rs.pos - p.window + 1 : 0;
+        rs.hi = min(rs.pos, c.len - 1);
+        rs.pre = rs.pos >= 0 ? c.pre : 0;
+        rs.slope = plain || !p.slopes || !alive ? 0.f : p.slopes[h * G + row % G] * kL2e;
+        rs.f = rule.factor(1.f);
+        float m = -INFINITY, l = 0.f;
+        if (t < active) {
+            // this row of Q to shared memory; bf16 queries over quantised pages become fp16, scaled by a power of two
+            const uint32_t qs = base + t * GE::q_bytes;
+            const TQ* src = alive ? (const TQ*)p.q + (int64_t)(c.row0 + row / G) * p.q_stride + ((int64_t)h * G + row % G) * D : nullptr;
+            float up = 1.f;
+            if constexpr (!std::is_same<T, TQ>::value) {
+                float a = 0.f;
+                if (src)
+                    for (int d = 0; d < D; d += 8) {
+                        float x[8];
+                        unpack8<TQ>(*reinterpret_cast<const uint4*>(src + d), x);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) a = fmaxf(a, fabsf(x[e]));
+                    }
+                const int ex = (int)((__float_as_uint(a) >> 23) & 255) - 127;
+                if (a > 0.f && ex < 128) {
+                    const int sh = min(max(14 - ex, -100), 100);
+                    up = __uint_as_float((uint32_t)(127 + sh) << 23);
+                    rs.f *= __uint_as_float((uint32_t)(127 - sh) << 23);
+                }
+            }
+#pragma unroll 4
+            for (int d = 0; d < D; d += 8) {
+                uint4 x = make_uint4(0, 0, 0, 0);
+                if (src) {
+                    x = *reinterpret_cast<const uint4*>(src + d);
+                    if constexpr (!std::is_same<T, TQ>::value) {
+                        float y[8];
+                        unpack8<TQ>(x, y);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) y[e] *= up;
+                        x = pack8<T>(y);
+                    }
+                }
+                st_shared16(qs + tile_byte(128, in, d), x);
+            }
+            fence_async_smem();
+            mbar_arrive(q_full);
+
+            const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16), o_addr = lanes + GE::o_col(t);
+            // positions of the row tile's first and last rows: what decides whether a KV tile is seen whole
+            const int first = c.pos0 + (r0 + 128 * t) / G, last = c.pos0 + (min(r1, r0 + 128 * t + 128) - 1) / G;
+            for (int i = 0; i < nt; ++i) {
+                const int buf = NT == 2 ? t : i & 1, p0 = kv.at(i0 + i);
+                const uint32_t s_addr = lanes + GE::s_col(buf);
+                wait(s_full + 8 * buf, NT == 2 ? i & 1 : (i >> 1) & 1);
+                tc_fence_after();
+                uint32_t sr[BN / 32][32];
+#pragma unroll
+                for (int k = 0; k < BN / 32; ++k) tmem_ld32(s_addr + 32 * k, sr[k]);
+                tmem_wait_ld();
+                float f = rs.f;
+                if (!plain) {
+                    f = 1.f;
+                    const float dp = (float)(rs.pos - p0);
+#pragma unroll
+                    for (int k = 0; k < BN / 32; ++k) {
+                        float big = 0.f;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            const float x = __uint_as_float(sr[k][e]) * rs.f;
+                            sr[k][e] = __float_as_uint(x);
+                            big = fmaxf(big, fabsf(x));
+                        }
+                        if (rule.cap > 0.f) {
+                            if (__all_sync(kAll, big < 0.25f)) {
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    sr[k][e] = __float_as_uint(rule.cap_l2 * tanh_small(__uint_as_float(sr[k][e])));
+                            } else {
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    sr[k][e] = __float_as_uint(rule.cap_l2 * tanh_any(__uint_as_float(sr[k][e])));
+                            }
+                        }
+                        if (rule.biased) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                sr[k][e] = __float_as_uint(__uint_as_float(sr[k][e]) - rs.slope * fabsf(dp - (float)(32 * k + e)));
+                        }
+                    }
+                }
+                const bool whole = p0 + BN <= c.pre ? first >= 0
+                                                    : p0 + BN - 1 <= first && p0 + BN <= c.len &&
+                                                          (p.window <= 0 || p0 >= last - p.window + 1);
+                if (!whole) {
+                    const int hi = rs.hi - p0, lo = rs.lo - p0, pre = rs.pre - p0;
+#pragma unroll
+                    for (int k = 0; k < BN / 32; ++k)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            const int j = 32 * k + e;
+                            if (!((j <= hi && j >= lo) || j < pre)) sr[k][e] = 0xff800000u;
+                        }
+                }
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int k = 0; k < BN / 32; ++k)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(sr[k][e]));
+                const float x = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * f;
+                const bool grow = x > m + kLazy || (m == -INFINITY && x > -INFINITY);
+                if constexpr (NT == 1) {
+                    // S runs ahead of the values here: those of tile i - 1 are done before this tile's weights go out
+                    // (with two row tiles, S of tile i was issued after them)
+                    if (i > 0) {
+                        wait(o_done, (i - 1) & 1);
+                        tc_fence_after();
+                    }
+                }
+                if (i == 0) {
+                    m = x;
+                } else if (__any_sync(kAll, grow)) {
+                    const float a = grow ? ex2(m - x) : 1.f;
+                    l *= a;
+                    if (grow) m = x;
+#pragma unroll 1
+                    for (int d = 0; d < D; d += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(o_addr + d, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
+                        tmem_st32(o_addr + d, o);
+                    }
+                }
+                const float mb = m == -INFINITY ? 0.f : m;
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int k = 0; k < BN / 64; ++k) {
+                    uint32_t pr[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const float u = ex2(fmaf(__uint_as_float(sr[2 * k + e / 16][2 * (e % 16)]), f, -mb));
+                        const float v = ex2(fmaf(__uint_as_float(sr[2 * k + e / 16][2 * (e % 16) + 1]), f, -mb));
+                        sum[2 * (e & 1)] += u;
+                        sum[2 * (e & 1) + 1] += v;
+                        pr[e] = Two<T>::pack(u, v);
+                    }
+                    tmem_st32(s_addr + 32 * k, pr);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                tmem_wait_st();
+                if (!whole) {
+                    // does the V tile hold an infinity or NaN that some row must not see?
+                    const int n = 2 * i + 1;
+                    const uint32_t v_tile = ring + (n & 3) * GE::slot;
+                    wait(full + 8 * (n & 3), (n >> 2) & 1);
+                    constexpr uint32_t top = BF ? 0x7f80u : 0x7c00u;
+                    uint32_t bad = 0;
+                    for (int e = in; e < BN * D / 8; e += 128) {
+                        const uint4 y = ld_shared16(v_tile + 16 * e);
+                        const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) bad |= (w[q] & top) == top || ((w[q] >> 16) & top) == top;
+                    }
+                    asm volatile("{ .reg .pred p, q; setp.ne.u32 p, %0, 0; barrier.cta.red.or.pred q, %1, 128, p; selp.u32 %0, 1, 0, q; }\n"
+                                 : "+r"(bad) : "r"(1 + t) : "memory");
+                    if (bad) add_seen<D, BN, T>(v_tile, o_addr, s_addr, rs, p0, i == 0);
+                    if (in == 0) s_skip[buf] = bad ? 1 : 0;
+                } else if (in == 0) {
+                    s_skip[buf] = 0;
+                }
+                tc_fence_before();
+                mbar_arrive(p_full + 8 * buf);
+            }
+            if (nt > 0) {
+                wait(o_done + 8 * t, (nt - 1) & 1);
+                tc_fence_after();
+            }
+            const float inv = l > 0.f ? 1.f / l : 0.f;
+            if (splits == 1) {
+                TQ* out = (TQ*)p.out + at * D;
+                if (p.lse && alive) p.lse[at] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+#pragma unroll 1
+                for (int d = 0; d < D; d += 32) {
+                    uint32_t o[32] = {};
+                    if (nt > 0) {
+                        tmem_ld32(o_addr + d, o);
+                        tmem_wait_ld();
+                    }
+                    if (!alive) continue;
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        float y[8];
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) y[q] = nt > 0 ? __uint_as_float(o[e + q]) * inv : 0.f;
+                        *reinterpret_cast<uint4*>(out + d + e) = pack8<TQ>(y);
+                    }
+                }
+            } else {
+                const int64_t part = (int64_t)split * p.n_rows * p.Hq + at, all = (int64_t)splits * p.n_rows * p.Hq;
+                float* o_part = p.ws + 2 * all + part * D;
+                if (alive) *reinterpret_cast<float2*>(p.ws + 2 * part) = make_float2(m, l);
+#pragma unroll 1
+                for (int d = 0; d < D && nt > 0; d += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(o_addr + d, o);
+                    tmem_wait_ld();
+                    if (!alive) continue;
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        *reinterpret_cast<uint4*>(o_part + d + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 4 * NT) tmem_free512(tmem);
+}
+
+// Joins the splits' partials: D / 8 threads a row, all rows of a chunk.
+constexpr int kJT = 128;
+template <int D, typename TQ> __global__ void __launch_bounds__(kJT) prefill_join_kernel(PagedAttnParams p, int splits) {
+    grid_dep_wait();
+    constexpr int L = D / 8;
     const int b = blockIdx.z, h = blockIdx.y, G = p.G;
-    const Chunk c = chunk_of(p, b, blockIdx.x == 0 && h == 0 && threadIdx.x == 0);
-    const int rows = c.n * G, base_row = blockIdx.x * kRowsCta + warp * 16;
-    if (base_row >= rows) return;
-    const ScoreRule rule = score_rule(p);
-    auto qrow = [&](int r) -> const TQ* {
-        const int i = base_row + r;
-        if (i >= rows) return nullptr;
-        return (const TQ*)p.q + (int64_t)(c.row0 + i / G) * p.q_stride + ((int64_t)h * G + i % G) * D;
-    };
-    uint32_t qf[D / 16][4];
-    float back[2], slope[2], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[D / 8][4] = {};
-    load_queries<D, KF, T, TQ>(qrow, g, t, qf, back);
-    int pos[2], lo[2], pre[2];
+    const Chunk c = chunk_of(p, b, false);
+    const int row = blockIdx.x * (kJT / L) + threadIdx.x / L, ch = threadIdx.x % L * 8;
+    if (row >= c.n * G) return;
+    const int64_t at = (int64_t)(c.row0 + row / G) * p.Hq + h * G + row % G, n = (int64_t)p.n_rows * p.Hq;
+    float m = -INFINITY;
+    for (int s = 0; s < splits; ++s) m = fmaxf(m, p.ws[2 * (s * n + at)]);
+    float l = 0.f, o[8] = {};
+    for (int s = 0; s < splits; ++s) {
+        const float2 ml = *reinterpret_cast<const float2*>(p.ws + 2 * (s * n + at));
+        if (ml.x == -INFINITY) continue;                 // nothing seen: no output was written
+        const float a = ex2(ml.x - m);
+        l += ml.y * a;
+        const float4* f = reinterpret_cast<const float4*>(p.ws + 2 * splits * n + (s * n + at) * D + ch);
+        const float4 x = f[0], y = f[1];
+        const float z[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const int i = base_row + g + 8 * k;
-        pos[k] = i < rows ? c.pos0 + i / G : -1;
-        lo[k] = p.window > 0 ? pos[k] - p.window + 1 : 0;
-        pre[k] = pos[k] >= 0 ? c.pre : 0;
-        slope[k] = p.slopes && i < rows ? p.slopes[h * G + i % G] * kL2e : 0.f;
+        for (int e = 0; e < 8; ++e) o[e] = fmaf(z[e], a, o[e]);
     }
-    // the warp's tiles: [0, n0) of the prefix, [t1, end) from its first row's window to its last row
-    const int last = c.pos0 + (min(base_row + 16, rows) - 1) / G, first = c.pos0 + base_row / G;
-    const int end = last < 0 ? 0 : (max(last + 1, c.pre) + kTile - 1) / kTile;
-    const int t1 = min(end, p.window > 0 ? max(0, first - p.window + 1) / kTile : 0);
-    const int n0 = min((last < 0 ? 0 : c.pre + kTile - 1) / kTile, t1);
-
-    for (int i = 0; i < n0 + end - t1; ++i) {
-        const int p0 = (i < n0 ? i : t1 + i - n0) * kTile, off = p0 & (p.v.ps - 1);
-        int page = p.table[b * p.table_stride + (p0 >> p.v.ps_shift)];
-        unsigned live = c.len - p0 >= kTile ? 0xffffu : (1u << max(0, c.len - p0)) - 1;
-        if (page < 0 || page >= p.v.n_pages) {
-            if (lane == 0) raise_status(p.v.status, KVQ_PAGED_BAD_INDEX);
-            page = 0;
-            live = 0;
-        }
-        float s[2][4] = {};
-        tile_scores<D, KF, T>(global_tile<KGeo<D, KF>::RB>(p.v, 0, page, h, off, live), g, t, qf, s);
-        float mx[2] = {-INFINITY, -INFINITY};
-        bool hidden = false;
+    const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int k = e >> 1, j = p0 + 8 * n + 2 * t + (e & 1);
-                const bool see = j < c.len && ((j <= pos[k] && j >= lo[k]) || j < pre[k]);
-                const float x = rule(s[n][e] * rule.factor(back[k]), abs(pos[k] - j), slope[k]);
-                s[n][e] = see ? x : -INFINITY;
-                hidden |= !see && base_row + g + 8 * k < rows;
-                mx[k] = fmaxf(mx[k], s[n][e]);
-            }
-        float base[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            mx[k] = fmaxf(mx[k], __shfl_xor_sync(kAll, mx[k], 1));
-            mx[k] = fmaxf(mx[k], __shfl_xor_sync(kAll, mx[k], 2));
-            const float mn = fmaxf(m[k], mx[k]);
-            base[k] = mn == -INFINITY ? 0.f : mn;
-            const float a = ex2(m[k] - base[k]);
-            m[k] = mn;
-            l[k] *= a;
-#pragma unroll
-            for (int d = 0; d < D / 8; ++d) {
-                o[d][2 * k] *= a;
-                o[d][2 * k + 1] *= a;
-            }
-        }
-        uint32_t pa[4], pl[4] = {};
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const float x = ex2(s[n][2 * k] - base[k]), y = ex2(s[n][2 * k + 1] - base[k]);
-                l[k] += x + y;
-                pa[2 * n + k] = Two<T>::pack(x, y);
-            }
-        const GlobalTile<VGeo<D, VF>::RB> vt = global_tile<VGeo<D, VF>::RB>(p.v, 1, page, h, off, live);
-        // a weight of 0 does not keep an infinity or NaN out of the product: where some row does not see the
-        // whole tile and the tile holds one, every row adds what it sees by itself
-        const bool part = __any_sync(kAll, hidden);
-        if (part && tile_nonfinite<D, VF, T>(vt, lane)) {
-            add_seen<D, VF, T>(vt, g, t, s, base, o);
-            continue;
-        }
-        tile_values<D, VF, T, false>(vt, g, t, pa, pl, o);
-    }
-    using V = VGeo<D, VF>;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        l[k] += __shfl_xor_sync(kAll, l[k], 1);
-        l[k] += __shfl_xor_sync(kAll, l[k], 2);
-        const int i = base_row + g + 8 * k;
-        if (i >= rows) continue;
-        const int64_t at = (int64_t)(c.row0 + i / G) * p.Hq + h * G + i % G;
-        const float inv = l[k] > 0.f ? 1.f / l[k] : 0.f;
-        TQ* out = (TQ*)p.out + at * D;
-#pragma unroll
-        for (int j = 0; j < V::NJ; ++j)
-#pragma unroll
-            for (int e = 0; e < V::CH; e += 2)
-#pragma unroll
-                for (int col = 0; col < 2; ++col)
-                    *reinterpret_cast<uint32_t*>(out + ochan<D, VF>(j, 2 * t + col) + e) =
-                        Two<TQ>::pack(o[V::CH * j + e][2 * k + col] * inv, o[V::CH * j + e + 1][2 * k + col] * inv);
-        if (p.lse && t == 0) p.lse[at] = l[k] > 0.f ? (m[k] + log2f(l[k])) * kLn2 : -INFINITY;
-    }
+    for (int e = 0; e < 8; ++e) o[e] *= inv;
+    *reinterpret_cast<uint4*>((TQ*)p.out + at * D + ch) = pack8<TQ>(o);
+    if (p.lse && ch == 0) p.lse[at] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
 }
 
-template <int D, int KF, int VF, typename T, typename TQ> int prefill_run(const PagedAttnParams& p, cudaStream_t s) {
-    const dim3 grid((unsigned)(((int64_t)p.max_q * p.G + kRowsCta - 1) / kRowsCta), p.v.H, p.n_seq);
-    prefill_kernel<D, KF, VF, T, TQ><<<grid, kPT, 0, s>>>(p);
-    return (int)cudaGetLastError();
+// Splits of the positions: as many as leave one CTA per SM, when the row tiles alone give fewer.
+int splits_of(int64_t rows, int n_seq, int H, int tile_rows, int sm_count) {
+    const int64_t ctas = (rows / tile_rows + n_seq) * H;       // at most one part-filled tile per sequence
+    int64_t s = (sm_count < kMaxSms ? sm_count : kMaxSms) / (ctas > 0 ? ctas : 1);
+    return (int)(s < 1 ? 1 : (s > kMaxSplits ? kMaxSplits : s));
 }
 
-template <int D> int prefill_d(const PagedAttnParams& p, cudaStream_t s) {
+template <int D, int KF, int VF, typename T, typename TQ> int prefill_run(PagedAttnParams p, int sm_count, cudaStream_t s) {
+    using GE = Geo<D>;
+    const auto k = prefill_kernel<D, KF, VF, T, TQ>;
+    int res = 0;
+    if (const int e = resident_ctas((const void*)k, GE::threads, GE::smem, &res)) return e;
+    const int64_t chunk = (int64_t)p.max_q * p.G;
+    const int splits = splits_of((int64_t)p.n_rows * p.G, p.n_seq, p.v.H, GE::rows, sm_count);
+    const dim3 grid(p.v.H, (unsigned)((chunk + GE::rows - 1) / GE::rows), (unsigned)(p.n_seq * splits));
+    cudaError_t e = launch_k(k, grid, dim3(GE::threads), GE::smem, s, true, p, splits);
+    if (e == cudaSuccess && splits > 1) {
+        constexpr int R = kJT / (D / 8);
+        e = launch_k(prefill_join_kernel<D, TQ>, dim3((unsigned)((chunk + R - 1) / R), p.v.H, p.n_seq), dim3(kJT), 0, s, true, p, splits);
+    }
+    return (int)e;
+}
+
+template <int D> int prefill_d(const PagedAttnParams& p, int n, cudaStream_t s) {
     const int kf = p.v.fmt[0], vf = p.v.fmt[1];
-    if (kf == KVQ_F16) return prefill_run<D, PF_16, PF_16, __half, __half>(p, s);
-    if (kf == KVQ_BF16) return prefill_run<D, PF_16, PF_16, __nv_bfloat16, __nv_bfloat16>(p, s);
+    if (kf == KVQ_F16) return prefill_run<D, 0, 0, __half, __half>(p, n, s);
+    if (kf == KVQ_BF16) return prefill_run<D, 0, 0, __nv_bfloat16, __nv_bfloat16>(p, n, s);
     if (p.dtype == KVQ_F16) {
-        if (kf == KVQ_Q4_0) return prefill_run<D, PF_Q4, PF_Q4, __half, __half>(p, s);
-        if (vf == KVQ_Q4_0) return prefill_run<D, PF_Q8, PF_Q4, __half, __half>(p, s);
-        return prefill_run<D, PF_Q8, PF_Q8, __half, __half>(p, s);
+        if (kf == KVQ_Q4_0) return prefill_run<D, 2, 2, __half, __half>(p, n, s);
+        if (vf == KVQ_Q4_0) return prefill_run<D, 1, 2, __half, __half>(p, n, s);
+        return prefill_run<D, 1, 1, __half, __half>(p, n, s);
     }
-    if (kf == KVQ_Q4_0) return prefill_run<D, PF_Q4, PF_Q4, __half, __nv_bfloat16>(p, s);
-    if (vf == KVQ_Q4_0) return prefill_run<D, PF_Q8, PF_Q4, __half, __nv_bfloat16>(p, s);
-    return prefill_run<D, PF_Q8, PF_Q8, __half, __nv_bfloat16>(p, s);
+    if (kf == KVQ_Q4_0) return prefill_run<D, 2, 2, __half, __nv_bfloat16>(p, n, s);
+    if (vf == KVQ_Q4_0) return prefill_run<D, 1, 2, __half, __nv_bfloat16>(p, n, s);
+    return prefill_run<D, 1, 1, __half, __nv_bfloat16>(p, n, s);
 }
 
 }  // namespace
 
-size_t paged_prefill_ws_floats(int, int, int, int64_t) { return 0; }
+// The splits times the rows stay below one CTA per SM's worth of row tiles, and below kMaxSplits times the rows.
+size_t paged_prefill_ws_floats(int D, int64_t head_rows) {
+    const int64_t most = head_rows * kMaxSplits, full = (int64_t)kMaxSms * 256;
+    return (size_t)((most < full ? most : full) * (D + 2));
+}
 
-int launch_paged_prefill(PagedAttnParams p, int, void* stream) {
+int launch_paged_prefill(PagedAttnParams p, int sm_count, void* stream) {
     cudaStream_t s = (cudaStream_t)stream;
-    if (p.v.D == 64) return prefill_d<64>(p, s);
-    if (p.v.D == 128) return prefill_d<128>(p, s);
-    return prefill_d<256>(p, s);
+    if (p.v.D == 64) return prefill_d<64>(p, sm_count, s);
+    if (p.v.D == 128) return prefill_d<128>(p, sm_count, s);
+    return prefill_d<256>(p, sm_count, s);
 }
 
 }  // namespace kvq

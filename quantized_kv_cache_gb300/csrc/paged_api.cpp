@@ -88,7 +88,7 @@ PagedView view(const kvq_paged* h, int layer) {
 size_t workspace_floats(const kvq_paged_config& c, int64_t seqs, int64_t rows) {
     const int G = c.n_q_heads / c.n_kv_heads;
     const size_t a = paged_decode_ws_floats(G, c.head_dim, seqs * c.n_kv_heads);
-    const size_t b = paged_prefill_ws_floats(G, c.head_dim, c.n_kv_heads, rows);
+    const size_t b = paged_prefill_ws_floats(c.head_dim, rows * c.n_q_heads);
     return a > b ? a : b;
 }
 
@@ -275,7 +275,8 @@ kvq_status kv_paged_prefill_attn(kvq_paged* h, int32_t layer, int32_t dtype, int
     if (!dtype16(dtype) || n_seq < 0 || n_rows < 0 || max_q < 0) return KVQ_EINVAL;
     if (n_seq == 0 || n_rows == 0 || max_q == 0) return KVQ_OK;
     if (!cu_q || !aligned4(cu_q)) return KVQ_EINVAL;
-    if (n_seq > 65535) return KVQ_EUNSUPPORTED;      // one grid row per sequence
+    // grid rows: one per sequence, one per 128 rows of the longest chunk; row counts stay below 2^31
+    if (n_seq > 65535 || (int64_t)(max_q < n_rows ? max_q : n_rows) * kMaxG > 65535 * (int64_t)128) return KVQ_EUNSUPPORTED;
     PagedAttnParams p;
     st = attn_params(h, layer, dtype, n_seq, n_rows, q, q_stride, page_table, max_pages, table_stride, lens, out, opts,
                      workspace, ws_bytes, &p);

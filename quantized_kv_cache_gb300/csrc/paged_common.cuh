@@ -51,5 +51,52 @@ __device__ __forceinline__ const uint8_t* unit_at(const PagedView& v, int w, int
     return v.base[w] + ((int64_t)page * v.H + head) * v.unit[w];
 }
 
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+    return y;
+}
+
+constexpr float kL2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+// tanh to about 2^-23 of 1 and, below 1/4, of itself (the odd series' first five terms there; 1 - 2 / (1 +
+// exp(2 |x|)) above).
+__device__ __forceinline__ float tanh_small(float x) {
+    const float q = x * x;
+    return x * fmaf(q, fmaf(q, fmaf(q, fmaf(q, 0.021869489f, -0.053968254f), 0.13333333f), -0.33333334f), 1.f);
+}
+__device__ __forceinline__ float tanh_any(float x) {
+    const float a = fabsf(x), t = 1.f - __fdividef(2.f, 1.f + ex2(2.f * kL2e * a));
+    return a < 0.25f ? tanh_small(x) : copysignf(t, x);
+}
+
+// The score options, in units of log2. A score x = q.k * f, f = (the row's power of two) * scale * log2(e);
+// with a cap, f = .. * scale / softcap and x = softcap * log2(e) * tanh(q.k * f); then the bias.
+struct ScoreRule {
+    float scale, cap, cap_l2;      // softmax scale; softcap (0: none); softcap * log2(e)
+    bool biased;
+    __device__ __forceinline__ bool plain() const { return cap == 0.f && !biased; }
+    __device__ __forceinline__ float factor(float back) const { return back * scale * (cap > 0.f ? 1.f / cap : kL2e); }
+    // dist: |distance| in positions; slope_l2: the head's slope * log2(e)
+    __device__ __forceinline__ float operator()(float x, int dist, float slope_l2) const {
+        if (cap > 0.f) x = cap_l2 * tanh_any(x);
+        return biased ? x - slope_l2 * (float)dist : x;
+    }
+};
+__device__ __forceinline__ ScoreRule score_rule(const PagedAttnParams& p) {
+    ScoreRule r;
+    r.scale = p.scale;
+    r.cap = p.softcap;
+    r.cap_l2 = p.softcap * kL2e;
+    r.biased = p.slopes != nullptr;
+    return r;
+}
+
+__device__ __forceinline__ __half2 h2(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
+__device__ __forceinline__ uint32_t u32(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+// raw halves (1024 + u), u = code + off, times the scale pair d: fp16(code x scale), one rounding.
+__device__ __forceinline__ uint32_t deq(uint32_t raw, float off1024, uint32_t d) {
+    return u32(__hmul2(__hsub2(h2(raw), __float2half2_rn(off1024)), h2(d)));
+}
 }  // namespace
 }  // namespace kvq

@@ -32,12 +32,6 @@ __device__ __forceinline__ void mma_t(float (&c)[4], const uint32_t (&a)[4], uin
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ __half2 h2(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
-__device__ __forceinline__ uint32_t u32(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
-// raw halves (1024 + u), u = code + off, times the scale pair d: fp16(code x scale), one rounding.
-__device__ __forceinline__ uint32_t deq(uint32_t raw, float off1024, uint32_t d) {
-    return u32(__hmul2(__hsub2(h2(raw), __float2half2_rn(off1024)), h2(d)));
-}
 // (r & 0x000f000f) | 0x64006400 and (r & 0x00ff00ff) ^ 0x64806480: one logic operation each.
 __device__ __forceinline__ uint32_t nib_raw(uint32_t r) { return (r & 0x000f000fu) | 0x64006400u; }
 // nibbles at bits 4-7 of each half: 1024 + 16 n
@@ -166,38 +160,6 @@ __device__ __forceinline__ void tile_values(const SRC& src, int g, int t, const 
     }
 }
 
-// Whether the tile holds an infinity or NaN among its values (16-bit values or scales of type T).
-template <int D, int PF, typename T, typename SRC>
-__device__ __forceinline__ bool tile_nonfinite(const SRC& src, int lane) {
-    constexpr uint32_t top = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
-    bool bad = false;
-    if constexpr (PF == PF_16) {
-        for (int i = lane; i < 16 * D / 8; i += 32) {
-            const Words<4> w = src.template piece<4>(i / (D / 8), i % (D / 8) * 16);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) bad |= (w.w[e] & top) == top || ((w.w[e] >> 16) & top) == top;
-        }
-    } else {
-        for (int i = lane; i < 16 * D / 32; i += 32) bad |= (src.scale(i / (D / 32), i % (D / 32)) & top) == top;
-    }
-    return __any_sync(kAll, bad);
-}
-
-// One value of the tile as the products see it.
-template <int D, int PF, typename T, typename SRC>
-__device__ __forceinline__ float tile_value(const SRC& src, int row, int ch) {
-    if constexpr (PF == PF_16) {
-        const uint32_t w = src.template piece<1>(row, ch / 2 * 4).w[0];
-        const float2 f = Two<T>::unpack(w);
-        return ch & 1 ? f.y : f.x;
-    } else {
-        const float d = __half2float(__ushort_as_half((uint16_t)src.scale(row, ch / 32)));
-        const uint32_t w = src.template piece<1>(row, (PF == PF_Q8 ? ch : ch / 2) / 4 * 4).w[0];
-        const int c = PF == PF_Q8 ? (int)(int8_t)(w >> (8 * (ch & 3))) : (int)((w >> (4 * (ch & 7))) & 15u) - 8;
-        return __half2float(__float2half_rn((float)c * d));
-    }
-}
-
 // Query fragments of the 16 rows of a warp; row r is at base + rows(r) (null: a row of zeros), of
 // type TQ. fp16 operands of bf16 queries are scaled by a power of two per row so that no exponent
 // is out of range; back[] undoes it (rows g, g + 8).
@@ -246,68 +208,6 @@ __device__ __forceinline__ void load_queries(const ROW& rows, int g, int t, uint
                 qf[ks][2 * hi + half] = u;
             }
     }
-}
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
-    return y;
-}
-
-constexpr float kL2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-
-// The score options, in units of log2. A score x = q.k * f, f = (the row's power of two) * scale * log2(e);
-// with a cap, f = .. * scale / softcap and x = softcap * log2(e) * tanh(q.k * f); then the bias.
-struct ScoreRule {
-    float scale, cap, cap_l2;      // softmax scale; softcap (0: none); softcap * log2(e)
-    bool biased;
-    __device__ __forceinline__ bool plain() const { return cap == 0.f && !biased; }
-    __device__ __forceinline__ float factor(float back) const { return back * scale * (cap > 0.f ? 1.f / cap : kL2e); }
-    // dist: |distance| in positions; slope_l2: the head's slope * log2(e)
-    __device__ __forceinline__ float operator()(float x, int dist, float slope_l2) const {
-        if (cap > 0.f) x = cap_l2 * tanhf(x);
-        return biased ? x - slope_l2 * (float)dist : x;
-    }
-};
-__device__ __forceinline__ ScoreRule score_rule(const PagedAttnParams& p) {
-    ScoreRule r;
-    r.scale = p.scale;
-    r.cap = p.softcap;
-    r.cap_l2 = p.softcap * kL2e;
-    r.biased = p.slopes != nullptr;
-    return r;
-}
-
-// A tile's rows in global memory; rows that no query of the call sees read as zeros.
-template <int RB> struct GlobalTile {
-    const uint8_t* codes;      // row 0 of the tile (null: the page number was out of range)
-    const uint8_t* scales;
-    int scale_row;             // bytes of a row's scales
-    uint32_t live;             // bit r: row r is visible
-    template <int N> __device__ __forceinline__ Words<N> piece(int row, int byte) const {
-        Words<N> w = {};
-        if ((live >> row) & 1) {
-            const uint8_t* a = codes + row * RB + byte;
-            if constexpr (N == 4) *reinterpret_cast<uint4*>(w.w) = *reinterpret_cast<const uint4*>(a);
-            else if constexpr (N == 2) *reinterpret_cast<uint2*>(w.w) = *reinterpret_cast<const uint2*>(a);
-            else w.w[0] = *reinterpret_cast<const uint32_t*>(a);
-        }
-        return w;
-    }
-    __device__ __forceinline__ uint32_t scale(int row, int blk) const {
-        return (live >> row) & 1 ? *reinterpret_cast<const uint16_t*>(scales + row * scale_row + 2 * blk) : 0u;
-    }
-};
-
-template <int RB>
-__device__ __forceinline__ GlobalTile<RB> global_tile(const PagedView& v, int w, int page, int head, int off, uint32_t live) {
-    GlobalTile<RB> s;
-    const uint8_t* u = unit_at(v, w, page, head);
-    s.codes = u + (int64_t)off * RB;
-    s.scale_row = v.D / 16;
-    s.scales = u + (int64_t)v.ps * RB + off * s.scale_row;
-    s.live = live;
-    return s;
 }
 
 // A tile staged in shared memory: 16 code rows of RB bytes, then (block formats) the rows' scales. The

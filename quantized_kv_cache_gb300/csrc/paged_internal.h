@@ -7,6 +7,7 @@
 namespace kvq {
 
 constexpr int kTile = 16;            // positions per attention tile: every page size is a multiple
+constexpr int kMaxSms = 192;         // bound of the SMs that a chunk's splits are spread over (sizes the workspace)
 constexpr int kMaxDecodeCtas = 1024; // bound of a decode launch's CTAs (sizes the workspace)
 
 // Bytes of one code row (D values) and of a row's scales.
@@ -72,6 +73,6 @@ int launch_paged_read(const ReadParams& p, void* stream);
 int launch_paged_decode(PagedAttnParams p, int sm_count, void* stream);
 int launch_paged_prefill(PagedAttnParams p, int sm_count, void* stream);
 size_t paged_decode_ws_floats(int G, int D, int64_t segments);
-size_t paged_prefill_ws_floats(int G, int D, int H, int64_t rows);
+size_t paged_prefill_ws_floats(int D, int64_t head_rows);   // query rows x query heads
 
 }  // namespace kvq
