@@ -122,13 +122,13 @@ __device__ __noinline__ void add_seen(uint32_t v_tile, uint32_t o_addr, uint32_t
             for (int i = 0; i < 32; ++i) o[i] = 0;
         } else {
             tmem_ld32(o_addr + d0, o);
-            tmem_wait_ld();
+            tmem_wait_ld(o);
         }
 #pragma unroll 1
         for (int c = 0; c < BN / 64; ++c) {
             uint32_t w[32];
             tmem_ld32(p_addr + 32 * c, w);
-            tmem_wait_ld();
+            tmem_wait_ld(w);
 #pragma unroll 1
             for (int e = 0; e < 64; ++e) {
                 const int j = p0 + 64 * c + e;
@@ -147,6 +147,31 @@ __device__ __noinline__ void add_seen(uint32_t v_tile, uint32_t o_addr, uint32_t
         }
         tmem_st32(o_addr + d0, o);
         tmem_wait_st();
+    }
+}
+
+// Raw scores of 32 positions from p0 on to scores in units of log2: the cap, then the bias.
+__device__ __forceinline__ void apply_rule(uint32_t (&s)[32], const ScoreRule& rule, const RowState& r, int p0) {
+    float big = 0.f;
+#pragma unroll
+    for (int e = 0; e < 32; ++e) {
+        const float x = __uint_as_float(s[e]) * r.f;
+        s[e] = __float_as_uint(x);
+        big = fmaxf(big, fabsf(x));
+    }
+    if (rule.cap > 0.f) {
+        if (__all_sync(kAll, big < 0.25f)) {                   // no exponential where all of them are small
+#pragma unroll
+            for (int e = 0; e < 32; ++e) s[e] = __float_as_uint(rule.cap_l2 * tanh_small(__uint_as_float(s[e])));
+        } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) s[e] = __float_as_uint(rule.cap_l2 * tanh_any(__uint_as_float(s[e])));
+        }
+    }
+    if (rule.biased) {
+        const float d = (float)(r.pos - p0);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) s[e] = __float_as_uint(__uint_as_float(s[e]) - r.slope * fabsf(d - (float)e));
     }
 }
 
@@ -197,7 +222,6 @@ __global__ void __launch_bounds__(Geo<D>::threads, 1) prefill_kernel(PagedAttnPa
     auto wait = [&](uint32_t bar, uint32_t parity) { mbar_wait(bar, parity, p.v.status, &s_abort); };
 
     if (warp >= 4 * NT) {
-        if constexpr (NT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
         if (warp == 4 * NT) {
             // ------------------------------------------------------------------ the products
             if (lane == 0 && nt > 0) {
@@ -262,6 +286,9 @@ __global__ void __launch_bounds__(Geo<D>::threads, 1) prefill_kernel(PagedAttnPa
             // ------------------------------------------------------------------ K and V tiles
             const int pw = warp - 4 * NT - 1;                   // 8-row blocks pw, pw + 3, ..
             const int32_t* table = p.table + (int64_t)b * p.table_stride;
+            uint32_t put[D / 32];                               // this lane's pieces of an 8-row block of 16-bit rows
+#pragma unroll
+            for (int e = 0; e < D / 32; ++e) put[e] = tile_byte(BN, (e * 32 + lane) / (D / 8), (e * 32 + lane) % (D / 8) * 8);
             int posted = 0;
             auto post = [&](int n) {                            // items before n are in place
                 fence_async_smem();
@@ -280,8 +307,6 @@ __global__ void __launch_bounds__(Geo<D>::threads, 1) prefill_kernel(PagedAttnPa
                         page = -1;
                     }
                 }
-                constexpr int F[2] = {KF, VF};
-                (void)F;
                 auto block_rows = [&](int blk, int& off) -> const uint8_t* {
                     const int pg = __shfl_sync(kAll, page, blk >> 1);
                     off = (p0 + 8 * blk) & (p.v.ps - 1);
@@ -293,15 +318,22 @@ __global__ void __launch_bounds__(Geo<D>::threads, 1) prefill_kernel(PagedAttnPa
                     for (int blk = pw; blk < BN / 8; blk += 3) {
                         int off;
                         const uint8_t* u = block_rows(blk, off);
+                        const uint8_t* src = u + off * (2 * D) + lane * 16;    // eight rows are contiguous
+                        const int live = u ? c.len - p0 - 8 * blk : 0;         // rows of the block that hold positions
+                        if (live >= 8) {
 #pragma unroll
-                        for (int e = 0; e < 8 * per / 32; ++e) {
-                            const int x = e * 32 + lane, r = x / per, ch = x % per * 8;
-                            const bool ok = u && p0 + 8 * blk + r < c.len;
-                            const uint8_t* src = ok ? u + (off + r) * (2 * D) + 2 * ch : p.v.base[0];
-                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(
-                                             dst + tile_byte(BN, 8 * blk + r, ch)),
-                                         "l"(src), "r"(ok ? 16 : 0)
-                                         : "memory");
+                            for (int e = 0; e < per / 4; ++e)
+                                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst + 1024 * blk + put[e]),
+                                             "l"(src + 512 * e)
+                                             : "memory");
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < per / 4; ++e) {
+                                const bool ok = (e * 32 + lane) / per < live;
+                                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst + 1024 * blk + put[e]),
+                                             "l"(ok ? src + 512 * e : p.v.base[0]), "r"(ok ? 16 : 0)
+                                             : "memory");
+                            }
                         }
                     }
                     asm volatile("cp.async.commit_group;\n" ::: "memory");
@@ -354,7 +386,6 @@ __global__ void __launch_bounds__(Geo<D>::threads, 1) prefill_kernel(PagedAttnPa
         }
     } else {
         // ---------------------------------------------------------------------- the softmax
-        if constexpr (NT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;\n");
         const int t = warp >> 2, in = threadIdx.x & 127, row = r0 + 128 * t + in;
         const bool alive = row < r1;
         const ScoreRule rule = score_rule(p);
@@ -415,60 +446,38 @@ __global__ void __launch_bounds__(Geo<D>::threads, 1) prefill_kernel(PagedAttnPa
                 const uint32_t s_addr = lanes + GE::s_col(buf);
                 wait(s_full + 8 * buf, NT == 2 ? i & 1 : (i >> 1) & 1);
                 tc_fence_after();
-                uint32_t sr[BN / 32][32];
-#pragma unroll
-                for (int k = 0; k < BN / 32; ++k) tmem_ld32(s_addr + 32 * k, sr[k]);
-                tmem_wait_ld();
-                float f = rs.f;
-                if (!plain) {
-                    f = 1.f;
-                    const float dp = (float)(rs.pos - p0);
-#pragma unroll
-                    for (int k = 0; k < BN / 32; ++k) {
-                        float big = 0.f;
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            const float x = __uint_as_float(sr[k][e]) * rs.f;
-                            sr[k][e] = __float_as_uint(x);
-                            big = fmaxf(big, fabsf(x));
-                        }
-                        if (rule.cap > 0.f) {
-                            if (__all_sync(kAll, big < 0.25f)) {
-#pragma unroll
-                                for (int e = 0; e < 32; ++e)
-                                    sr[k][e] = __float_as_uint(rule.cap_l2 * tanh_small(__uint_as_float(sr[k][e])));
-                            } else {
-#pragma unroll
-                                for (int e = 0; e < 32; ++e)
-                                    sr[k][e] = __float_as_uint(rule.cap_l2 * tanh_any(__uint_as_float(sr[k][e])));
-                            }
-                        }
-                        if (rule.biased) {
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                sr[k][e] = __float_as_uint(__uint_as_float(sr[k][e]) - rs.slope * fabsf(dp - (float)(32 * k + e)));
-                        }
-                    }
-                }
                 const bool whole = p0 + BN <= c.pre ? first >= 0
                                                     : p0 + BN - 1 <= first && p0 + BN <= c.len &&
                                                           (p.window <= 0 || p0 >= last - p.window + 1);
-                if (!whole) {
-                    const int hi = rs.hi - p0, lo = rs.lo - p0, pre = rs.pre - p0;
+                // first pass: the row's maximum; scores that the options or the visibility change go back to S
+                const float f = plain ? rs.f : 1.f;
+                float mx = -INFINITY;
+                uint32_t sr[2][32];
+                tmem_ld32(s_addr, sr[0]);
 #pragma unroll
-                    for (int k = 0; k < BN / 32; ++k)
+                for (int k = 0; k < BN / 32; ++k) {
+                    uint32_t(&x)[32] = sr[k & 1];
+                    tmem_wait_ld(x);
+                    if (k + 1 < BN / 32) tmem_ld32(s_addr + 32 * (k + 1), sr[(k + 1) & 1]);
+                    if (!plain) apply_rule(x, rule, rs, p0 + 32 * k);
+                    if (!whole) {
+                        const int hi = rs.hi - p0 - 32 * k, lo = rs.lo - p0 - 32 * k, pre = rs.pre - p0 - 32 * k;
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            const int j = 32 * k + e;
-                            if (!((j <= hi && j >= lo) || j < pre)) sr[k][e] = 0xff800000u;
-                        }
+                        for (int e = 0; e < 32; ++e)
+                            if (!((e <= hi && e >= lo) || e < pre)) x[e] = 0xff800000u;
+                    }
+                    if (!plain || !whole) tmem_st32(s_addr + 32 * k, x);
+                    float y[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            y[q] = fmaxf(fmaxf(y[q], __uint_as_float(x[e + 2 * q])), __uint_as_float(x[e + 2 * q + 1]));
+                    mx = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
                 }
-                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                for (int k = 0; k < BN / 32; ++k)
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(sr[k][e]));
-                const float x = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * f;
+                if (!plain || !whole) tmem_wait_st();
+                tmem_ld32(s_addr, sr[0]);                      // the second pass's first scores are on their way
+                const float x = mx * f;
                 const bool grow = x > m + kLazy || (m == -INFINITY && x > -INFINITY);
                 if constexpr (NT == 1) {
                     // S runs ahead of the values here: those of tile i - 1 are done before this tile's weights go out
@@ -488,28 +497,32 @@ __global__ void __launch_bounds__(Geo<D>::threads, 1) prefill_kernel(PagedAttnPa
                     for (int d = 0; d < D; d += 32) {
                         uint32_t o[32];
                         tmem_ld32(o_addr + d, o);
-                        tmem_wait_ld();
+                        tmem_wait_ld(o);
 #pragma unroll
                         for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
                         tmem_st32(o_addr + d, o);
                     }
                 }
-                const float mb = m == -INFINITY ? 0.f : m;
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                // second pass: weights, their sum, and P over the scores read so far
+                const float2 f2 = make_float2(f, f), mb = m == -INFINITY ? make_float2(0.f, 0.f) : make_float2(-m, -m);
+                float2 sum[2] = {};
+                uint32_t pr[32];
 #pragma unroll
-                for (int k = 0; k < BN / 64; ++k) {
-                    uint32_t pr[32];
+                for (int k = 0; k < BN / 32; ++k) {
+                    uint32_t(&x)[32] = sr[k & 1];
+                    tmem_wait_ld(x);
+                    if (k + 1 < BN / 32) tmem_ld32(s_addr + 32 * (k + 1), sr[(k + 1) & 1]);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        const float u = ex2(fmaf(__uint_as_float(sr[2 * k + e / 16][2 * (e % 16)]), f, -mb));
-                        const float v = ex2(fmaf(__uint_as_float(sr[2 * k + e / 16][2 * (e % 16) + 1]), f, -mb));
-                        sum[2 * (e & 1)] += u;
-                        sum[2 * (e & 1) + 1] += v;
-                        pr[e] = Two<T>::pack(u, v);
+                    for (int e = 0; e < 16; ++e) {
+                        float2 u = __ffma2_rn(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), f2, mb);
+                        u.x = ex2(u.x);
+                        u.y = ex2(u.y);
+                        sum[e & 1] = __fadd2_rn(sum[e & 1], u);
+                        pr[16 * (k & 1) + e] = Two<T>::pack(u.x, u.y);
                     }
-                    tmem_st32(s_addr + 32 * k, pr);
+                    if (k & 1) tmem_st32(s_addr + 16 * (k - 1), pr);
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                 tmem_wait_st();
                 if (!whole) {
                     // does the V tile hold an infinity or NaN that some row must not see?
@@ -547,7 +560,7 @@ __global__ void __launch_bounds__(Geo<D>::threads, 1) prefill_kernel(PagedAttnPa
                     uint32_t o[32] = {};
                     if (nt > 0) {
                         tmem_ld32(o_addr + d, o);
-                        tmem_wait_ld();
+                        tmem_wait_ld(o);
                     }
                     if (!alive) continue;
 #pragma unroll
@@ -566,7 +579,7 @@ __global__ void __launch_bounds__(Geo<D>::threads, 1) prefill_kernel(PagedAttnPa
                 for (int d = 0; d < D && nt > 0; d += 32) {
                     uint32_t o[32];
                     tmem_ld32(o_addr + d, o);
-                    tmem_wait_ld();
+                    tmem_wait_ld(o);
                     if (!alive) continue;
 #pragma unroll
                     for (int e = 0; e < 32; e += 4)
