@@ -4,15 +4,17 @@
 // head r % G, so K and V tiles serve all of them. A CTA holds NT tiles of 128 rows (two up to D = 128, one
 // at D = 256, where the output takes half of the tensor memory) and walks the BN-position tiles that any of
 // its rows sees. Its warps have fixed parts:
-//  - producers bring K and V tiles into a ring of four shared-memory slots, row by row of the pages (any
-//    page size), as fp16 / bf16 in the 128-byte-swizzled layout both products read: K with the summed axis
-//    contiguous, V with its other axis contiguous. 16-bit rows are copied asynchronously, quantised rows
-//    are decoded on the way;
+//  - producers bring K and V tiles into a ring of four shared-memory slots, page by page, as fp16 / bf16 in
+//    the 128-byte-swizzled layout both products read: K with the summed axis contiguous, V with its other
+//    axis contiguous. 16-bit pages come by tensor-map copies, one lane per page and 64 channels (16-byte
+//    copies by the threads took 1,550 of the 2,400 cycles of a tile); a tile that ends behind the last position
+//    is copied by the threads, zeros in place of the rows behind it. Quantised rows are decoded on the way;
 //  - one thread issues the products: S = Q K^T into tensor memory, and O += P V with P read from tensor memory;
 //  - one thread per row does the softmax: S from tensor memory to registers, maximum, exponentials, P back
 //    over S. The running maximum moves only when it grows by more than 2^8, so that O is rescaled rarely.
 // With two row tiles, the products of one run while the other's softmax does; with one, S of the next
 // tile is computed meanwhile (two S buffers).
+#include <cuda.h>
 #include "stream_common.cuh"
 #include "paged_common.cuh"
 #include "tcgen05.cuh"
@@ -176,7 +178,9 @@ __device__ __forceinline__ void apply_rule(uint32_t (&s)[32], const ScoreRule& r
 }
 
 template <int D, int KF, int VF, typename T, typename TQ>
-__global__ void __launch_bounds__(Geo<D>::threads, 1) prefill_kernel(PagedAttnParams p, int splits) {
+__global__ void __launch_bounds__(Geo<D>::threads, 1) prefill_kernel(const __grid_constant__ PagedAttnParams p,
+                                                                        const __grid_constant__ CUtensorMap k_map,
+                                                                        const __grid_constant__ CUtensorMap v_map, int splits) {
     using GE = Geo<D>;
     constexpr int NT = GE::NT, BN = GE::BN;
     constexpr bool BF = std::is_same<T, __nv_bfloat16>::value;
@@ -224,26 +228,37 @@ __global__ void __launch_bounds__(Geo<D>::threads, 1) prefill_kernel(PagedAttnPa
     if (warp >= 4 * NT) {
         if (warp == 4 * NT) {
             // ------------------------------------------------------------------ the products
-            if (lane == 0 && nt > 0) {
-                const auto scores = [&](int t, int i) {         // S of row tile t, KV tile i
-                    const uint32_t q = base + t * GE::q_bytes, k = ring + ((2 * i) & 3) * GE::slot;
-                    const int buf = NT == 2 ? t : i & 1;
+            if (nt > 0) {
+                const uint32_t tm = __shfl_sync(kAll, tmem, 0);
+                const uint64_t q_desc = smem_desc(base, 0), k_desc = smem_desc(ring, 0), v_desc = smem_desc(ring, BN * 128);
+                const auto scores = [&](int t, int i, bool last) {   // S of row tile t, KV tile i; the last reader of K
+                    const int slot = (2 * i) & 3, buf = NT == 2 ? t : i & 1;
+                    const uint64_t q = desc_at(q_desc, t * GE::q_bytes), k = desc_at(k_desc, slot * GE::slot);
+                    if (elect_one()) {
 #pragma unroll
-                    for (int s = 0; s < D / 16; ++s)
-                        mma_ss(tmem + GE::s_col(buf), smem_desc(q + (s / 4) * 128 * 128 + (s % 4) * 32, 0),
-                               smem_desc(k + (s / 4) * BN * 128 + (s % 4) * 32, 0), mma_desc(BF, false, BN), s > 0);
-                    tc_commit(s_full + 8 * buf);
-                };
-                const auto values = [&](int t, int i) {         // O of row tile t += P V of KV tile i
-                    const uint32_t v = ring + ((2 * i + 1) & 3) * GE::slot;
-                    const int buf = NT == 2 ? t : i & 1;
-                    if (!*(volatile int*)&s_skip[buf]) {
-#pragma unroll
-                        for (int s = 0; s < BN / 16; ++s)
-                            mma_ts(tmem + GE::o_col(t), tmem + GE::s_col(buf) + 8 * s, smem_desc(v + s * 2048, BN * 128),
-                                   mma_desc(BF, true, D), i > 0 || s > 0);
+                        for (int s = 0; s < D / 16; ++s)
+                            mma_ss(tm + GE::s_col(buf), desc_at(q, (s / 4) * 128 * 128 + (s % 4) * 32),
+                                   desc_at(k, (s / 4) * BN * 128 + (s % 4) * 32), mma_desc(BF, false, BN), s > 0);
+                        tc_commit(s_full + 8 * buf);
+                        if (last) tc_commit(empty + 8 * slot);
                     }
-                    tc_commit(o_done + 8 * t);
+                    __syncwarp();
+                };
+                const auto values = [&](int t, int i, bool last) {   // O of row tile t += P V of KV tile i
+                    const int slot = (2 * i + 1) & 3, buf = NT == 2 ? t : i & 1;
+                    const uint64_t v = desc_at(v_desc, slot * GE::slot);
+                    const int skip = *(volatile int*)&s_skip[buf];
+                    if (elect_one()) {
+                        if (!skip) {
+#pragma unroll
+                            for (int s = 0; s < BN / 16; ++s)
+                                mma_ts(tm + GE::o_col(t), tm + GE::s_col(buf) + 8 * s, desc_at(v, s * 2048),
+                                       mma_desc(BF, true, D), i > 0 || s > 0);
+                        }
+                        tc_commit(o_done + 8 * t);
+                        if (last) tc_commit(empty + 8 * slot);
+                    }
+                    __syncwarp();
                 };
                 const auto wait_item = [&](int n) {
                     wait(full + 8 * (n & 3), (n >> 2) & 1);
@@ -251,96 +266,92 @@ __global__ void __launch_bounds__(Geo<D>::threads, 1) prefill_kernel(PagedAttnPa
                 };
                 wait(q_full, 0);
                 wait_item(0);
-                for (int t = 0; t < (NT == 2 ? active : 1); ++t) scores(t, 0);
-                tc_commit(empty);
+                for (int t = 0; t < active; ++t) scores(t, 0, t == active - 1);
                 for (int i = 0; i < nt; ++i) {
                     if constexpr (NT == 2) {
                         for (int t = 0; t < active; ++t) {
                             wait(p_full + 8 * t, i & 1);
                             tc_fence_after();
                             if (t == 0) wait_item(2 * i + 1);
-                            values(t, i);
-                            if (t == active - 1) tc_commit(empty + 8 * ((2 * i + 1) & 3));
+                            values(t, i, t == active - 1);
                             if (i + 1 < nt) {
                                 if (t == 0) wait_item(2 * i + 2);
-                                scores(t, i + 1);
-                                if (t == active - 1) tc_commit(empty + 8 * ((2 * i + 2) & 3));
+                                scores(t, i + 1, t == active - 1);
                             }
                         }
                     } else {
                         if (i + 1 < nt) {
                             wait_item(2 * i + 2);
-                            scores(0, i + 1);
-                            tc_commit(empty + 8 * ((2 * i + 2) & 3));
+                            scores(0, i + 1, true);
                         }
                         wait(p_full + 8 * (i & 1), (i >> 1) & 1);
                         tc_fence_after();
                         wait_item(2 * i + 1);
-                        values(0, i);
-                        tc_commit(empty + 8 * ((2 * i + 1) & 3));
+                        values(0, i, true);
                     }
                 }
             }
-            __syncwarp();
         } else {
             // ------------------------------------------------------------------ K and V tiles
             const int pw = warp - 4 * NT - 1;                   // 8-row blocks pw, pw + 3, ..
             const int32_t* table = p.table + (int64_t)b * p.table_stride;
-            uint32_t put[D / 32];                               // this lane's pieces of an 8-row block of 16-bit rows
-#pragma unroll
-            for (int e = 0; e < D / 32; ++e) put[e] = tile_byte(BN, (e * 32 + lane) / (D / 8), (e * 32 + lane) % (D / 8) * 8);
-            int posted = 0;
-            auto post = [&](int n) {                            // items before n are in place
-                fence_async_smem();
-                for (; posted < n; ++posted) mbar_arrive(full + 8 * (posted & 3));
-            };
-            for (int n = 0; n < 2 * nt; ++n) {
-                if (n >= 4) wait(empty + 8 * (n & 3), ((n >> 2) - 1) & 1);
-                const int w = n & 1, p0 = kv.at(i0 + (n >> 1));
-                const uint32_t dst = ring + (n & 3) * GE::slot;
-                // page numbers of the tile's 16-row blocks, one per lane
+            // page numbers of a tile's 16-row blocks, one per lane, loaded a tile ahead
+            auto pages_of = [&](int i) {
                 int page = -1;
-                if (lane < BN / 16 && p0 + 16 * lane < c.len) {
-                    page = table[(p0 + 16 * lane) >> p.v.ps_shift];
-                    if (page < 0 || page >= p.v.n_pages) {
+                const int at = i < nt ? kv.at(i0 + i) + 16 * lane : c.len;
+                if (lane < BN / 16 && at < c.len) page = table[at >> p.v.ps_shift];
+                return page;
+            };
+            int page = -1, next_page = pages_of(0);
+            for (int n = 0; n < 2 * nt; ++n) {
+                const int w = n & 1, p0 = kv.at(i0 + (n >> 1));
+                if (w == 0) {
+                    page = next_page;
+                    if (lane < BN / 16 && p0 + 16 * lane < c.len && (page < 0 || page >= p.v.n_pages)) {
                         raise_status(p.v.status, KVQ_PAGED_BAD_INDEX);
                         page = -1;
                     }
+                    next_page = pages_of((n >> 1) + 1);
                 }
+                if (n >= 4) wait(empty + 8 * (n & 3), ((n >> 2) - 1) & 1);
+                const uint32_t dst = ring + (n & 3) * GE::slot;
                 auto block_rows = [&](int blk, int& off) -> const uint8_t* {
                     const int pg = __shfl_sync(kAll, page, blk >> 1);
                     off = (p0 + 8 * blk) & (p.v.ps - 1);
                     return pg < 0 ? nullptr : unit_at(p.v, w, pg, h);
                 };
                 const int fmt = w ? VF : KF;
-                if (KF == 0) {
-                    constexpr int per = D / 8;                  // pieces of a row
+                if (KF == 0 && __all_sync(kAll, lane >= BN / 16 || page >= 0) && p0 + BN <= c.len) {
+                    // boxes of min(page_size, BN) rows x 64 channels, one per lane of the first producer
+                    const int rows = min(p.v.ps, BN), boxes = BN / rows * (D / 64);
+                    const int k = lane / (D / 64), col = lane % (D / 64) * 64, at = p0 + k * rows;
+                    const int pg = __shfl_sync(kAll, page, (k * rows >> 4) & (BN / 16 - 1));
+                    if (pw == 0) {
+                        if (lane == 0) mbar_expect_tx(full + 8 * (n & 3), GE::slot);
+                        else mbar_arrive(full + 8 * (n & 3));
+                        __syncwarp();
+                        if (lane < boxes)
+                            tma_load3(dst + tile_byte(BN, k * rows, col), w ? &v_map : &k_map, col, at & (p.v.ps - 1),
+                                      pg * p.v.H + h, full + 8 * (n & 3));
+                    } else {
+                        mbar_arrive(full + 8 * (n & 3));
+                    }
+                } else if (KF == 0) {
+                    constexpr int per = D / 8;                  // 16-byte pieces of a row
                     for (int blk = pw; blk < BN / 8; blk += 3) {
                         int off;
                         const uint8_t* u = block_rows(blk, off);
-                        const uint8_t* src = u + off * (2 * D) + lane * 16;    // eight rows are contiguous
                         const int live = u ? c.len - p0 - 8 * blk : 0;         // rows of the block that hold positions
-                        if (live >= 8) {
 #pragma unroll
-                            for (int e = 0; e < per / 4; ++e)
-                                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst + 1024 * blk + put[e]),
-                                             "l"(src + 512 * e)
-                                             : "memory");
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < per / 4; ++e) {
-                                const bool ok = (e * 32 + lane) / per < live;
-                                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst + 1024 * blk + put[e]),
-                                             "l"(ok ? src + 512 * e : p.v.base[0]), "r"(ok ? 16 : 0)
-                                             : "memory");
-                            }
+                        for (int e = 0; e < per / 4; ++e) {
+                            const int x = e * 32 + lane, r = x / per, ch = x % per * 8;
+                            uint4 y = make_uint4(0, 0, 0, 0);
+                            if (r < live) y = *reinterpret_cast<const uint4*>(u + (off + r) * (2 * D) + 2 * ch);
+                            st_shared16(dst + tile_byte(BN, 8 * blk + r, ch), y);
                         }
                     }
-                    asm volatile("cp.async.commit_group;\n" ::: "memory");
-                    if (n > 0) {
-                        asm volatile("cp.async.wait_group 1;\n" ::: "memory");
-                        post(n);
-                    }
+                    fence_async_smem();
+                    mbar_arrive(full + 8 * (n & 3));
                 } else {
                     constexpr int per = D / 16;                 // 16-channel pieces of a row
                     constexpr int E = 8 * per / 32;             // of a lane in an 8-row block (D = 64: 1)
@@ -376,12 +387,9 @@ __global__ void __launch_bounds__(Geo<D>::threads, 1) prefill_kernel(PagedAttnPa
                             st_shared16(dst + tile_byte(BN, 8 * blk + r, ch + 8), hi);
                         }
                     }
-                    post(n + 1);
+                    fence_async_smem();
+                    mbar_arrive(full + 8 * (n & 3));
                 }
-            }
-            if (KF == 0) {
-                asm volatile("cp.async.wait_group 0;\n" ::: "memory");
-                post(2 * nt);
             }
         }
     } else {
@@ -632,7 +640,8 @@ int splits_of(int64_t rows, int n_seq, int H, int tile_rows, int sm_count) {
     return (int)(s < 1 ? 1 : (s > kMaxSplits ? kMaxSplits : s));
 }
 
-template <int D, int KF, int VF, typename T, typename TQ> int prefill_run(PagedAttnParams p, int sm_count, cudaStream_t s) {
+template <int D, int KF, int VF, typename T, typename TQ>
+int prefill_run(const PagedAttnParams& p, const CUtensorMap* maps, int sm_count, cudaStream_t s) {
     using GE = Geo<D>;
     const auto k = prefill_kernel<D, KF, VF, T, TQ>;
     int res = 0;
@@ -640,7 +649,7 @@ template <int D, int KF, int VF, typename T, typename TQ> int prefill_run(PagedA
     const int64_t chunk = (int64_t)p.max_q * p.G;
     const int splits = splits_of((int64_t)p.n_rows * p.G, p.n_seq, p.v.H, GE::rows, sm_count);
     const dim3 grid(p.v.H, (unsigned)((chunk + GE::rows - 1) / GE::rows), (unsigned)(p.n_seq * splits));
-    cudaError_t e = launch_k(k, grid, dim3(GE::threads), GE::smem, s, true, p, splits);
+    cudaError_t e = launch_k(k, grid, dim3(GE::threads), GE::smem, s, true, p, maps[0], maps[1], splits);
     if (e == cudaSuccess && splits > 1) {
         constexpr int R = kJT / (D / 8);
         e = launch_k(prefill_join_kernel<D, TQ>, dim3((unsigned)((chunk + R - 1) / R), p.v.H, p.n_seq), dim3(kJT), 0, s, true, p, splits);
@@ -648,18 +657,18 @@ template <int D, int KF, int VF, typename T, typename TQ> int prefill_run(PagedA
     return (int)e;
 }
 
-template <int D> int prefill_d(const PagedAttnParams& p, int n, cudaStream_t s) {
+template <int D> int prefill_d(const PagedAttnParams& p, const CUtensorMap* m, int n, cudaStream_t s) {
     const int kf = p.v.fmt[0], vf = p.v.fmt[1];
-    if (kf == KVQ_F16) return prefill_run<D, 0, 0, __half, __half>(p, n, s);
-    if (kf == KVQ_BF16) return prefill_run<D, 0, 0, __nv_bfloat16, __nv_bfloat16>(p, n, s);
+    if (kf == KVQ_F16) return prefill_run<D, 0, 0, __half, __half>(p, m, n, s);
+    if (kf == KVQ_BF16) return prefill_run<D, 0, 0, __nv_bfloat16, __nv_bfloat16>(p, m, n, s);
     if (p.dtype == KVQ_F16) {
-        if (kf == KVQ_Q4_0) return prefill_run<D, 2, 2, __half, __half>(p, n, s);
-        if (vf == KVQ_Q4_0) return prefill_run<D, 1, 2, __half, __half>(p, n, s);
-        return prefill_run<D, 1, 1, __half, __half>(p, n, s);
+        if (kf == KVQ_Q4_0) return prefill_run<D, 2, 2, __half, __half>(p, m, n, s);
+        if (vf == KVQ_Q4_0) return prefill_run<D, 1, 2, __half, __half>(p, m, n, s);
+        return prefill_run<D, 1, 1, __half, __half>(p, m, n, s);
     }
-    if (kf == KVQ_Q4_0) return prefill_run<D, 2, 2, __half, __nv_bfloat16>(p, n, s);
-    if (vf == KVQ_Q4_0) return prefill_run<D, 1, 2, __half, __nv_bfloat16>(p, n, s);
-    return prefill_run<D, 1, 1, __half, __nv_bfloat16>(p, n, s);
+    if (kf == KVQ_Q4_0) return prefill_run<D, 2, 2, __half, __nv_bfloat16>(p, m, n, s);
+    if (vf == KVQ_Q4_0) return prefill_run<D, 1, 2, __half, __nv_bfloat16>(p, m, n, s);
+    return prefill_run<D, 1, 1, __half, __nv_bfloat16>(p, m, n, s);
 }
 
 }  // namespace
@@ -670,11 +679,14 @@ size_t paged_prefill_ws_floats(int D, int64_t head_rows) {
     return (size_t)((most < full ? most : full) * (D + 2));
 }
 
-int launch_paged_prefill(PagedAttnParams p, int sm_count, void* stream) {
+int prefill_box_rows(int D, int ps) { return ps < (D == 256 ? 64 : 128) ? ps : (D == 256 ? 64 : 128); }
+
+int launch_paged_prefill(const PagedAttnParams& p, const void* maps, int sm_count, void* stream) {
     cudaStream_t s = (cudaStream_t)stream;
-    if (p.v.D == 64) return prefill_d<64>(p, sm_count, s);
-    if (p.v.D == 128) return prefill_d<128>(p, sm_count, s);
-    return prefill_d<256>(p, sm_count, s);
+    const CUtensorMap* m = (const CUtensorMap*)maps;
+    if (p.v.D == 64) return prefill_d<64>(p, m, sm_count, s);
+    if (p.v.D == 128) return prefill_d<128>(p, m, sm_count, s);
+    return prefill_d<256>(p, m, sm_count, s);
 }
 
 }  // namespace kvq

@@ -1,5 +1,6 @@
 // Host side of the paged cache's C ABI (include/kvq_paged.h): configuration and argument checks, the
 // pool's layout and the launches. Everything that is refused is refused here, before anything is enqueued.
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <cmath>
 #include <cstring>
@@ -7,6 +8,7 @@
 #include <mutex>
 #include <new>
 #include <utility>
+#include <vector>
 #include "paged_internal.h"
 
 using namespace kvq;
@@ -15,6 +17,7 @@ struct kvq_paged {
     kvq_paged_config cfg;
     uint8_t* pool;
     int device, sm_count;
+    std::vector<CUtensorMap> maps;   // 16-bit pages: K and V area of every layer
 };
 
 namespace {
@@ -38,7 +41,7 @@ bool geometry(const kvq_paged_config& c, Geometry* g) {
     const int64_t units = (int64_t)c.n_pages * c.n_kv_heads;
     for (int w = 0; w < 2; ++w) {
         const int64_t u = paged_unit_bytes(fmt[w], c.head_dim, c.page_size);
-        if (units > limit / u) return false;
+        if (units >= (int64_t)1 << 31 || units > limit / u) return false;
         g->area[w] = align256(units * u);
     }
     g->layer = g->area[0] + g->area[1];
@@ -90,6 +93,32 @@ size_t workspace_floats(const kvq_paged_config& c, int64_t seqs, int64_t rows) {
     const size_t a = paged_decode_ws_floats(G, c.head_dim, seqs * c.n_kv_heads);
     const size_t b = paged_prefill_ws_floats(c.head_dim, rows * c.n_q_heads);
     return a > b ? a : b;
+}
+
+// The tensor maps of a 16-bit pool: per layer K, then V, as [units][page_size][head_dim].
+bool make_maps(kvq_paged* h) {
+    const kvq_paged_config& c = h->cfg;
+    h->maps.resize(2 * (size_t)c.n_layers);
+    if (c.k_fmt != KVQ_F16 && c.k_fmt != KVQ_BF16) return true;
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+        return false;
+    const auto encode = (decltype(&cuTensorMapEncodeTiled))fn;
+    for (int l = 0; l < c.n_layers; ++l) {
+        const PagedView v = view(h, l);
+        for (int w = 0; w < 2; ++w) {
+            const cuuint64_t dims[3] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.page_size, (cuuint64_t)c.n_pages * c.n_kv_heads};
+            const cuuint64_t strides[2] = {(cuuint64_t)c.head_dim * 2, (cuuint64_t)v.unit[w]};
+            const cuuint32_t box[3] = {64, (cuuint32_t)prefill_box_rows(c.head_dim, c.page_size), 1}, one[3] = {1, 1, 1};
+            if (encode(&h->maps[2 * l + w], c.k_fmt == KVQ_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                       3, v.base[w], dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+                return false;
+        }
+    }
+    return true;
 }
 
 kvq_status launched(int e) { return e == 0 ? KVQ_OK : KVQ_ECUDA; }
@@ -184,6 +213,15 @@ kvq_status kv_paged_create(const kvq_paged_config* cfg, void* pool, size_t pool_
     h->pool = (uint8_t*)pool;
     h->device = device;
     h->sm_count = sms;
+    try {
+        if (!make_maps(h)) {
+            delete h;
+            return KVQ_ECUDA;
+        }
+    } catch (const std::bad_alloc&) {
+        delete h;
+        return KVQ_EINVAL;
+    }
     *out = h;
     return KVQ_OK;
 }
@@ -284,7 +322,7 @@ kvq_status kv_paged_prefill_attn(kvq_paged* h, int32_t layer, int32_t dtype, int
     p.cu = cu_q;
     p.n_rows = n_rows;
     p.max_q = max_q < n_rows ? max_q : n_rows;
-    return launched(launch_paged_prefill(p, h->sm_count, stream));
+    return launched(launch_paged_prefill(p, &h->maps[2 * (size_t)layer], h->sm_count, stream));
 }
 
 kvq_status kv_qk_norm_rope(const kvq_norm_rope_args* a, void* stream) {

@@ -57,12 +57,30 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]
         : "memory");
 }
 
+// Copies a box of a 3D tensor map to shared memory; `bar` receives its bytes.
+__device__ __forceinline__ void tma_load3(uint32_t dst, const void* map, int x, int y, int z, uint32_t bar) {
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n"
+                 ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+                 : "memory");
+}
+
 // Shared-memory matrix descriptor, 128-byte swizzle: rows of 128 bytes, eight of them a 1,024-byte block whose
 // 16-byte pieces sit at piece ^ (row mod 8); blocks of the next eight rows follow 1,024 bytes on. `blocks`: bytes to
 // the next 64 values along the contiguous axis (used where that axis is not the summed one).
 __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t blocks) {
     return (uint64_t)((addr & 0x3ffff) >> 4) | ((uint64_t)(blocks >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
            (1ull << 46) | (2ull << 61);
+}
+// The descriptor of the place `bytes` further on (within the 256 KB that addresses span).
+__device__ __forceinline__ uint64_t desc_at(uint64_t desc, uint32_t bytes) {
+    return (desc & 0xffffffff00000000ull) | (uint32_t)((uint32_t)desc + (bytes >> 4));
+}
+// True in one lane of a converged warp. The products are issued under it from code that the whole warp runs,
+// so that addresses and descriptors stay in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t x;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }\n" : "=r"(x));
+    return x != 0;
 }
 // Instruction descriptor: fp32 accumulators; A and B both bf16 or both fp16; B's summed axis contiguous, or its
 // other one (b_cols); M = 128.
