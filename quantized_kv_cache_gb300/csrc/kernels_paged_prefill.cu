@@ -9,7 +9,7 @@
 //    axis contiguous. 16-bit pages come by tensor-map copies, one lane per page and 64 channels (16-byte
 //    copies by the threads took 1,550 of the 2,400 cycles of a tile); a tile that ends behind the last position
 //    is copied by the threads, zeros in place of the rows behind it. Quantised rows are decoded on the way;
-//  - one thread issues the products: S = Q K^T into tensor memory, and O += P V with P read from tensor memory;
+//  - one warp per row tile issues the products: S = Q K^T into tensor memory, and O += P V with P read from tensor memory;
 //  - one thread per row does the softmax: S from tensor memory to registers, maximum, exponentials, P back
 //    over S. The running maximum moves only when it grows by more than 2^8, so that O is rescaled rarely.
 // With two row tiles, the products of one run while the other's softmax does; with one, S of the next
@@ -22,19 +22,24 @@
 namespace kvq {
 namespace {
 
-template <int D> struct Geo {
+template <int D, bool CODES> struct Geo {
     static constexpr int NT = D == 256 ? 1 : 2;              // row tiles of a CTA
     static constexpr int BN = D == 256 ? 64 : 128;           // positions of a KV tile
     static constexpr int rows = 128 * NT;
-    static constexpr int threads = 128 * NT + 128;           // softmax, then one issuing and three producing warps
+    // warps: four softmax warps per row tile, one that issues the products, producers (decoding codes takes more)
+    static constexpr int mma_warp = 4 * NT, first_prod = mma_warp + 1, prod = CODES ? 7 : 3;
+    static constexpr int threads = 32 * (first_prod + prod);
+    // registers of two row tiles: 256 softmax threads and the others share what the block is launched with (384 x 168,
+    // 512 x 128)
+    static constexpr int soft_regs = CODES ? 184 : 208, other_regs = CODES ? 72 : 88;   // (one row tile: not moved)
     static constexpr int q_bytes = 128 * D * 2;              // of a row tile
     static constexpr int slot = BN * D * 2;
     static constexpr int smem = 1024 + NT * q_bytes + 4 * slot;
+    // slots: K of tile i in place i & 1, V in place 2 + (i & 1)
     // tensor memory columns: S (and P over it), two buffers; O
     static constexpr int s_col(int i) { return i * BN; }
     static constexpr int o_col(int t) { return 256 + t * D; }
 };
-constexpr int kProducers = 96;
 constexpr float kLazy = 8.f;                                  // log2 of what a weight may exceed 1 by
 constexpr int kMaxSplits = 16;
 
@@ -104,6 +109,23 @@ __device__ __forceinline__ uint4 decode_q4(uint32_t c, uint32_t d) {
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
+// A wait on a barrier's phase, bounded as the streaming kernels' are (2 s, then the status bit and the CTA's
+// abort flag), that looks at the clock and the flag only every 32nd time.
+__device__ __forceinline__ void bounded_wait(uint32_t bar, uint32_t parity, uint32_t* status, volatile int* abort_flag) {
+    uint64_t t0 = 0;
+    for (int n = 1; !mbar_try(bar, parity); ++n) {
+        if (n & 31) continue;
+        if (*abort_flag) return;
+        const uint64_t t = gtime();
+        if (t0 == 0) t0 = t;
+        if (t - t0 > kWaitNs) {
+            raise_status(status, KVQ_PAGED_TIMEOUT);
+            *abort_flag = 1;
+            return;
+        }
+    }
+}
+
 // What one row's thread keeps.
 struct RowState {
     int pos, lo;             // position (rows that see nothing: -1), first position of the window
@@ -152,6 +174,12 @@ __device__ __noinline__ void add_seen(uint32_t v_tile, uint32_t o_addr, uint32_t
     }
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;\n" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 // Raw scores of 32 positions from p0 on to scores in units of log2: the cap, then the bias.
 __device__ __forceinline__ void apply_rule(uint32_t (&s)[32], const ScoreRule& rule, const RowState& r, int p0) {
     float big = 0.f;
@@ -178,21 +206,22 @@ __device__ __forceinline__ void apply_rule(uint32_t (&s)[32], const ScoreRule& r
 }
 
 template <int D, int KF, int VF, typename T, typename TQ>
-__global__ void __launch_bounds__(Geo<D>::threads, 1) prefill_kernel(const __grid_constant__ PagedAttnParams p,
+__global__ void __launch_bounds__(Geo<D, KF != 0>::threads, 1) prefill_kernel(const __grid_constant__ PagedAttnParams p,
                                                                         const __grid_constant__ CUtensorMap k_map,
                                                                         const __grid_constant__ CUtensorMap v_map, int splits) {
-    using GE = Geo<D>;
+    using GE = Geo<D, KF != 0>;
     constexpr int NT = GE::NT, BN = GE::BN;
     constexpr bool BF = std::is_same<T, __nv_bfloat16>::value;
     extern __shared__ uint8_t raw[];
-    // full / empty of the ring's slots; Q in place; S ready, P ready (by S buffer); O of a row tile up to date
-    __shared__ uint64_t bars[4 + 4 + 1 + 2 + 2 + 2];
+    // full / empty of the load stages; Q in place; S ready, P ready (by S buffer); O of a row tile up to date.
+    // Stage u loads what the products take together: V of tile u - 1 and K of tile u.
+    __shared__ uint64_t bars[2 + 2 + 1 + 2 + 2 + 2];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort, s_skip[2];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int h = blockIdx.x, b = blockIdx.z / splits, split = blockIdx.z % splits, G = p.G;
-    const uint32_t full = su32(bars), empty = full + 32, q_full = full + 64, s_full = full + 72, p_full = full + 88,
-                   o_done = full + 104;
+    const uint32_t full = su32(bars), empty = full + 16, q_full = full + 32, s_full = full + 40, p_full = full + 56,
+                   o_done = full + 72;
     grid_dep_wait();
     const Chunk c = chunk_of(p, b, h == 0 && blockIdx.y == 0 && split == 0 && threadIdx.x == 0);
     // tiles in descending order: the last rows see the most positions and start first
@@ -205,12 +234,10 @@ __global__ void __launch_bounds__(Geo<D>::threads, 1) prefill_kernel(const __gri
 
     const uint32_t base = (su32(raw) + 1023) & ~1023u, ring = base + NT * GE::q_bytes;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 4; ++i) {
-            mbar_init(full + 8 * i, kProducers);
-            mbar_init(empty + 8 * i, 1);
-        }
         mbar_init(q_full, 128 * active);
         for (int i = 0; i < 2; ++i) {
+            mbar_init(full + 8 * i, 32 * GE::prod);
+            mbar_init(empty + 8 * i, 1);
             mbar_init(s_full + 8 * i, 1);
             mbar_init(p_full + 8 * i, 128);
             mbar_init(o_done + 8 * i, 1);
@@ -218,103 +245,101 @@ __global__ void __launch_bounds__(Geo<D>::threads, 1) prefill_kernel(const __gri
         s_abort = s_skip[0] = s_skip[1] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
-    if (warp == 4 * NT) tmem_alloc512(su32(&s_tmem));
+    if (warp == GE::mma_warp) tmem_alloc512(su32(&s_tmem));
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s_tmem;
-    auto wait = [&](uint32_t bar, uint32_t parity) { mbar_wait(bar, parity, p.v.status, &s_abort); };
+    auto wait = [&](uint32_t bar, uint32_t parity) { bounded_wait(bar, parity, p.v.status, &s_abort); };
 
-    if (warp >= 4 * NT) {
-        if (warp == 4 * NT) {
+    if (warp >= GE::mma_warp) {
+        if constexpr (NT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(GE::other_regs));
+        if (warp == GE::mma_warp) {
             // ------------------------------------------------------------------ the products
+            // One warp for both row tiles: it keeps them half a period apart, so that the softmax of one runs beside
+            // the products of the other (with a warp each they fell into step: 594 us for what takes 478 us here).
             if (nt > 0) {
                 const uint32_t tm = __shfl_sync(kAll, tmem, 0);
-                const uint64_t q_desc = smem_desc(base, 0), k_desc = smem_desc(ring, 0), v_desc = smem_desc(ring, BN * 128);
-                const auto scores = [&](int t, int i, bool last) {   // S of row tile t, KV tile i; the last reader of K
-                    const int slot = (2 * i) & 3, buf = NT == 2 ? t : i & 1;
-                    const uint64_t q = desc_at(q_desc, t * GE::q_bytes), k = desc_at(k_desc, slot * GE::slot);
-                    if (elect_one()) {
+                const uint64_t q_desc = smem_desc(base, 0), k_desc = smem_desc(ring, 0), v_desc = smem_desc(ring + 2 * GE::slot, BN * 128);
+                const auto scores = [&](int t, int i) {         // S of row tile t and KV tile i
+                    const int buf = NT == 2 ? t : i & 1;
+                    const uint64_t q = desc_at(q_desc, t * GE::q_bytes), k = desc_at(k_desc, (i & 1) * GE::slot);
 #pragma unroll
-                        for (int s = 0; s < D / 16; ++s)
-                            mma_ss(tm + GE::s_col(buf), desc_at(q, (s / 4) * 128 * 128 + (s % 4) * 32),
-                                   desc_at(k, (s / 4) * BN * 128 + (s % 4) * 32), mma_desc(BF, false, BN), s > 0);
-                        tc_commit(s_full + 8 * buf);
-                        if (last) tc_commit(empty + 8 * slot);
-                    }
-                    __syncwarp();
+                    for (int s = 0; s < D / 16; ++s)
+                        mma_ss(tm + GE::s_col(buf), desc_at(q, (s / 4) * 128 * 128 + (s % 4) * 32),
+                               desc_at(k, (s / 4) * BN * 128 + (s % 4) * 32), mma_desc(BF, false, BN), s > 0);
+                    tc_commit(s_full + 8 * buf);
                 };
-                const auto values = [&](int t, int i, bool last) {   // O of row tile t += P V of KV tile i
-                    const int slot = (2 * i + 1) & 3, buf = NT == 2 ? t : i & 1;
-                    const uint64_t v = desc_at(v_desc, slot * GE::slot);
-                    const int skip = *(volatile int*)&s_skip[buf];
-                    if (elect_one()) {
-                        if (!skip) {
+                const auto values = [&](int t, int i) {         // O of row tile t += P V of KV tile i
+                    const int buf = NT == 2 ? t : i & 1;
+                    const uint64_t v = desc_at(v_desc, (i & 1) * GE::slot);
 #pragma unroll
-                            for (int s = 0; s < BN / 16; ++s)
-                                mma_ts(tm + GE::o_col(t), tm + GE::s_col(buf) + 8 * s, desc_at(v, s * 2048),
-                                       mma_desc(BF, true, D), i > 0 || s > 0);
-                        }
-                        tc_commit(o_done + 8 * t);
-                        if (last) tc_commit(empty + 8 * slot);
-                    }
-                    __syncwarp();
-                };
-                const auto wait_item = [&](int n) {
-                    wait(full + 8 * (n & 3), (n >> 2) & 1);
-                    tc_fence_after();
+                    for (int s = 0; s < BN / 16; ++s)
+                        mma_ts(tm + GE::o_col(t), tm + GE::s_col(buf) + 8 * s, desc_at(v, s * 2048), mma_desc(BF, true, D), i > 0 || s > 0);
                 };
                 wait(q_full, 0);
-                wait_item(0);
-                for (int t = 0; t < active; ++t) scores(t, 0, t == active - 1);
+                wait(full, 0);
+                tc_fence_after();
+                if (elect_one()) {
+                    for (int t = 0; t < active; ++t) scores(t, 0);
+                    tc_commit(empty);
+                }
+                __syncwarp();
                 for (int i = 0; i < nt; ++i) {
-                    if constexpr (NT == 2) {
-                        for (int t = 0; t < active; ++t) {
-                            wait(p_full + 8 * t, i & 1);
-                            tc_fence_after();
-                            if (t == 0) wait_item(2 * i + 1);
-                            values(t, i, t == active - 1);
-                            if (i + 1 < nt) {
-                                if (t == 0) wait_item(2 * i + 2);
-                                scores(t, i + 1, t == active - 1);
-                            }
-                        }
-                    } else {
-                        if (i + 1 < nt) {
-                            wait_item(2 * i + 2);
-                            scores(0, i + 1, true);
-                        }
-                        wait(p_full + 8 * (i & 1), (i >> 1) & 1);
+                    const int u = i + 1;
+                    const bool more = u < nt;
+                    wait(full + 8 * (u & 1), (u >> 1) & 1);
+                    if (NT == 1 && more) {
                         tc_fence_after();
-                        wait_item(2 * i + 1);
-                        values(0, i, true);
+                        if (elect_one()) scores(0, u);
+                        __syncwarp();
+                    }
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        if (t >= active) break;
+                        const int buf = NT == 2 ? t : i & 1;
+                        wait(p_full + 8 * buf, NT == 2 ? i & 1 : (i >> 1) & 1);
+                        tc_fence_after();
+                        const int skip = *(volatile int*)&s_skip[buf];
+                        if (elect_one()) {
+                            if (!skip) values(t, i);
+                            if (NT == 1 || !more) tc_commit(o_done + 8 * t);
+                            if (NT == 2 && more) scores(t, u);
+                            if (t == active - 1) tc_commit(empty + 8 * (u & 1));
+                        }
+                        __syncwarp();
                     }
                 }
             }
         } else {
             // ------------------------------------------------------------------ K and V tiles
-            const int pw = warp - 4 * NT - 1;                   // 8-row blocks pw, pw + 3, ..
+            const int pw = warp - GE::first_prod;               // 8-row blocks pw, pw + prod, ..
             const int32_t* table = p.table + (int64_t)b * p.table_stride;
             // page numbers of a tile's 16-row blocks, one per lane, loaded a tile ahead
             auto pages_of = [&](int i) {
                 int page = -1;
                 const int at = i < nt ? kv.at(i0 + i) + 16 * lane : c.len;
-                if (lane < BN / 16 && at < c.len) page = table[at >> p.v.ps_shift];
-                return page;
-            };
-            int page = -1, next_page = pages_of(0);
-            for (int n = 0; n < 2 * nt; ++n) {
-                const int w = n & 1, p0 = kv.at(i0 + (n >> 1));
-                if (w == 0) {
-                    page = next_page;
-                    if (lane < BN / 16 && p0 + 16 * lane < c.len && (page < 0 || page >= p.v.n_pages)) {
+                if (lane < BN / 16 && at < c.len) {
+                    page = table[at >> p.v.ps_shift];
+                    if (page < 0 || page >= p.v.n_pages) {
                         raise_status(p.v.status, KVQ_PAGED_BAD_INDEX);
                         page = -1;
                     }
-                    next_page = pages_of((n >> 1) + 1);
                 }
-                if (n >= 4) wait(empty + 8 * (n & 3), ((n >> 2) - 1) & 1);
-                const uint32_t dst = ring + (n & 3) * GE::slot;
+                return page;
+            };
+            int page = -1, next_page = pages_of(0);
+            // items: V of tile u - 1 and K of tile u, for u = 0 .. nt (no V in the first, no K in the last)
+            for (int n = 1; n <= 2 * nt; ++n) {
+                const int u = n >> 1, w = n & 1 ? 0 : 1, i = w ? u - 1 : u, p0 = kv.at(i0 + i);
+                const uint32_t bar = full + 8 * (u & 1);
+                if (w == 0) {
+                    page = next_page;
+                    next_page = pages_of(i + 1);
+                }
+                if (w && u >= 2) wait(empty + 8 * (u & 1), ((u >> 1) - 1) & 1);
+                const uint32_t dst = ring + (2 * w + (i & 1)) * GE::slot;
+                const bool arrive = w == 0 || u == nt;          // the last item of the stage
                 auto block_rows = [&](int blk, int& off) -> const uint8_t* {
                     const int pg = __shfl_sync(kAll, page, blk >> 1);
                     off = (p0 + 8 * blk) & (p.v.ps - 1);
@@ -327,18 +352,15 @@ __global__ void __launch_bounds__(Geo<D>::threads, 1) prefill_kernel(const __gri
                     const int k = lane / (D / 64), col = lane % (D / 64) * 64, at = p0 + k * rows;
                     const int pg = __shfl_sync(kAll, page, (k * rows >> 4) & (BN / 16 - 1));
                     if (pw == 0) {
-                        if (lane == 0) mbar_expect_tx(full + 8 * (n & 3), GE::slot);
-                        else mbar_arrive(full + 8 * (n & 3));
+                        if (lane == 0) tc_expect(bar, GE::slot);
                         __syncwarp();
                         if (lane < boxes)
                             tma_load3(dst + tile_byte(BN, k * rows, col), w ? &v_map : &k_map, col, at & (p.v.ps - 1),
-                                      pg * p.v.H + h, full + 8 * (n & 3));
-                    } else {
-                        mbar_arrive(full + 8 * (n & 3));
+                                      pg * p.v.H + h, bar);
                     }
                 } else if (KF == 0) {
                     constexpr int per = D / 8;                  // 16-byte pieces of a row
-                    for (int blk = pw; blk < BN / 8; blk += 3) {
+                    for (int blk = pw; blk < BN / 8; blk += GE::prod) {
                         int off;
                         const uint8_t* u = block_rows(blk, off);
                         const int live = u ? c.len - p0 - 8 * blk : 0;         // rows of the block that hold positions
@@ -350,12 +372,10 @@ __global__ void __launch_bounds__(Geo<D>::threads, 1) prefill_kernel(const __gri
                             st_shared16(dst + tile_byte(BN, 8 * blk + r, ch), y);
                         }
                     }
-                    fence_async_smem();
-                    mbar_arrive(full + 8 * (n & 3));
                 } else {
                     constexpr int per = D / 16;                 // 16-channel pieces of a row
                     constexpr int E = 8 * per / 32;             // of a lane in an 8-row block (D = 64: 1)
-                    for (int blk = pw; blk < BN / 8; blk += 3) {
+                    for (int blk = pw; blk < BN / 8; blk += GE::prod) {
                         int off;
                         const uint8_t* u = block_rows(blk, off);
                         uint4 code[E] = {};
@@ -387,13 +407,16 @@ __global__ void __launch_bounds__(Geo<D>::threads, 1) prefill_kernel(const __gri
                             st_shared16(dst + tile_byte(BN, 8 * blk + r, ch + 8), hi);
                         }
                     }
+                }
+                if (arrive) {
                     fence_async_smem();
-                    mbar_arrive(full + 8 * (n & 3));
+                    mbar_arrive(bar);
                 }
             }
         }
     } else {
         // ---------------------------------------------------------------------- the softmax
+        if constexpr (NT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(GE::soft_regs));
         const int t = warp >> 2, in = threadIdx.x & 127, row = r0 + 128 * t + in;
         const bool alive = row < r1;
         const ScoreRule rule = score_rule(p);
@@ -457,36 +480,28 @@ __global__ void __launch_bounds__(Geo<D>::threads, 1) prefill_kernel(const __gri
                 const bool whole = p0 + BN <= c.pre ? first >= 0
                                                     : p0 + BN - 1 <= first && p0 + BN <= c.len &&
                                                           (p.window <= 0 || p0 >= last - p.window + 1);
-                // first pass: the row's maximum; scores that the options or the visibility change go back to S
                 const float f = plain ? rs.f : 1.f;
-                float mx = -INFINITY;
-                uint32_t sr[2][32];
-                tmem_ld32(s_addr, sr[0]);
+                uint32_t sr[2][32], pr[BN / 64][32];
+                float mx = -INFINITY, sum = 0.f;
+                // scores that the options or the visibility change go back to S first
+                if (!plain || !whole) {
+                    tmem_ld32(s_addr, sr[0]);
 #pragma unroll
-                for (int k = 0; k < BN / 32; ++k) {
-                    uint32_t(&x)[32] = sr[k & 1];
-                    tmem_wait_ld(x);
-                    if (k + 1 < BN / 32) tmem_ld32(s_addr + 32 * (k + 1), sr[(k + 1) & 1]);
-                    if (!plain) apply_rule(x, rule, rs, p0 + 32 * k);
-                    if (!whole) {
-                        const int hi = rs.hi - p0 - 32 * k, lo = rs.lo - p0 - 32 * k, pre = rs.pre - p0 - 32 * k;
+                    for (int k = 0; k < BN / 32; ++k) {
+                        uint32_t(&x)[32] = sr[k & 1];
+                        tmem_wait_ld(x);
+                        if (k + 1 < BN / 32) tmem_ld32(s_addr + 32 * (k + 1), sr[(k + 1) & 1]);
+                        if (!plain) apply_rule(x, rule, rs, p0 + 32 * k);
+                        if (!whole) {
+                            const int hi = rs.hi - p0 - 32 * k, lo = rs.lo - p0 - 32 * k, pre = rs.pre - p0 - 32 * k;
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (!((e <= hi && e >= lo) || e < pre)) x[e] = 0xff800000u;
+                            for (int e = 0; e < 32; ++e)
+                                if (!((e <= hi && e >= lo) || e < pre)) x[e] = 0xff800000u;
+                        }
+                        tmem_st32(s_addr + 32 * k, x);
                     }
-                    if (!plain || !whole) tmem_st32(s_addr + 32 * k, x);
-                    float y[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                    for (int e = 0; e < 32; e += 8)
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            y[q] = fmaxf(fmaxf(y[q], __uint_as_float(x[e + 2 * q])), __uint_as_float(x[e + 2 * q + 1]));
-                    mx = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
+                    tmem_wait_st();
                 }
-                if (!plain || !whole) tmem_wait_st();
-                tmem_ld32(s_addr, sr[0]);                      // the second pass's first scores are on their way
-                const float x = mx * f;
-                const bool grow = x > m + kLazy || (m == -INFINITY && x > -INFINITY);
                 if constexpr (NT == 1) {
                     // S runs ahead of the values here: those of tile i - 1 are done before this tile's weights go out
                     // (with two row tiles, S of tile i was issued after them)
@@ -495,48 +510,56 @@ __global__ void __launch_bounds__(Geo<D>::threads, 1) prefill_kernel(const __gri
                         tc_fence_after();
                     }
                 }
-                if (i == 0) {
-                    m = x;
-                } else if (__any_sync(kAll, grow)) {
-                    const float a = grow ? ex2(m - x) : 1.f;
+                // The weights are formed with the maximum as it stands while the tile's own is found; only where that
+                // is more than 2^kLazy above (and for the first tile) the maximum moves and the weights are formed again.
+                for (bool last_try = false;; last_try = true) {
+                    const float2 f2 = make_float2(f, f), mb = m == -INFINITY ? make_float2(0.f, 0.f) : make_float2(-m, -m);
+                    float2 s2[2] = {};
+                    float y[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    tmem_ld32(s_addr, sr[0]);
+#pragma unroll
+                    for (int k = 0; k < BN / 32; ++k) {
+                        uint32_t(&x)[32] = sr[k & 1];
+                        tmem_wait_ld(x);
+                        if (k + 1 < BN / 32) tmem_ld32(s_addr + 32 * (k + 1), sr[(k + 1) & 1]);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const float a = __uint_as_float(x[2 * e]), b = __uint_as_float(x[2 * e + 1]);
+                            y[e & 3] = max3(y[e & 3], a, b);
+                            float2 u = __ffma2_rn(make_float2(a, b), f2, mb);
+                            u.x = ex2(u.x);
+                            u.y = ex2(u.y);
+                            s2[e & 1] = __fadd2_rn(s2[e & 1], u);
+                            pr[k / 2][16 * (k & 1) + e] = Two<T>::pack(u.x, u.y);
+                        }
+                    }
+                    sum = (s2[0].x + s2[0].y) + (s2[1].x + s2[1].y);
+                    if (last_try) break;
+                    mx = max3(fmaxf(y[0], y[1]), y[2], y[3]) * f;
+                    const bool grow = mx > m + kLazy || (m == -INFINITY && mx > -INFINITY);
+                    if (!__any_sync(kAll, grow)) break;
+                    const float a = grow ? ex2(m - mx) : 1.f;
+                    if (grow) m = mx;
                     l *= a;
-                    if (grow) m = x;
+                    if (i > 0) {
 #pragma unroll 1
-                    for (int d = 0; d < D; d += 32) {
-                        uint32_t o[32];
-                        tmem_ld32(o_addr + d, o);
-                        tmem_wait_ld(o);
+                        for (int d = 0; d < D; d += 32) {
+                            tmem_ld32(o_addr + d, sr[0]);
+                            tmem_wait_ld(sr[0]);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
-                        tmem_st32(o_addr + d, o);
+                            for (int e = 0; e < 32; ++e) sr[0][e] = __float_as_uint(__uint_as_float(sr[0][e]) * a);
+                            tmem_st32(o_addr + d, sr[0]);
+                        }
                     }
                 }
-                // second pass: weights, their sum, and P over the scores read so far
-                const float2 f2 = make_float2(f, f), mb = m == -INFINITY ? make_float2(0.f, 0.f) : make_float2(-m, -m);
-                float2 sum[2] = {};
-                uint32_t pr[32];
+                l += sum;
 #pragma unroll
-                for (int k = 0; k < BN / 32; ++k) {
-                    uint32_t(&x)[32] = sr[k & 1];
-                    tmem_wait_ld(x);
-                    if (k + 1 < BN / 32) tmem_ld32(s_addr + 32 * (k + 1), sr[(k + 1) & 1]);
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        float2 u = __ffma2_rn(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), f2, mb);
-                        u.x = ex2(u.x);
-                        u.y = ex2(u.y);
-                        sum[e & 1] = __fadd2_rn(sum[e & 1], u);
-                        pr[16 * (k & 1) + e] = Two<T>::pack(u.x, u.y);
-                    }
-                    if (k & 1) tmem_st32(s_addr + 16 * (k - 1), pr);
-                }
-                l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                for (int k = 0; k < BN / 64; ++k) tmem_st32(s_addr + 32 * k, pr[k]);
                 tmem_wait_st();
                 if (!whole) {
                     // does the V tile hold an infinity or NaN that some row must not see?
-                    const int n = 2 * i + 1;
-                    const uint32_t v_tile = ring + (n & 3) * GE::slot;
-                    wait(full + 8 * (n & 3), (n >> 2) & 1);
+                    const uint32_t v_tile = ring + (2 + (i & 1)) * GE::slot;
+                    wait(full + 8 * ((i + 1) & 1), ((i + 1) >> 1) & 1);
                     constexpr uint32_t top = BF ? 0x7f80u : 0x7c00u;
                     uint32_t bad = 0;
                     for (int e = in; e < BN * D / 8; e += 128) {
@@ -556,7 +579,7 @@ __global__ void __launch_bounds__(Geo<D>::threads, 1) prefill_kernel(const __gri
                 mbar_arrive(p_full + 8 * buf);
             }
             if (nt > 0) {
-                wait(o_done + 8 * t, (nt - 1) & 1);
+                wait(o_done + 8 * t, NT == 2 ? 0 : (nt - 1) & 1);   // two row tiles: reported once, at the end
                 tc_fence_after();
             }
             const float inv = l > 0.f ? 1.f / l : 0.f;
@@ -599,7 +622,7 @@ __global__ void __launch_bounds__(Geo<D>::threads, 1) prefill_kernel(const __gri
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 4 * NT) tmem_free512(tmem);
+    if (warp == GE::mma_warp) tmem_free512(tmem);
 }
 
 // Joins the splits' partials: D / 8 threads a row, all rows of a chunk.
@@ -642,7 +665,7 @@ int splits_of(int64_t rows, int n_seq, int H, int tile_rows, int sm_count) {
 
 template <int D, int KF, int VF, typename T, typename TQ>
 int prefill_run(const PagedAttnParams& p, const CUtensorMap* maps, int sm_count, cudaStream_t s) {
-    using GE = Geo<D>;
+    using GE = Geo<D, KF != 0>;
     const auto k = prefill_kernel<D, KF, VF, T, TQ>;
     int res = 0;
     if (const int e = resident_ctas((const void*)k, GE::threads, GE::smem, &res)) return e;
@@ -679,7 +702,10 @@ size_t paged_prefill_ws_floats(int D, int64_t head_rows) {
     return (size_t)((most < full ? most : full) * (D + 2));
 }
 
-int prefill_box_rows(int D, int ps) { return ps < (D == 256 ? 64 : 128) ? ps : (D == 256 ? 64 : 128); }
+int prefill_box_rows(int D, int ps) {
+    const int bn = D == 256 ? Geo<256, false>::BN : Geo<128, false>::BN;
+    return ps < bn ? ps : bn;
+}
 
 int launch_paged_prefill(const PagedAttnParams& p, const void* maps, int sm_count, void* stream) {
     cudaStream_t s = (cudaStream_t)stream;
