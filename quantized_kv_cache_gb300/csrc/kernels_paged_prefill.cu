@@ -180,6 +180,46 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return d;
 }
 
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+    return (uint64_t)__float_as_uint(a) | ((uint64_t)__float_as_uint(b) << 32);
+}
+__device__ __forceinline__ float2 unpair(uint64_t x) { return make_float2(__uint_as_float((uint32_t)x), __uint_as_float((uint32_t)(x >> 32))); }
+
+// Weights 2^(s f - m) of 32 scores, packed two by two into w; adds them to the sums and finds the largest score. A warp
+// has its scheduler almost to itself here, and the exponential unit takes one instruction in four cycles: the
+// instructions are written in the order in which they should issue, between two exponentials a multiply-add of
+// the next pairs and the rounding, sum and maximum of the last (grouped by kind they took 240 cycles, not 128).
+template <typename T>
+__device__ __forceinline__ void weights32(const uint32_t (&x)[32], uint64_t f, uint64_t m, uint32_t* w, uint64_t (&sum)[4], float (&top)[4]) {
+    uint64_t u[16];
+    float v[32];
+    const auto first = [&](int e) {
+        const uint64_t a = (uint64_t)x[2 * e] | ((uint64_t)x[2 * e + 1] << 32);
+        asm volatile("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(u[e]) : "l"(a), "l"(f), "l"(m));
+    };
+    const auto last = [&](int e) {
+        if constexpr (std::is_same<T, __half>::value)
+            asm volatile("cvt.rn.f16x2.f32 %0, %1, %2;\n" : "=r"(w[e]) : "f"(v[2 * e + 1]), "f"(v[2 * e]));
+        else
+            asm volatile("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(w[e]) : "f"(v[2 * e + 1]), "f"(v[2 * e]));
+        asm volatile("add.rn.f32x2 %0, %0, %1;\n" : "+l"(sum[e & 3]) : "l"(pair(v[2 * e], v[2 * e + 1])));
+    };
+    constexpr int A = 2;                                      // pairs that the multiply-adds and the roundings are apart by
+#pragma unroll
+    for (int e = 0; e < A; ++e) first(e);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+        const float2 y = unpair(u[e]);
+        asm volatile("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(v[2 * e]) : "f"(y.x));
+        if (e + A < 16) first(e + A);
+        asm volatile("max.f32 %0, %0, %1, %2;\n" : "+f"(top[e & 3]) : "f"(__uint_as_float(x[2 * e])), "f"(__uint_as_float(x[2 * e + 1])));
+        asm volatile("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(v[2 * e + 1]) : "f"(y.y));
+        if (e >= A) last(e - A);
+    }
+#pragma unroll
+    for (int e = 16 - A; e < 16; ++e) last(e);
+}
+
 // Raw scores of 32 positions from p0 on to scores in units of log2: the cap, then the bias.
 __device__ __forceinline__ void apply_rule(uint32_t (&s)[32], const ScoreRule& rule, const RowState& r, int p0) {
     float big = 0.f;
@@ -514,7 +554,7 @@ __global__ void __launch_bounds__(Geo<D, KF != 0>::threads, 1) prefill_kernel(co
                 // is more than 2^kLazy above (and for the first tile) the maximum moves and the weights are formed again.
                 for (bool last_try = false;; last_try = true) {
                     const float2 f2 = make_float2(f, f), mb = m == -INFINITY ? make_float2(0.f, 0.f) : make_float2(-m, -m);
-                    float2 s2[2] = {};
+                    uint64_t s2[4] = {};
                     float y[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
                     tmem_ld32(s_addr, sr[0]);
 #pragma unroll
@@ -522,18 +562,12 @@ __global__ void __launch_bounds__(Geo<D, KF != 0>::threads, 1) prefill_kernel(co
                         uint32_t(&x)[32] = sr[k & 1];
                         tmem_wait_ld(x);
                         if (k + 1 < BN / 32) tmem_ld32(s_addr + 32 * (k + 1), sr[(k + 1) & 1]);
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const float a = __uint_as_float(x[2 * e]), b = __uint_as_float(x[2 * e + 1]);
-                            y[e & 3] = max3(y[e & 3], a, b);
-                            float2 u = __ffma2_rn(make_float2(a, b), f2, mb);
-                            u.x = ex2(u.x);
-                            u.y = ex2(u.y);
-                            s2[e & 1] = __fadd2_rn(s2[e & 1], u);
-                            pr[k / 2][16 * (k & 1) + e] = Two<T>::pack(u.x, u.y);
-                        }
+                        weights32<T>(x, pair(f2.x, f2.y), pair(mb.x, mb.y), &pr[k / 2][16 * (k & 1)], s2, y);
                     }
-                    sum = (s2[0].x + s2[0].y) + (s2[1].x + s2[1].y);
+                    {
+                        const float2 a = unpair(s2[0]), b = unpair(s2[1]), c2 = unpair(s2[2]), d = unpair(s2[3]);
+                        sum = ((a.x + a.y) + (b.x + b.y)) + ((c2.x + c2.y) + (d.x + d.y));
+                    }
                     if (last_try) break;
                     mx = max3(fmaxf(y[0], y[1]), y[2], y[3]) * f;
                     const bool grow = mx > m + kLazy || (m == -INFINITY && mx > -INFINITY);
