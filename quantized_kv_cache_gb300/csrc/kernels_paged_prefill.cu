@@ -27,11 +27,12 @@ template <int D, bool CODES> struct Geo {
     static constexpr int BN = D == 256 ? 64 : 128;           // positions of a KV tile
     static constexpr int rows = 128 * NT;
     // warps: four softmax warps per row tile, one that issues the products, producers (decoding codes takes more)
-    static constexpr int mma_warp = 4 * NT, first_prod = mma_warp + 1, prod = CODES ? 7 : 3;
+    static constexpr int mma_warp = 4 * NT, first_prod = mma_warp + 1, prod = CODES ? 15 - mma_warp : 3;
     static constexpr int threads = 32 * (first_prod + prod);
-    // registers of two row tiles: 256 softmax threads and the others share what the block is launched with (384 x 168,
-    // 512 x 128)
-    static constexpr int soft_regs = CODES ? 184 : 208, other_regs = CODES ? 72 : 88;   // (one row tile: not moved)
+    // registers (0: not moved): what the block is launched with, 384 x 168 or 512 x 128, is shared out between the softmax's
+    // 128 NT threads and the others
+    static constexpr int soft_regs = NT == 2 ? (CODES ? 168 : 208) : (CODES ? 200 : 0);
+    static constexpr int other_regs = NT == 2 ? 88 : (CODES ? 104 : 0);
     static constexpr int q_bytes = 128 * D * 2;              // of a row tile
     static constexpr int slot = BN * D * 2;
     static constexpr int smem = 1024 + NT * q_bytes + 4 * slot;
@@ -293,7 +294,7 @@ __global__ void __launch_bounds__(Geo<D, KF != 0>::threads, 1) prefill_kernel(co
     auto wait = [&](uint32_t bar, uint32_t parity) { bounded_wait(bar, parity, p.v.status, &s_abort); };
 
     if (warp >= GE::mma_warp) {
-        if constexpr (NT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(GE::other_regs));
+        if constexpr (GE::other_regs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(GE::other_regs));
         if (warp == GE::mma_warp) {
             // ------------------------------------------------------------------ the products
             // One warp for both row tiles: it keeps them half a period apart, so that the softmax of one runs beside
@@ -368,95 +369,128 @@ __global__ void __launch_bounds__(Geo<D, KF != 0>::threads, 1) prefill_kernel(co
                 }
                 return page;
             };
-            int page = -1, next_page = pages_of(0);
-            // items: V of tile u - 1 and K of tile u, for u = 0 .. nt (no V in the first, no K in the last)
-            for (int n = 1; n <= 2 * nt; ++n) {
-                const int u = n >> 1, w = n & 1 ? 0 : 1, i = w ? u - 1 : u, p0 = kv.at(i0 + i);
-                const uint32_t bar = full + 8 * (u & 1);
-                if (w == 0) {
-                    page = next_page;
-                    next_page = pages_of(i + 1);
-                }
-                if (w && u >= 2) wait(empty + 8 * (u & 1), ((u >> 1) - 1) & 1);
-                const uint32_t dst = ring + (2 * w + (i & 1)) * GE::slot;
-                const bool arrive = w == 0 || u == nt;          // the last item of the stage
-                auto block_rows = [&](int blk, int& off) -> const uint8_t* {
-                    const int pg = __shfl_sync(kAll, page, blk >> 1);
-                    off = (p0 + 8 * blk) & (p.v.ps - 1);
-                    return pg < 0 ? nullptr : unit_at(p.v, w, pg, h);
-                };
-                const int fmt = w ? VF : KF;
-                if (KF == 0 && __all_sync(kAll, lane >= BN / 16 || page >= 0) && p0 + BN <= c.len) {
-                    // boxes of min(page_size, BN) rows x 64 channels, one per lane of the first producer
-                    const int rows = min(p.v.ps, BN), boxes = BN / rows * (D / 64);
-                    const int k = lane / (D / 64), col = lane % (D / 64) * 64, at = p0 + k * rows;
-                    const int pg = __shfl_sync(kAll, page, (k * rows >> 4) & (BN / 16 - 1));
-                    if (pw == 0) {
-                        if (lane == 0) tc_expect(bar, GE::slot);
-                        __syncwarp();
-                        if (lane < boxes)
-                            tma_load3(dst + tile_byte(BN, k * rows, col), w ? &v_map : &k_map, col, at & (p.v.ps - 1),
-                                      pg * p.v.H + h, bar);
+            if constexpr (KF == 0) {
+                int page = -1, next_page = pages_of(0);
+                // items: V of tile u - 1 and K of tile u, for u = 0 .. nt (no V in the first, no K in the last)
+                for (int n = 1; n <= 2 * nt; ++n) {
+                    const int u = n >> 1, w = n & 1 ? 0 : 1, i = w ? u - 1 : u, p0 = kv.at(i0 + i);
+                    const uint32_t bar = full + 8 * (u & 1);
+                    if (w == 0) {
+                        page = next_page;
+                        next_page = pages_of(i + 1);
                     }
-                } else if (KF == 0) {
-                    constexpr int per = D / 8;                  // 16-byte pieces of a row
-                    for (int blk = pw; blk < BN / 8; blk += GE::prod) {
-                        int off;
-                        const uint8_t* u = block_rows(blk, off);
-                        const int live = u ? c.len - p0 - 8 * blk : 0;         // rows of the block that hold positions
-#pragma unroll
-                        for (int e = 0; e < per / 4; ++e) {
-                            const int x = e * 32 + lane, r = x / per, ch = x % per * 8;
-                            uint4 y = make_uint4(0, 0, 0, 0);
-                            if (r < live) y = *reinterpret_cast<const uint4*>(u + (off + r) * (2 * D) + 2 * ch);
-                            st_shared16(dst + tile_byte(BN, 8 * blk + r, ch), y);
+                    if (w && u >= 2) wait(empty + 8 * (u & 1), ((u >> 1) - 1) & 1);
+                    const uint32_t dst = ring + (2 * w + (i & 1)) * GE::slot;
+                    const bool arrive = w == 0 || u == nt;          // the last item of the stage
+                    auto block_rows = [&](int blk, int& off) -> const uint8_t* {
+                        const int pg = __shfl_sync(kAll, page, blk >> 1);
+                        off = (p0 + 8 * blk) & (p.v.ps - 1);
+                        return pg < 0 ? nullptr : unit_at(p.v, w, pg, h);
+                    };
+                    if (__all_sync(kAll, lane >= BN / 16 || page >= 0) && p0 + BN <= c.len) {
+                        // boxes of min(page_size, BN) rows x 64 channels, one per lane of the first producer
+                        const int rows = min(p.v.ps, BN), boxes = BN / rows * (D / 64);
+                        const int k = lane / (D / 64), col = lane % (D / 64) * 64, at = p0 + k * rows;
+                        const int pg = __shfl_sync(kAll, page, (k * rows >> 4) & (BN / 16 - 1));
+                        if (pw == 0) {
+                            if (lane == 0) tc_expect(bar, GE::slot);
+                            __syncwarp();
+                            if (lane < boxes)
+                                tma_load3(dst + tile_byte(BN, k * rows, col), w ? &v_map : &k_map, col, at & (p.v.ps - 1),
+                                          pg * p.v.H + h, bar);
                         }
-                    }
-                } else {
-                    constexpr int per = D / 16;                 // 16-channel pieces of a row
-                    constexpr int E = 8 * per / 32;             // of a lane in an 8-row block (D = 64: 1)
-                    for (int blk = pw; blk < BN / 8; blk += GE::prod) {
-                        int off;
-                        const uint8_t* u = block_rows(blk, off);
-                        uint4 code[E] = {};
-                        uint32_t d[E] = {};
+                    } else {
+                        constexpr int per = D / 8;                  // 16-byte pieces of a row
+                        for (int blk = pw; blk < BN / 8; blk += GE::prod) {
+                            int off;
+                            const uint8_t* u = block_rows(blk, off);
+                            const int live = u ? c.len - p0 - 8 * blk : 0;         // rows of the block that hold positions
 #pragma unroll
-                        for (int e = 0; e < E; ++e) {
-                            const int x = e * 32 + lane, r = x / per, ch = x % per * 16;
-                            if (u && p0 + 8 * blk + r < c.len) {
-                                const int rb = fmt == 1 ? D : D / 2;
-                                const uint8_t* a = u + (off + r) * rb;
-                                if (fmt == 1) {
-                                    code[e] = *reinterpret_cast<const uint4*>(a + ch);
-                                } else {
-                                    const uint2 y = *reinterpret_cast<const uint2*>(a + ch / 2);
-                                    code[e].x = y.x;
-                                    code[e].y = y.y;
-                                }
-                                d[e] = *reinterpret_cast<const uint16_t*>(u + (int64_t)p.v.ps * rb + (off + r) * (D / 16) +
-                                                                          ch / 32 * 2);
+                            for (int e = 0; e < per / 4; ++e) {
+                                const int x = e * 32 + lane, r = x / per, ch = x % per * 8;
+                                uint4 y = make_uint4(0, 0, 0, 0);
+                                if (r < live) y = *reinterpret_cast<const uint4*>(u + (off + r) * (2 * D) + 2 * ch);
+                                st_shared16(dst + tile_byte(BN, 8 * blk + r, ch), y);
                             }
                         }
-#pragma unroll
-                        for (int e = 0; e < E; ++e) {
-                            const int x = e * 32 + lane, r = x / per, ch = x % per * 16;
-                            const uint32_t dd = d[e] | (d[e] << 16);
-                            const uint4 lo = fmt == 1 ? decode_q8(make_uint2(code[e].x, code[e].y), dd) : decode_q4(code[e].x, dd);
-                            const uint4 hi = fmt == 1 ? decode_q8(make_uint2(code[e].z, code[e].w), dd) : decode_q4(code[e].y, dd);
-                            st_shared16(dst + tile_byte(BN, 8 * blk + r, ch), lo);
-                            st_shared16(dst + tile_byte(BN, 8 * blk + r, ch + 8), hi);
-                        }
+                    }
+                    if (arrive) {
+                        fence_async_smem();
+                        mbar_arrive(bar);
                     }
                 }
-                if (arrive) {
-                    fence_async_smem();
-                    mbar_arrive(bar);
+            } else {
+                // Codes: a thread has the same pieces (16 channels of a row) of every item; those of the next item are
+                // on their way while this item's are decoded (loaded and decoded in turn, an item took 3,300 cycles).
+                constexpr int per = D / 16, step = 32 * GE::prod / per, E = (BN + step - 1) / step;   // rows apart, of a thread
+                const int id = 32 * pw + lane, row0 = id / per, ch = id % per * 16;
+                uint4 code[E];
+                uint32_t d[E];
+                int page = -1, next_page = pages_of(0);
+                auto load = [&](int n) {                        // items in order: the page numbers follow the K items
+                    const int u = n >> 1, w = n & 1 ? 0 : 1, i = w ? u - 1 : u, p0 = kv.at(i0 + i);
+                    if (w == 0) {
+                        page = next_page;
+                        next_page = pages_of(i + 1);
+                    }
+                    const bool q8 = (w ? VF : KF) == 1;
+                    const int rb = q8 ? D : D / 2;
+                    const uint32_t unit = (uint32_t)p.v.unit[w];
+                    const uint8_t* base_w = p.v.base[w] + (int64_t)h * unit;
+#pragma unroll
+                    for (int e = 0; e < E; ++e) {
+                        const int r = row0 + e * step;
+                        const int pg = __shfl_sync(kAll, page, (r >> 4) & (BN / 16 - 1));
+                        code[e] = make_uint4(0, 0, 0, 0);
+                        d[e] = 0;
+                        if (r < BN && pg >= 0 && p0 + r < c.len) {
+                            const int row = (p0 + r) & (p.v.ps - 1);
+                            const uint8_t* a = base_w + (uint64_t)(uint32_t)(pg * p.v.H) * unit;
+                            d[e] = *reinterpret_cast<const uint16_t*>(a + (p.v.ps * rb + row * (D / 16) + ch / 32 * 2));
+                            a += row * rb + (q8 ? ch : ch / 2);
+                            if (q8) {
+                                code[e] = *reinterpret_cast<const uint4*>(a);
+                            } else {
+                                const uint2 y = *reinterpret_cast<const uint2*>(a);
+                                code[e].x = y.x;
+                                code[e].y = y.y;
+                            }
+                        }
+                    }
+                };
+                if (nt > 0) load(1);
+                for (int n = 1; n <= 2 * nt; ++n) {
+                    const int u = n >> 1, w = n & 1 ? 0 : 1, i = w ? u - 1 : u;
+                    uint4 now[E];
+                    uint32_t dn[E];
+#pragma unroll
+                    for (int e = 0; e < E; ++e) {
+                        now[e] = code[e];
+                        dn[e] = d[e] | (d[e] << 16);
+                    }
+                    if (n < 2 * nt) load(n + 1);
+                    if (w && u >= 2) wait(empty + 8 * (u & 1), ((u >> 1) - 1) & 1);
+                    const uint32_t dst = ring + (2 * w + (i & 1)) * GE::slot;
+                    const bool q8 = (w ? VF : KF) == 1;
+#pragma unroll
+                    for (int e = 0; e < E; ++e) {
+                        const int r = row0 + e * step;
+                        if (r >= BN) continue;
+                        const uint4 lo = q8 ? decode_q8(make_uint2(now[e].x, now[e].y), dn[e]) : decode_q4(now[e].x, dn[e]);
+                        const uint4 hi = q8 ? decode_q8(make_uint2(now[e].z, now[e].w), dn[e]) : decode_q4(now[e].y, dn[e]);
+                        st_shared16(dst + tile_byte(BN, r, ch), lo);
+                        st_shared16(dst + tile_byte(BN, r, ch + 8), hi);
+                    }
+                    if (w == 0 || u == nt) {                    // the last item of the stage
+                        fence_async_smem();
+                        mbar_arrive(full + 8 * (u & 1));
+                    }
                 }
             }
         }
     } else {
         // ---------------------------------------------------------------------- the softmax
-        if constexpr (NT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(GE::soft_regs));
+        if constexpr (GE::soft_regs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(GE::soft_regs));
         const int t = warp >> 2, in = threadIdx.x & 127, row = r0 + 128 * t + in;
         const bool alive = row < r1;
         const ScoreRule rule = score_rule(p);
