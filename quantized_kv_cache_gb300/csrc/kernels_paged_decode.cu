@@ -108,6 +108,9 @@ __global__ void __launch_bounds__(kDT, D == 256 ? 2 : 3) decode_kernel(PagedAttn
     }
     before -= mine;
     const int64_t U = run_tiles(total, p.n_cta), first = blockIdx.x * U;
+    // a launch that leaves half of its CTAs without work lets the merge's start beside it (in a full one they would
+    // take the place of its own)
+    if (total <= p.n_cta / 2 * U) grid_dep_launch();
     int64_t left = min(U, total - first);
     if (left <= 0) return;
     if (first >= before && first < before + mine) {
@@ -337,8 +340,7 @@ __global__ void __launch_bounds__(kMT) merge_kernel(PagedAttnParams p) {
     __shared__ float s_w[kMaxDecodeCtas + 1], s_x[kMT / 32];
     __shared__ float4 s_o[N][L];
     const int b = blockIdx.x / p.Hq, hq = blockIdx.x % p.Hq, h = hq / p.G, r = hq % p.G, H = p.v.H, G = p.G;
-    grid_dep_wait();
-    int64_t all = 0, before = 0;
+    int64_t all = 0, before = 0;                         // the lengths: settled before the decode kernel lets this one start
     for (int i = threadIdx.x; i < p.n_seq; i += kMT) {
         const int64_t n = (int64_t)seq_tiles(p, i).n * H;
         all += n;
@@ -347,6 +349,7 @@ __global__ void __launch_bounds__(kMT) merge_kernel(PagedAttnParams p) {
     all = block_sum<kMT>(all, red);
     before = block_sum<kMT>(before, red);
     const int n = seq_tiles(p, b).n;
+    grid_dep_wait();
     TQ* out = (TQ*)p.out + (int64_t)blockIdx.x * D;
     if (n == 0) {
         if (threadIdx.x < D / 2) reinterpret_cast<uint32_t*>(out)[threadIdx.x] = 0;

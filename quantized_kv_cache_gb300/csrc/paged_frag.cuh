@@ -5,7 +5,7 @@
 // them: the channel order of the score product is free (the query fragments follow it), and so is
 // the channel order of the output tiles. With g = lane / 4, t = lane % 4:
 //  - scores, S[16 x 8 positions] = Q K^T: lane (g, t) reads pieces t, t + 4, .. of row g; each piece
-//    feeds k-steps whose channels qchan() names;
+//    feeds k-steps whose channels qchan() names (eight consecutive ones for two steps);
 //  - values, O[16 x 8 channels] = P V: lane (g, t) reads pieces g, g + 8, .. of rows 2t, 2t+1, 2t+8,
 //    2t+9 and pairs the rows channel by channel (byte permutes); a piece's i-th channel is the
 //    lane's column of output tile i, so a lane ends with runs of consecutive output channels.
@@ -70,12 +70,11 @@ template <int D, int PF> struct VGeo {
     static constexpr int CH = PF == PF_16 ? CB / 2 : (PF == PF_Q8 ? CB : CB * 2);
 };
 
-// Channel of element e (0, 1: the low k pair, 2, 3: the high pair) of k-step ks of lane t.
-template <int D, int PF> __device__ __forceinline__ int qchan(int ks, int t, int e) {
-    constexpr int CH = KGeo<D, PF>::CH, KS = CH / 4;            // k-steps of a piece
-    const int base = CH * (t + 4 * (ks / KS)), r = ks % KS;
-    if (PF != PF_Q4) return base + 4 * r + e;
-    return base + 8 * (r / 2) + 2 * (r & 1) + (e >> 1) + 4 * (e & 1);
+// First of the eight consecutive channels that k-steps 2 i and 2 i + 1 of lane t take. Their operand pairs are
+// (0, 1), (2, 3) | (4, 5), (6, 7), or for nibbles (0, 4), (1, 5) | (2, 6), (3, 7), as the rows decode.
+template <int D, int PF> __device__ __forceinline__ int qchan(int i, int t) {
+    constexpr int CH = KGeo<D, PF>::CH, N = CH / 8;             // groups of eight in a piece
+    return CH * (t + 4 * (i / N)) + 8 * (i % N);
 }
 
 // First of the CH consecutive output channels that column `col` (0..7) has in piece j's tiles.
@@ -192,21 +191,26 @@ __device__ __forceinline__ void load_queries(const ROW& rows, int g, int t, uint
             }
         }
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks)
+        for (int i = 0; i < D / 32; ++i) {
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (p) {
+                x = *reinterpret_cast<const uint4*>(p + qchan<D, PF>(i, t));
+                if constexpr (!same) {
+                    float y[8];
+                    unpack8<TQ>(x, y);
 #pragma unroll
-            for (int hi = 0; hi < 2; ++hi) {
-                uint32_t u = 0;
-                if (p) {
-                    const uint32_t a = *reinterpret_cast<const uint16_t*>(p + qchan<D, PF>(ks, t, 2 * hi));
-                    const uint32_t b = *reinterpret_cast<const uint16_t*>(p + qchan<D, PF>(ks, t, 2 * hi + 1));
-                    u = a | (b << 16);
-                    if constexpr (!same) {
-                        const float2 f = Two<TQ>::unpack(u);
-                        u = Two<T>::pack(f.x * up, f.y * up);
-                    }
+                    for (int e = 0; e < 8; ++e) y[e] *= up;
+                    x = pack8<T>(y);
                 }
-                qf[ks][2 * hi + half] = u;
             }
+            if constexpr (PF == PF_Q4)
+                x = make_uint4(__byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632), __byte_perm(x.y, x.w, 0x5410),
+                               __byte_perm(x.y, x.w, 0x7632));
+            qf[2 * i][half] = x.x;
+            qf[2 * i][2 + half] = x.y;
+            qf[2 * i + 1][half] = x.z;
+            qf[2 * i + 1][2 + half] = x.w;
+        }
     }
 }
 
