@@ -130,6 +130,7 @@ __global__ void __launch_bounds__(kDT, D == 256 ? 2 : 3) decode_kernel(PagedAttn
     int b = s_b, h = s_h, i0 = s_i;
     const ScoreRule rule = score_rule(p);
     const bool plain = rule.plain();
+    const LanePlace<D, KF, VF> place(g, t);
     const uint32_t k_at = copy_lane<D, KF, false>(lane), v_at = copy_lane<D, VF, true>(lane);
 
     for (; left > 0; ++h, i0 = 0) {
@@ -152,13 +153,15 @@ __global__ void __launch_bounds__(kDT, D == 256 ? 2 : 3) decode_kernel(PagedAttn
                         if (pages < 0 || pages >= p.v.n_pages) {
                             raise_status(p.v.status, KVQ_PAGED_BAD_INDEX);
                             pages = -1;
+                        } else {
+                            pages = pages * H + h;               // the unit's number
                         }
                     }
                     unit_page = __shfl_sync(kAll, pages, i & 31);
                     unit_off = (st.tile(i * kDW + i0 + warp) * kTile) & (p.v.ps - 1);
-                    copy_tile<D, KF, false>(dst, k_at, unit_page < 0 ? nullptr : unit_at(p.v, 0, unit_page, h), p.v.ps, unit_off, lane);
+                    copy_tile<D, KF, false>(dst, k_at, unit_page < 0 ? nullptr : p.v.base[0] + (uint64_t)(uint32_t)unit_page * (uint32_t)p.v.unit[0], p.v.ps, unit_off, lane);
                 } else {
-                    copy_tile<D, VF, true>(dst, v_at, unit_page < 0 ? nullptr : unit_at(p.v, 1, unit_page, h), p.v.ps, unit_off, lane);
+                    copy_tile<D, VF, true>(dst, v_at, unit_page < 0 ? nullptr : p.v.base[1] + (uint64_t)(uint32_t)unit_page * (uint32_t)p.v.unit[1], p.v.ps, unit_off, lane);
                 }
             }
             cp_commit();
@@ -188,11 +191,10 @@ __global__ void __launch_bounds__(kDT, D == 256 ? 2 : 3) decode_kernel(PagedAttn
 
         for (int i = 0; i < nt; ++i) {
             const int p0 = st.tile(i * kDW + i0 + warp) * kTile;
-            SharedTile<D, KF, false> kt;
-            kt.base = take();
+            const uint32_t k_tile = take();
             copy_next();
             float s[2][4] = {};
-            tile_scores<D, KF, T>(kt, g, t, qf, s);
+            tile_scores<D, KF, T>(k_tile, place, qf, s);
             const bool all = p0 + kTile <= st.len && (p0 >= st.lo || p0 + kTile <= st.pre);
             unsigned see = 0xffffu;
             if (!all) see = __ballot_sync(kAll, lane < 16 && st.sees(p0 + lane));
@@ -253,14 +255,13 @@ __global__ void __launch_bounds__(kDT, D == 256 ? 2 : 3) decode_kernel(PagedAttn
                         pl[2 * n + k] = Two<T>::pack(x - hi.x, y - hi.y);
                     }
                 }
-            SharedTile<D, VF, true> vt;
-            vt.base = take();
+            const uint32_t v_tile = take();
             copy_next();
             if (!all) {
-                clear_rows<D, VF>(vt.base, see, lane);
+                clear_rows<D, VF>(v_tile, see, lane);
                 __syncwarp();
             }
-            tile_values<D, VF, T, LO>(vt, g, t, pa, pl, o);
+            tile_values<D, VF, T, LO>(v_tile, place, pa, pl, o);
         }
         cp_wait<0>();
         __syncthreads();                                          // the rings become the join's space

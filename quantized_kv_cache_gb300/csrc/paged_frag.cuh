@@ -80,22 +80,62 @@ template <int D, int PF> __device__ __forceinline__ int qchan(int i, int t) {
 // First of the CH consecutive output channels that column `col` (0..7) has in piece j's tiles.
 template <int D, int PF> __device__ __forceinline__ int ochan(int j, int col) { return VGeo<D, PF>::CH * (col + 8 * j); }
 
-// s[n] += q K^T of positions 8n .. 8n+7. `src` gives piece(row, byte) and scale(row, block) of the tile.
-template <int D, int PF, typename T, typename SRC>
-__device__ __forceinline__ void tile_scores(const SRC& src, int g, int t, const uint32_t (&qf)[D / 16][4], float (&s)[2][4]) {
+// Where a lane finds its pieces and scales in a tile, fixed over the tiles: a tile in shared memory is 16 code rows of RB
+// bytes, then (block formats) the rows' scales. The 16-byte pieces of a 128-byte line are permuted by row so
+// that the eight lanes of a load phase (K: two rows, four neighbouring pieces; V: rows 0, 2, 4, 6, two
+// neighbouring pieces) hit all banks.
+template <int RB, bool VALUES> __device__ __forceinline__ uint32_t tile_swizzle(uint32_t byte) {
+    const uint32_t row = byte / RB;
+    if (VALUES) return byte ^ (RB >= 64 ? ((row >> 1) & 3) << 5 : ((row >> 2) & 1) << 5);
+    return RB >= 128 ? byte ^ ((row & 1) << 6) : byte;
+}
+template <int D, int KF, int VF> struct LanePlace {
+    using K = KGeo<D, KF>;
+    using V = VGeo<D, VF>;
+    uint32_t k[2], ks;        // K: pieces of even and odd j of row g; the row's first scale
+    uint32_t v[2], vs;        // V: piece 0 of rows 2t, 2t + 1; the first scale of row 2t
+    __device__ __forceinline__ LanePlace(int g, int t) {
+        k[0] = tile_swizzle<K::RB, false>(g * K::RB + K::CB * t);
+        k[1] = tile_swizzle<K::RB, false>(g * K::RB + (K::NJ > 1 ? K::CB * (t + 4) : K::CB * t));
+        ks = 16 * K::RB + g * (D / 16) + K::CH * t / 32 * 2;
+        v[0] = tile_swizzle<V::RB, true>(2 * t * V::RB + V::CB * g);
+        v[1] = tile_swizzle<V::RB, true>((2 * t + 1) * V::RB + V::CB * g);
+        vs = 16 * V::RB + 2 * t * (D / 16) + V::CH * g / 32 * 2;
+    }
+};
+template <int N> __device__ __forceinline__ Words<N> ld_words(uint32_t a) {
+    Words<N> w;
+    if constexpr (N == 4)
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n" : "=r"(w.w[0]), "=r"(w.w[1]), "=r"(w.w[2]), "=r"(w.w[3]) : "r"(a));
+    else if constexpr (N == 2)
+        asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];\n" : "=r"(w.w[0]), "=r"(w.w[1]) : "r"(a));
+    else
+        asm volatile("ld.shared.u32 %0, [%1];\n" : "=r"(w.w[0]) : "r"(a));
+    return w;
+}
+__device__ __forceinline__ uint32_t ld_half(uint32_t a) {
+    uint16_t x;
+    asm volatile("ld.shared.u16 %0, [%1];\n" : "=h"(x) : "r"(a));
+    return x;
+}
+
+// s[n] += q K^T of positions 8n .. 8n+7 of the tile at `base`.
+template <int D, int PF, typename T, typename PLACE>
+__device__ __forceinline__ void tile_scores(uint32_t base, const PLACE& at, const uint32_t (&qf)[D / 16][4], float (&s)[2][4]) {
     using K = KGeo<D, PF>;
+    static_assert(K::NJ == 1 || K::CB == 16, "pieces j and j + 2 are 128 bytes apart");
+    const uint32_t even = base + at.k[0], odd = base + at.k[1], sc = base + at.ks;
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
-        const int row = g + 8 * n;
 #pragma unroll
         for (int j = 0; j < K::NJ; ++j) {
-            const Words<K::NW> p = src.template piece<K::NW>(row, K::CB * (t + 4 * j));
+            const Words<K::NW> p = ld_words<K::NW>((j & 1 ? odd : even) + j / 2 * 128 + 8 * n * K::RB);
             constexpr int KS = K::CH / 4;
             if constexpr (PF == PF_16) {
                 mma_t(s[n], qf[KS * j], p.w[0], p.w[1], T());
                 mma_t(s[n], qf[KS * j + 1], p.w[2], p.w[3], T());
             } else {
-                const uint32_t d1 = src.scale(row, K::CH * (t + 4 * j) / 32), d = d1 | (d1 << 16);
+                const uint32_t d1 = ld_half(sc + 8 * n * (D / 16) + K::CH * j / 4), d = __byte_perm(d1, d1, 0x1010);
 #pragma unroll
                 for (int i = 0; i < K::NW; ++i) {
                     if constexpr (PF == PF_Q8) {
@@ -115,20 +155,22 @@ __device__ __forceinline__ void tile_scores(const SRC& src, int g, int t, const 
 }
 
 // o += P V of the tile's 16 positions. With LO, P = pa + pl (two bf16 parts).
-template <int D, int PF, typename T, bool LO, typename SRC>
-__device__ __forceinline__ void tile_values(const SRC& src, int g, int t, const uint32_t (&pa)[4], const uint32_t (&pl)[4],
+template <int D, int PF, typename T, bool LO, typename PLACE>
+__device__ __forceinline__ void tile_values(uint32_t base, const PLACE& at, const uint32_t (&pa)[4], const uint32_t (&pl)[4],
                                             float (&o)[D / 8][4]) {
     using V = VGeo<D, PF>;
+    static_assert(V::NJ == 1 || V::CB == 16, "pieces j and j + 1 are 128 bytes apart");
+    // rows 2t + 8 and 2t + 9: the same permutation (that of 32-byte rows too: four lines on)
+    const uint32_t a0 = base + at.v[0], a1 = base + at.v[1], sc = base + at.vs;
 #pragma unroll
     for (int j = 0; j < V::NJ; ++j) {
-        const int at = V::CB * (g + 8 * j);
-        const Words<V::NW> r0 = src.template piece<V::NW>(2 * t, at), r1 = src.template piece<V::NW>(2 * t + 1, at);
-        const Words<V::NW> r2 = src.template piece<V::NW>(2 * t + 8, at), r3 = src.template piece<V::NW>(2 * t + 9, at);
+        const Words<V::NW> r0 = ld_words<V::NW>(a0 + 128 * j), r1 = ld_words<V::NW>(a1 + 128 * j);
+        const Words<V::NW> r2 = ld_words<V::NW>(a0 + 128 * j + 8 * V::RB), r3 = ld_words<V::NW>(a1 + 128 * j + 8 * V::RB);
         uint32_t d01 = 0, d23 = 0;
         if constexpr (PF != PF_16) {
-            const int blk = V::CH * (g + 8 * j) / 32;
-            d01 = src.scale(2 * t, blk) | (src.scale(2 * t + 1, blk) << 16);
-            d23 = src.scale(2 * t + 8, blk) | (src.scale(2 * t + 9, blk) << 16);
+            const uint32_t x = sc + V::CH * j / 2;
+            d01 = __byte_perm(ld_half(x), ld_half(x + D / 16), 0x5410);
+            d23 = __byte_perm(ld_half(x + 8 * (D / 16)), ld_half(x + 9 * (D / 16)), 0x5410);
         }
 #pragma unroll
         for (int i = 0; i < V::NW; ++i) {
@@ -213,36 +255,6 @@ __device__ __forceinline__ void load_queries(const ROW& rows, int g, int t, uint
         }
     }
 }
-
-// A tile staged in shared memory: 16 code rows of RB bytes, then (block formats) the rows' scales. The
-// 16-byte pieces of a 128-byte line are permuted by row so that the eight lanes of a load phase (K:
-// two rows, four neighbouring pieces; V: rows 0, 2, 4, 6, two neighbouring pieces) hit all banks.
-template <int RB, bool VALUES> __device__ __forceinline__ uint32_t tile_swizzle(uint32_t byte) {
-    const uint32_t row = byte / RB;
-    if (VALUES) return byte ^ (RB >= 64 ? ((row >> 1) & 3) << 5 : ((row >> 2) & 1) << 5);
-    return RB >= 128 ? byte ^ ((row & 1) << 6) : byte;
-}
-
-template <int D, int PF, bool VALUES> struct SharedTile {
-    static constexpr int RB = KGeo<D, PF>::RB;
-    uint32_t base;
-    template <int N> __device__ __forceinline__ Words<N> piece(int row, int byte) const {
-        Words<N> w;
-        const uint32_t a = base + tile_swizzle<RB, VALUES>(row * RB + byte);
-        if constexpr (N == 4)
-            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n" : "=r"(w.w[0]), "=r"(w.w[1]), "=r"(w.w[2]), "=r"(w.w[3]) : "r"(a));
-        else if constexpr (N == 2)
-            asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];\n" : "=r"(w.w[0]), "=r"(w.w[1]) : "r"(a));
-        else
-            asm volatile("ld.shared.u32 %0, [%1];\n" : "=r"(w.w[0]) : "r"(a));
-        return w;
-    }
-    __device__ __forceinline__ uint32_t scale(int row, int blk) const {
-        uint16_t x;
-        asm volatile("ld.shared.u16 %0, [%1];\n" : "=h"(x) : "r"(base + 16 * RB + row * (D / 16) + 2 * blk));
-        return x;
-    }
-};
 
 template <int D, int PF> constexpr int tile_bytes() { return 16 * KGeo<D, PF>::RB + (PF == PF_16 ? 0 : D); }
 
