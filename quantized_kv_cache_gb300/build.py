@@ -31,7 +31,9 @@ UNITS = {
     "synth.cu": [],
     "paged_api.cpp": [],
     "kernels_paged_rows.cu": [],
-    "kernels_paged_decode.cu": [],
+    "kernels_paged_decode.cu:64": ["-DKVQ_D=64"],
+    "kernels_paged_decode.cu:128": ["-DKVQ_D=128"],
+    "kernels_paged_decode.cu:256": ["-DKVQ_D=256"],
     "kernels_paged_prefill.cu": [],
 }
 
@@ -64,8 +66,9 @@ def build(force=False, verbose=False, ptxas_info=False):
     extra = ["-Xptxas", "-v"] if ptxas_info else []
 
     def one(item):
-        src, flags = item
-        obj = os.path.join(BUILD_DIR, src + ".o")
+        unit, flags = item                     # source file, or "source file:name" where one is compiled several times
+        src = unit.split(":")[0]
+        obj = os.path.join(BUILD_DIR, unit.replace(":", "_") + ".o")
         lang = ["-x", "cu"] if src.endswith(".cu") else ["-x", "c++"]
         cmd = [cc] + lang + COMMON + ARCH + flags + extra + ["-c", os.path.join(CSRC, src), "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)

@@ -56,26 +56,25 @@ __device__ __forceinline__ int64_t run_tiles(int64_t total, int n_cta) {
     return u < kMinTiles ? kMinTiles : u;
 }
 
-KVQ_HD int64_t partial_floats(int G, int D) { return 32 + (int64_t)G * D; }
-
 // Each warp stages its tiles through a ring of its own in shared memory, K and V tiles in turn, NS slots
-// with NS - 1 copies in flight (cp.async; no barrier but the warp's). The budget leaves three CTAs to an SM
-// (two at D = 256, where registers allow no more).
-template <int D, int KF, int VF> struct Ring {
+// with NS - 1 copies in flight (cp.async; no barrier but the warp's). Rows of codes keep the warps busy with decoding, so
+// there a third (D = 256) or fourth CTA an SM is worth more than deeper rings; 16-bit rows want the bytes in flight.
+template <int D, int KF, int VF, int NQ> struct Ring {
+    static constexpr int ctas = (D == 256 ? 2 : 3) + (KF != PF_16 && NQ == 1 ? 1 : 0);   // per SM
     static constexpr int kb = tile_bytes<D, KF>(), vb = tile_bytes<D, VF>();
     static constexpr int slot = kb > vb ? kb : vb;
-    static constexpr int budget = (D == 256 ? 112 : 74) * 1024 / kDW;
+    static constexpr int budget = (226 / ctas - 2) * 1024 / kDW;
     static constexpr int fit = budget / slot;
     static constexpr int NS = fit > 8 ? 8 : fit;
-    static constexpr int join = 16 * D * 4 * kDW;          // the warps' outputs at a head's end
+    static constexpr int join = 8 * NQ * D * 4 * kDW;      // the warps' outputs at a head's end
     static constexpr int bytes = NS * slot * kDW > join ? NS * slot * kDW : join;
     static_assert(NS >= 3, "a tile of each kind in flight beside the one in use");
 };
 
-template <int D, int KF, int VF, typename T, typename TQ>
-__global__ void __launch_bounds__(kDT, D == 256 ? 2 : 3) decode_kernel(PagedAttnParams p) {
+template <int D, int KF, int VF, int NQ, typename T, typename TQ>
+__global__ void __launch_bounds__(kDT, (Ring<D, KF, VF, NQ>::ctas)) decode_kernel(PagedAttnParams p) {
     constexpr bool LO = std::is_same<T, __nv_bfloat16>::value;   // P in two bf16 parts: 16 bits of it
-    using R = Ring<D, KF, VF>;
+    using R = Ring<D, KF, VF, NQ>;
     extern __shared__ __align__(128) float smem[];               // the rings; [kDW][G][D] outputs at a head's end
     __shared__ float s_m[kDW][16], s_l[kDW][16];
     __shared__ int64_t red[kDW];
@@ -181,78 +180,89 @@ __global__ void __launch_bounds__(kDT, D == 256 ? 2 : 3) decode_kernel(PagedAttn
         };
 
         const TQ* q = (const TQ*)p.q + b * p.q_stride + (int64_t)h * G * D;
-        uint32_t qf[D / 16][4];
-        float back[2], slope[2], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[D / 8][4] = {};
-        load_queries<D, KF, T, TQ>([&](int r) { return r < G ? q + r * D : (const TQ*)nullptr; }, g, t, qf, back);
+        // by query group and the lane's two queries in it (8 q + 2 t, 8 q + 2 t + 1)
+        uint32_t qf[D / 16][NQ][2];
+        float f[NQ][2], slope[NQ][2], m[NQ][2], l[NQ][2] = {}, o[D / 16][NQ][4] = {}, back[NQ];
+        load_queries<D, KF, NQ, T, TQ>([&](int r) { return r < G ? q + r * D : (const TQ*)nullptr; }, g, t, qf, back);
 #pragma unroll
-        for (int k = 0; k < 2; ++k) back[k] = rule.factor(back[k]);
+        for (int k = 0; k < NQ; ++k)
 #pragma unroll
-        for (int k = 0; k < 2; ++k) slope[k] = p.slopes && g + 8 * k < G ? p.slopes[h * G + g + 8 * k] * kL2e : 0.f;
+            for (int e = 0; e < 2; ++e) {
+                const int r = 8 * k + 2 * t + e;
+                f[k][e] = rule.factor(__shfl_sync(kAll, back[k], 4 * (2 * t + e)));
+                slope[k][e] = p.slopes && r < G ? p.slopes[h * G + r] * kL2e : 0.f;
+                m[k][e] = -INFINITY;
+            }
 
         for (int i = 0; i < nt; ++i) {
             const int p0 = st.tile(i * kDW + i0 + warp) * kTile;
             const uint32_t k_tile = take();
             copy_next();
-            float s[2][4] = {};
-            tile_scores<D, KF, T>(k_tile, place, qf, s);
+            float s[NQ][4] = {};                                  // (position g, g + 8) x (query 2t, 2t + 1)
+            tile_scores<D, KF, NQ, T>(k_tile, place, qf, s);
             const bool all = p0 + kTile <= st.len && (p0 >= st.lo || p0 + kTile <= st.pre);
             unsigned see = 0xffffu;
             if (!all) see = __ballot_sync(kAll, lane < 16 && st.sees(p0 + lane));
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
+            for (int k = 0; k < NQ; ++k)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) s[n][c] *= back[c >> 1];
+                for (int c = 0; c < 4; ++c) s[k][c] *= f[k][c & 1];
             if (!plain) {
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
+                for (int k = 0; k < NQ; ++k)
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        if (c < 2 || G > 8) s[n][c] = rule(s[n][c], st.len - 1 - p0 - (8 * n + 2 * t + (c & 1)), slope[c >> 1]);
+                    for (int c = 0; c < 4; ++c) s[k][c] = rule(s[k][c], st.len - 1 - p0 - (g + 8 * (c >> 1)), slope[k][c & 1]);
             }
             if (!all) {
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
+                for (int k = 0; k < NQ; ++k)
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
-                        if (!((see >> (8 * n + 2 * t + (c & 1))) & 1)) s[n][c] = -INFINITY;
+                        if (!((see >> (g + 8 * (c >> 1))) & 1)) s[k][c] = -INFINITY;
             }
-            float mx[2];
+            float base[NQ][2], a[NQ][2];
+            bool moved = false;
 #pragma unroll
-            for (int k = 0; k < 2; ++k) mx[k] = fmaxf(fmaxf(s[0][2 * k], s[0][2 * k + 1]), fmaxf(s[1][2 * k], s[1][2 * k + 1]));
-            float base[2] = {0.f, 0.f}, a[2] = {1.f, 1.f};
+            for (int k = 0; k < NQ; ++k)
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                if (k == 1 && G <= 8) continue;
-                mx[k] = fmaxf(mx[k], __shfl_xor_sync(kAll, mx[k], 1));
-                mx[k] = fmaxf(mx[k], __shfl_xor_sync(kAll, mx[k], 2));
-                const float mn = fmaxf(m[k], mx[k]);
-                base[k] = mn == -INFINITY ? 0.f : mn;
-                a[k] = m[k] == mn ? 1.f : ex2(m[k] - base[k]);
-                m[k] = mn;
-            }
-            if (__any_sync(kAll, a[0] != 1.f || a[1] != 1.f)) {
-                l[0] *= a[0];
-                l[1] *= a[1];
-#pragma unroll
-                for (int d = 0; d < D / 8; ++d) {
-                    o[d][0] *= a[0];
-                    o[d][1] *= a[0];
-                    o[d][2] *= a[1];
-                    o[d][3] *= a[1];
+                for (int e = 0; e < 2; ++e) {
+                    float mx = fmaxf(s[k][e], s[k][2 + e]);
+                    mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 4));
+                    mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 8));
+                    mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 16));
+                    const float mn = fmaxf(m[k][e], mx);
+                    base[k][e] = mn == -INFINITY ? 0.f : mn;
+                    moved |= m[k][e] != mn;
+                    a[k][e] = m[k][e];
+                    m[k][e] = mn;
                 }
+            if (__any_sync(kAll, moved)) {
+#pragma unroll
+                for (int k = 0; k < NQ; ++k)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        a[k][e] = a[k][e] == m[k][e] ? 1.f : ex2(a[k][e] - base[k][e]);
+                        l[k][e] *= a[k][e];
+#pragma unroll
+                        for (int d = 0; d < D / 16; ++d) {
+                            o[d][k][e] *= a[k][e];
+                            o[d][k][2 + e] *= a[k][e];
+                        }
+                    }
             }
-            uint32_t pa[4] = {}, pl[4] = {};
+            uint32_t pb[NQ][2], lo[NQ][2] = {};
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
+            for (int k = 0; k < NQ; ++k)
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    if (k == 1 && G <= 8) continue;
-                    const float x = ex2(s[n][2 * k] - base[k]), y = ex2(s[n][2 * k + 1] - base[k]);
-                    l[k] += x + y;
-                    pa[2 * n + k] = Two<T>::pack(x, y);
+                for (int n = 0; n < 2; ++n) {
+                    const float x = ex2(s[k][2 * n] - base[k][0]), y = ex2(s[k][2 * n + 1] - base[k][1]);
+                    l[k][0] += x;
+                    l[k][1] += y;
+                    const uint32_t w = Two<T>::pack(x, y);
+                    pb[k][n] = transpose8(w);
                     if constexpr (LO) {
-                        const float2 hi = Two<T>::unpack(pa[2 * n + k]);
-                        pl[2 * n + k] = Two<T>::pack(x - hi.x, y - hi.y);
+                        const float2 hi = Two<T>::unpack(w);
+                        lo[k][n] = transpose8(Two<T>::pack(x - hi.x, y - hi.y));
                     }
                 }
             const uint32_t v_tile = take();
@@ -261,39 +271,41 @@ __global__ void __launch_bounds__(kDT, D == 256 ? 2 : 3) decode_kernel(PagedAttn
                 clear_rows<D, VF>(v_tile, see, lane);
                 __syncwarp();
             }
-            tile_values<D, VF, T, LO>(v_tile, place, pa, pl, o);
+            tile_values<D, VF, NQ, T, LO>(v_tile, place, pb, lo, o);
         }
         cp_wait<0>();
         __syncthreads();                                          // the rings become the join's space
 
         // join the warps: rows' maxima and sums, then the outputs rescaled to the common maximum
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            l[k] += __shfl_xor_sync(kAll, l[k], 1);
-            l[k] += __shfl_xor_sync(kAll, l[k], 2);
-            if (t == 0) {
-                s_m[warp][g + 8 * k] = m[k];
-                s_l[warp][g + 8 * k] = l[k];
+        for (int k = 0; k < NQ; ++k)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                l[k][e] += __shfl_xor_sync(kAll, l[k][e], 4);
+                l[k][e] += __shfl_xor_sync(kAll, l[k][e], 8);
+                l[k][e] += __shfl_xor_sync(kAll, l[k][e], 16);
+                if (g == 0) {
+                    s_m[warp][8 * k + 2 * t + e] = m[k][e];
+                    s_l[warp][8 * k + 2 * t + e] = l[k][e];
+                }
             }
-        }
         __syncthreads();
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int r = g + 8 * k;
-            if (r >= G) continue;
-            float mm = -INFINITY;
-            for (int w = 0; w < kDW; ++w) mm = fmaxf(mm, s_m[w][r]);
-            const float a = mm == -INFINITY ? 0.f : ex2(m[k] - mm);
-            float* dst = smem + ((int64_t)warp * G + r) * D;
-            using V = VGeo<D, VF>;
+        for (int k = 0; k < NQ; ++k)
 #pragma unroll
-            for (int j = 0; j < V::NJ; ++j)
+            for (int e = 0; e < 2; ++e) {
+                const int r = 8 * k + 2 * t + e;
+                if (r >= G) continue;
+                float mm = -INFINITY;
+                for (int w = 0; w < kDW; ++w) mm = fmaxf(mm, s_m[w][r]);
+                const float a = mm == -INFINITY ? 0.f : ex2(m[k][e] - mm);
+                float* dst = smem + ((int64_t)warp * G + r) * D;
+                using V = VGeo<D, VF>;
 #pragma unroll
-                for (int c = 0; c < V::CH; ++c) {
-                    dst[ochan<D, VF>(j, 2 * t) + c] = o[V::CH * j + c][2 * k] * a;
-                    dst[ochan<D, VF>(j, 2 * t + 1) + c] = o[V::CH * j + c][2 * k + 1] * a;
-                }
-        }
+                for (int j = 0; j < V::NJ; ++j)
+#pragma unroll
+                    for (int c = 0; c < V::CH; ++c) dst[ochan<D, VF>(j, g) + c] = o[(V::CH * j + c) / 2][k][2 * (c & 1) + e] * a;
+            }
         __syncthreads();
         const bool whole = i0 == 0 && i1 == st.n;
         float* part = p.ws + ((int64_t)blockIdx.x + (int64_t)b * H + h) * partial_floats(G, D);
@@ -411,44 +423,40 @@ __global__ void __launch_bounds__(kMT) merge_kernel(PagedAttnParams p) {
     }
 }
 
-template <int D, int KF, int VF, typename T, typename TQ>
+template <int KF, int VF, int NQ, typename T, typename TQ>
 int decode_run(const PagedAttnParams& p, int sm_count, cudaStream_t s) {
     PagedAttnParams a = p;
-    using R = Ring<D, KF, VF>;
-    const auto k = decode_kernel<D, KF, VF, T, TQ>;
+    using R = Ring<KVQ_D, KF, VF, NQ>;
+    const auto k = decode_kernel<KVQ_D, KF, VF, NQ, T, TQ>;
     int res = 0;
     if (const int e = resident_ctas((const void*)k, kDT, R::bytes, &res)) return e;
     a.n_cta = min(kMaxDecodeCtas, sm_count * res);
     cudaError_t e = launch_k(k, dim3(a.n_cta), dim3(kDT), R::bytes, s, true, a);
-    if (e == cudaSuccess) e = launch_k(merge_kernel<D, TQ>, dim3((unsigned)p.n_seq * p.Hq), dim3(kMT), 0, s, true, a);
+    if (e == cudaSuccess) e = launch_k(merge_kernel<KVQ_D, TQ>, dim3((unsigned)p.n_seq * p.Hq), dim3(kMT), 0, s, true, a);
     return (int)e;
 }
-
-template <int D> int decode_d(const PagedAttnParams& p, int sms, cudaStream_t s) {
-    const int kf = p.v.fmt[0], vf = p.v.fmt[1];
-    if (kf == KVQ_F16) return decode_run<D, PF_16, PF_16, __half, __half>(p, sms, s);
-    if (kf == KVQ_BF16) return decode_run<D, PF_16, PF_16, __nv_bfloat16, __nv_bfloat16>(p, sms, s);
-    if (p.dtype == KVQ_F16) {
-        if (kf == KVQ_Q4_0) return decode_run<D, PF_Q4, PF_Q4, __half, __half>(p, sms, s);
-        if (vf == KVQ_Q4_0) return decode_run<D, PF_Q8, PF_Q4, __half, __half>(p, sms, s);
-        return decode_run<D, PF_Q8, PF_Q8, __half, __half>(p, sms, s);
-    }
-    if (kf == KVQ_Q4_0) return decode_run<D, PF_Q4, PF_Q4, __half, __nv_bfloat16>(p, sms, s);
-    if (vf == KVQ_Q4_0) return decode_run<D, PF_Q8, PF_Q4, __half, __nv_bfloat16>(p, sms, s);
-    return decode_run<D, PF_Q8, PF_Q8, __half, __nv_bfloat16>(p, sms, s);
+template <int KF, int VF, typename T, typename TQ> int decode_g(const PagedAttnParams& p, int sms, cudaStream_t s) {
+    return p.G <= 8 ? decode_run<KF, VF, 1, T, TQ>(p, sms, s) : decode_run<KF, VF, 2, T, TQ>(p, sms, s);
 }
 
 }  // namespace
 
-size_t paged_decode_ws_floats(int G, int D, int64_t segments) {
-    return (size_t)((kMaxDecodeCtas + segments) * partial_floats(G, D));
-}
-
-int launch_paged_decode(PagedAttnParams p, int sm_count, void* stream) {
+// One head dimension per compilation of this file (KVQ_D), so that they build side by side.
+#define KVQ_NAME2(d) launch_paged_decode_##d
+#define KVQ_NAME(d) KVQ_NAME2(d)
+int KVQ_NAME(KVQ_D)(const PagedAttnParams& p, int sms, void* stream) {
     cudaStream_t s = (cudaStream_t)stream;
-    if (p.v.D == 64) return decode_d<64>(p, sm_count, s);
-    if (p.v.D == 128) return decode_d<128>(p, sm_count, s);
-    return decode_d<256>(p, sm_count, s);
+    const int kf = p.v.fmt[0], vf = p.v.fmt[1];
+    if (kf == KVQ_F16) return decode_g<PF_16, PF_16, __half, __half>(p, sms, s);
+    if (kf == KVQ_BF16) return decode_g<PF_16, PF_16, __nv_bfloat16, __nv_bfloat16>(p, sms, s);
+    if (p.dtype == KVQ_F16) {
+        if (kf == KVQ_Q4_0) return decode_g<PF_Q4, PF_Q4, __half, __half>(p, sms, s);
+        if (vf == KVQ_Q4_0) return decode_g<PF_Q8, PF_Q4, __half, __half>(p, sms, s);
+        return decode_g<PF_Q8, PF_Q8, __half, __half>(p, sms, s);
+    }
+    if (kf == KVQ_Q4_0) return decode_g<PF_Q4, PF_Q4, __half, __nv_bfloat16>(p, sms, s);
+    if (vf == KVQ_Q4_0) return decode_g<PF_Q8, PF_Q4, __half, __nv_bfloat16>(p, sms, s);
+    return decode_g<PF_Q8, PF_Q8, __half, __nv_bfloat16>(p, sms, s);
 }
 
 }  // namespace kvq

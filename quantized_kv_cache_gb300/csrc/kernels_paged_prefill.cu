@@ -221,19 +221,29 @@ __device__ __forceinline__ void weights32(const uint32_t (&x)[32], uint64_t f, u
     for (int e = 16 - A; e < 16; ++e) last(e);
 }
 
-// Raw scores of 32 positions from p0 on to scores in units of log2: the cap, then the bias.
+// Raw scores of 32 positions from p0 on to scores in units of log2: the cap, then the bias. Two scores an instruction;
+// where all capped ones are below 1/4 of the cap no exponential is taken (the odd series of tanh, five terms).
 __device__ __forceinline__ void apply_rule(uint32_t (&s)[32], const ScoreRule& rule, const RowState& r, int p0) {
+    const float2 f = make_float2(r.f, r.f);
     float big = 0.f;
 #pragma unroll
-    for (int e = 0; e < 32; ++e) {
-        const float x = __uint_as_float(s[e]) * r.f;
-        s[e] = __float_as_uint(x);
-        big = fmaxf(big, fabsf(x));
+    for (int e = 0; e < 32; e += 2) {
+        const float2 x = __fmul2_rn(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), f);
+        s[e] = __float_as_uint(x.x);
+        s[e + 1] = __float_as_uint(x.y);
+        big = max3(big, fabsf(x.x), fabsf(x.y));
     }
     if (rule.cap > 0.f) {
-        if (__all_sync(kAll, big < 0.25f)) {                   // no exponential where all of them are small
+        if (__all_sync(kAll, big < 0.25f)) {
+            const auto both = [&](float c) { return make_float2(c * rule.cap_l2, c * rule.cap_l2); };
+            const float2 c0 = both(1.f), c1 = both(-0.33333334f), c2 = both(0.13333333f), c3 = both(-0.053968254f), c4 = both(0.021869489f);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) s[e] = __float_as_uint(rule.cap_l2 * tanh_small(__uint_as_float(s[e])));
+            for (int e = 0; e < 32; e += 2) {
+                const float2 x = make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), q = __fmul2_rn(x, x);
+                const float2 y = __fmul2_rn(x, __ffma2_rn(q, __ffma2_rn(q, __ffma2_rn(q, __ffma2_rn(q, c4, c3), c2), c1), c0));
+                s[e] = __float_as_uint(y.x);
+                s[e + 1] = __float_as_uint(y.y);
+            }
         } else {
 #pragma unroll
             for (int e = 0; e < 32; ++e) s[e] = __float_as_uint(rule.cap_l2 * tanh_any(__uint_as_float(s[e])));

@@ -90,7 +90,7 @@ PagedView view(const kvq_paged* h, int layer) {
 
 size_t workspace_floats(const kvq_paged_config& c, int64_t seqs, int64_t rows) {
     const int G = c.n_q_heads / c.n_kv_heads;
-    const size_t a = paged_decode_ws_floats(G, c.head_dim, seqs * c.n_kv_heads);
+    const size_t a = (size_t)((kMaxDecodeCtas + seqs * c.n_kv_heads) * partial_floats(G, c.head_dim));
     const size_t b = paged_prefill_ws_floats(c.head_dim, rows * c.n_q_heads);
     return a > b ? a : b;
 }
@@ -300,7 +300,8 @@ kvq_status kv_paged_decode_attn(kvq_paged* h, int32_t layer, int32_t dtype, int3
     st = attn_params(h, layer, dtype, n_seq, 0, q, q_stride, page_table, max_pages, table_stride, lens, out, opts,
                      workspace, ws_bytes, &p);
     if (st != KVQ_OK) return st;
-    return launched(launch_paged_decode(p, h->sm_count, stream));
+    const auto launch = p.v.D == 64 ? launch_paged_decode_64 : (p.v.D == 128 ? launch_paged_decode_128 : launch_paged_decode_256);
+    return launched(launch(p, h->sm_count, stream));
 }
 
 kvq_status kv_paged_prefill_attn(kvq_paged* h, int32_t layer, int32_t dtype, int32_t n_seq, int32_t n_rows,

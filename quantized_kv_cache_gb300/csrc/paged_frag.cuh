@@ -1,17 +1,17 @@
-// Warp-level pieces of the paged attention kernels: page rows turned into mma.sync operands.
+// Warp-level pieces of the paged decode kernel: page rows turned into mma.sync operands.
 //
-// One warp holds 16 query rows (M of m16n8k16) against a tile of 16 positions of one page. Both
-// products take their operands from 16-byte pieces of the rows, in whatever order the lanes read
-// them: the channel order of the score product is free (the query fragments follow it), and so is
-// the channel order of the output tiles. With g = lane / 4, t = lane % 4:
-//  - scores, S[16 x 8 positions] = Q K^T: lane (g, t) reads pieces t, t + 4, .. of row g; each piece
+// One warp holds 8 NQ query rows (N of m16n8k16) against a tile of 16 positions of one page. Both products take
+// their operands from 16-byte pieces of the rows, in whatever order the lanes read them: the channel order of the
+// score product is free (the query fragments follow it), and so is the channel order of the output. With
+// g = lane / 4, t = lane % 4:
+//  - scores, S^T[16 positions x 8] = K Q^T: lane (g, t) reads pieces t, t + 4, .. of rows g and g + 8; each piece
 //    feeds k-steps whose channels qchan() names (eight consecutive ones for two steps);
-//  - values, O[16 x 8 channels] = P V: lane (g, t) reads pieces g, g + 8, .. of rows 2t, 2t+1, 2t+8,
-//    2t+9 and pairs the rows channel by channel (byte permutes); a piece's i-th channel is the
-//    lane's column of output tile i, so a lane ends with runs of consecutive output channels.
-// The accumulator layout of S is the A-operand layout of P, so no data crosses lanes but the row
-// maxima. Codes become exact fp16 integers (an exponent placed around the code bits, one subtract),
-// then code x scale is rounded to fp16 once.
+//  - values, O^T[16 channels x 8] = V^T P^T: lane (g, t) reads pieces g, g + 8, .. of rows 2t, 2t+1, 2t+8, 2t+9 and
+//    pairs the rows channel by channel (byte permutes); channels 2i and 2i + 1 of its piece are rows g and g + 8
+//    of a product, so a lane ends with runs of consecutive output channels of queries 2t and 2t + 1.
+// P^T comes from the accumulators of S^T by one 8 x 8 transposition per 8 positions. Codes become exact fp16
+// integers (an exponent placed around the code bits, one subtract), then code x scale is rounded to fp16 once.
+// Queries on N: a group of up to eight takes half of the products and of the registers that they would take on M.
 #pragma once
 #include <type_traits>
 #include "paged_common.cuh"
@@ -77,8 +77,8 @@ template <int D, int PF> __device__ __forceinline__ int qchan(int i, int t) {
     return CH * (t + 4 * (i / N)) + 8 * (i % N);
 }
 
-// First of the CH consecutive output channels that column `col` (0..7) has in piece j's tiles.
-template <int D, int PF> __device__ __forceinline__ int ochan(int j, int col) { return VGeo<D, PF>::CH * (col + 8 * j); }
+// First of the CH consecutive output channels of lane group g in piece j.
+template <int D, int PF> __device__ __forceinline__ int ochan(int j, int g) { return VGeo<D, PF>::CH * (g + 8 * j); }
 
 // Where a lane finds its pieces and scales in a tile, fixed over the tiles: a tile in shared memory is 16 code rows of RB
 // bytes, then (block formats) the rows' scales. The 16-byte pieces of a 128-byte line are permuted by row so
@@ -119,48 +119,53 @@ __device__ __forceinline__ uint32_t ld_half(uint32_t a) {
     return x;
 }
 
-// s[n] += q K^T of positions 8n .. 8n+7 of the tile at `base`.
-template <int D, int PF, typename T, typename PLACE>
-__device__ __forceinline__ void tile_scores(uint32_t base, const PLACE& at, const uint32_t (&qf)[D / 16][4], float (&s)[2][4]) {
+// s[q] += K Q^T of the tile at `base` and query group q.
+template <int D, int PF, int NQ, typename T, typename PLACE>
+__device__ __forceinline__ void tile_scores(uint32_t base, const PLACE& at, const uint32_t (&qf)[D / 16][NQ][2], float (&s)[NQ][4]) {
     using K = KGeo<D, PF>;
     static_assert(K::NJ == 1 || K::CB == 16, "pieces j and j + 2 are 128 bytes apart");
     const uint32_t even = base + at.k[0], odd = base + at.k[1], sc = base + at.ks;
+    const auto step = [&](int ks, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+        const uint32_t a[4] = {a0, a1, a2, a3};
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
+        for (int q = 0; q < NQ; ++q) mma_t(s[q], a, qf[ks][q][0], qf[ks][q][1], T());
+    };
 #pragma unroll
-        for (int j = 0; j < K::NJ; ++j) {
-            const Words<K::NW> p = ld_words<K::NW>((j & 1 ? odd : even) + j / 2 * 128 + 8 * n * K::RB);
-            constexpr int KS = K::CH / 4;
-            if constexpr (PF == PF_16) {
-                mma_t(s[n], qf[KS * j], p.w[0], p.w[1], T());
-                mma_t(s[n], qf[KS * j + 1], p.w[2], p.w[3], T());
-            } else {
-                const uint32_t d1 = ld_half(sc + 8 * n * (D / 16) + K::CH * j / 4), d = __byte_perm(d1, d1, 0x1010);
+    for (int j = 0; j < K::NJ; ++j) {
+        const uint32_t a = (j & 1 ? odd : even) + j / 2 * 128;
+        const Words<K::NW> x = ld_words<K::NW>(a), y = ld_words<K::NW>(a + 8 * K::RB);     // rows g, g + 8
+        constexpr int KS = K::CH / 4;
+        if constexpr (PF == PF_16) {
+            step(KS * j, x.w[0], y.w[0], x.w[1], y.w[1]);
+            step(KS * j + 1, x.w[2], y.w[2], x.w[3], y.w[3]);
+        } else {
+            const uint32_t d1 = ld_half(sc + K::CH * j / 4), e1 = ld_half(sc + 8 * (D / 16) + K::CH * j / 4);
+            const uint32_t d = __byte_perm(d1, d1, 0x1010), e = __byte_perm(e1, e1, 0x1010);
 #pragma unroll
-                for (int i = 0; i < K::NW; ++i) {
-                    if constexpr (PF == PF_Q8) {
-                        const uint32_t x = p.w[i] ^ 0x80808080u;               // 1024 + 128 + b by an exponent byte
-                        mma_t(s[n], qf[KS * j + i], deq(__byte_perm(x, 0x64646464u, 0x4140), 1152.f, d),
-                              deq(__byte_perm(x, 0x64646464u, 0x4342), 1152.f, d), T());
-                    } else {
-                        uint32_t o[4];
-                        nib_pairs(p.w[i], d, o);                               // (n0, n4), (n1, n5), (n2, n6), (n3, n7)
-                        mma_t(s[n], qf[KS * j + 2 * i], o[0], o[1], T());
-                        mma_t(s[n], qf[KS * j + 2 * i + 1], o[2], o[3], T());
-                    }
+            for (int i = 0; i < K::NW; ++i) {
+                if constexpr (PF == PF_Q8) {
+                    const uint32_t u = x.w[i] ^ 0x80808080u, v = y.w[i] ^ 0x80808080u;     // 1024 + 128 + b by an exponent byte
+                    step(KS * j + i, deq(__byte_perm(u, 0x64646464u, 0x4140), 1152.f, d), deq(__byte_perm(v, 0x64646464u, 0x4140), 1152.f, e),
+                         deq(__byte_perm(u, 0x64646464u, 0x4342), 1152.f, d), deq(__byte_perm(v, 0x64646464u, 0x4342), 1152.f, e));
+                } else {
+                    uint32_t o[4], r[4];                                   // (n0, n4), (n1, n5), (n2, n6), (n3, n7)
+                    nib_pairs(x.w[i], d, o);
+                    nib_pairs(y.w[i], e, r);
+                    step(KS * j + 2 * i, o[0], r[0], o[1], r[1]);
+                    step(KS * j + 2 * i + 1, o[2], r[2], o[3], r[3]);
                 }
             }
         }
     }
 }
 
-// o += P V of the tile's 16 positions. With LO, P = pa + pl (two bf16 parts).
-template <int D, int PF, typename T, bool LO, typename PLACE>
-__device__ __forceinline__ void tile_values(uint32_t base, const PLACE& at, const uint32_t (&pa)[4], const uint32_t (&pl)[4],
-                                            float (&o)[D / 8][4]) {
+// o += V^T P^T of the tile's 16 positions. With LO, P = p + lo (two bf16 parts).
+template <int D, int PF, int NQ, typename T, bool LO, typename PLACE>
+__device__ __forceinline__ void tile_values(uint32_t base, const PLACE& at, const uint32_t (&p)[NQ][2], const uint32_t (&lo)[NQ][2],
+                                            float (&o)[D / 16][NQ][4]) {
     using V = VGeo<D, PF>;
     static_assert(V::NJ == 1 || V::CB == 16, "pieces j and j + 1 are 128 bytes apart");
-    // rows 2t + 8 and 2t + 9: the same permutation (that of 32-byte rows too: four lines on)
+    // rows 2t + 8 and 2t + 9: the same permutation (that of 32-byte rows too: two lines on)
     const uint32_t a0 = base + at.v[0], a1 = base + at.v[1], sc = base + at.vs;
 #pragma unroll
     for (int j = 0; j < V::NJ; ++j) {
@@ -192,26 +197,29 @@ __device__ __forceinline__ void tile_values(uint32_t base, const PLACE& at, cons
                 nib_pairs(yh, d23, *(uint32_t(*)[4])&b1[4]);
             }
 #pragma unroll
-            for (int c = 0; c < N; ++c) {
-                float (&acc)[4] = o[V::CH * j + N * i + c];
-                mma_t(acc, pa, b0[c], b1[c], T());
-                if constexpr (LO) mma_t(acc, pl, b0[c], b1[c], T());
+            for (int c = 0; c < N; c += 2) {
+                const uint32_t a[4] = {b0[c], b0[c + 1], b1[c], b1[c + 1]};
+#pragma unroll
+                for (int q = 0; q < NQ; ++q) {
+                    float (&acc)[4] = o[(V::CH * j + N * i + c) / 2][q];
+                    mma_t(acc, a, p[q][0], p[q][1], T());
+                    if constexpr (LO) mma_t(acc, a, lo[q][0], lo[q][1], T());
+                }
             }
         }
     }
 }
 
-// Query fragments of the 16 rows of a warp; row r is at base + rows(r) (null: a row of zeros), of
-// type TQ. fp16 operands of bf16 queries are scaled by a power of two per row so that no exponent
-// is out of range; back[] undoes it (rows g, g + 8).
-template <int D, int PF, typename T, typename TQ, typename ROW>
-__device__ __forceinline__ void load_queries(const ROW& rows, int g, int t, uint32_t (&qf)[D / 16][4], float (&back)[2]) {
+// Query fragments of a warp's 8 NQ rows; row r is at rows(r) (null: a row of zeros), of type TQ. fp16 operands of bf16
+// queries are scaled by a power of two per row so that no exponent is out of range; back[] undoes it (of row g + 8q).
+template <int D, int PF, int NQ, typename T, typename TQ, typename ROW>
+__device__ __forceinline__ void load_queries(const ROW& rows, int g, int t, uint32_t (&qf)[D / 16][NQ][2], float (&back)[NQ]) {
     constexpr bool same = std::is_same<T, TQ>::value;
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-        const TQ* p = rows(g + 8 * half);
+    for (int q = 0; q < NQ; ++q) {
+        const TQ* p = rows(g + 8 * q);
         float up = 1.f;
-        back[half] = 1.f;
+        back[q] = 1.f;
         if constexpr (!same) {
             float a = 0.f;
             if (p) {
@@ -229,7 +237,7 @@ __device__ __forceinline__ void load_queries(const ROW& rows, int g, int t, uint
             if (a > 0.f && ex < 128) {
                 const int sh = min(max(14 - ex, -100), 100);         // the largest magnitude to [2^14, 2^15)
                 up = __uint_as_float((uint32_t)(127 + sh) << 23);
-                back[half] = __uint_as_float((uint32_t)(127 - sh) << 23);
+                back[q] = __uint_as_float((uint32_t)(127 - sh) << 23);
             }
         }
 #pragma unroll
@@ -248,12 +256,18 @@ __device__ __forceinline__ void load_queries(const ROW& rows, int g, int t, uint
             if constexpr (PF == PF_Q4)
                 x = make_uint4(__byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632), __byte_perm(x.y, x.w, 0x5410),
                                __byte_perm(x.y, x.w, 0x7632));
-            qf[2 * i][half] = x.x;
-            qf[2 * i][2 + half] = x.y;
-            qf[2 * i + 1][half] = x.z;
-            qf[2 * i + 1][2 + half] = x.w;
+            qf[2 * i][q][0] = x.x;
+            qf[2 * i][q][1] = x.y;
+            qf[2 * i + 1][q][0] = x.z;
+            qf[2 * i + 1][q][1] = x.w;
         }
     }
+}
+
+__device__ __forceinline__ uint32_t transpose8(uint32_t a) {
+    uint32_t d;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(d) : "r"(a));
+    return d;
 }
 
 template <int D, int PF> constexpr int tile_bytes() { return 16 * KGeo<D, PF>::RB + (PF == PF_16 ? 0 : D); }

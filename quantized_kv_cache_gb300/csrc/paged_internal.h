@@ -70,12 +70,15 @@ int resident_ctas(const void* kernel, int threads, int smem, int* ctas);
 int launch_norm_rope(const kvq_norm_rope_args& a, int sm_count, void* stream);
 int launch_paged_write(const WriteParams& p, void* stream);
 int launch_paged_read(const ReadParams& p, void* stream);
-int launch_paged_decode(PagedAttnParams p, int sm_count, void* stream);
+int launch_paged_decode_64(const PagedAttnParams& p, int sm_count, void* stream);
+int launch_paged_decode_128(const PagedAttnParams& p, int sm_count, void* stream);
+int launch_paged_decode_256(const PagedAttnParams& p, int sm_count, void* stream);
 // maps: two CUtensorMap, the layer's K and V area as [units][page_size][head_dim] of 16-bit values in boxes of
 // prefill_box_rows rows x 64 (16-bit pages; read for no other format)
 int launch_paged_prefill(const PagedAttnParams& p, const void* maps, int sm_count, void* stream);
 int prefill_box_rows(int D, int ps);
-size_t paged_decode_ws_floats(int G, int D, int64_t segments);
+// A run's partial result of a head: 16 maxima, 16 sums, the outputs.
+KVQ_HD int64_t partial_floats(int G, int D) { return 32 + (int64_t)G * D; }
 size_t paged_prefill_ws_floats(int D, int64_t head_rows);   // query rows x query heads
 
 }  // namespace kvq
