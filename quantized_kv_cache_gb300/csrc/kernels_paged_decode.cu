@@ -37,20 +37,6 @@ __device__ __forceinline__ SeqTiles seq_tiles(const PagedAttnParams& p, int b) {
     return s;
 }
 
-// Tiles of all sequences before b0 and of all, by the whole block (`b0` any, `red` shared scratch).
-template <int T>
-__device__ __forceinline__ int64_t block_sum(int64_t x, int64_t* red) {
-#pragma unroll
-    for (int s = 16; s >= 1; s >>= 1) x += __shfl_xor_sync(kAll, x, s);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
-    __syncthreads();
-    int64_t y = 0;
-#pragma unroll
-    for (int i = 0; i < T / 32; ++i) y += red[i];
-    __syncthreads();
-    return y;
-}
-
 __device__ __forceinline__ int64_t run_tiles(int64_t total, int n_cta) {
     const int64_t u = (total + n_cta - 1) / n_cta;
     return u < kMinTiles ? kMinTiles : u;
@@ -110,6 +96,22 @@ __global__ void __launch_bounds__(kDT, (Ring<D, KF, VF, NQ>::ctas)) decode_kerne
     // a launch that leaves half of its CTAs without work lets the merge's start beside it (in a full one they would
     // take the place of its own)
     if (total <= p.n_cta / 2 * U) grid_dep_launch();
+    if (blockIdx.x == 0) {                                       // tiles before each sequence, for the merge
+        int64_t* line = (int64_t*)p.ws;
+        int64_t at = before;
+        for (int b = threadIdx.x * per; b < min(p.n_seq, (int)(threadIdx.x + 1) * per); ++b) {
+            line[b] = at;
+            at += (int64_t)seq_tiles(p, b).n * H;
+        }
+        if (threadIdx.x == 0) line[p.n_seq] = total;
+    }
+    for (int b = blockIdx.x; b < p.n_seq; b += gridDim.x) {      // sequences without a visible position give zeros
+        if (seq_tiles(p, b).n) continue;
+        uint32_t* out = reinterpret_cast<uint32_t*>((TQ*)p.out + (int64_t)b * p.Hq * D);
+        for (int e = threadIdx.x; e < p.Hq * D / 2; e += kDT) out[e] = 0;
+        if (p.lse)
+            for (int e = threadIdx.x; e < p.Hq; e += kDT) p.lse[(int64_t)b * p.Hq + e] = -INFINITY;
+    }
     int64_t left = min(U, total - first);
     if (left <= 0) return;
     if (first >= before && first < before + mine) {
@@ -308,7 +310,7 @@ __global__ void __launch_bounds__(kDT, (Ring<D, KF, VF, NQ>::ctas)) decode_kerne
             }
         __syncthreads();
         const bool whole = i0 == 0 && i1 == st.n;
-        float* part = p.ws + ((int64_t)blockIdx.x + (int64_t)b * H + h) * partial_floats(G, D);
+        float* part = p.ws + line_floats(p.n_seq) + ((int64_t)blockIdx.x + (int64_t)b * H + h) * partial_floats(G, D);
         for (int e = threadIdx.x; e < G * D / 2; e += kDT) {
             const int r = 2 * e / D;
             float x = 0.f, y = 0.f;
@@ -343,37 +345,39 @@ __global__ void __launch_bounds__(kDT, (Ring<D, KF, VF, NQ>::ctas)) decode_kerne
     }
 }
 
-// One CTA per (sequence, query head): joins the runs' partials, and writes zeros for a head without tiles.
-// The runs' maxima and sums give one weight per run; then the CTA's thread groups take the runs in turn.
+// Joins the runs' partials of the heads that runs share: a CTA per (head, query of its group). Where there are more
+// heads than runs, the CTAs go by runs instead: at most one head is cut by the start of a run, and its first cut joins
+// it. The runs' maxima and sums give one weight per run; then the CTA's thread groups take the runs in turn.
 constexpr int kMT = 256;
 template <int D, typename TQ>
-__global__ void __launch_bounds__(kMT) merge_kernel(PagedAttnParams p) {
+__global__ void __launch_bounds__(kMT) merge_kernel(PagedAttnParams p, bool by_runs) {
     constexpr int L = D / 4, N = kMT / L;                // threads of an output row (four channels each); groups
-    __shared__ int64_t red[kMT / 32];
     __shared__ float s_w[kMaxDecodeCtas + 1], s_x[kMT / 32];
     __shared__ float4 s_o[N][L];
-    const int b = blockIdx.x / p.Hq, hq = blockIdx.x % p.Hq, h = hq / p.G, r = hq % p.G, H = p.v.H, G = p.G;
-    int64_t all = 0, before = 0;                         // the lengths: settled before the decode kernel lets this one start
-    for (int i = threadIdx.x; i < p.n_seq; i += kMT) {
-        const int64_t n = (int64_t)seq_tiles(p, i).n * H;
-        all += n;
-        if (i < b) before += n;
-    }
-    all = block_sum<kMT>(all, red);
-    before = block_sum<kMT>(before, red);
-    const int n = seq_tiles(p, b).n;
+    const int H = p.v.H, G = p.G, r = blockIdx.x % G, id = blockIdx.x / G;
     grid_dep_wait();
-    TQ* out = (TQ*)p.out + (int64_t)blockIdx.x * D;
-    if (n == 0) {
-        if (threadIdx.x < D / 2) reinterpret_cast<uint32_t*>(out)[threadIdx.x] = 0;
-        if (p.lse && threadIdx.x == 0) p.lse[blockIdx.x] = -INFINITY;
-        return;
+    const int64_t* line = (const int64_t*)p.ws;
+    const int64_t U = run_tiles(line[p.n_seq], p.n_cta);
+    int b = id / H, h = id % H;
+    if (by_runs) {
+        const int64_t at = (int64_t)id * U;
+        if (id == 0 || at >= line[p.n_seq]) return;
+        int lo = 0, hi = p.n_seq - 1;                    // the last sequence that starts at or before the run
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (line[mid] <= at) lo = mid; else hi = mid - 1;
+        }
+        b = lo;
+        h = (int)((at - line[b]) / ((line[b + 1] - line[b]) / H));
     }
-    const int64_t U = run_tiles(all, p.n_cta), s0 = before + (int64_t)h * n;
+    const int64_t n = (line[b + 1] - line[b]) / H, s0 = line[b] + (int64_t)h * n;
+    if (n == 0) return;
     const int c0 = (int)(s0 / U), nc = (int)((s0 + n - 1) / U) - c0 + 1;
-    if (nc == 1) return;
+    if (nc == 1 || (by_runs && (s0 == (int64_t)id * U || c0 != id - 1))) return;
+    const int64_t row = (int64_t)b * p.Hq + h * G + r;
+    TQ* out = (TQ*)p.out + row * D;
     const int64_t pf = partial_floats(G, D);
-    const float* part = p.ws + ((int64_t)b * H + h + c0) * pf;
+    const float* part = p.ws + line_floats(p.n_seq) + ((int64_t)b * H + h + c0) * pf;
     float m = -INFINITY, l = 0.f;
     for (int c = threadIdx.x; c < nc; c += kMT) m = fmaxf(m, s_w[c] = part[c * pf + r]);
 #pragma unroll
@@ -419,7 +423,7 @@ __global__ void __launch_bounds__(kMT) merge_kernel(PagedAttnParams p) {
         }
         const float inv = l > 0.f ? 1.f / l : 0.f;
         *reinterpret_cast<uint2*>(out + 4 * col) = make_uint2(Two<TQ>::pack(o.x * inv, o.y * inv), Two<TQ>::pack(o.z * inv, o.w * inv));
-        if (p.lse && col == 0) p.lse[blockIdx.x] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+        if (p.lse && col == 0) p.lse[row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
     }
 }
 
@@ -432,7 +436,10 @@ int decode_run(const PagedAttnParams& p, int sm_count, cudaStream_t s) {
     if (const int e = resident_ctas((const void*)k, kDT, R::bytes, &res)) return e;
     a.n_cta = min(kMaxDecodeCtas, sm_count * res);
     cudaError_t e = launch_k(k, dim3(a.n_cta), dim3(kDT), R::bytes, s, true, a);
-    if (e == cudaSuccess) e = launch_k(merge_kernel<KVQ_D, TQ>, dim3((unsigned)p.n_seq * p.Hq), dim3(kMT), 0, s, true, a);
+    const int64_t heads = (int64_t)p.n_seq * p.v.H;
+    const bool by_runs = heads > a.n_cta;
+    if (e == cudaSuccess)
+        e = launch_k(merge_kernel<KVQ_D, TQ>, dim3((unsigned)(by_runs ? a.n_cta : heads) * p.G), dim3(kMT), 0, s, true, a, by_runs);
     return (int)e;
 }
 template <int KF, int VF, typename T, typename TQ> int decode_g(const PagedAttnParams& p, int sms, cudaStream_t s) {

@@ -79,6 +79,8 @@ int launch_paged_prefill(const PagedAttnParams& p, const void* maps, int sm_coun
 int prefill_box_rows(int D, int ps);
 // A run's partial result of a head: 16 maxima, 16 sums, the outputs.
 KVQ_HD int64_t partial_floats(int G, int D) { return 32 + (int64_t)G * D; }
+// Before the partials: n_seq + 1 int64, the tiles before each sequence.
+KVQ_HD int64_t line_floats(int64_t n_seq) { return (2 * (n_seq + 1) + 3) & ~(int64_t)3; }
 size_t paged_prefill_ws_floats(int D, int64_t head_rows);   // query rows x query heads
 
 }  // namespace kvq

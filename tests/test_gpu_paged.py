@@ -215,6 +215,8 @@ def test_decode_ignores_what_no_query_sees():
 
 def test_decode_many_sequences_and_one_long():
     decode_case(("bf16", "bf16"), "bf16", 1, 2, 64, 16, [(7 * i) % 61 for i in range(300)], {})
+    # more heads than a launch has CTAs, some of them cut by a CTA's run, some empty
+    decode_case(("q8_0", "q8_0"), "bf16", 4, 2, 64, 16, [0] + [(37 * i) % 400 if i % 5 else 0 for i in range(600)] + [9000, 0], {})
     decode_case(("q8_0", "q8_0"), "f16", 1, 4, 128, 64, [30001], {})
 
 
