@@ -42,14 +42,16 @@ __device__ __forceinline__ int64_t run_tiles(int64_t total, int n_cta) {
     return u < kMinTiles ? kMinTiles : u;
 }
 
-// Each warp stages its tiles through a ring of its own in shared memory, K and V tiles in turn, NS slots
+// Each warp stages its tiles through a ring of its own in shared memory, K and V tiles in turn or together, NS slots
 // with NS - 1 copies in flight (cp.async; no barrier but the warp's). Rows of codes keep the warps busy with decoding, so
 // there a third (D = 256) or fourth CTA an SM is worth more than deeper rings; 16-bit rows want the bytes in flight.
 template <int D, int KF, int VF, int NQ> struct Ring {
     static constexpr int ctas = (D == 256 ? 2 : 3) + (KF != PF_16 && NQ == 1 ? 1 : 0);   // per SM
     static constexpr int kb = tile_bytes<D, KF>(), vb = tile_bytes<D, VF>();
-    static constexpr int slot = kb > vb ? kb : vb;
     static constexpr int budget = (226 / ctas - 2) * 1024 / kDW;
+    // K and V of a tile in one slot, copied and awaited together (half of the bookkeeping), where three such slots fit
+    static constexpr bool one = KF != PF_16 && budget / (kb + vb) >= 3;
+    static constexpr int slot = one ? kb + vb : (kb > vb ? kb : vb);
     static constexpr int fit = budget / slot;
     static constexpr int NS = fit > 8 ? 8 : fit;
     static constexpr int join = 8 * NQ * D * 4 * kDW;      // the warps' outputs at a head's end
@@ -141,13 +143,13 @@ __global__ void __launch_bounds__(kDT, (Ring<D, KF, VF, NQ>::ctas)) decode_kerne
         const int i1 = (int)min((int64_t)st.n, i0 + left);
         left -= i1 - i0;
         const int nt = (i1 - i0 - warp + kDW - 1) / kDW;          // this warp's tiles
-        // the copies run ahead: item 2i is K of the warp's tile i, item 2i + 1 its V
+        // the copies run ahead: item 2i is K of the warp's tile i, item 2i + 1 its V; with one slot for both, item i
         int pages = 0, unit_page = 0, unit_off = 0, put = 0, item = 0;
         auto copy_next = [&]() {
-            const int i = item >> 1;
+            const int i = R::one ? item : item >> 1;
             if (i < nt) {
                 const uint32_t dst = ring + put * R::slot;
-                if (!(item & 1)) {
+                if (R::one || !(item & 1)) {
                     if ((i & 31) == 0) {                         // the next 32 tiles' page numbers, one per lane
                         const int k = min(i + lane, nt - 1) * kDW + i0 + warp;
                         pages = p.table[b * p.table_stride + ((st.tile(k) * kTile) >> p.v.ps_shift)];
@@ -160,10 +162,12 @@ __global__ void __launch_bounds__(kDT, (Ring<D, KF, VF, NQ>::ctas)) decode_kerne
                     }
                     unit_page = __shfl_sync(kAll, pages, i & 31);
                     unit_off = (st.tile(i * kDW + i0 + warp) * kTile) & (p.v.ps - 1);
-                    copy_tile<D, KF, false>(dst, k_at, unit_page < 0 ? nullptr : p.v.base[0] + (uint64_t)(uint32_t)unit_page * (uint32_t)p.v.unit[0], p.v.ps, unit_off, lane);
-                } else {
-                    copy_tile<D, VF, true>(dst, v_at, unit_page < 0 ? nullptr : p.v.base[1] + (uint64_t)(uint32_t)unit_page * (uint32_t)p.v.unit[1], p.v.ps, unit_off, lane);
                 }
+                const auto unit = [&](int w) -> const uint8_t* {
+                    return unit_page < 0 ? nullptr : p.v.base[w] + (uint64_t)(uint32_t)unit_page * (uint32_t)p.v.unit[w];
+                };
+                if (R::one || !(item & 1)) copy_tile<D, KF, false>(dst, k_at, unit(0), p.v.ps, unit_off, lane);
+                if (R::one || (item & 1)) copy_tile<D, VF, true>(dst + (R::one ? R::kb : 0), v_at, unit(1), p.v.ps, unit_off, lane);
             }
             cp_commit();
             ++item;
@@ -267,8 +271,11 @@ __global__ void __launch_bounds__(kDT, (Ring<D, KF, VF, NQ>::ctas)) decode_kerne
                         lo[k][n] = transpose8(Two<T>::pack(x - hi.x, y - hi.y));
                     }
                 }
-            const uint32_t v_tile = take();
-            copy_next();
+            uint32_t v_tile = k_tile + R::kb;
+            if constexpr (!R::one) {
+                v_tile = take();
+                copy_next();
+            }
             if (!all) {
                 clear_rows<D, VF>(v_tile, see, lane);
                 __syncwarp();
