@@ -59,7 +59,7 @@ typedef struct kvq_paged kvq_paged;   /* opaque host-side handle */
 
 /* Options of the two attention calls; a null pointer in their place means none. Applied in this
  * order to the score s = scale <q, k_j> of the query at position i and position j:
- *   softcap > 0:  s = softcap * tanh(s / softcap)
+ *   softcap > 0:  s = softcap * tanh(s / softcap)          (at least 1e-30)
  *   slopes:       s = s - slopes[query head] * |i - j|        (device fp32 [n_q_heads])
  *   visibility:   j <= i, and j > i - window when window > 0; positions j < prefix[sequence] are
  *                 visible to every query, behind the window and after it too (device int32 [n_seq])
@@ -123,7 +123,7 @@ kvq_status kv_paged_decode_attn(kvq_paged* h, int32_t layer, int32_t dtype, int3
  * cu_q[b] .. cu_q[b+1] - 1 of q ([n_rows][n_q_heads][head_dim], stride q_stride) are the last
  * positions of sequence b, which holds lens[b] positions with the chunk (its rows already in the
  * pages). cu_q: device int32 [n_seq + 1], non-decreasing; max_q (host): at least the longest
- * chunk. Rows at a negative position (a chunk longer than lens[b]) see nothing: zeros. Rows of out
+ * chunk. n_seq up to 65,535, n_rows below 2^27, max_q up to 524,280. Rows at a negative position (a chunk longer than lens[b]) see nothing: zeros. Rows of out
  * and lse outside [cu_q[0], cu_q[n_seq]) stay as they are. Types, table and workspace as above. */
 kvq_status kv_paged_prefill_attn(kvq_paged* h, int32_t layer, int32_t dtype, int32_t n_seq, int32_t n_rows,
                                  int32_t max_q, const void* q, int64_t q_stride, const int32_t* cu_q,
@@ -132,7 +132,7 @@ kvq_status kv_paged_prefill_attn(kvq_paged* h, int32_t layer, int32_t dtype, int
                                  size_t ws_bytes, void* stream);
 
 /* Arguments of kv_qk_norm_rope. Outputs may be the inputs (in place, equal strides); otherwise they
- * must not overlap them. */
+ * must not overlap them. The rows of q and k are different rows (slices of one buffer, not the same slice). */
 typedef struct {
     int32_t dtype;             /* KVQ_F16 or KVQ_BF16: q, k, weights, outputs */
     int32_t n_tok;

@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 #include <cmath>
 #include <cstring>
+#include <exception>
 #include <map>
 #include <mutex>
 #include <new>
@@ -137,6 +138,7 @@ kvq_status attn_params(kvq_paged* h, int layer, int dtype, int n_seq, int64_t ro
     *p = PagedAttnParams{};
     if (opts) {
         if (!(opts->softcap >= 0.f) || !std::isfinite(opts->softcap) || opts->window < 0) return KVQ_EINVAL;
+        if (opts->softcap > 0.f && opts->softcap < 1e-30f) return KVQ_EINVAL;    // its reciprocal has to be finite
         if (!aligned4(opts->slopes) || !aligned4(opts->prefix) || !aligned4(opts->lse)) return KVQ_EINVAL;
         p->softcap = opts->softcap;
         p->window = opts->window;
@@ -166,7 +168,7 @@ kvq_status attn_params(kvq_paged* h, int layer, int dtype, int n_seq, int64_t ro
 
 namespace kvq {
 
-int resident_ctas(const void* kernel, int threads, int smem, int* ctas) {
+int resident_ctas(const void* kernel, int threads, int smem, int* ctas) try {
     static std::mutex mu;
     static std::map<std::pair<const void*, int>, int> known;
     int d = 0;
@@ -184,6 +186,8 @@ int resident_ctas(const void* kernel, int threads, int smem, int* ctas) {
     if (*ctas < 1) return (int)cudaErrorInvalidConfiguration;
     known[{kernel, d}] = *ctas;
     return 0;
+} catch (const std::exception&) {     // of the map or the mutex: none leaves the C ABI
+    return (int)cudaErrorMemoryAllocation;
 }
 
 }  // namespace kvq
@@ -314,8 +318,8 @@ kvq_status kv_paged_prefill_attn(kvq_paged* h, int32_t layer, int32_t dtype, int
     if (!dtype16(dtype) || n_seq < 0 || n_rows < 0 || max_q < 0) return KVQ_EINVAL;
     if (n_seq == 0 || n_rows == 0 || max_q == 0) return KVQ_OK;
     if (!cu_q || !aligned4(cu_q)) return KVQ_EINVAL;
-    // grid rows: one per sequence, one per 128 rows of the longest chunk; row counts stay below 2^31
-    if (n_seq > 65535 || (int64_t)(max_q < n_rows ? max_q : n_rows) * kMaxG > 65535 * (int64_t)128) return KVQ_EUNSUPPORTED;
+    // grid rows: one per sequence, one per 128 rows of the longest chunk; a head's row numbers stay below 2^31
+    if (n_seq > 65535 || (int64_t)n_rows * kMaxG >= (int64_t)1 << 31 || (int64_t)(max_q < n_rows ? max_q : n_rows) * kMaxG > 65535 * (int64_t)128) return KVQ_EUNSUPPORTED;
     PagedAttnParams p;
     st = attn_params(h, layer, dtype, n_seq, n_rows, q, q_stride, page_table, max_pages, table_stride, lens, out, opts,
                      workspace, ws_bytes, &p);

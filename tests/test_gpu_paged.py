@@ -528,6 +528,31 @@ def test_captured_step_follows_lengths_and_slots():
         assert torch.equal(out, want)
 
 
+def test_captured_chunk_follows_its_offsets():
+    """A chunk's attention captured once and replayed with other chunk bounds, lengths and queries."""
+    for fmt, dtype in ((("bf16", "bf16"), "bf16"), (("q8_0", "q8_0"), "f16")):
+        p = Pages(2, 128, 32, 40, *fmt, Hq=6, max_seqs=2, max_tokens=300, seed=3)
+        table, _, _ = pc.fill(p, 0, [600, 333], 4, dtype)
+        cu, lens = ints([0, 100, 300]), ints([600, 333])
+        q = torch.randn((300, 6, 128), generator=torch.Generator().manual_seed(0)).to(DT[dtype]).cuda()
+        out, lse = torch.empty_like(q), torch.empty((300, 6), device="cuda")
+        g, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        with torch.cuda.stream(side):
+            p.cache.prefill_attn(0, q, cu, 300, table, lens, out, lse=lse, stream=stream())
+            side.synchronize()
+            with torch.cuda.graph(g, stream=side):
+                p.cache.prefill_attn(0, q, cu, 300, table, lens, out, lse=lse, stream=stream())
+        for i, (c, n) in enumerate((([0, 100, 300], [600, 333]), ([0, 299, 300], [299, 20]), ([0, 0, 7], [600, 7]))):
+            cu.copy_(ints(c))
+            lens.copy_(ints(n))
+            q.copy_(torch.randn(q.shape, generator=torch.Generator().manual_seed(i)).to(DT[dtype]).cuda())
+            g.replay()
+            want, want_lse = torch.empty_like(q), torch.empty_like(lse)
+            p.cache.prefill_attn(0, q, cu, 300, table, lens, want, lse=want_lse)
+            torch.cuda.synchronize()
+            assert torch.equal(out[:c[2]], want[:c[2]]) and torch.equal(lse[:c[2]], want_lse[:c[2]])
+
+
 def test_two_streams_with_workspaces_of_their_own():
     p, table, q, out, _ = decode_case(("f16", "f16"), "f16", 2, 4, 128, 32, [3000, 20, 700], {})
     lens = ints([3000, 20, 700])
@@ -599,7 +624,14 @@ def test_refusals():
         (1, lambda: c.decode_attn(-1, q, table, lens, out)),
         (1, lambda: c.decode_attn(0, q, table, lens, out, softcap=-1.0)),
         (1, lambda: c.decode_attn(0, q, table, lens, out, softcap=float("inf"))),
+        (1, lambda: c.decode_attn(0, q, table, lens, out, softcap=1e-38)),
         (1, lambda: c.decode_attn(0, q, table, lens, out, window=-1)),
+        (3, lambda: _lib.kv_paged_prefill_attn(c.h, 0, _lib.F16, 2, 1 << 27, 8, q.data_ptr(), 1024, ints([0, 1, 2]).data_ptr(),
+                                               table.data_ptr(), 2, 2, lens.data_ptr(), out.data_ptr(), None, c.ws.data_ptr(),
+                                               c.ws_bytes)),
+        (3, lambda: _lib.kv_paged_prefill_attn(c.h, 0, _lib.F16, 2, 1 << 26, 1 << 20, q.data_ptr(), 1024,
+                                               ints([0, 1, 2]).data_ptr(), table.data_ptr(), 2, 2, lens.data_ptr(), out.data_ptr(),
+                                               None, c.ws.data_ptr(), c.ws_bytes)),
         (1, lambda: c.decode_attn(0, q, table, lens, out, ws=torch.empty(16, dtype=torch.uint8, device=cu))),
         (3, lambda: c.decode_attn(0, q.bfloat16(), table, lens, out.bfloat16())),
         (1, lambda: c.prefill_attn(0, q, ints([0, 1, 2]), -1, table, lens, out)),
