@@ -68,9 +68,15 @@ def _type_of(x, name, types):
     return t
 
 
+_one_device = None
+
+
 def _guarded(dev, call, *args):
     """call(*args) with device `dev` current."""
-    if torch.cuda.current_device() == dev:
+    global _one_device
+    if _one_device is None:
+        _one_device = torch.cuda.device_count() == 1
+    if _one_device or torch.cuda.current_device() == dev:
         return call(*args)
     with torch.cuda.device(dev):
         return call(*args)
