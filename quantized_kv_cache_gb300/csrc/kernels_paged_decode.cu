@@ -6,6 +6,11 @@
 // lengths. A CTA's four warps take the tiles of a run in turn, each with its own running maximum, sum
 // and output (fp32, registers); at the end of a head they join through shared memory. A head that lies
 // in one run is written out at once; others leave (m, l, o) per run, which the merge kernel joins.
+//
+// Bound by HBM over 16-bit pages (48 ragged sequences up to 24,001 positions, 8 x 128 bf16: 409 us, 99% of the measured
+// rate; 4 up to 262,144, 4 x 256 fp16: 467 us, 103%), by the instructions that turn codes into operands over
+// quantised ones (131,072 positions, 8 x 128, q8_0 / q4_0: 59 us, 54%; issue slots 64% busy, two thirds of the 550
+// instructions of a tile in the two products' decoding).
 #include "device_common.cuh"
 #include "paged_frag.cuh"
 
