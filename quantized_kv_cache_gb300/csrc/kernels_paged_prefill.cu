@@ -198,7 +198,7 @@ __device__ __forceinline__ float2 unpair(uint64_t x) { return make_float2(__uint
 template <typename T>
 __device__ __forceinline__ void weights32(const uint32_t (&x)[32], uint64_t f, uint64_t m, uint32_t* w, uint64_t (&sum)[4], float (&top)[4]) {
     uint64_t u[16];
-    float v[32];
+    float v[32] = {};
     const auto first = [&](int e) {
         const uint64_t a = (uint64_t)x[2 * e] | ((uint64_t)x[2 * e + 1] << 32);
         asm volatile("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(u[e]) : "l"(a), "l"(f), "l"(m));

@@ -3,7 +3,7 @@
 //
 // All three move bytes: each input is read once and each output written once with 16-byte accesses, several vectors
 // in flight per thread, fp32 arithmetic. On GB300 (measured HBM rate 6.79 TB/s): norm and rotation of 8,191 tokens x 48
-// heads x 128 in 38.4 us, 78% of that rate (issue slots 67% busy, 72 registers); q8_0 rows of 65,536 + 59,000 + 47,000
+// heads x 128 in 38.4 us, 78% of that rate (issue slots 67% busy, 72 registers); q8_0 rows of 65,536 + 57,855 + 60,559
 // positions x 4 x 256 read as bf16 in 173 us, 98%; 16,383 tokens x 8 x 128 written as q8_0 / q4_0 in 22 us (bound by the
 // quantiser's instructions, issue 83% busy).
 #include <type_traits>

@@ -312,6 +312,13 @@ def test_prefill_long_context_few_rows():
     prefill_case(("q8_0", "q4_0"), "f16", 1, 5, 128, 64, [20011], [9], {})
 
 
+def test_prefill_sharp_scores_and_large_queries():
+    """One position far above the others, and bf16 queries beyond fp16's range on quantised pages."""
+    prefill_case(("f16", "f16"), "f16", 2, 4, 128, 16, [300, 5], [60, 5], {}, q_scale=20.0)
+    prefill_case(("q8_0", "q8_0"), "bf16", 2, 4, 64, 16, [300, 5], [60, 5], dict(softcap=1.0), q_scale=1e6)
+    prefill_case(("q8_0", "q4_0"), "bf16", 2, 4, 256, 16, [300, 5], [60, 5], {}, q_scale=1e-9)
+
+
 def test_prefill_rows_before_the_first_position_see_nothing():
     """A chunk longer than the positions held: rows at negative positions give zeros and lse -inf."""
     p = Pages(1, 64, 16, 4, "f16", "f16", Hq=2)
