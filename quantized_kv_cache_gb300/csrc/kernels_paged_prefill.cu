@@ -15,9 +15,9 @@
 // With two row tiles, the products of one run while the other's softmax does; with one, S of the next
 // tile is computed meanwhile (two S buffers).
 //
-// 4,096 tokens at 8,192 positions, 40 heads on 8 x 128, bf16: 414 us, 1,245 TFLOP/s (64% of the measured matrix rate).
+// 4,096 tokens at 8,192 positions, 40 heads on 8 x 128, bf16: 413 us, 1,250 TFLOP/s (65% of the measured matrix rate).
 // A row tile's turn is a chain: softmax 1,000 cycles, products 1,130 (1,024 at the peak), barriers and wake-ups 850;
-// the other tile's turn fills most of the rest. Over codes at D = 256 (6 prompts, cap, window, prefix: 335 us) the
+// the other tile's turn fills most of the rest. Over codes at D = 256 (6 prompts, cap, window, prefix: 321 us) the
 // decoding warps bind: every 128 rows decode their positions anew.
 #include <cuda.h>
 #include "stream_common.cuh"
@@ -435,70 +435,84 @@ __global__ void __launch_bounds__(Geo<D, KF != 0>::threads, 1) prefill_kernel(co
                     }
                 }
             } else {
-                // Codes: a thread has the same pieces (16 channels of a row) of every item; those of the next item are
-                // on their way while this item's are decoded (loaded and decoded in turn, an item took 3,300 cycles).
+                // Codes: a thread has the same pieces (16 channels of a row) of every tile; those of the next stage are on their
+                // way while the products run. K and V have code of their own, with constant formats, and a tile's page
+                // numbers are loaded a stage before they are looked at (item by item, with the number checked at once,
+                // an item's loads took 1,500 cycles and the 6 prompts above 336 us, against 321).
                 constexpr int per = D / 16, step = 32 * GE::prod / per, E = (BN + step - 1) / step;   // rows apart, of a thread
                 const int id = 32 * pw + lane, row0 = id / per, ch = id % per * 16;
-                uint4 code[E];
-                uint32_t d[E];
-                int page = -1, next_page = pages_of(0);
-                auto load = [&](int n) {                        // items in order: the page numbers follow the K items
-                    const int u = n >> 1, w = n & 1 ? 0 : 1, i = w ? u - 1 : u, p0 = kv.at(i0 + i);
-                    if (w == 0) {
-                        page = next_page;
-                        next_page = pages_of(i + 1);
-                    }
-                    const bool q8 = (w ? VF : KF) == 1;
-                    const int rb = q8 ? D : D / 2;
-                    const uint32_t unit = (uint32_t)p.v.unit[w];
-                    const uint8_t* base_w = p.v.base[w] + (int64_t)h * unit;
+                struct Codes {
+                    uint4 c[E];
+                    uint32_t d[E];
+                } kc, vc;
+                const auto load = [&](auto fmt, int w, int tile, int units, Codes& x) {   // units: of the tile's 16-row blocks, by lane
+                    constexpr bool Q8 = decltype(fmt)::value == 1;
+                    constexpr int RB = Q8 ? D : D / 2;
+                    const uint8_t* base_w = w ? p.v.base[1] : p.v.base[0];
+                    const uint32_t unit = (uint32_t)(w ? p.v.unit[1] : p.v.unit[0]);
+                    const int p0 = kv.at(i0 + tile), live = c.len - p0;
 #pragma unroll
                     for (int e = 0; e < E; ++e) {
-                        const int r = row0 + e * step;
-                        const int pg = __shfl_sync(kAll, page, (r >> 4) & (BN / 16 - 1));
-                        code[e] = make_uint4(0, 0, 0, 0);
-                        d[e] = 0;
-                        if (r < BN && pg >= 0 && p0 + r < c.len) {
+                        const int r = row0 + e * step, un = __shfl_sync(kAll, units, (r >> 4) & (BN / 16 - 1));
+                        x.c[e] = make_uint4(0, 0, 0, 0);
+                        x.d[e] = 0;
+                        if (r < BN && un >= 0 && r < live) {
                             const int row = (p0 + r) & (p.v.ps - 1);
-                            const uint8_t* a = base_w + (uint64_t)(uint32_t)(pg * p.v.H) * unit;
-                            d[e] = *reinterpret_cast<const uint16_t*>(a + (p.v.ps * rb + row * (D / 16) + ch / 32 * 2));
-                            a += row * rb + (q8 ? ch : ch / 2);
-                            if (q8) {
-                                code[e] = *reinterpret_cast<const uint4*>(a);
+                            const uint8_t* a = base_w + (uint64_t)(uint32_t)un * unit;
+                            x.d[e] = *reinterpret_cast<const uint16_t*>(a + (p.v.ps * RB + row * (D / 16) + ch / 32 * 2));
+                            a += row * RB + (Q8 ? ch : ch / 2);
+                            if constexpr (Q8) {
+                                x.c[e] = *reinterpret_cast<const uint4*>(a);
                             } else {
                                 const uint2 y = *reinterpret_cast<const uint2*>(a);
-                                code[e].x = y.x;
-                                code[e].y = y.y;
+                                x.c[e].x = y.x;
+                                x.c[e].y = y.y;
                             }
                         }
                     }
                 };
-                if (nt > 0) load(1);
-                for (int n = 1; n <= 2 * nt; ++n) {
-                    const int u = n >> 1, w = n & 1 ? 0 : 1, i = w ? u - 1 : u;
-                    uint4 now[E];
-                    uint32_t dn[E];
-#pragma unroll
-                    for (int e = 0; e < E; ++e) {
-                        now[e] = code[e];
-                        dn[e] = d[e] | (d[e] << 16);
-                    }
-                    if (n < 2 * nt) load(n + 1);
-                    if (w && u >= 2) wait(empty + 8 * (u & 1), ((u >> 1) - 1) & 1);
-                    const uint32_t dst = ring + (2 * w + (i & 1)) * GE::slot;
-                    const bool q8 = (w ? VF : KF) == 1;
+                const auto store = [&](auto fmt, uint32_t dst, const Codes& x) {
+                    constexpr bool Q8 = decltype(fmt)::value == 1;
 #pragma unroll
                     for (int e = 0; e < E; ++e) {
                         const int r = row0 + e * step;
                         if (r >= BN) continue;
-                        const uint4 lo = q8 ? decode_q8(make_uint2(now[e].x, now[e].y), dn[e]) : decode_q4(now[e].x, dn[e]);
-                        const uint4 hi = q8 ? decode_q8(make_uint2(now[e].z, now[e].w), dn[e]) : decode_q4(now[e].y, dn[e]);
-                        st_shared16(dst + tile_byte(BN, r, ch), lo);
-                        st_shared16(dst + tile_byte(BN, r, ch + 8), hi);
+                        const uint32_t dd = x.d[e] | (x.d[e] << 16);
+                        const uint4 y = x.c[e];
+                        st_shared16(dst + tile_byte(BN, r, ch), Q8 ? decode_q8(make_uint2(y.x, y.y), dd) : decode_q4(y.x, dd));
+                        st_shared16(dst + tile_byte(BN, r, ch + 8), Q8 ? decode_q8(make_uint2(y.z, y.w), dd) : decode_q4(y.y, dd));
                     }
-                    if (w == 0 || u == nt) {                    // the last item of the stage
-                        fence_async_smem();
-                        mbar_arrive(full + 8 * (u & 1));
+                };
+                const std::integral_constant<int, KF> kf;
+                const std::integral_constant<int, VF> vf;
+                // a tile's page numbers, one per lane: loaded a stage before they are looked at
+                const auto table_of = [&](int tile) {
+                    const int at = tile < nt ? kv.at(i0 + tile) + 16 * lane : c.len;
+                    return lane < BN / 16 && at < c.len ? table[at >> p.v.ps_shift] : 0;
+                };
+                const auto units_of = [&](int page) {
+                    if (page >= 0 && page < p.v.n_pages) return page * p.v.H + h;
+                    raise_status(p.v.status, KVQ_PAGED_BAD_INDEX);
+                    return -1;
+                };
+                int page = table_of(0), units = -1;
+                if (nt > 0) {
+                    units = units_of(page);
+                    load(kf, 0, 0, units, kc);
+                }
+                page = table_of(1);
+#pragma unroll 1
+                for (int u = 0; u <= nt && nt > 0; ++u) {
+                    if (u >= 2) wait(empty + 8 * (u & 1), ((u >> 1) - 1) & 1);
+                    if (u > 0) store(vf, ring + (2 + ((u - 1) & 1)) * GE::slot, vc);
+                    if (u < nt) store(kf, ring + (u & 1) * GE::slot, kc);
+                    fence_async_smem();
+                    mbar_arrive(full + 8 * (u & 1));
+                    if (u < nt) load(vf, 1, u, units, vc);
+                    if (u + 1 < nt) {
+                        units = units_of(page);
+                        page = table_of(u + 2);
+                        load(kf, 0, u + 1, units, kc);
                     }
                 }
             }
@@ -540,7 +554,7 @@ __global__ void __launch_bounds__(Geo<D, KF != 0>::threads, 1) prefill_kernel(co
                     rs.f *= __uint_as_float((uint32_t)(127 - sh) << 23);
                 }
             }
-#pragma unroll 4
+#pragma unroll 16
             for (int d = 0; d < D; d += 8) {
                 uint4 x = make_uint4(0, 0, 0, 0);
                 if (src) {
