@@ -371,20 +371,20 @@ __global__ void __launch_bounds__(Geo<D, KF != 0>::threads, 1) prefill_kernel(co
             // ------------------------------------------------------------------ K and V tiles
             const int pw = warp - GE::first_prod;               // 8-row blocks pw, pw + prod, ..
             const int32_t* table = p.table + (int64_t)b * p.table_stride;
-            // page numbers of a tile's 16-row blocks, one per lane, loaded a tile ahead
-            auto pages_of = [&](int i) {
-                int page = -1;
-                const int at = i < nt ? kv.at(i0 + i) + 16 * lane : c.len;
-                if (lane < BN / 16 && at < c.len) {
-                    page = table[at >> p.v.ps_shift];
-                    if (page < 0 || page >= p.v.n_pages) {
-                        raise_status(p.v.status, KVQ_PAGED_BAD_INDEX);
-                        page = -1;
-                    }
-                }
-                return page;
-            };
             if constexpr (KF == 0) {
+                // page numbers of a tile's 16-row blocks, one per lane, loaded a tile ahead
+                auto pages_of = [&](int i) {
+                    int page = -1;
+                    const int at = i < nt ? kv.at(i0 + i) + 16 * lane : c.len;
+                    if (lane < BN / 16 && at < c.len) {
+                        page = table[at >> p.v.ps_shift];
+                        if (page < 0 || page >= p.v.n_pages) {
+                            raise_status(p.v.status, KVQ_PAGED_BAD_INDEX);
+                            page = -1;
+                        }
+                    }
+                    return page;
+                };
                 int page = -1, next_page = pages_of(0);
                 // items: V of tile u - 1 and K of tile u, for u = 0 .. nt (no V in the first, no K in the last)
                 for (int n = 1; n <= 2 * nt; ++n) {
