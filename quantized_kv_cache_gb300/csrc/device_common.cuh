@@ -84,10 +84,11 @@ __device__ __forceinline__ void flag_nonfinite(const Layout& L, const void* pool
 // grid_dep_wait blocks until the launches it depends on have completed and their memory
 // operations are visible; it returns at once in a kernel launched without the attribute.
 // Every kernel launched this way executes grid_dep_wait before its first global memory access,
-// except the decode kernel's items when the launch ahead is the merge kernel (AttnParams::early).
+// except the decode kernel's items when the launch ahead is the merge kernel (AttnParams::early), and the paged cache's
+// merge, which reads the call's lengths before it.
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
-// Lets the next launch in the stream start. Only the merge kernel calls it, after its own
-// grid_dep_wait: when the next launch starts, the launch ahead of the merge has completed.
+// Lets the next launch in the stream start. The merge kernel and the paged decode kernel call it, after their own
+// grid_dep_wait: when the next launch starts, the launch ahead of theirs has completed.
 __device__ __forceinline__ void grid_dep_launch() {
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
 }

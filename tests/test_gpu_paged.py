@@ -220,6 +220,40 @@ def test_decode_many_sequences_and_one_long():
     decode_case(("q8_0", "q8_0"), "f16", 1, 4, 128, 64, [30001], {})
 
 
+@pytest.mark.parametrize("n", [1, 2, 31, 32, 33, 34, 64])
+@pytest.mark.parametrize("opts", [{}, dict(window=300)])
+def test_decode_heads_cut_by_runs_at_any_number_of_sequences(n, opts):
+    """Every count of sequences around a warp's width, with empty ones first, between and last, and heads in several runs."""
+    lens = [(977 * (i + 1)) % 3001 if i % 4 != 1 else 0 for i in range(n)]
+    lens[-1] = 0 if n == 34 else 4000
+    if n == 33:
+        lens[0] = 0
+    decode_case(("f16", "f16"), "f16", 3, 2, 64, 32, lens, opts)
+
+
+@pytest.mark.parametrize("n", [5, 40])
+def test_captured_decodes_back_to_back_follow_their_lengths(n):
+    """Two captured calls in a row over one workspace, replayed with other lengths: what the calls give outside a graph."""
+    lens = [700, 0, 33, 1500, 1] + [(91 * i) % 900 for i in range(n - 5)]
+    p, table, q, out, lse = decode_case(("f16", "f16"), "f16", 2, 4, 64, 16, lens, {})
+    now, out2 = ints(lens), torch.empty_like(out)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        side = torch.cuda.current_stream().cuda_stream
+        p.cache.decode_attn(0, q, table, now, out, stream=side)
+        p.cache.decode_attn(0, q, table, now, out2, window=50, stream=side)
+    for shift in (0, 1, 2):
+        turned = ints([min(lens[i], (i + 1) * 97 * shift) if shift else lens[i] for i in range(n)])
+        now.copy_(turned)
+        graph.replay()
+        got, got2 = out.clone(), out2.clone()
+        a, b = torch.empty_like(out), torch.empty_like(out)
+        p.cache.decode_attn(0, q, table, turned, a)
+        p.cache.decode_attn(0, q, table, turned, b, window=50)
+        assert torch.equal(got, a) and torch.equal(got2, b)
+
+
 def test_decode_reports_bad_pages_and_lengths():
     p, table, q, out, _ = decode_case(("f16", "f16"), "f16", 1, 2, 64, 16, [40, 20], {})
     bad = table.clone()
