@@ -47,7 +47,6 @@ template <int D, bool CODES> struct Geo {
     static constexpr int o_col(int t) { return 256 + t * D; }
 };
 constexpr float kLazy = 8.f;                                  // log2 of what a weight may exceed 1 by
-constexpr int kMaxSplits = 16;
 
 // One sequence's chunk: rows of q, and the positions they sit at.
 struct Chunk {
@@ -701,7 +700,7 @@ __global__ void __launch_bounds__(Geo<D, KF != 0>::threads, 1) prefill_kernel(co
                 }
             } else {
                 const int64_t part = (int64_t)split * p.n_rows * p.Hq + at, all = (int64_t)splits * p.n_rows * p.Hq;
-                float* o_part = p.ws + 2 * all + part * D;
+                float* o_part = p.ws + split_out_at(all) + part * D;
                 if (alive) *reinterpret_cast<float2*>(p.ws + 2 * part) = make_float2(m, l);
 #pragma unroll 1
                 for (int d = 0; d < D && nt > 0; d += 32) {
@@ -740,7 +739,7 @@ template <int D, typename TQ> __global__ void __launch_bounds__(kJT) prefill_joi
         if (ml.x == -INFINITY) continue;                 // nothing seen: no output was written
         const float a = ex2(ml.x - m);
         l += ml.y * a;
-        const float4* f = reinterpret_cast<const float4*>(p.ws + 2 * splits * n + (s * n + at) * D + ch);
+        const float4* f = reinterpret_cast<const float4*>(p.ws + split_out_at(splits * n) + (s * n + at) * D + ch);
         const float4 x = f[0], y = f[1];
         const float z[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
@@ -753,13 +752,6 @@ template <int D, typename TQ> __global__ void __launch_bounds__(kJT) prefill_joi
     if (p.lse && ch == 0) p.lse[at] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
 }
 
-// Splits of the positions: as many as leave one CTA per SM, when the row tiles alone give fewer.
-int splits_of(int64_t rows, int n_seq, int H, int tile_rows, int sm_count) {
-    const int64_t ctas = (rows / tile_rows + n_seq) * H;       // at most one part-filled tile per sequence
-    int64_t s = (sm_count < kMaxSms ? sm_count : kMaxSms) / (ctas > 0 ? ctas : 1);
-    return (int)(s < 1 ? 1 : (s > kMaxSplits ? kMaxSplits : s));
-}
-
 template <int D, int KF, int VF, typename T, typename TQ>
 int prefill_run(const PagedAttnParams& p, const CUtensorMap* maps, int sm_count, cudaStream_t s) {
     using GE = Geo<D, KF != 0>;
@@ -767,7 +759,7 @@ int prefill_run(const PagedAttnParams& p, const CUtensorMap* maps, int sm_count,
     int res = 0;
     if (const int e = resident_ctas((const void*)k, GE::threads, GE::smem, &res)) return e;
     const int64_t chunk = (int64_t)p.max_q * p.G;
-    const int splits = splits_of((int64_t)p.n_rows * p.G, p.n_seq, p.v.H, GE::rows, sm_count);
+    const int splits = prefill_splits((int64_t)p.n_rows * p.G, p.n_seq, p.v.H, GE::rows, sm_count);
     const dim3 grid(p.v.H, (unsigned)((chunk + GE::rows - 1) / GE::rows), (unsigned)(p.n_seq * splits));
     cudaError_t e = launch_k(k, grid, dim3(GE::threads), GE::smem, s, true, p, maps[0], maps[1], splits);
     if (e == cudaSuccess && splits > 1) {
@@ -792,12 +784,6 @@ template <int D> int prefill_d(const PagedAttnParams& p, const CUtensorMap* m, i
 }
 
 }  // namespace
-
-// The splits times the rows stay below one CTA per SM's worth of row tiles, and below kMaxSplits times the rows.
-size_t paged_prefill_ws_floats(int D, int64_t head_rows) {
-    const int64_t most = head_rows * kMaxSplits, full = (int64_t)kMaxSms * 256;
-    return (size_t)((most < full ? most : full) * (D + 2));
-}
 
 int prefill_box_rows(int D, int ps) {
     const int bn = D == 256 ? Geo<256, false>::BN : Geo<128, false>::BN;

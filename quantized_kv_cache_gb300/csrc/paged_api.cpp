@@ -92,7 +92,7 @@ PagedView view(const kvq_paged* h, int layer) {
 size_t workspace_floats(const kvq_paged_config& c, int64_t seqs, int64_t rows) {
     const int G = c.n_q_heads / c.n_kv_heads;
     const size_t a = (size_t)(line_floats(seqs) + (kMaxDecodeCtas + seqs * c.n_kv_heads) * partial_floats(G, c.head_dim));
-    const size_t b = paged_prefill_ws_floats(c.head_dim, rows * c.n_q_heads);
+    const size_t b = (size_t)paged_prefill_ws_floats(c.head_dim, rows * c.n_q_heads);
     return a > b ? a : b;
 }
 

@@ -81,6 +81,21 @@ int prefill_box_rows(int D, int ps);
 KVQ_HD int64_t partial_floats(int G, int D) { return 32 + (int64_t)G * D; }
 // Before the partials: n_seq + 1 int64, the tiles before each sequence.
 KVQ_HD int64_t line_floats(int64_t n_seq) { return (2 * (n_seq + 1) + 3) & ~(int64_t)3; }
-size_t paged_prefill_ws_floats(int D, int64_t head_rows);   // query rows x query heads
+
+// A chunk's positions are split when its row tiles alone leave SMs without work: as many splits as leave one CTA per SM.
+constexpr int kMaxSplits = 16;
+KVQ_HD int prefill_splits(int64_t rows, int n_seq, int H, int tile_rows, int sm_count) {
+    const int64_t ctas = (rows / tile_rows + n_seq) * H;       // at most one part-filled tile per sequence
+    const int64_t s = (sm_count < kMaxSms ? sm_count : kMaxSms) / (ctas > 0 ? ctas : 1);
+    return (int)(s < 1 ? 1 : (s > kMaxSplits ? kMaxSplits : s));
+}
+// The splits' partials in the workspace: (maximum, sum) of all `pairs` (split, query row, head), then from float
+// split_out_at on their outputs. Those go by 16-byte accesses, and pairs may be odd: rounded up to four floats.
+KVQ_HD int64_t split_out_at(int64_t pairs) { return (2 * pairs + 3) & ~(int64_t)3; }
+// The splits times the rows stay below one CTA per SM's worth of row tiles, and below kMaxSplits times the rows.
+KVQ_HD int64_t paged_prefill_ws_floats(int D, int64_t head_rows) {   // query rows x query heads
+    const int64_t most = head_rows * kMaxSplits, full = (int64_t)kMaxSms * 256, pairs = most < full ? most : full;
+    return split_out_at(pairs) + pairs * D;
+}
 
 }  // namespace kvq
