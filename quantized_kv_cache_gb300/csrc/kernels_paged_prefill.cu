@@ -736,7 +736,7 @@ template <int D, typename TQ> __global__ void __launch_bounds__(kJT) prefill_joi
     float l = 0.f, o[8] = {};
     for (int s = 0; s < splits; ++s) {
         const float2 ml = *reinterpret_cast<const float2*>(p.ws + 2 * (s * n + at));
-        if (ml.x == -INFINITY) continue;                 // nothing seen: no output was written
+        if (ml.y == 0.f) continue;                       // nothing seen: no output was written (NaN scores: the sum is NaN)
         const float a = ex2(ml.x - m);
         l += ml.y * a;
         const float4* f = reinterpret_cast<const float4*>(p.ws + split_out_at(splits * n) + (s * n + at) * D + ch);

@@ -52,3 +52,41 @@ def test_split_chunk_with_odd_counts(H, G, qlens, fmt, dtype, D):
         r = slice(cu[b], cu[b + 1])
         want = pc.attention64(q[r].double(), ks[b], vs[b], torch.arange(n - m, n, device="cuda"), 1 / math.sqrt(D))
         pc.check_attention(out[r], lse[r], want, dtype, HALF_ULP["bf16" if fmt[0] == "bf16" else "f16"], steps_of(n))
+
+
+# ------------------------------------------------------------------------------------------------ NaN
+def nan_case(fmt, dtype, what, how):
+    """(out, lse, rows that see a NaN) of 3 queries over 700 positions, the second query NaN, or the keys of positions 0-255;
+    in one split call, in a call that is not split (160 equal sequences), or as a decode step each."""
+    H, G, D, ps, n, m = 1, 2, 64, 32, 700, 3
+    p = Pages(H, D, ps, 23, *fmt, Hq=H * G, max_seqs=160, max_tokens=160 * m)
+    table, _, _ = pc.fill(p, 0, [n], 3, dtype)
+    q = normal((m, H * G, D), 4, dtype)
+    bad = torch.zeros(m, dtype=torch.bool, device="cuda")
+    if what == "query":
+        q[1], bad[1] = float("nan"), True
+    else:
+        k = torch.full((256, H, D), float("nan"), dtype=DT[dtype], device="cuda")
+        v = normal((256, H, D), 5, dtype)
+        tab = table[0].cpu().numpy()
+        p.cache.write(0, k, v, ints([int(tab[i // ps]) * ps + i % ps for i in range(256)]))
+        bad[:] = True
+    p.cache.status()
+    copies = 160 if how == "whole" else 1
+    many = q.repeat(copies, 1, 1)
+    out, lse = torch.full_like(many, 7.0), torch.full((m * copies, H * G), 7.0, device="cuda")
+    if how == "decode":
+        p.cache.decode_attn(0, many, table.repeat(m, 1), ints([n] * m), out, lse=lse)
+    else:
+        p.cache.prefill_attn(0, many, ints([m * i for i in range(copies + 1)]), m, table.repeat(copies, 1), ints([n] * copies),
+                             out, lse=lse)
+    assert p.cache.status() == 0
+    return out, lse, bad.repeat(copies)
+
+
+@pytest.mark.parametrize("fmt,dtype", [(("f16", "f16"), "f16"), (("bf16", "bf16"), "bf16"), (("q8_0", "q4_0"), "bf16")])
+@pytest.mark.parametrize("what", ["query", "keys"])
+@pytest.mark.parametrize("how", ["split", "whole", "decode"])
+def test_nan_among_what_a_query_sees_gives_nan(fmt, dtype, what, how):
+    out, lse, bad = nan_case(fmt, dtype, what, how)
+    assert torch.isnan(out[bad]).all() and torch.isfinite(out[~bad]).all()
