@@ -63,7 +63,7 @@ typedef struct kvq_paged kvq_paged;   /* opaque host-side handle */
  *   slopes:       s = s - slopes[query head] * |i - j|        (device fp32 [n_q_heads])
  *   visibility:   j <= i, and j > i - window when window > 0; positions j < prefix[sequence] are
  *                 visible to every query, behind the window and after it too (device int32 [n_seq])
- * A query that sees no position gives zeros and lse = -inf.
+ * A query that sees no position gives zeros and lse = -inf; a NaN among the scores it sees gives NaN in both.
  *   lse:          device fp32 [query rows][n_q_heads], the log of the sum of exp(s) (may be null) */
 typedef struct {
     float softcap;

@@ -334,8 +334,8 @@ __global__ void __launch_bounds__(kDT, (Ring<D, KF, VF, NQ>::ctas)) decode_kerne
             if (whole) {
                 float mm = -INFINITY, ll = 0.f;
                 for (int w = 0; w < kDW; ++w) mm = fmaxf(mm, s_m[w][r]);
-                for (int w = 0; w < kDW; ++w) ll += mm == -INFINITY ? 0.f : s_l[w][r] * ex2(s_m[w][r] - mm);
-                const float inv = ll > 0.f ? 1.f / ll : 0.f;
+                for (int w = 0; w < kDW; ++w) ll += s_l[w][r] * (mm == -INFINITY ? 0.f : ex2(s_m[w][r] - mm));
+                const float inv = inverse_sum(ll);
                 reinterpret_cast<uint32_t*>((TQ*)p.out + ((int64_t)b * p.Hq + h * G) * D)[e] = Two<TQ>::pack(x * inv, y * inv);
             } else {
                 *reinterpret_cast<float2*>(part + 32 + 2 * e) = make_float2(x, y);
@@ -345,12 +345,12 @@ __global__ void __launch_bounds__(kDT, (Ring<D, KF, VF, NQ>::ctas)) decode_kerne
             const int r = threadIdx.x;
             float mm = -INFINITY, ll = 0.f;
             for (int w = 0; w < kDW; ++w) mm = fmaxf(mm, s_m[w][r]);
-            for (int w = 0; w < kDW; ++w) ll += mm == -INFINITY ? 0.f : s_l[w][r] * ex2(s_m[w][r] - mm);
+            for (int w = 0; w < kDW; ++w) ll += s_l[w][r] * (mm == -INFINITY ? 0.f : ex2(s_m[w][r] - mm));
             if (!whole) {
                 part[r] = mm;
                 part[16 + r] = ll;
             } else if (p.lse) {
-                p.lse[(int64_t)b * p.Hq + h * G + r] = ll > 0.f ? (mm + log2f(ll)) * kLn2 : -INFINITY;
+                p.lse[(int64_t)b * p.Hq + h * G + r] = log_sum(mm, ll);
             }
         }
         __syncthreads();
@@ -456,9 +456,9 @@ __global__ void __launch_bounds__(kMT) merge_kernel(PagedAttnParams p, bool by_r
             o.z += f.z;
             o.w += f.w;
         }
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float inv = inverse_sum(l);
         *reinterpret_cast<uint2*>(out + 4 * col) = make_uint2(Two<TQ>::pack(o.x * inv, o.y * inv), Two<TQ>::pack(o.z * inv, o.w * inv));
-        if (p.lse && col == 0) p.lse[row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+        if (p.lse && col == 0) p.lse[row] = log_sum(m, l);
     }
 }
 

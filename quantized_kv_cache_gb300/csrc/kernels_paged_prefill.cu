@@ -678,10 +678,10 @@ __global__ void __launch_bounds__(Geo<D, KF != 0>::threads, 1) prefill_kernel(co
                 wait(o_done + 8 * t, NT == 2 ? 0 : (nt - 1) & 1);   // two row tiles: reported once, at the end
                 tc_fence_after();
             }
-            const float inv = l > 0.f ? 1.f / l : 0.f;
+            const float inv = inverse_sum(l);
             if (splits == 1) {
                 TQ* out = (TQ*)p.out + at * D;
-                if (p.lse && alive) p.lse[at] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+                if (p.lse && alive) p.lse[at] = log_sum(m, l);
 #pragma unroll 1
                 for (int d = 0; d < D; d += 32) {
                     uint32_t o[32] = {};
@@ -745,11 +745,11 @@ template <int D, typename TQ> __global__ void __launch_bounds__(kJT) prefill_joi
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[e] = fmaf(z[e], a, o[e]);
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = inverse_sum(l);
 #pragma unroll
     for (int e = 0; e < 8; ++e) o[e] *= inv;
     *reinterpret_cast<uint4*>((TQ*)p.out + at * D + ch) = pack8<TQ>(o);
-    if (p.lse && ch == 0) p.lse[at] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    if (p.lse && ch == 0) p.lse[at] = log_sum(m, l);
 }
 
 template <int D, int KF, int VF, typename T, typename TQ>

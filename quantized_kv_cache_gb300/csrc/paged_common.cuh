@@ -59,6 +59,11 @@ __device__ __forceinline__ float ex2(float x) {
 
 constexpr float kL2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
+// A row's maximum m (units of log2) and sum l of 2^(s - m): the log of its sum of exp, and what its output is multiplied
+// by. l is 0 only where nothing was seen. NaN scores leave m as it was (a maximum drops them) and make l NaN: so are both.
+__device__ __forceinline__ float log_sum(float m, float l) { return l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2; }
+__device__ __forceinline__ float inverse_sum(float l) { return l == 0.f ? 0.f : 1.f / l; }
+
 // tanh to about 2^-23 of 1 and, below 1/4, of itself (the odd series' first five terms there; 1 - 2 / (1 +
 // exp(2 |x|)) above).
 __device__ __forceinline__ float tanh_small(float x) {

@@ -90,3 +90,30 @@ def nan_case(fmt, dtype, what, how):
 def test_nan_among_what_a_query_sees_gives_nan(fmt, dtype, what, how):
     out, lse, bad = nan_case(fmt, dtype, what, how)
     assert torch.isnan(out[bad]).all() and torch.isfinite(out[~bad]).all()
+
+
+@pytest.mark.parametrize("fmt,dtype", [(("f16", "f16"), "f16"), (("bf16", "bf16"), "bf16"), (("q8_0", "q4_0"), "bf16")])
+@pytest.mark.parametrize("what", ["query", "keys"])
+@pytest.mark.parametrize("how", ["split", "whole", "decode"])
+def test_log_sum_exp_of_nan_scores_is_nan(fmt, dtype, what, how):
+    """-inf is kept for queries that see nothing."""
+    out, lse, bad = nan_case(fmt, dtype, what, how)
+    assert torch.isnan(lse[bad]).all() and torch.isfinite(lse[~bad]).all()
+
+
+@pytest.mark.parametrize("what", ["query", "keys"])
+def test_log_sum_exp_of_nan_scores_inside_one_run(what):
+    """Short sequences: a head's partials are joined inside one CTA."""
+    p = Pages(2, 128, 16, 8, "f16", "f16", Hq=4, max_seqs=3)
+    table, _, _ = pc.fill(p, 0, [20, 0, 33], 3)
+    q = normal((3, 4, 128), 4)
+    if what == "query":
+        q[0, 1] = float("nan")
+    else:
+        nan = torch.full((20, 2, 128), float("nan"), dtype=torch.float16, device="cuda")
+        p.cache.write(0, nan, nan, ints([int(table[0, i // 16]) * 16 + i % 16 for i in range(20)]))
+    out, lse = torch.empty_like(q), torch.empty((3, 4), device="cuda")
+    p.cache.decode_attn(0, q, table, ints([20, 0, 33]), out, lse=lse)
+    bad = torch.isnan(out).all(-1)
+    assert torch.equal(bad[0], torch.tensor([what == "keys", True, what == "keys", what == "keys"], device="cuda"))
+    assert torch.equal(torch.isnan(lse), bad) and (lse[1] == -math.inf).all() and not out[1].any() and not bad[1:].any()
