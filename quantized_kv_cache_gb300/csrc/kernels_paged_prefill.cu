@@ -71,7 +71,7 @@ template <int BN> struct KvTiles {
     int n0, t1, n;
     __device__ __forceinline__ KvTiles(const Chunk& c, int first, int last, int window) {
         const int end = last < 0 ? 0 : (max(last + 1, c.pre) + BN - 1) / BN;
-        t1 = min(end, window > 0 ? max(0, first - window + 1) / BN : 0);
+        t1 = min(end, window > 0 && first >= window ? (first - window + 1) / BN : 0);   // first may be far below 0
         n0 = last < 0 ? 0 : min((c.pre + BN - 1) / BN, t1);
         n = n0 + end - t1;
     }
@@ -526,7 +526,7 @@ __global__ void __launch_bounds__(Geo<D, KF != 0>::threads, 1) prefill_kernel(co
         RowState rs;
         const int64_t at = (int64_t)(c.row0 + (alive ? row / G : 0)) * p.Hq + h * G + (alive ? row % G : 0);
         rs.pos = alive ? c.pos0 + row / G : -1;
-        rs.lo = p.window > 0 ? rs.pos - p.window + 1 : 0;
+        rs.lo = p.window > 0 && rs.pos >= p.window ? rs.pos - p.window + 1 : 0;
         rs.hi = min(rs.pos, c.len - 1);
         rs.pre = rs.pos >= 0 ? c.pre : 0;
         rs.slope = plain || !p.slopes || !alive ? 0.f : p.slopes[h * G + row % G] * kL2e;

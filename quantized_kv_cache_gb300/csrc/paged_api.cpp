@@ -141,7 +141,8 @@ kvq_status attn_params(kvq_paged* h, int layer, int dtype, int n_seq, int64_t ro
         if (opts->softcap > 0.f && opts->softcap < 1e-30f) return KVQ_EINVAL;    // its reciprocal has to be finite
         if (!aligned4(opts->slopes) || !aligned4(opts->prefix) || !aligned4(opts->lse)) return KVQ_EINVAL;
         p->softcap = opts->softcap;
-        p->window = opts->window;
+        // a window of all that the table holds hides nothing
+        p->window = opts->window >= (int64_t)max_pages * c.page_size ? 0 : opts->window;
         p->slopes = opts->slopes;
         p->prefix = opts->prefix;
         p->lse = opts->lse;

@@ -117,3 +117,28 @@ def test_log_sum_exp_of_nan_scores_inside_one_run(what):
     bad = torch.isnan(out).all(-1)
     assert torch.equal(bad[0], torch.tensor([what == "keys", True, what == "keys", what == "keys"], device="cuda"))
     assert torch.equal(torch.isnan(lse), bad) and (lse[1] == -math.inf).all() and not out[1].any() and not bad[1:].any()
+
+
+# ------------------------------------------------------------------------------------------------ lengths
+@pytest.mark.parametrize("window", [(1 << 31) - 1, (1 << 31) - 3, 65, 64])
+@pytest.mark.parametrize("prefix", [None, [3]])
+@pytest.mark.parametrize("copies", [1, 160])
+def test_window_as_wide_as_the_table_changes_nothing(window, prefix, copies):
+    """A chunk longer than its sequence, so that positions start below zero, and windows up to the largest number."""
+    p = Pages(1, 64, 16, 4, "f16", "f16", Hq=2, max_seqs=160, max_tokens=160 * 40)
+    table, ks, vs = pc.fill(p, 0, [33], 1)
+    table = table.repeat(copies, 1)
+    q = normal((40, 2, 64), 2).repeat(copies, 1, 1)
+    cu, lens = ints([40 * i for i in range(copies + 1)]), ints([33] * copies)
+    pre = None if prefix is None else ints(prefix * copies)
+    got = []
+    for w in (0, window):
+        out, lse = torch.full_like(q, 7.0), torch.full((40 * copies, 2), 7.0, device="cuda")
+        p.cache.prefill_attn(0, q, cu, 40, table, lens, out, lse=lse, window=w, prefix=pre)
+        got += [out, lse]
+    assert torch.equal(got[0], got[2]) and torch.equal(got[1], got[3])
+    assert torch.isfinite(got[3].view(copies, 40, 2)[:, 7:]).all() and (got[3].view(copies, 40, 2)[:, :7] == -math.inf).all()
+    one = [torch.empty((copies, 2, 64), dtype=torch.float16, device="cuda") for _ in range(2)]
+    for w, o in zip((0, window), one):
+        p.cache.decode_attn(0, q.view(copies, 40, 2, 64)[:, 39], table, lens, o, window=w, prefix=pre)
+    assert torch.equal(*one)
