@@ -122,9 +122,10 @@ kvq_status kv_paged_decode_attn(kvq_paged* h, int32_t layer, int32_t dtype, int3
 /* kv_paged_prefill_attn — attention of a chunk of new tokens per sequence: the rows
  * cu_q[b] .. cu_q[b+1] - 1 of q ([n_rows][n_q_heads][head_dim], stride q_stride) are the last
  * positions of sequence b, which holds lens[b] positions with the chunk (its rows already in the
- * pages). cu_q: device int32 [n_seq + 1], non-decreasing; max_q (host): at least the longest
- * chunk. n_seq up to 65,535, n_rows below 2^27, max_q up to 524,280. Rows at a negative position (a chunk longer than lens[b]) see nothing: zeros. Rows of out
- * and lse outside [cu_q[0], cu_q[n_seq]) stay as they are. Types, table and workspace as above. */
+ * pages). cu_q: device int32 [n_seq + 1], non-decreasing; max_q (host): at least the longest chunk; of a longer
+ * one the first max_q rows are computed, the others stay as they are, and the status word says so. n_seq up to 65,535,
+ * n_rows below 2^27, max_q up to 524,280. Rows at a negative position (a chunk longer than lens[b]) see nothing:
+ * zeros. Rows of out and lse outside [cu_q[0], cu_q[n_seq]) stay as they are. Types, table and workspace as above. */
 kvq_status kv_paged_prefill_attn(kvq_paged* h, int32_t layer, int32_t dtype, int32_t n_seq, int32_t n_rows,
                                  int32_t max_q, const void* q, int64_t q_stride, const int32_t* cu_q,
                                  const int32_t* page_table, int32_t max_pages, int64_t table_stride,

@@ -50,7 +50,7 @@ constexpr float kLazy = 8.f;                                  // log2 of what a 
 
 // One sequence's chunk: rows of q, and the positions they sit at.
 struct Chunk {
-    int row0, n, len, pos0, pre;     // first row of q, tokens, positions held, position of the first token, prefix
+    int row0, n, len, pos0, pre;     // first row of q, tokens worked on, positions held, position of the first token, prefix
 };
 __device__ __forceinline__ Chunk chunk_of(const PagedAttnParams& p, int b, bool report) {
     Chunk c;
@@ -62,6 +62,7 @@ __device__ __forceinline__ Chunk chunk_of(const PagedAttnParams& p, int b, bool 
     c.n = bad ? 0 : c1 - c0;
     if (report && (len < 0 || len > cap || bad || c.n > p.max_q)) raise_status(p.v.status, KVQ_PAGED_BAD_LENGTH);
     c.pos0 = c.len - c.n;
+    c.n = min(c.n, p.max_q);                 // the grids hold max_q tokens of a chunk: its first ones
     c.pre = p.prefix ? min(max(p.prefix[b], 0), c.len) : 0;
     return c;
 }

@@ -199,7 +199,7 @@ class PagedKVCache:
                      prefix=None, ws=None, stream=0):
         """Attention of a chunk of new tokens per sequence, whose rows are in the pages already: rows
         cu_q[b] .. cu_q[b+1]-1 of q ([rows, Hq, D]) are the last positions of the lens[b] that sequence b holds.
-        max_q: at least the longest chunk."""
+        max_q: at least the longest chunk (of a longer one only the first max_q rows are computed)."""
         dt, dev = _type_of(q, "q", _DT), self._dev
         tp, n, w, ts = self._table(page_table)
         rows, qs = _rows(q, "q", self._Hq, self._D, dev, q.dtype)

@@ -11,6 +11,7 @@ torch = pytest.importorskip("torch")
 
 import paged_cases as pc                                                                 # noqa: E402
 from paged_cases import DT, HALF_ULP, Pages                                              # noqa: E402
+from quantized_kv_cache_gb300 import _lib                                                # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -142,3 +143,23 @@ def test_window_as_wide_as_the_table_changes_nothing(window, prefix, copies):
     for w, o in zip((0, window), one):
         p.cache.decode_attn(0, q.view(copies, 40, 2, 64)[:, 39], table, lens, o, window=w, prefix=pre)
     assert torch.equal(*one)
+
+
+@pytest.mark.parametrize("H,G,D,seqs", [(1, 4, 128, 1), (2, 3, 256, 1), (16, 1, 128, 6), (16, 2, 256, 6)])
+@pytest.mark.parametrize("max_q", [1, 100, 130])
+def test_chunk_longer_than_max_q_leaves_the_rest(H, G, D, seqs, max_q):
+    """Chunks of 300 tokens (several row tiles), split and not: the first max_q rows of each are what they should be, the
+    rows behind stay as they were, and the status says so."""
+    n, m = 333, 300
+    p = Pages(H, D, 32, seqs * 11 + 1, "f16", "f16", Hq=H * G, max_seqs=seqs, max_tokens=seqs * m)
+    table, ks, vs = pc.fill(p, 0, [n] * seqs, 3)
+    q = normal((seqs * m, H * G, D), 4)
+    out, lse = torch.full_like(q, 7.0), torch.full((seqs * m, H * G), 7.0, device="cuda")
+    p.cache.ws.fill_(0xff)                               # what the workspace holds is not read before it is written
+    p.cache.prefill_attn(0, q, ints([m * i for i in range(seqs + 1)]), max_q, table, ints([n] * seqs), out, lse=lse)
+    assert p.cache.status() == _lib.PAGED_BAD_LENGTH
+    for b in range(seqs):
+        r, rest = slice(b * m, b * m + max_q), slice(b * m + max_q, b * m + m)
+        assert (out[rest] == 7).all() and (lse[rest] == 7).all()
+        want = pc.attention64(q[r].double(), ks[b], vs[b], torch.arange(n - m, n - m + max_q, device="cuda"), 1 / math.sqrt(D))
+        pc.check_attention(out[r], lse[r], want, "f16", HALF_ULP["f16"], steps_of(n))
