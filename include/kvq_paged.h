@@ -112,7 +112,8 @@ kvq_status kv_paged_read(kvq_paged* h, int32_t layer, int32_t dtype, int32_t n_s
  * holds lens[b] positions (device int32, the new one included and already written), its query
  * sits at position lens[b] - 1. q [n_seq][n_q_heads][head_dim] (stride q_stride), out contiguous.
  * 16-bit pages take queries of their own type; rows of Q8_0 / Q4_0 pages enter as code x scale
- * rounded to fp16, with queries of either type. lens[b] = 0 gives zeros. workspace: device,
+ * rounded to fp16, with queries of either type. lens[b] = 0 gives zeros. max_pages x page_size is at most
+ * 2^31 - 256. workspace: device,
  * 16-byte aligned, >= kv_paged_required_bytes for n_seq; written before it is read. */
 kvq_status kv_paged_decode_attn(kvq_paged* h, int32_t layer, int32_t dtype, int32_t n_seq, const void* q,
                                 int64_t q_stride, const int32_t* page_table, int32_t max_pages, int64_t table_stride,

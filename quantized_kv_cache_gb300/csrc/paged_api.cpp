@@ -133,7 +133,7 @@ kvq_status attn_params(kvq_paged* h, int layer, int dtype, int n_seq, int64_t ro
     if (!aligned16(q) || !aligned16(out) || !aligned16(ws) || !aligned4(table) || !aligned4(lens)) return KVQ_EINVAL;
     if (!stride_ok(q_stride, (int64_t)c.n_q_heads * c.head_dim)) return KVQ_EINVAL;
     if (max_pages <= 0 || table_stride < max_pages) return KVQ_EINVAL;
-    if ((int64_t)max_pages * c.page_size >= (int64_t)1 << 31) return KVQ_EINVAL;
+    if ((int64_t)max_pages * c.page_size > ((int64_t)1 << 31) - 256) return KVQ_EINVAL;   // the end of a tile behind the last position too is below 2^31
     if (dtype16(c.k_fmt) && dtype != c.k_fmt) return KVQ_EUNSUPPORTED;
     *p = PagedAttnParams{};
     if (opts) {

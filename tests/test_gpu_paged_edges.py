@@ -11,7 +11,7 @@ torch = pytest.importorskip("torch")
 
 import paged_cases as pc                                                                 # noqa: E402
 from paged_cases import DT, HALF_ULP, Pages                                              # noqa: E402
-from quantized_kv_cache_gb300 import _lib                                                # noqa: E402
+from quantized_kv_cache_gb300 import KVQError, _lib                                      # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -163,3 +163,17 @@ def test_chunk_longer_than_max_q_leaves_the_rest(H, G, D, seqs, max_q):
         assert (out[rest] == 7).all() and (lse[rest] == 7).all()
         want = pc.attention64(q[r].double(), ks[b], vs[b], torch.arange(n - m, n - m + max_q, device="cuda"), 1 / math.sqrt(D))
         pc.check_attention(out[r], lse[r], want, "f16", HALF_ULP["f16"], steps_of(n))
+
+
+def test_tables_of_nearly_2_31_positions_refused():
+    """Positions are counted in 32 bits, a tile beyond the last one too: refused on the host, the pointers are never followed."""
+    p = Pages(1, 64, 16, 4, "f16", "f16")
+    x = torch.zeros((1, 1, 64), dtype=torch.float16, device="cuda")
+    t = ints([[0]])
+    for pages in ((1 << 27) - 1, (1 << 27) - 15):
+        for call, extra in ((_lib.kv_paged_decode_attn, ()), (_lib.kv_paged_prefill_attn, (1, 1))):
+            args = [p.cache.h, 0, _lib.F16, 1, *extra, x.data_ptr(), 64] + ([t.data_ptr()] if extra else [])
+            args += [t.data_ptr(), pages, pages, t.data_ptr(), x.data_ptr(), None, p.cache.ws.data_ptr(), p.cache.ws_bytes]
+            with pytest.raises(KVQError) as e:
+                call(*args)
+            assert e.value.code == 1
