@@ -67,6 +67,10 @@ template <int D, int KF, int VF, int NQ> struct Ring {
 template <int D, int KF, int VF, int NQ, typename T, typename TQ>
 __global__ void __launch_bounds__(kDT, (Ring<D, KF, VF, NQ>::ctas)) decode_kernel(PagedAttnParams p) {
     constexpr bool LO = std::is_same<T, __nv_bfloat16>::value;   // P in two bf16 parts: 16 bits of it
+    // fp16 weights are 2^(s - (max - 15)): the largest is 2^15, and those down to 2^-29 of it keep all bits, down to 2^-40 some
+    // (at 2^(s - max) what lies 2^-25 below the largest would be lost to the outputs but not to the sums). m is max - kUp
+    // everywhere, sums and outputs are in its units; bf16 has the exponents.
+    constexpr float kUp = LO ? 0.f : 15.f;
     using R = Ring<D, KF, VF, NQ>;
     extern __shared__ __align__(128) float smem[];               // the rings; [kDW][G][D] outputs at a head's end
     __shared__ float s_m[kDW][16], s_l[kDW][16];
@@ -241,7 +245,7 @@ __global__ void __launch_bounds__(kDT, (Ring<D, KF, VF, NQ>::ctas)) decode_kerne
                     mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 4));
                     mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 8));
                     mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 16));
-                    const float mn = fmaxf(m[k][e], mx);
+                    const float mn = fmaxf(m[k][e], mx - kUp);
                     base[k][e] = mn == -INFINITY ? 0.f : mn;
                     moved |= m[k][e] != mn;
                     a[k][e] = m[k][e];

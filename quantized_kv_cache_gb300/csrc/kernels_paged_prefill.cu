@@ -46,7 +46,6 @@ template <int D, bool CODES> struct Geo {
     static constexpr int s_col(int i) { return i * BN; }
     static constexpr int o_col(int t) { return 256 + t * D; }
 };
-constexpr float kLazy = 8.f;                                  // log2 of what a weight may exceed 1 by
 
 // One sequence's chunk: rows of q, and the positions they sit at.
 struct Chunk {
@@ -268,6 +267,11 @@ __global__ void __launch_bounds__(Geo<D, KF != 0>::threads, 1) prefill_kernel(co
     using GE = Geo<D, KF != 0>;
     constexpr int NT = GE::NT, BN = GE::BN;
     constexpr bool BF = std::is_same<T, __nv_bfloat16>::value;
+    // Weights are 2^(s - m), m = the largest score when m last moved, less kUp; it moves when a score is more than kLazy
+    // above. fp16: up to 2^15, so that weights down to 2^-25 of the largest keep all bits and down to 2^-36 some (with
+    // kUp = 0 what lies 2^-25 below the largest was lost to the outputs but not to the sums). bf16 has the exponents, so
+    // that m moves more rarely; of a weight it keeps 8 bits (half a step is 2^-8 of it, which averages out over positions).
+    constexpr float kUp = BF ? 0.f : 11.f, kLazy = BF ? 8.f : 4.f;
     extern __shared__ uint8_t raw[];
     // full / empty of the load stages; Q in place; S ready, P ready (by S buffer); O of a row tile up to date.
     // Stage u loads what the products take together: V of tile u - 1 and K of tile u.
@@ -614,7 +618,7 @@ __global__ void __launch_bounds__(Geo<D, KF != 0>::threads, 1) prefill_kernel(co
                     }
                 }
                 // The weights are formed with the maximum as it stands while the tile's own is found; only where that
-                // is more than 2^kLazy above (and for the first tile) the maximum moves and the weights are formed again.
+                // is more than kLazy above (and for the first tile) the maximum moves and the weights are formed again.
                 for (bool last_try = false;; last_try = true) {
                     const float2 f2 = make_float2(f, f), mb = m == -INFINITY ? make_float2(0.f, 0.f) : make_float2(-m, -m);
                     uint64_t s2[4] = {};
@@ -632,7 +636,7 @@ __global__ void __launch_bounds__(Geo<D, KF != 0>::threads, 1) prefill_kernel(co
                         sum = ((a.x + a.y) + (b.x + b.y)) + ((c2.x + c2.y) + (d.x + d.y));
                     }
                     if (last_try) break;
-                    mx = max3(fmaxf(y[0], y[1]), y[2], y[3]) * f;
+                    mx = max3(fmaxf(y[0], y[1]), y[2], y[3]) * f - kUp;
                     const bool grow = mx > m + kLazy || (m == -INFINITY && mx > -INFINITY);
                     if (!__any_sync(kAll, grow)) break;
                     const float a = grow ? ex2(m - mx) : 1.f;

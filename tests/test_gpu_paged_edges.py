@@ -177,3 +177,40 @@ def test_tables_of_nearly_2_31_positions_refused():
             with pytest.raises(KVQError) as e:
                 call(*args)
             assert e.value.code == 1
+
+
+# ------------------------------------------------------------------------------------------------ small weights
+@pytest.mark.parametrize("fmt", [("f16", "f16"), ("q8_0", "q8_0"), ("q4_0", "q4_0")])
+@pytest.mark.parametrize("gap", [22.3, 24.4, 25.1, 28.3])
+@pytest.mark.parametrize("where", [0, 29999])
+@pytest.mark.parametrize("how", ["decode", "chunk"])
+def test_weights_far_below_the_largest_keep_their_share(fmt, gap, where, how):
+    """One position 2^gap above 29,999 others, its value row zero, so that the output is the others'. Sequences enough
+    that none is split (they read the same pages)."""
+    n, D, ps = 30000, 64, 256
+    B = 1216 if how == "decode" else 160
+    p = Pages(1, D, ps, 118, *fmt, Hq=2, max_seqs=B, max_tokens=B)
+    k, v = torch.zeros((n, 1, D), dtype=torch.float16, device="cuda"), 100 + 10 * normal((n, 1, D), 1)
+    k[:, :, 0] = -gap * math.log(2)
+    k[where], v[where] = 0, 0
+    p.cache.write(0, k, v, torch.arange(n, dtype=torch.int32, device="cuda"))
+    table = torch.arange(118, dtype=torch.int32, device="cuda").repeat(B, 1)
+    rows = [torch.empty((n, 1, D), device="cuda") for _ in range(2)]
+    p.cache.read(0, table[:1], ints([0, n]), *rows)
+    kk, vv = (r.half().double() for r in rows)
+    q = torch.zeros((B, 2, D), dtype=torch.float16, device="cuda")
+    q[:, :, 0] = 8
+    out, lse = torch.empty_like(q), torch.empty((B, 2), device="cuda")
+    if how == "decode":
+        p.cache.decode_attn(0, q, table, ints([n] * B), out, lse=lse)
+    else:
+        p.cache.prefill_attn(0, q, ints(range(B + 1)), 1, table, ints([n] * B), out, lse=lse)
+    want, lse64, wabs, ds = pc.attention64(q[:1].double(), kk, vv, torch.tensor([n - 1], device="cuda"), 1 / 8)
+    # a weight is rounded to fp16 2^15 (decode: above the warp's largest) or at least 2^11 (chunk: above the largest met) times
+    # itself: half a step is 2^-11 of it, or 2^-25 where that is subnormal. Then the scores, the fp32 sums and the output.
+    floor = 2.0 ** -(40 if how == "decode" else 36)
+    rel = HALF_ULP["f16"] + 4 * ds[..., None] + steps_of(n) * 2.0 ** -23
+    tol = HALF_ULP["f16"] * want.abs() + (1 + HALF_ULP["f16"]) * (rel * wabs + n * floor * vv.abs().max()) + 2.0 ** -25
+    err = (out.double() - want).abs()
+    assert (err <= tol).all(), f"{float((err / tol).max()):.3g} of the tolerance"
+    assert ((lse.double() - lse64).abs() <= 2 * ds + 2.0 ** -21 * (lse64.abs() + 1) + steps_of(n) * 2.0 ** -24).all()
