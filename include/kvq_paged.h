@@ -87,8 +87,8 @@ kvq_status kv_paged_required_bytes(const kvq_paged_config* cfg, int32_t max_seqs
 kvq_status kv_paged_create(const kvq_paged_config* cfg, void* pool, size_t pool_bytes, int device, kvq_paged** out);
 kvq_status kv_paged_destroy(kvq_paged* h);
 
-/* kv_paged_get_status — read (synchronously) and clear the status word. KVQ_EDEVICE if any bit
- * was set. */
+/* kv_paged_get_status — wait for all work on the device, then read the status word and clear the bits
+ * read. KVQ_EDEVICE if any bit was set. */
 kvq_status kv_paged_get_status(kvq_paged* h, uint32_t* word);
 
 /* kv_paged_write — k, v [n_tok][n_kv_heads][head_dim] (strides k_stride, v_stride) to the pages of

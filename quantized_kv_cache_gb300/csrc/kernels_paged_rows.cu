@@ -399,6 +399,8 @@ template <typename TO, int KF, int VF, int D> __global__ void __launch_bounds__(
     else read_rows<TO, VF, D>(p, 1, s_page, s_row);
 }
 
+__global__ void clear_status_kernel(uint32_t* status, uint32_t bits) { atomicAnd(status, ~bits); }
+
 // fn(key format, value format) as constants, of the pairs a config may have.
 template <typename F> int by_formats(const PagedView& v, F fn) {
     if (v.fmt[0] == KVQ_F16) return fn(std::integral_constant<int, KVQ_F16>(), std::integral_constant<int, KVQ_F16>());
@@ -428,6 +430,10 @@ template <typename TO> int read_t(const ReadParams& p, cudaStream_t s) {
 }
 
 }  // namespace
+
+int launch_paged_clear_status(uint32_t* status, uint32_t bits) {
+    return (int)launch_k(clear_status_kernel, dim3(1), dim3(1), 0, nullptr, false, status, bits);
+}
 
 int launch_norm_rope(const kvq_norm_rope_args& a, int sm_count, void* stream) {
     return a.dtype == KVQ_F16 ? norm_rope_t<__half>(a, sm_count, (cudaStream_t)stream)

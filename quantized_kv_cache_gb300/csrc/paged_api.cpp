@@ -210,7 +210,7 @@ kvq_status kv_paged_create(const kvq_paged_config* cfg, void* pool, size_t pool_
     if (pool_bytes < (size_t)g.total || ((uintptr_t)pool & 255)) return KVQ_EINVAL;
     int d = -1, sms = 0;
     if (cudaGetDevice(&d) != cudaSuccess || d != device) return KVQ_EINVAL;
-    if (cudaMemset(pool, 0, 256) != cudaSuccess) return KVQ_ECUDA;
+    if (cudaMemset(pool, 0, 256) != cudaSuccess || cudaStreamSynchronize(nullptr) != cudaSuccess) return KVQ_ECUDA;
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) return KVQ_ECUDA;
     kvq_paged* h = new (std::nothrow) kvq_paged;
     if (!h) return KVQ_EINVAL;
@@ -240,9 +240,12 @@ kvq_status kv_paged_destroy(kvq_paged* h) {
 kvq_status kv_paged_get_status(kvq_paged* h, uint32_t* word) {
     const kvq_status st = check(h, 0);
     if (st != KVQ_OK) return st;
+    // the word of all that was enqueued before, on any stream; then exactly the bits that are reported are taken out, so
+    // that one that a later call sets meanwhile stays for the next reading
     uint32_t w = 0;
+    if (cudaDeviceSynchronize() != cudaSuccess) return KVQ_ECUDA;
     if (cudaMemcpy(&w, h->pool, 4, cudaMemcpyDeviceToHost) != cudaSuccess) return KVQ_ECUDA;
-    if (w && cudaMemset(h->pool, 0, 4) != cudaSuccess) return KVQ_ECUDA;
+    if (w && (launch_paged_clear_status((uint32_t*)h->pool, w) || cudaStreamSynchronize(nullptr) != cudaSuccess)) return KVQ_ECUDA;
     if (word) *word = w;
     return w ? KVQ_EDEVICE : KVQ_OK;
 }

@@ -67,6 +67,7 @@ struct PagedAttnParams {
 // Asked once per kernel and device. Returns a cudaError_t as int.
 int resident_ctas(const void* kernel, int threads, int smem, int* ctas);
 
+int launch_paged_clear_status(uint32_t* status, uint32_t bits);   // on the legacy stream
 int launch_norm_rope(const kvq_norm_rope_args& a, int sm_count, void* stream);
 int launch_paged_write(const WriteParams& p, void* stream);
 int launch_paged_read(const ReadParams& p, void* stream);

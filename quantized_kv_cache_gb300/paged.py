@@ -120,7 +120,7 @@ class PagedKVCache:
             pass
 
     def status(self):
-        """The device status word (bits PAGED_* of ``_lib``), read synchronously and cleared."""
+        """The device status word (bits PAGED_* of ``_lib``), read when the device has finished all work, and cleared."""
         return _guarded(self._dev, _lib.kv_paged_get_status, self.h)
 
     def write(self, layer, k, v, slots, stream=0):

@@ -11,7 +11,7 @@ torch = pytest.importorskip("torch")
 
 import paged_cases as pc                                                                 # noqa: E402
 from paged_cases import DT, HALF_ULP, Pages                                              # noqa: E402
-from quantized_kv_cache_gb300 import KVQError, _lib                                      # noqa: E402
+from quantized_kv_cache_gb300 import KVQError, PagedKVCache, _lib                        # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -214,3 +214,32 @@ def test_weights_far_below_the_largest_keep_their_share(fmt, gap, where, how):
     err = (out.double() - want).abs()
     assert (err <= tol).all(), f"{float((err / tol).max()):.3g} of the tolerance"
     assert ((lse.double() - lse64).abs() <= 2 * ds + 2.0 ** -21 * (lse64.abs() + 1) + steps_of(n) * 2.0 ** -24).all()
+
+
+# ------------------------------------------------------------------------------------------------ the status word
+def test_status_waits_for_every_stream():
+    """A call still running on a stream of its own: its bit is in the word that is read next, and in no later one."""
+    p = Pages(1, 64, 16, 4, "f16", "f16")
+    x, slots = torch.ones((1, 1, 64), dtype=torch.float16, device="cuda"), ints([64])
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)
+    p.cache.write(0, x, x, slots, stream=side.cuda_stream)
+    assert p.cache.status() == _lib.PAGED_BAD_INDEX
+    torch.cuda.synchronize()
+    assert p.cache.status() == 0
+
+
+def test_creation_has_cleared_the_status_word_when_it_returns():
+    """Created beside a busy default stream, used on another one at once: the bit that a first call sets stays."""
+    p = Pages(1, 64, 16, 4, "f16", "f16")
+    x, slots = torch.ones((1, 1, 64), dtype=torch.float16, device="cuda"), ints([64])
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)
+    with torch.cuda.stream(side):
+        cache = PagedKVCache(p.cfg, 0, pool=p.pool)
+        cache.write(0, x, x, slots, stream=side.cuda_stream)
+    torch.cuda.synchronize()
+    assert cache.status() == _lib.PAGED_BAD_INDEX
