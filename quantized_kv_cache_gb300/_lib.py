@@ -25,7 +25,7 @@ REGION_SINK, REGION_JOURNAL, REGION_JOURNAL_SCALE, REGION_TAIL, REGION_BODY = ra
 ENOSPC = 2
 # dtype of kv_paged_read beside F16 and BF16; bits of the paged status word
 PAGED_F32 = 100
-PAGED_NONFINITE, PAGED_TIMEOUT, PAGED_BAD_INDEX, PAGED_BAD_LENGTH = 1, 2, 4, 8
+PAGED_NONFINITE, PAGED_TIMEOUT, PAGED_BAD_INDEX, PAGED_BAD_LENGTH, PAGED_RANGE = 1, 2, 4, 8, 16
 STATUS = {0: "KVQ_OK", 1: "KVQ_EINVAL", 2: "KVQ_ENOSPC", 3: "KVQ_EUNSUPPORTED", 4: "KVQ_ECUDA", 5: "KVQ_EDEVICE"}
 
 

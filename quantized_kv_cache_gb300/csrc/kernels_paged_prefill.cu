@@ -481,7 +481,7 @@ __global__ void __launch_bounds__(Geo<D, KF != 0>::threads, 1) prefill_kernel(co
                     for (int e = 0; e < E; ++e) {
                         const int r = row0 + e * step;
                         if (r >= BN) continue;
-                        const uint32_t dd = x.d[e] | (x.d[e] << 16);
+                        const uint32_t dd = cut_scales<Q8>(x.d[e] | (x.d[e] << 16));
                         const uint4 y = x.c[e];
                         st_shared16(dst + tile_byte(BN, r, ch), Q8 ? decode_q8(make_uint2(y.x, y.y), dd) : decode_q4(y.x, dd));
                         st_shared16(dst + tile_byte(BN, r, ch + 8), Q8 ? decode_q8(make_uint2(y.z, y.w), dd) : decode_q4(y.y, dd));

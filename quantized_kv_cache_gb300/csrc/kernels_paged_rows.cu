@@ -273,7 +273,9 @@ template <typename T, int FMT, int D> __device__ __forceinline__ void write_rows
                 *reinterpret_cast<uint2*>(unit + at / 2) = make_uint2(o[0], o[1]);
             }
             if ((ch & 31) == 0) {
-                if (!isfinite(__half2float(dh))) raise_status(v.status, KVQ_PAGED_NONFINITE);
+                const uint32_t bits = __half_as_ushort(dh);
+                if (bits > (FMT == KVQ_Q8_0 ? kMaxScaleQ8 : kMaxScaleQ4))
+                    raise_status(v.status, bits < 0x7c00 ? KVQ_PAGED_RANGE : KVQ_PAGED_NONFINITE);
                 constexpr int RB = FMT == KVQ_Q8_0 ? D : D / 2;
                 reinterpret_cast<__half*>(unit + v.ps * RB)[row * (D / 32) + ch / 32] = dh;
             }

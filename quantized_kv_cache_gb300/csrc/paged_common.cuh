@@ -103,5 +103,11 @@ __device__ __forceinline__ uint32_t u32(__half2 h) { return *reinterpret_cast<ui
 __device__ __forceinline__ uint32_t deq(uint32_t raw, float off1024, uint32_t d) {
     return u32(__hmul2(__hsub2(h2(raw), __float2half2_rn(off1024)), h2(d)));
 }
+// A pair of block scales (d <= 0x7c00 as they are written) cut to kMaxScale, so that code x scale stays below fp16's
+// infinity; scales that are no number become NaN (0 x d), as the minimum alone would not keep them.
+template <bool Q8> __device__ __forceinline__ uint32_t cut_scales(uint32_t d) {
+    const uint32_t top = Q8 ? kMaxScaleQ8 * 0x10001u : kMaxScaleQ4 * 0x10001u;
+    return u32(__hfma2(h2(d), h2(0u), __hmin2(h2(d), h2(top))));
+}
 }  // namespace
 }  // namespace kvq

@@ -10,7 +10,8 @@
 //    pairs the rows channel by channel (byte permutes); channels 2i and 2i + 1 of its piece are rows g and g + 8
 //    of a product, so a lane ends with runs of consecutive output channels of queries 2t and 2t + 1.
 // P^T comes from the accumulators of S^T by one 8 x 8 transposition per 8 positions. Codes become exact fp16
-// integers (an exponent placed around the code bits, one subtract), then code x scale is rounded to fp16 once.
+// integers (an exponent placed around the code bits, one subtract), then code x scale is rounded to fp16 once (scales cut to what keeps
+// that finite: two operations a pair of blocks).
 // Queries on N: a group of up to eight takes half of the products and of the registers that they would take on M.
 #pragma once
 #include <type_traits>
@@ -140,7 +141,7 @@ __device__ __forceinline__ void tile_scores(uint32_t base, const PLACE& at, cons
             step(KS * j + 1, x.w[2], y.w[2], x.w[3], y.w[3]);
         } else {
             const uint32_t d1 = ld_half(sc + K::CH * j / 4), e1 = ld_half(sc + 8 * (D / 16) + K::CH * j / 4);
-            const uint32_t d = __byte_perm(d1, d1, 0x1010), e = __byte_perm(e1, e1, 0x1010);
+            const uint32_t d = cut_scales<PF == PF_Q8>(__byte_perm(d1, d1, 0x1010)), e = cut_scales<PF == PF_Q8>(__byte_perm(e1, e1, 0x1010));
 #pragma unroll
             for (int i = 0; i < K::NW; ++i) {
                 if constexpr (PF == PF_Q8) {
@@ -174,8 +175,8 @@ __device__ __forceinline__ void tile_values(uint32_t base, const PLACE& at, cons
         uint32_t d01 = 0, d23 = 0;
         if constexpr (PF != PF_16) {
             const uint32_t x = sc + V::CH * j / 2;
-            d01 = __byte_perm(ld_half(x), ld_half(x + D / 16), 0x5410);
-            d23 = __byte_perm(ld_half(x + 8 * (D / 16)), ld_half(x + 9 * (D / 16)), 0x5410);
+            d01 = cut_scales<PF == PF_Q8>(__byte_perm(ld_half(x), ld_half(x + D / 16), 0x5410));
+            d23 = cut_scales<PF == PF_Q8>(__byte_perm(ld_half(x + 8 * (D / 16)), ld_half(x + 9 * (D / 16)), 0x5410));
         }
 #pragma unroll
         for (int i = 0; i < V::NW; ++i) {

@@ -9,6 +9,9 @@ namespace kvq {
 constexpr int kTile = 16;            // positions per attention tile: every page size is a multiple
 constexpr int kMaxSms = 192;         // bound of the SMs that a chunk's splits are spread over (sizes the workspace)
 constexpr int kMaxDecodeCtas = 1024; // bound of a decode launch's CTAs (sizes the workspace)
+// Largest scales that the attention takes as they are (fp16 bits of 515.5 and 9352): 127 and 7 times the next ones round to
+// fp16's infinity.
+constexpr uint32_t kMaxScaleQ8 = 0x6007, kMaxScaleQ4 = 0x7091;
 
 // Bytes of one code row (D values) and of a row's scales.
 KVQ_HD int paged_row_bytes(int fmt, int D) { return fmt == KVQ_Q8_0 ? D : (fmt == KVQ_Q4_0 ? D / 2 : 2 * D); }

@@ -243,3 +243,74 @@ def test_creation_has_cleared_the_status_word_when_it_returns():
         cache.write(0, x, x, slots, stream=side.cuda_stream)
     torch.cuda.synchronize()
     assert cache.status() == _lib.PAGED_BAD_INDEX
+
+
+# ------------------------------------------------------------------------------------------------ ranges
+LARGEST = {"q8_0": 515.5, "q4_0": 9352.0}          # 127 or 7 times it is the largest fp16 that is no infinity, or less
+
+
+def taken(p, w, table, n):
+    """Rows [n, H, D] (fp64) of a side's pages as the attention takes them: scales cut at LARGEST, code x scale as fp16."""
+    raw, fmt, out = p.host(), p.fmt[w], []
+    tab = table.cpu().numpy()
+    for j in range(n):
+        page, row = int(tab[j // p.ps]), j % p.ps
+        y = p.get(raw, 0, w, page, row).astype(np.float64).reshape(p.H, -1, 32)
+        at = p.ps * pc.row_bytes(fmt, p.D) + row * (p.D // 16)
+        d = np.stack([np.ascontiguousarray(p.unit(raw, 0, w, page, h)[at:at + p.D // 16]).view(np.float16) for h in range(p.H)])
+        d = d.astype(np.float64)[..., None]
+        code = np.rint(y / np.where(d > 0, d, 1.0))
+        out.append((code * np.minimum(d, LARGEST[fmt])).reshape(p.H, p.D))
+    return torch.from_numpy(np.stack(out)).cuda().half().double()
+
+
+@pytest.mark.parametrize("fmt", [("q8_0", "q8_0"), ("q8_0", "q4_0"), ("q4_0", "q4_0")])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_blocks_beyond_fp16_stay_finite_and_are_reported(fmt, dtype, D):
+    """Blocks whose largest value is fp16's, or (bf16 rows) far beyond it: read back as they are stored; the attention takes
+    their scales cut to what keeps code x scale finite, and the write has said so."""
+    H, G, ps, n = 2, 3, 32, 150
+    p = Pages(H, D, ps, 6, *fmt, Hq=H * G, max_seqs=2, max_tokens=20)
+    x = [normal((n, H, D), s, dtype) for s in (1, 2)]
+    table = torch.randperm(6, generator=torch.Generator().manual_seed(0)).to(torch.int32).cuda()[None, :5].contiguous()
+    slots = ints([int(table[0, j // ps]) * ps + j % ps for j in range(n)])
+    p.cache.write(0, *x, slots)
+    assert p.cache.status() == 0
+    for y in x:
+        y[7, 0, 5] = 65504.0 if dtype == "f16" else 65280.0
+        y[70:75, 1, 33:37] = -65504.0 if dtype == "f16" else 4.0e5
+    p.cache.write(0, *x, slots)
+    assert p.cache.status() == _lib.PAGED_RANGE
+    back = [torch.empty((n, H, D), device="cuda") for _ in range(2)]
+    p.cache.read(0, table, ints([0, n]), *back)
+    for y, z in zip(x, back):
+        big = y.float().abs() > 6e4
+        assert ((z[big] - y.float()[big]).abs() <= y.float()[big].abs() * 2.0 ** -10).all()
+    kk, vv = (taken(p, w, table[0], n) for w in range(2))
+    assert torch.isfinite(kk).all() and torch.isfinite(vv).all()
+    q = normal((20, H * G, D), 4, dtype, 1e-4)
+    out, lse = torch.empty_like(q), torch.empty((20, H * G), device="cuda")
+    p.cache.prefill_attn(0, q, ints([0, 20]), 20, table, ints([n]), out, lse=lse)
+    want = pc.attention64(q.double(), kk, vv, torch.arange(n - 20, n, device="cuda"), 1 / math.sqrt(D))
+    pc.check_attention(out, lse, want, dtype, HALF_ULP["f16"], steps_of(n))
+    one, one_lse = torch.empty_like(q[:1]), torch.empty_like(lse[:1])
+    p.cache.decode_attn(0, q[19:], table, ints([n]), one, lse=one_lse)
+    pc.check_attention(one, one_lse, tuple(y[19:] for y in want), dtype, HALF_ULP["f16"], steps_of(n))
+    assert p.cache.status() == 0
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+def test_non_finite_blocks_still_give_nan(bad):
+    """A block with a scale that is no number is not cut: what sees it is NaN."""
+    p = Pages(1, 64, 16, 4, "q8_0", "q8_0", Hq=2, max_tokens=8)
+    x = normal((40, 1, 64), 1)
+    x[20, 0, 40] = bad
+    p.cache.write(0, x, x, ints(range(40)))
+    assert p.cache.status() == _lib.PAGED_NONFINITE
+    q = normal((8, 2, 64), 2)
+    out = torch.empty_like(q)
+    p.cache.prefill_attn(0, q, ints([0, 8]), 8, ints([[0, 1, 2]]), ints([40]), out)
+    one = torch.empty_like(q[:1])
+    p.cache.decode_attn(0, q[:1], ints([[0, 1, 2]]), ints([40]), one)
+    assert torch.isnan(out).all() and torch.isnan(one).all()
