@@ -61,7 +61,7 @@ typedef struct kvq_paged kvq_paged;   /* opaque host-side handle */
 
 /* Options of the two attention calls; a null pointer in their place means none. Applied in this
  * order to the score s = scale <q, k_j> of the query at position i and position j:
- *   softcap > 0:  s = softcap * tanh(s / softcap)          (at least 1e-30)
+ *   softcap > 0:  s = softcap * tanh(s / softcap)          (1e-30 to 2e38)
  *   slopes:       s = s - slopes[query head] * |i - j|        (device fp32 [n_q_heads])
  *   visibility:   j <= i, and j > i - window when window > 0; positions j < prefix[sequence] are
  *                 visible to every query, behind the window and after it too (device int32 [n_seq])

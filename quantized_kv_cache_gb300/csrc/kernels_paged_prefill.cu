@@ -553,9 +553,9 @@ __global__ void __launch_bounds__(Geo<D, KF != 0>::threads, 1) prefill_kernel(co
                     }
                 const int ex = (int)((__float_as_uint(a) >> 23) & 255) - 127;
                 if (a > 0.f && ex < 128) {
-                    const int sh = min(max(14 - ex, -100), 100);
+                    const int sh = min(14 - ex, 100);                // from -113 on
                     up = __uint_as_float((uint32_t)(127 + sh) << 23);
-                    rs.f *= __uint_as_float((uint32_t)(127 - sh) << 23);
+                    rs.f = rule.factor(__uint_as_float((uint32_t)(127 - sh) << 23));
                 }
             }
 #pragma unroll 16

@@ -139,6 +139,7 @@ kvq_status attn_params(kvq_paged* h, int layer, int dtype, int n_seq, int64_t ro
     if (opts) {
         if (!(opts->softcap >= 0.f) || !std::isfinite(opts->softcap) || opts->window < 0) return KVQ_EINVAL;
         if (opts->softcap > 0.f && opts->softcap < 1e-30f) return KVQ_EINVAL;    // its reciprocal has to be finite
+        if (opts->softcap > 2e38f) return KVQ_EINVAL;                            // and its multiple by log2(e)
         if (!aligned4(opts->slopes) || !aligned4(opts->prefix) || !aligned4(opts->lse)) return KVQ_EINVAL;
         p->softcap = opts->softcap;
         // a window of all that the table holds hides nothing

@@ -81,7 +81,10 @@ struct ScoreRule {
     float scale, cap, cap_l2;      // softmax scale; softcap (0: none); softcap * log2(e)
     bool biased;
     __device__ __forceinline__ bool plain() const { return cap == 0.f && !biased; }
-    __device__ __forceinline__ float factor(float back) const { return back * scale * (cap > 0.f ? 1.f / cap : kL2e); }
+    // kept among fp32's normal numbers: 0 or an infinity times a score of infinity or 0 is no score
+    __device__ __forceinline__ float factor(float back) const {
+        return fminf(fmaxf(back * scale * (cap > 0.f ? 1.f / cap : kL2e), 1.17549435e-38f), 3.40282347e38f);
+    }
     // dist: |distance| in positions; slope_l2: the head's slope * log2(e)
     __device__ __forceinline__ float operator()(float x, int dist, float slope_l2) const {
         if (cap > 0.f) x = cap_l2 * tanh_any(x);

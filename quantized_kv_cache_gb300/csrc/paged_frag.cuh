@@ -236,7 +236,7 @@ __device__ __forceinline__ void load_queries(const ROW& rows, int g, int t, uint
             a = fmaxf(a, __shfl_xor_sync(kAll, a, 2));
             const int ex = (int)((__float_as_uint(a) >> 23) & 255) - 127;
             if (a > 0.f && ex < 128) {
-                const int sh = min(max(14 - ex, -100), 100);         // the largest magnitude to [2^14, 2^15)
+                const int sh = min(14 - ex, 100);                    // the largest magnitude to [2^14, 2^15): from -113 on
                 up = __uint_as_float((uint32_t)(127 + sh) << 23);
                 back[q] = __uint_as_float((uint32_t)(127 - sh) << 23);
             }

@@ -314,3 +314,45 @@ def test_non_finite_blocks_still_give_nan(bad):
     one = torch.empty_like(q[:1])
     p.cache.decode_attn(0, q[:1], ints([[0, 1, 2]]), ints([40]), one)
     assert torch.isnan(out).all() and torch.isnan(one).all()
+
+
+@pytest.mark.parametrize("big", [2.0 ** 118, 2.0 ** 126, 2.0 ** -126])
+@pytest.mark.parametrize("softcap", [0.0, 1e-30, 1e38])
+@pytest.mark.parametrize("how", ["decode", "chunk"])
+def test_bf16_queries_of_any_size_over_codes(big, softcap, how):
+    """Query rows at the ends of bf16's range, keys of zeros but for one position: no product and no factor of a score leaves
+    fp32's range, so that one position takes all (a large query), or all weigh the same (a tiny one, or a tiny cap)."""
+    n, D = 200, 64
+    p = Pages(1, D, 16, 13, "q8_0", "q8_0", Hq=2, max_tokens=4)
+    k, v = torch.zeros((n, 1, D), dtype=torch.bfloat16, device="cuda"), normal((n, 1, D), 1, "bf16")
+    k[5] = 2.0 ** -10
+    p.cache.write(0, k, v, ints(range(n)))
+    table = ints([list(range(13))])
+    rows = torch.empty((n, 1, D), dtype=torch.float32, device="cuda")
+    p.cache.read(0, table, ints([0, n]), None, rows)
+    vv = rows.half().double()[:, 0]
+    q = torch.full((1, 2, D), big, dtype=torch.bfloat16, device="cuda")
+    out, lse = torch.empty_like(q), torch.empty((1, 2), device="cuda")
+    if how == "decode":
+        p.cache.decode_attn(0, q, table, ints([n]), out, lse=lse, softcap=softcap)
+    else:
+        p.cache.prefill_attn(0, q, ints([0, 1]), 1, table, ints([n]), out, lse=lse, softcap=softcap)
+    if big > 1 and softcap != 1e-30:
+        want, mag = vv[5], vv[5].abs()
+    else:
+        want, mag = vv.mean(0), vv.abs().mean(0)
+        assert ((lse - math.log(n)).abs() < 2.0 ** -19 * 8).all()
+    assert (torch.isfinite(lse)).all()
+    tol = HALF_ULP["bf16"] * want.abs() + (HALF_ULP["f16"] + n * 2.0 ** -23) * mag
+    assert ((out.double() - want).abs() <= tol).all()
+
+
+def test_caps_beyond_fp32_in_units_of_log2_refused():
+    p = Pages(1, 64, 16, 4, "f16", "f16", max_tokens=1)
+    x = torch.zeros((1, 1, 64), dtype=torch.float16, device="cuda")
+    out = torch.empty_like(x)
+    for f in (lambda: p.cache.decode_attn(0, x, ints([[0]]), ints([1]), out, softcap=3e38),
+              lambda: p.cache.prefill_attn(0, x, ints([0, 1]), 1, ints([[0]]), ints([1]), out, softcap=3e38)):
+        with pytest.raises(KVQError) as e:
+            f()
+        assert e.value.code == 1
