@@ -3,7 +3,9 @@
 ``PagedKVCache`` owns (or takes) a pool of pages and a workspace and forwards to the C ABI of
 ``include/kvq_paged.h``; ``qk_norm_rope`` needs no cache. The tensors are checked here (device, type,
 shape, strides) and an argument that does not fit raises ``ValueError`` before anything is enqueued;
-what the C side refuses raises ``KVQError``. As in ``KVCache``, ``stream`` is a raw CUDA stream handle
+what the C side refuses raises ``KVQError``. Nothing here has a gradient: where autograd records, a tensor that
+requires one raises ``ValueError`` too (``torch.no_grad()`` or ``detach()`` says that none is wanted), and tensors that a
+call writes count as changed in place. As in ``KVCache``, ``stream`` is a raw CUDA stream handle
 and 0 the legacy default stream; a caller on another stream passes its handle
 (``torch.cuda.current_stream().cuda_stream``) and keeps the tensors alive until the work is done.
 Page tables, lengths, slots, offsets and positions are int32 CUDA tensors, read when the call runs on the
@@ -67,6 +69,17 @@ def _type_of(x, name, types):
         _bad(f"{name}: one of {', '.join(map(str, types))} is wanted, not {x.dtype}")
     return t
 
+
+def _no_grad(*tensors):
+    """Refuses tensors whose gradient would be lost, or wrong after a write in place."""
+    if torch.is_grad_enabled():
+        for x in tensors:
+            if x is not None and x.requires_grad:
+                _bad("a tensor requires a gradient, which this call does not have: call it under torch.no_grad() or detach")
+
+
+# Written tensors: autograd finds out if it had saved one of them.
+_changed = torch.autograd.graph.increment_version
 
 _one_device = None
 
@@ -132,6 +145,7 @@ class PagedKVCache:
         if nv != n:
             _bad("k and v: the same number of tokens is wanted")
         sp = _ints(slots, "slots", n, self._dev)
+        _no_grad(k, v)
         _guarded(self._dev, _lib.kv_paged_write, self.h, layer, dt, n, k.data_ptr(), ks, v.data_ptr(), vs, sp, stream)
 
     def _table(self, table):
@@ -155,7 +169,9 @@ class PagedKVCache:
         vp = None if v_out is None else _out_rows(v_out, "v_out", rows, self._H, self._D, self._dev, x.dtype)
         cp = _ints(cu_rows, "cu_rows", n + 1, self._dev)
         sp = None if start is None else _ints(start, "start", n, self._dev)
+        _no_grad(k_out, v_out)
         _guarded(self._dev, _lib.kv_paged_read, self.h, layer, dt, n, tp, w, ts, cp, sp, rows, kp, vp, stream)
+        _changed([x for x in (k_out, v_out) if x is not None])
 
     def _opts(self, n, rows, lse, softcap, window, slopes, prefix):
         sp = pp = lp = None
@@ -193,7 +209,9 @@ class PagedKVCache:
         op = _out_rows(out, "out", n, self._Hq, self._D, dev, q.dtype)
         o = self._opts(n, n, lse, softcap, window, slopes, prefix)
         wp, wb = self._space(ws)
+        _no_grad(q, out, slopes)
         _guarded(dev, _lib.kv_paged_decode_attn, self.h, layer, dt, n, q.data_ptr(), qs, tp, w, ts, lp, op, o, wp, wb, stream)
+        _changed(out if lse is None else (out, lse))
 
     def prefill_attn(self, layer, q, cu_q, max_q, page_table, lens, out, lse=None, softcap=0.0, window=0, slopes=None,
                      prefix=None, ws=None, stream=0):
@@ -207,8 +225,10 @@ class PagedKVCache:
         op = _out_rows(out, "out", rows, self._Hq, self._D, dev, q.dtype)
         o = self._opts(n, rows, lse, softcap, window, slopes, prefix)
         wp, wb = self._space(ws)
+        _no_grad(q, out, slopes)
         _guarded(dev, _lib.kv_paged_prefill_attn, self.h, layer, dt, n, rows, max_q, q.data_ptr(), qs, cp, tp, w, ts, lp, op,
                  o, wp, wb, stream)
+        _changed(out if lse is None else (out, lse))
 
 
 def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, q_out=None, k_out=None, eps=1e-6, interleaved=False,
@@ -256,4 +276,6 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, q_out=None, k_out
     (hq, qp, qw, qo, qs, qos), (hk, kp, kw, ko, ks, kos) = sides
     a = _lib.kvq_norm_rope_args(dt, n, hq, hk, D, rot, 1 if interleaved else 0, max_pos, eps, 0, qp, kp, qw, kw, cp, pp, qo, ko,
                                 qs, ks, qos, kos)
+    _no_grad(q, k, q_weight, k_weight, q_out, k_out, cos_sin)
     _guarded(dev, _lib.kv_qk_norm_rope, ctypes.byref(a), stream)
+    _changed([t if o is None else o for t, o in ((q, q_out), (k, k_out)) if t is not None])

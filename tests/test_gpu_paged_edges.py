@@ -11,7 +11,7 @@ torch = pytest.importorskip("torch")
 
 import paged_cases as pc                                                                 # noqa: E402
 from paged_cases import DT, HALF_ULP, Pages                                              # noqa: E402
-from quantized_kv_cache_gb300 import KVQError, PagedKVCache, _lib                        # noqa: E402
+from quantized_kv_cache_gb300 import KVQError, PagedKVCache, _lib, qk_norm_rope          # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -356,3 +356,38 @@ def test_caps_beyond_fp32_in_units_of_log2_refused():
         with pytest.raises(KVQError) as e:
             f()
         assert e.value.code == 1
+
+
+# ------------------------------------------------------------------------------------------------ autograd
+def test_calls_without_a_gradient_say_so():
+    """Tensors that require a gradient are refused while autograd records, and a value saved for a backward pass that a call
+    writes over is found out."""
+    p = Pages(1, 64, 16, 4, "f16", "f16", Hq=2, max_tokens=2)
+    x, w = normal((2, 3, 64), 1).requires_grad_(), normal((64,), 2).requires_grad_()
+    y = x * 1
+    q, k, v = y[:, :2], y[:, :1], y[:, 2:]
+    one, lens, table, cu = normal((64,), 2), ints([2]), ints([[0, 1]]), ints([0, 2])
+    out = torch.empty((2, 2, 64), dtype=torch.float16, device="cuda")
+    rows = torch.empty((2, 1, 64), device="cuda")
+    calls = [lambda: qk_norm_rope(q, k, one, one, None, None), lambda: qk_norm_rope(q.detach(), None, w, None, None, None, out),
+             lambda: p.cache.write(0, k, v, ints([0, 1])), lambda: p.cache.decode_attn(0, q[:1], table, lens, out[:1]),
+             lambda: p.cache.prefill_attn(0, q, cu, 2, table, lens, out),
+             lambda: p.cache.read(0, table, cu, rows.clone().requires_grad_())]
+    before = y.detach().clone()
+    for f in calls:
+        with pytest.raises(ValueError, match="gradient"):
+            f()
+    assert torch.equal(y, before)
+    with torch.no_grad():
+        for f in calls:
+            f()
+    assert p.cache.status() == 0 and torch.isfinite(out).all()
+    for over in (lambda t: qk_norm_rope(t, None, one, None, None, None),
+                 lambda t: p.cache.prefill_attn(0, out, cu, 2, table, lens, t),
+                 lambda t: p.cache.decode_attn(0, out[:1], table, lens, t[:1])):
+        z = x[:, :2] * 2
+        loss = (z * z).sum()                              # saves z
+        with torch.no_grad():
+            over(z)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.backward()
