@@ -115,20 +115,21 @@ __device__ __forceinline__ uint4 decode_q4(uint32_t c, uint32_t d) {
 }
 
 // A wait on a barrier's phase, bounded as the streaming kernels' are (2 s, then the status bit and the CTA's
-// abort flag), that looks at the clock and the flag only every 32nd time.
-__device__ __forceinline__ void bounded_wait(uint32_t bar, uint32_t parity, uint32_t* status, volatile int* abort_flag) {
+// abort flag), that looks at the clock and the flag only every 32nd time. False where it gave up.
+__device__ __forceinline__ bool bounded_wait(uint32_t bar, uint32_t parity, uint32_t* status, volatile int* abort_flag) {
     uint64_t t0 = 0;
     for (int n = 1; !mbar_try(bar, parity); ++n) {
         if (n & 31) continue;
-        if (*abort_flag) return;
+        if (*abort_flag) return false;
         const uint64_t t = gtime();
         if (t0 == 0) t0 = t;
         if (t - t0 > kWaitNs) {
             raise_status(status, KVQ_PAGED_TIMEOUT);
             *abort_flag = 1;
-            return;
+            return false;
         }
     }
+    return true;
 }
 
 // What one row's thread keeps.
@@ -310,7 +311,7 @@ __global__ void __launch_bounds__(Geo<D, KF != 0>::threads, 1) prefill_kernel(co
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s_tmem;
-    auto wait = [&](uint32_t bar, uint32_t parity) { bounded_wait(bar, parity, p.v.status, &s_abort); };
+    auto wait = [&](uint32_t bar, uint32_t parity) { return bounded_wait(bar, parity, p.v.status, &s_abort); };
 
     if (warp >= GE::mma_warp) {
         if constexpr (GE::other_regs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(GE::other_regs));
@@ -337,10 +338,10 @@ __global__ void __launch_bounds__(Geo<D, KF != 0>::threads, 1) prefill_kernel(co
                     for (int s = 0; s < BN / 16; ++s)
                         mma_ts(tm + GE::o_col(t), tm + GE::s_col(buf) + 8 * s, desc_at(v, s * 2048), mma_desc(BF, true, D), i > 0 || s > 0);
                 };
-                wait(q_full, 0);
-                wait(full, 0);
+                bool may = wait(q_full, 0);                     // after a wait that gave up nothing more is issued
+                may &= wait(full, 0);
                 tc_fence_after();
-                if (elect_one()) {
+                if (elect_one() && may) {
                     for (int t = 0; t < active; ++t) scores(t, 0);
                     tc_commit(empty);
                 }
@@ -348,20 +349,20 @@ __global__ void __launch_bounds__(Geo<D, KF != 0>::threads, 1) prefill_kernel(co
                 for (int i = 0; i < nt; ++i) {
                     const int u = i + 1;
                     const bool more = u < nt;
-                    wait(full + 8 * (u & 1), (u >> 1) & 1);
+                    may &= wait(full + 8 * (u & 1), (u >> 1) & 1);
                     if (NT == 1 && more) {
                         tc_fence_after();
-                        if (elect_one()) scores(0, u);
+                        if (elect_one() && may) scores(0, u);
                         __syncwarp();
                     }
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
                         if (t >= active) break;
                         const int buf = NT == 2 ? t : i & 1;
-                        wait(p_full + 8 * buf, NT == 2 ? i & 1 : (i >> 1) & 1);
+                        may &= wait(p_full + 8 * buf, NT == 2 ? i & 1 : (i >> 1) & 1);
                         tc_fence_after();
                         const int skip = *(volatile int*)&s_skip[buf];
-                        if (elect_one()) {
+                        if (elect_one() && may) {
                             if (!skip) values(t, i);
                             if (NT == 1 || !more) tc_commit(o_done + 8 * t);
                             if (NT == 2 && more) scores(t, u);
@@ -390,6 +391,7 @@ __global__ void __launch_bounds__(Geo<D, KF != 0>::threads, 1) prefill_kernel(co
                     return page;
                 };
                 int page = -1, next_page = pages_of(0);
+                bool may = true;                                // as for the products
                 // items: V of tile u - 1 and K of tile u, for u = 0 .. nt (no V in the first, no K in the last)
                 for (int n = 1; n <= 2 * nt; ++n) {
                     const int u = n >> 1, w = n & 1 ? 0 : 1, i = w ? u - 1 : u, p0 = kv.at(i0 + i);
@@ -398,7 +400,7 @@ __global__ void __launch_bounds__(Geo<D, KF != 0>::threads, 1) prefill_kernel(co
                         page = next_page;
                         next_page = pages_of(i + 1);
                     }
-                    if (w && u >= 2) wait(empty + 8 * (u & 1), ((u >> 1) - 1) & 1);
+                    if (w && u >= 2) may &= wait(empty + 8 * (u & 1), ((u >> 1) - 1) & 1);
                     const uint32_t dst = ring + (2 * w + (i & 1)) * GE::slot;
                     const bool arrive = w == 0 || u == nt;          // the last item of the stage
                     auto block_rows = [&](int blk, int& off) -> const uint8_t* {
@@ -412,9 +414,9 @@ __global__ void __launch_bounds__(Geo<D, KF != 0>::threads, 1) prefill_kernel(co
                         const int k = lane / (D / 64), col = lane % (D / 64) * 64, at = p0 + k * rows;
                         const int pg = __shfl_sync(kAll, page, (k * rows >> 4) & (BN / 16 - 1));
                         if (pw == 0) {
-                            if (lane == 0) tc_expect(bar, GE::slot);
+                            if (lane == 0 && may) tc_expect(bar, GE::slot);
                             __syncwarp();
-                            if (lane < boxes)
+                            if (lane < boxes && may)
                                 tma_load3(dst + tile_byte(BN, k * rows, col), w ? &v_map : &k_map, col, at & (p.v.ps - 1),
                                           pg * p.v.H + h, bar);
                         }
@@ -723,6 +725,13 @@ __global__ void __launch_bounds__(Geo<D, KF != 0>::threads, 1) prefill_kernel(co
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    // A wait ran out: copies and products may still be on their way into this block's memory. They take microseconds; they
+    // are given a millisecond before it is handed back.
+    if (*(volatile int*)&s_abort) {
+        const uint64_t t0 = gtime();
+        for (int n = 0; n < 1 << 20 && gtime() - t0 < 1000000; ++n) {}
+        __syncthreads();
+    }
     if (warp == GE::mma_warp) tmem_free512(tmem);
 }
 
