@@ -12,6 +12,7 @@ torch = pytest.importorskip("torch")
 import paged_cases as pc                                                                 # noqa: E402
 from paged_cases import DT, HALF_ULP, Pages                                              # noqa: E402
 from quantized_kv_cache_gb300 import KVQError, PagedKVCache, _lib, qk_norm_rope          # noqa: E402
+from test_gpu_paged import decode_case, prefill_case                                     # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -391,3 +392,16 @@ def test_calls_without_a_gradient_say_so():
             over(z)
         with pytest.raises(RuntimeError, match="modified by an inplace operation"):
             loss.backward()
+
+
+# ------------------------------------------------------------------------------------------------ wide groups, wide heads
+@pytest.mark.parametrize("fmt,dtype", [(("f16", "f16"), "f16"), (("bf16", "bf16"), "bf16"), (("q8_0", "q8_0"), "bf16"),
+                                       (("q8_0", "q4_0"), "f16"), (("q4_0", "q4_0"), "bf16")])
+@pytest.mark.parametrize("H,G,ps", [(1, 16, 256), (2, 9, 128), (3, 1, 64)])
+def test_heads_of_256(fmt, dtype, H, G, ps):
+    """Groups of 9 and 16 query heads, and pages longer than a tile, at the widest head."""
+    lens, opts = [1, 0, 600, 257, 64], dict(window=200, prefix=ints([1, 1, 70, 1, 0]))
+    decode_case(fmt, dtype, H, G, 256, ps, lens, {})
+    decode_case(fmt, dtype, H, G, 256, ps, lens, opts)
+    prefill_case(fmt, dtype, H, G, 256, ps, lens, [1, 0, 33, 257, 5], {})
+    prefill_case(fmt, dtype, H, G, 256, ps, lens, [1, 0, 33, 257, 5], opts)
