@@ -3,6 +3,9 @@ than max_q, the largest windows, scales and queries, weights far below the large
 """
 
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -405,3 +408,92 @@ def test_heads_of_256(fmt, dtype, H, G, ps):
     decode_case(fmt, dtype, H, G, 256, ps, lens, opts)
     prefill_case(fmt, dtype, H, G, 256, ps, lens, [1, 0, 33, 257, 5], {})
     prefill_case(fmt, dtype, H, G, 256, ps, lens, [1, 0, 33, 257, 5], opts)
+
+
+# ------------------------------------------------------------------------------------------------ calls together
+FIRST_CALL = """
+import torch, math
+from quantized_kv_cache_gb300 import PagedKVCache, paged_config, qk_norm_rope
+def ints(x): return torch.tensor(x, dtype=torch.int32, device="cuda")
+c = PagedKVCache(paged_config(1, 2, 128, 8, 16, 8, "{fmt}"), 0, max_seqs=1, max_tokens=40)
+x = torch.randn((40, 12, 128), device="cuda").{dtype}()
+w, cs = torch.ones(128, device="cuda").{dtype}(), torch.rand((64, 128), device="cuda")
+q, k, v = x[:, :8], x[:, 8:10], x[:, 10:]
+pos, cu, lens, table = ints(range(40)), ints([0, 40]), ints([40]), ints([list(range(3))])
+qo, ko = torch.empty((40, 8, 128), dtype=x.dtype, device="cuda"), torch.empty((40, 2, 128), dtype=x.dtype, device="cuda")
+out, one, rows = torch.zeros_like(qo), torch.zeros_like(qo[:1]), torch.zeros((40, 2, 128), device="cuda")
+def step():
+    s = torch.cuda.current_stream().cuda_stream
+    qk_norm_rope(q, k, w, w, cs, pos, qo, ko, stream=s)
+    c.write(0, ko, v, pos, stream=s)
+    c.read(0, table, cu, rows, stream=s)
+    c.prefill_attn(0, qo, cu, 40, table, lens, out, stream=s)
+    c.decode_attn(0, qo[39:], table, lens, one, stream=s)
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    step()
+g.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in (qo, ko, rows, out, one)]
+step()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, (qo, ko, rows, out, one))) and got[3].abs().sum() > 0
+assert (got[3][39].float() - got[4][0].float()).abs().max() < 0.05 and c.status() == 0
+print("same")
+"""
+
+
+@pytest.mark.parametrize("fmt,dtype", [("bf16", "bfloat16"), ("q8_0", "half")])
+def test_a_process_may_begin_with_a_captured_call(fmt, dtype):
+    """No call comes before the capture that could have loaded a kernel or asked for its occupancy."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL.format(fmt=fmt, dtype=dtype)], cwd=root, capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and r.stdout.split()[-1:] == ["same"], r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("fmt,dtype", [(("f16", "f16"), "f16"), (("q8_0", "q4_0"), "bf16")])
+def test_chunks_on_two_streams_repeat_themselves(fmt, dtype):
+    """Split and unsplit chunks and decode steps side by side, each with a workspace of its own: bit for bit the same every
+    time."""
+    p = Pages(2, 128, 32, 70, *fmt, Hq=8, max_seqs=4, max_tokens=900)
+    table, _, _ = pc.fill(p, 0, [900, 300, 0, 77], 4, dtype)
+    lens, q = ints([900, 300, 0, 77]), normal((900, 8, 128), 5, dtype)
+    cus = [ints([0, 5, 8, 8, 12]), ints([0, 600, 850, 850, 900])]
+    want = [torch.zeros_like(q) for _ in cus] + [torch.zeros_like(q[:4])]
+    for cu, o in zip(cus, want):
+        p.cache.prefill_attn(0, q[:int(cu[-1])], cu, 600, table, lens, o[:int(cu[-1])])
+    p.cache.decode_attn(0, q[:4], table, lens, want[2])
+    streams, ws = [torch.cuda.Stream() for _ in range(3)], [p.cache.new_workspace() for _ in range(3)]
+    got = [[torch.zeros_like(w) for w in want] for _ in range(6)]
+    n = [int(cu[-1]) for cu in cus]
+    torch.cuda.synchronize()
+    for outs in got:
+        for i, s in enumerate(streams):
+            if i < 2:
+                p.cache.prefill_attn(0, q[:n[i]], cus[i], 600, table, lens, outs[i][:n[i]], ws=ws[i], stream=s.cuda_stream)
+            else:
+                p.cache.decode_attn(0, q[:4], table, lens, outs[2], ws=ws[2], stream=s.cuda_stream)
+    torch.cuda.synchronize()
+    assert p.cache.status() == 0
+    for outs in got:
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+def test_lengths_that_a_kernel_moves_between_calls():
+    """Lengths advanced on the device between steps, nothing waited for: each step sees its own."""
+    p = Pages(2, 64, 16, 200, "f16", "f16", Hq=4, max_seqs=2)
+    table, ks, vs = pc.fill(p, 0, [1500, 900], 4)
+    q, lens = normal((2, 4, 64), 5), ints([1000, 3])
+    outs = [torch.empty_like(q) for _ in range(40)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for o in outs:
+            lens.add_(1)
+            p.cache.decode_attn(0, q, table, lens, o, stream=side.cuda_stream)
+    torch.cuda.synchronize()
+    for i, o in enumerate(outs):
+        want = torch.empty_like(o)
+        p.cache.decode_attn(0, q, table, ints([1001 + i, 4 + i]), want)
+        assert torch.equal(o, want)
