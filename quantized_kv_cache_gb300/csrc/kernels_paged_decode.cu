@@ -7,10 +7,11 @@
 // and output (fp32, registers); at the end of a head they join through shared memory. A head that lies
 // in one run is written out at once; others leave (m, l, o) per run, which the merge kernel joins.
 //
-// Bound by HBM over 16-bit pages (48 ragged sequences up to 24,001 positions, 8 x 128 bf16: 409 us, 99% of the measured
-// rate; 4 up to 262,144, 4 x 256 fp16: 467 us, 103%), by the instructions that turn codes into operands over
-// quantised ones (131,072 positions, 8 x 128, q8_0 / q4_0: 59 us, 54%; issue slots 64% busy, two thirds of the 550
-// instructions of a tile in the two products' decoding).
+// Bound by HBM over 16-bit pages (48 ragged sequences up to 24,001 positions, 8 x 128 bf16: 407 us, 99% of the measured
+// rate; 4 up to 262,144, 4 x 256 fp16: 465 us, 104%), by the instructions that turn codes into operands over
+// quantised ones (131,072 positions, 8 x 128, q8_0 / q4_0: 59 us, 54%; issue slots 65% busy, two thirds of the 566
+// instructions of a tile in the two products' decoding). Groups of 16, two query tiles a warp: 16 sequences up to 32,768 on
+// 2 x 128, fp16 94 us (65%), q8_0 / q4_0 68 us (37%).
 #include "device_common.cuh"
 #include "paged_frag.cuh"
 
@@ -373,7 +374,7 @@ __global__ void __launch_bounds__(kMT) merge_kernel(PagedAttnParams p, bool by_r
     const int H = p.v.H, G = p.G, r = blockIdx.x % G, id = blockIdx.x / G;
     // Up to 32 sequences: the line is known from their lengths, before the decode kernel has ended (its blocks wait for
     // what came before them first, so the lengths stand when this kernel starts). Else it is read as the kernel left it
-    // (always read: 1,024 positions of 2 heads took 8.3 us in a graph, with the early line 6.9-7.3).
+    // (always read: 1,024 positions of 2 heads took 8.3 us in a graph, with the early line 7.1-7.2).
     const bool early = !by_runs && p.n_seq <= 32;
     const int64_t* line = (const int64_t*)p.ws;
     int b = id / H, h = id % H;

@@ -9,16 +9,18 @@
 //    axis contiguous. 16-bit pages come by tensor-map copies, one lane per page and 64 channels (16-byte
 //    copies by the threads took 1,550 of the 2,400 cycles of a tile); a tile that ends behind the last position
 //    is copied by the threads, zeros in place of the rows behind it. Quantised rows are decoded on the way;
-//  - one warp per row tile issues the products: S = Q K^T into tensor memory, and O += P V with P read from tensor memory;
+//  - one warp issues the products: S = Q K^T into tensor memory, and O += P V with P read from tensor memory;
 //  - one thread per row does the softmax: S from tensor memory to registers, maximum, exponentials, P back
-//    over S. The running maximum moves only when it grows by more than 2^8, so that O is rescaled rarely.
+//    over S. The running maximum moves only when it grows by more than 2^4 (bf16 pages: 2^8), so that O is
+//    rescaled rarely.
 // With two row tiles, the products of one run while the other's softmax does; with one, S of the next
 // tile is computed meanwhile (two S buffers).
 //
-// 4,096 tokens at 8,192 positions, 40 heads on 8 x 128, bf16: 413 us, 1,250 TFLOP/s (65% of the measured matrix rate).
+// 4,096 tokens at 8,192 positions, 40 heads on 8 x 128, bf16: 414 us, 1,240 TFLOP/s (64% of the measured matrix rate).
 // A row tile's turn is a chain: softmax 1,000 cycles, products 1,130 (1,024 at the peak), barriers and wake-ups 850;
-// the other tile's turn fills most of the rest. Over codes at D = 256 (6 prompts, cap, window, prefix: 321 us) the
-// decoding warps bind: every 128 rows decode their positions anew.
+// the other tile's turn fills most of the rest. Over codes at D = 256 (6 prompts, cap, window, prefix: 332 us) the
+// decoding warps bind: every 128 rows decode their positions anew. 16-bit pages at D = 256 (4,096 tokens at 8,192, 24 heads
+// on 4): 627 us, 51%, the scores of 64 positions taking as long as those of 128 would; D = 64 (40 heads on 8): 336 us, 40%.
 #include <cuda.h>
 #include "stream_common.cuh"
 #include "paged_common.cuh"
@@ -444,7 +446,7 @@ __global__ void __launch_bounds__(Geo<D, KF != 0>::threads, 1) prefill_kernel(co
                 // Codes: a thread has the same pieces (16 channels of a row) of every tile; those of the next stage are on their
                 // way while the products run. K and V have code of their own, with constant formats, and a tile's page
                 // numbers are loaded a stage before they are looked at (item by item, with the number checked at once,
-                // an item's loads took 1,500 cycles and the 6 prompts above 336 us, against 321).
+                // an item's loads took 1,500 cycles and the 6 prompts above 336 us, against 321 at that time).
                 constexpr int per = D / 16, step = 32 * GE::prod / per, E = (BN + step - 1) / step;   // rows apart, of a thread
                 const int id = 32 * pw + lane, row0 = id / per, ch = id % per * 16;
                 struct Codes {

@@ -62,7 +62,7 @@ struct PagedAttnParams {
     int32_t n_seq, max_pages, Hq, G, dtype;
     int32_t n_rows, max_q;   // prefill only
     int32_t window;
-    int32_t n_cta;           // decode: CTAs of the split launch; prefill: splits of a sequence
+    int32_t n_cta;           // decode only: CTAs of the split launch
     float scale, softcap;
 };
 
