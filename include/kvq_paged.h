@@ -38,10 +38,10 @@ enum {
     KVQ_PAGED_NONFINITE = 1,    /* a quantised block had a non-finite scale (the page holds it) */
     KVQ_PAGED_TIMEOUT = 2,      /* a bounded device wait ran out; that launch's outputs are invalid */
     KVQ_PAGED_BAD_INDEX = 4,    /* a slot or a page number was out of range: a write was skipped, a page read as zeros */
-    KVQ_PAGED_RANGE = 16,       /* a quantised block reaches beyond fp16's 65,504: the page holds it and kv_paged_read
+    KVQ_PAGED_BAD_LENGTH = 8,   /* a length, row offset or max_q was out of range: lengths are cut to what the page
+                                   table holds, rows beyond the call's buffers or max_q are skipped */
+    KVQ_PAGED_RANGE = 16        /* a quantised block reaches beyond fp16's 65,504: the page holds it and kv_paged_read
                                    gives it, the attentions cut its scale (kv_paged_decode_attn) */
-    KVQ_PAGED_BAD_LENGTH = 8    /* a length, row offset or max_q was out of range: lengths are cut to what the page
-                                   table holds, rows beyond the call's buffers are skipped */
 };
 
 typedef struct {
@@ -114,10 +114,10 @@ kvq_status kv_paged_read(kvq_paged* h, int32_t layer, int32_t dtype, int32_t n_s
  * holds lens[b] positions (device int32, the new one included and already written), its query
  * sits at position lens[b] - 1. q [n_seq][n_q_heads][head_dim] (stride q_stride), out contiguous.
  * 16-bit pages take queries of their own type; rows of Q8_0 / Q4_0 pages enter as code x scale
- * rounded to fp16, with queries of either type; scales above 515.5 (Q8_0) or 9352 (Q4_0) are taken as these,
- * above which code x scale is no fp16 number (their write has set KVQ_PAGED_RANGE). lens[b] = 0 gives zeros. max_pages x page_size is at most
- * 2^31 - 256. workspace: device,
- * 16-byte aligned, >= kv_paged_required_bytes for n_seq; written before it is read. */
+ * rounded to fp16, with queries of either type. Scales above 515.5 (Q8_0) or 9352 (Q4_0) are taken as
+ * these, as code x scale would be no fp16 number (their write has set KVQ_PAGED_RANGE). lens[b] = 0 gives
+ * zeros. max_pages x page_size is at most 2^31 - 256. workspace: device, 16-byte aligned,
+ * >= kv_paged_required_bytes for n_seq; written before it is read. */
 kvq_status kv_paged_decode_attn(kvq_paged* h, int32_t layer, int32_t dtype, int32_t n_seq, const void* q,
                                 int64_t q_stride, const int32_t* page_table, int32_t max_pages, int64_t table_stride,
                                 const int32_t* lens, void* out, const kvq_attn_opts* opts, void* workspace,
