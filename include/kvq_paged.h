@@ -32,10 +32,15 @@ extern "C" {
 #endif
 
 enum { KVQ_PAGED_F32 = 100 };   /* dtype of kv_paged_read: fp32 rows */
+/* A page format of its own: e4m3 codes with one scale for 16 positions of a head (a block: positions 16 i .. 16 i + 15 of a
+ * sequence), a power of two: the smallest with the block's largest magnitude within 448 times it, 2^-126 at least. It grows
+ * as rows come (kv_paged_append); the rows that are there are then rounded to it. */
+enum { KVQ_PAGED_E4M3 = 101 };
 
 /* Bits of the status word (kv_paged_get_status). */
 enum {
-    KVQ_PAGED_NONFINITE = 1,    /* a quantised block had a non-finite scale (the page holds it) */
+    KVQ_PAGED_NONFINITE = 1,    /* a quantised block had a non-finite scale (the page holds it); KVQ_PAGED_E4M3: a value was no
+                                   finite number (it is stored as NaN, the block's others by their own scale) */
     KVQ_PAGED_TIMEOUT = 2,      /* a bounded device wait ran out; that launch's outputs are invalid */
     KVQ_PAGED_BAD_INDEX = 4,    /* a slot or a page number was out of range: a write was skipped, a page read as zeros */
     KVQ_PAGED_BAD_LENGTH = 8,   /* a length, row offset or max_q was out of range: lengths are cut to what the page
@@ -51,7 +56,7 @@ typedef struct {
     int32_t n_q_heads;      /* a multiple of n_kv_heads, with n_q_heads / n_kv_heads <= 16 */
     int32_t page_size;      /* positions per page: 16, 32, 64, 128 or 256 */
     int32_t n_pages;        /* pages per layer (one page table serves all layers); n_pages x page_size < 2^31 */
-    int32_t k_fmt;          /* KVQ_F16, KVQ_BF16, KVQ_Q8_0 or KVQ_Q4_0 */
+    int32_t k_fmt;          /* KVQ_F16, KVQ_BF16, KVQ_Q8_0, KVQ_Q4_0 or KVQ_PAGED_E4M3 */
     int32_t v_fmt;          /* equal to k_fmt, or KVQ_Q4_0 beside KVQ_Q8_0 keys */
     float softmax_scale;    /* 0 selects 1/sqrt(head_dim) */
     int32_t reserved;
@@ -85,7 +90,8 @@ kvq_status kv_paged_required_bytes(const kvq_paged_config* cfg, int32_t max_seqs
  * current device `device`. Zeroes the status word (synchronously); the pages keep their contents.
  * The layout (byte offsets) is fixed: [256 B status area], then per layer the K area and the V area,
  * each padded to 256 bytes; an area holds one unit per (page, KV head), page-major: page_size code
- * rows of head_dim values, then for Q8_0 / Q4_0 the scales [page_size][head_dim / 32] fp16. */
+ * rows of head_dim values, then for Q8_0 / Q4_0 the scales [page_size][head_dim / 32] fp16, for KVQ_PAGED_E4M3 the
+ * scales [page_size / 16] fp32, padded to 32 bytes. */
 kvq_status kv_paged_create(const kvq_paged_config* cfg, void* pool, size_t pool_bytes, int device, kvq_paged** out);
 kvq_status kv_paged_destroy(kvq_paged* h);
 
@@ -97,9 +103,21 @@ kvq_status kv_paged_get_status(kvq_paged* h, uint32_t* word);
  * `layer`: token t goes to page slots[t] / page_size, row slots[t] % page_size (device int32
  * [n_tok]). A negative slot skips the token (padding). Values are rounded to the nearest even (16-bit
  * pages) or quantised by the block codec's definition. Slots of one call must be distinct: of two
- * tokens with one slot either may be stored, or parts of both. Nothing else of the pool changes. */
+ * tokens with one slot either may be stored, or parts of both. Nothing else of the pool changes.
+ * KVQ_EUNSUPPORTED for KVQ_PAGED_E4M3 pages, whose scales serve 16 positions: kv_paged_append. */
 kvq_status kv_paged_write(kvq_paged* h, int32_t layer, int32_t dtype, int32_t n_tok, const void* k, int64_t k_stride,
                           const void* v, int64_t v_stride, const int32_t* slots, void* stream);
+
+/* kv_paged_append — rows cu_rows[b] .. cu_rows[b+1] - 1 of k, v ([n_rows][n_kv_heads][head_dim], strides k_stride,
+ * v_stride) become the positions start[b].. of each sequence b, in KVQ_PAGED_E4M3 pages of `layer` (KVQ_EUNSUPPORTED for other
+ * formats: kv_paged_write). cu_rows, start and the page table as for kv_paged_read. A block whose first position is among the rows
+ * begins anew; otherwise its positions up to start[b] - 1 are there and count: its scale grows to what the rows need, never
+ * shrinks, and where it grows those positions' codes are rounded to the new one. What the blocks hold behind the rows is not
+ * looked at and stays as it is. A row of positions that the table does not hold is skipped (KVQ_PAGED_BAD_LENGTH).
+ * Sequences that share a page must not write in it (kv_pages_extend sees to it). */
+kvq_status kv_paged_append(kvq_paged* h, int32_t layer, int32_t dtype, int32_t n_seq, const int32_t* page_table,
+                           int32_t max_pages, int64_t table_stride, const int32_t* cu_rows, const int32_t* start,
+                           int32_t n_rows, const void* k, int64_t k_stride, const void* v, int64_t v_stride, void* stream);
 
 /* kv_paged_read — positions start[b] .. start[b] + cu_rows[b+1] - cu_rows[b] - 1 of each sequence b
  * into rows cu_rows[b].. of k_out and v_out ([n_rows][n_kv_heads][head_dim], contiguous; either may
@@ -115,7 +133,8 @@ kvq_status kv_paged_read(kvq_paged* h, int32_t layer, int32_t dtype, int32_t n_s
  * sits at position lens[b] - 1. q [n_seq][n_q_heads][head_dim] (stride q_stride), out contiguous.
  * 16-bit pages take queries of their own type; rows of Q8_0 / Q4_0 pages enter as code x scale
  * rounded to fp16, with queries of either type. Scales above 515.5 (Q8_0) or 9352 (Q4_0) are taken as
- * these, as code x scale would be no fp16 number (their write has set KVQ_PAGED_RANGE). lens[b] = 0 gives
+ * these, as code x scale would be no fp16 number (their write has set KVQ_PAGED_RANGE). KVQ_PAGED_E4M3 rows likewise, with
+ * scales up to 2^7 (here code x scale is not rounded; a chunk takes it as an fp16 number, which it is from 2^-15 on). lens[b] = 0 gives
  * zeros. max_pages x page_size is at most 2^31 - 256. workspace: device, 16-byte aligned,
  * >= kv_paged_required_bytes for n_seq; written before it is read. */
 kvq_status kv_paged_decode_attn(kvq_paged* h, int32_t layer, int32_t dtype, int32_t n_seq, const void* q,

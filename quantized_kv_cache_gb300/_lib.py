@@ -23,8 +23,10 @@ KVARN_BALANCE = {"final16": 0, "best8": 1}
 # regions
 REGION_SINK, REGION_JOURNAL, REGION_JOURNAL_SCALE, REGION_TAIL, REGION_BODY = range(5)
 ENOSPC = 2
-# dtype of kv_paged_read beside F16 and BF16; bits of the paged status word
+# dtype of kv_paged_read beside F16 and BF16; a format of pages alone; bits of the paged status word
 PAGED_F32 = 100
+PAGED_E4M3 = 101
+PAGED_FMT_NAMES = dict(FMT_NAMES, e4m3=PAGED_E4M3)
 PAGED_NONFINITE, PAGED_TIMEOUT, PAGED_BAD_INDEX, PAGED_BAD_LENGTH, PAGED_RANGE = 1, 2, 4, 8, 16
 STATUS = {0: "KVQ_OK", 1: "KVQ_EINVAL", 2: "KVQ_ENOSPC", 3: "KVQ_EUNSUPPORTED", 4: "KVQ_ECUDA", 5: "KVQ_EDEVICE"}
 
@@ -113,6 +115,7 @@ _SIGS = {
     "kv_paged_destroy": [P],
     "kv_paged_get_status": [P, ctypes.POINTER(ctypes.c_uint32)],
     "kv_paged_write": [P, I32, I32, I32, P, I64, P, I64, P, P],
+    "kv_paged_append": [P, I32, I32, I32, P, I32, I64, P, P, I32, P, I64, P, I64, P],
     "kv_paged_read": [P, I32, I32, I32, P, I32, I64, P, P, I32, P, P, P],
     "kv_paged_decode_attn": [P, I32, I32, I32, P, I64, P, I32, I64, P, P, ctypes.POINTER(kvq_attn_opts), P, SZ, P],
     "kv_paged_prefill_attn": [P, I32, I32, I32, I32, I32, P, I64, P, P, I32, I64, P, P, ctypes.POINTER(kvq_attn_opts), P,
@@ -346,6 +349,12 @@ def kv_paged_get_status(h):
 def kv_paged_write(h, layer, dtype, n_tok, k_ptr, k_stride, v_ptr, v_stride, slots_ptr, stream=0):
     _check("kv_paged_write", load().kv_paged_write(h, layer, dtype, n_tok, k_ptr, k_stride, v_ptr, v_stride, slots_ptr,
                                                    stream))
+
+
+def kv_paged_append(h, layer, dtype, n_seq, table_ptr, max_pages, table_stride, cu_ptr, start_ptr, n_rows, k_ptr, k_stride,
+                    v_ptr, v_stride, stream=0):
+    _check("kv_paged_append", load().kv_paged_append(h, layer, dtype, n_seq, table_ptr, max_pages, table_stride, cu_ptr,
+                                                     start_ptr, n_rows, k_ptr, k_stride, v_ptr, v_stride, stream))
 
 
 def kv_paged_read(h, layer, dtype, n_seq, table_ptr, max_pages, table_stride, cu_ptr, start_ptr, n_rows, k_ptr, v_ptr,

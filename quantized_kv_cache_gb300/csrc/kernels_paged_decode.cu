@@ -219,10 +219,23 @@ __global__ void __launch_bounds__(kDT, (Ring<D, KF, VF, NQ>::ctas)) decode_kerne
             const bool all = p0 + kTile <= st.len && (p0 >= st.lo || p0 + kTile <= st.pre);
             unsigned see = 0xffffu;
             if (!all) see = __ballot_sync(kAll, lane < 16 && st.sees(p0 + lane));
+            if constexpr (KF == PF_E4) {
+                const float d = tile_scale<D>(k_tile);
 #pragma unroll
-            for (int k = 0; k < NQ; ++k)
+                for (int k = 0; k < NQ; ++k) {
+                    // among the normal numbers, as the factor itself (score_rule)
+                    const float f0 = normal_factor(f[k][0] * d), f1 = normal_factor(f[k][1] * d);
+                    s[k][0] *= f0;
+                    s[k][1] *= f1;
+                    s[k][2] *= f0;
+                    s[k][3] *= f1;
+                }
+            } else {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) s[k][c] *= f[k][c & 1];
+                for (int k = 0; k < NQ; ++k)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) s[k][c] *= f[k][c & 1];
+            }
             if (!plain) {
 #pragma unroll
                 for (int k = 0; k < NQ; ++k)
@@ -496,6 +509,8 @@ int KVQ_NAME(KVQ_D)(const PagedAttnParams& p, int sms, void* stream) {
     const int kf = p.v.fmt[0], vf = p.v.fmt[1];
     if (kf == KVQ_F16) return decode_g<PF_16, PF_16, __half, __half>(p, sms, s);
     if (kf == KVQ_BF16) return decode_g<PF_16, PF_16, __nv_bfloat16, __nv_bfloat16>(p, sms, s);
+    if (kf == KVQ_PAGED_E4M3)
+        return p.dtype == KVQ_F16 ? decode_g<PF_E4, PF_E4, __half, __half>(p, sms, s) : decode_g<PF_E4, PF_E4, __half, __nv_bfloat16>(p, sms, s);
     if (p.dtype == KVQ_F16) {
         if (kf == KVQ_Q4_0) return decode_g<PF_Q4, PF_Q4, __half, __half>(p, sms, s);
         if (vf == KVQ_Q4_0) return decode_g<PF_Q8, PF_Q4, __half, __half>(p, sms, s);

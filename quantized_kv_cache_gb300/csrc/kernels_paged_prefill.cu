@@ -31,7 +31,7 @@ namespace {
 
 template <int D, bool CODES> struct Geo {
     static constexpr int NT = D == 256 ? 1 : 2;              // row tiles of a CTA
-    static constexpr int BN = D == 256 ? 64 : 128;           // positions of a KV tile
+    static constexpr int BN = prefill_tile(D);               // positions of a KV tile
     static constexpr int rows = 128 * NT;
     // warps: four softmax warps per row tile, one that issues the products, producers (decoding codes takes more)
     static constexpr int mma_warp = 4 * NT, first_prod = mma_warp + 1, prod = CODES ? 15 - mma_warp : 3;
@@ -112,6 +112,19 @@ __device__ __forceinline__ uint4 decode_q4(uint32_t c, uint32_t d) {
     for (int i = 0; i < 4; ++i) {
         const uint32_t r = (__byte_perm(c, 0, 0x4040 + 0x101 * i) & 0x00f0000fu) | 0x64006400u;
         o[i] = u32(__hmul2(__hfma2(h2(r), mul, add), h2(d)));
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// Eight e4m3 codes as fp16: code x power, rounded once. The power comes as a factor of 2^-13 at least (with it a code is an fp16
+// number) and, where `small`, what is left of it.
+__device__ __forceinline__ uint4 decode_e4(uint2 c, uint32_t mul, uint32_t rest, bool small) {
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t x = i & 2 ? c.y : c.x;
+        o[i] = u32(__hmul2(h2(e4m3_pair(i & 1 ? x >> 16 : x & 0xffffu)), h2(mul)));
+        if (small) o[i] = u32(__hmul2(h2(o[i]), h2(rest)));
     }
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
@@ -454,7 +467,7 @@ __global__ void __launch_bounds__(Geo<D, KF != 0>::threads, 1) prefill_kernel(co
                     uint32_t d[E];
                 } kc, vc;
                 const auto load = [&](auto fmt, int w, int tile, int units, Codes& x) {   // units: of the tile's 16-row blocks, by lane
-                    constexpr bool Q8 = decltype(fmt)::value == 1;
+                    constexpr bool E4 = decltype(fmt)::value == 3, Q8 = decltype(fmt)::value == 1 || E4;   // a byte a value
                     constexpr int RB = Q8 ? D : D / 2;
                     const uint8_t* base_w = w ? p.v.base[1] : p.v.base[0];
                     const uint32_t unit = (uint32_t)(w ? p.v.unit[1] : p.v.unit[0]);
@@ -467,7 +480,8 @@ __global__ void __launch_bounds__(Geo<D, KF != 0>::threads, 1) prefill_kernel(co
                         if (r < BN && un >= 0 && r < live) {
                             const int row = (p0 + r) & (p.v.ps - 1);
                             const uint8_t* a = base_w + (uint64_t)(uint32_t)un * unit;
-                            x.d[e] = *reinterpret_cast<const uint16_t*>(a + (p.v.ps * RB + row * (D / 16) + ch / 32 * 2));
+                            if constexpr (E4) x.d[e] = *reinterpret_cast<const uint32_t*>(a + p.v.ps * RB + row / kTile * 4);
+                            else x.d[e] = *reinterpret_cast<const uint16_t*>(a + (p.v.ps * RB + row * (D / 16) + ch / 32 * 2));
                             a += row * RB + (Q8 ? ch : ch / 2);
                             if constexpr (Q8) {
                                 x.c[e] = *reinterpret_cast<const uint4*>(a);
@@ -485,6 +499,15 @@ __global__ void __launch_bounds__(Geo<D, KF != 0>::threads, 1) prefill_kernel(co
                     for (int e = 0; e < E; ++e) {
                         const int r = row0 + e * step;
                         if (r >= BN) continue;
+                        if constexpr (decltype(fmt)::value == 3) {
+                            const float d = fminf(__uint_as_float(x.d[e]), (float)(1 << kMaxPowerAttn)), mul = fmaxf(d, power_of(-13));
+                            const bool small = mul > d;
+                            const uint32_t dd = Two<__half>::pack(mul, mul), rest = Two<__half>::pack(d * 8192.f, d * 8192.f);
+                            const uint4 y = x.c[e];
+                            st_shared16(dst + tile_byte(BN, r, ch), decode_e4(make_uint2(y.x, y.y), dd, rest, small));
+                            st_shared16(dst + tile_byte(BN, r, ch + 8), decode_e4(make_uint2(y.z, y.w), dd, rest, small));
+                            continue;
+                        }
                         const uint32_t dd = cut_scales<Q8>(x.d[e] | (x.d[e] << 16));
                         const uint4 y = x.c[e];
                         st_shared16(dst + tile_byte(BN, r, ch), Q8 ? decode_q8(make_uint2(y.x, y.y), dd) : decode_q4(y.x, dd));
@@ -789,6 +812,8 @@ template <int D> int prefill_d(const PagedAttnParams& p, const CUtensorMap* m, i
     const int kf = p.v.fmt[0], vf = p.v.fmt[1];
     if (kf == KVQ_F16) return prefill_run<D, 0, 0, __half, __half>(p, m, n, s);
     if (kf == KVQ_BF16) return prefill_run<D, 0, 0, __nv_bfloat16, __nv_bfloat16>(p, m, n, s);
+    if (kf == KVQ_PAGED_E4M3)
+        return p.dtype == KVQ_F16 ? prefill_run<D, 3, 3, __half, __half>(p, m, n, s) : prefill_run<D, 3, 3, __half, __nv_bfloat16>(p, m, n, s);
     if (p.dtype == KVQ_F16) {
         if (kf == KVQ_Q4_0) return prefill_run<D, 2, 2, __half, __half>(p, m, n, s);
         if (vf == KVQ_Q4_0) return prefill_run<D, 1, 2, __half, __half>(p, m, n, s);
@@ -801,17 +826,11 @@ template <int D> int prefill_d(const PagedAttnParams& p, const CUtensorMap* m, i
 
 }  // namespace
 
-int prefill_box_rows(int D, int ps) {
-    const int bn = D == 256 ? Geo<256, false>::BN : Geo<128, false>::BN;
-    return ps < bn ? ps : bn;
-}
-
-int launch_paged_prefill(const PagedAttnParams& p, const void* maps, int sm_count, void* stream) {
-    cudaStream_t s = (cudaStream_t)stream;
-    const CUtensorMap* m = (const CUtensorMap*)maps;
-    if (p.v.D == 64) return prefill_d<64>(p, m, sm_count, s);
-    if (p.v.D == 128) return prefill_d<128>(p, m, sm_count, s);
-    return prefill_d<256>(p, m, sm_count, s);
+// One head dimension per compilation of this file (KVQ_D), so that they build side by side.
+#define KVQ_NAME2(d) launch_paged_prefill_##d
+#define KVQ_NAME(d) KVQ_NAME2(d)
+int KVQ_NAME(KVQ_D)(const PagedAttnParams& p, const void* maps, int sms, void* stream) {
+    return prefill_d<KVQ_D>(p, (const CUtensorMap*)maps, sms, (cudaStream_t)stream);
 }
 
 }  // namespace kvq

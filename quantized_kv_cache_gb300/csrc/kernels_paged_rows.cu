@@ -1,5 +1,5 @@
 // Row kernels of the paged cache: the norm and rotation of query and key heads, rows written to
-// pages (copied, rounded or quantised) and read back.
+// pages (copied, rounded or quantised), appended to blocks of e4m3 codes, and read back.
 //
 // All three move bytes: each input is read once and each output written once with 16-byte accesses, several vectors
 // in flight per thread, fp32 arithmetic. On GB300 (measured HBM rate 6.79 TB/s): norm and rotation of 8,191 tokens x 48
@@ -289,6 +289,140 @@ template <typename T, int KF, int VF, int D> __global__ void __launch_bounds__(k
     else write_rows<T, VF, D>(p, 1);
 }
 
+// ---------------------------------------------------------------------------- append
+// e4m3 blocks: 16 positions of a head under one power of two. A warp takes a whole block (one head of K or V), all its new rows
+// in registers: their largest magnitude on the bits, the power, the codes. Rows that were there are rounded to the new power
+// where it grew; their codes are loaded beside the new rows, before that is known (a decode step is one such load after the other).
+// No two warps touch the same bytes, and no order of anything matters.
+//
+// The warps find their blocks from the rows: a row that begins a block, or its sequence's rows, leads one. With R = 16 a CTA looks at
+// 16 rows, of which one leads where sequences bring many; with R = 1 (a decode step) a CTA takes one row's block.
+constexpr int kAppendWarps = 4;
+template <typename T, int D, int R> __global__ void __launch_bounds__(32 * kAppendWarps) paged_append_kernel(PagedAppendParams p) {
+    const PagedView& v = p.v;
+    const int lane = threadIdx.x & 31, task = blockIdx.y * kAppendWarps + (threadIdx.x >> 5);
+    grid_dep_wait();
+    if (task >= 2 * v.H) return;
+    const int w = task >= v.H, head = task - (w ? v.H : 0), r0 = blockIdx.x * R, r = r0 + (lane < R ? lane : 0);
+    const bool tell = task == 0;
+    // the last sequence whose rows begin at or before this lane's row
+    int b = 0;
+    if (p.n_seq <= (R == 1 ? 1024 : 64)) {
+        for (int i = 0; i < p.n_seq; i += 32) {
+            const int c = i + lane + 1 < p.n_seq ? p.cu[i + lane + 1] : 0x7fffffff;
+#pragma unroll
+            for (int k = 0; k < R; ++k) {
+                const int n = __popc(__ballot_sync(kAll, c <= r0 + k));
+                if (R == 1 || lane == k) b += n;
+            }
+        }
+    } else {
+        int hi = p.n_seq - 1;
+        while (b < hi) {
+            const int mid = (b + hi + 1) >> 1;
+            if (p.cu[mid] <= r) b = mid; else hi = mid - 1;
+        }
+    }
+    const int c0 = p.cu[b], c1 = min(p.cu[b + 1], p.n_rows);
+    if (tell && r0 == 0 && lane == 0 && (p.cu[0] < 0 || p.cu[p.n_seq] > p.n_rows)) raise_status(v.status, KVQ_PAGED_BAD_LENGTH);
+    const int64_t pos = (int64_t)(p.start ? p.start[b] : 0) + r - c0;
+    int off = (int)(pos & (kTile - 1)), n = min(kTile - off, c1 - r), unit = -1;
+    if (lane < R && r >= c0 && r < c1 && c0 >= 0 && (off == 0 || r == c0)) {
+        const int64_t e = pos >> v.ps_shift;
+        if (pos < 0 || e >= p.max_pages) {
+            if (tell) raise_status(v.status, KVQ_PAGED_BAD_LENGTH);
+        } else {
+            const int page = p.table[b * p.table_stride + e];
+            if (page >= 0 && page < v.n_pages) unit = page * v.H + head;
+            else if (tell) raise_status(v.status, KVQ_PAGED_BAD_INDEX);
+        }
+    }
+    constexpr int VPR = D / 8, RPI = 32 / VPR, IT = kTile / RPI;    // vectors of a row, rows of an iteration, iterations
+    const int sub = lane / VPR, col = lane % VPR * 8;
+    for (unsigned lead = __ballot_sync(kAll, unit >= 0); lead; lead &= lead - 1) {
+        const int from = __ffs(lead) - 1;
+        const int un = __shfl_sync(kAll, unit, from), o = __shfl_sync(kAll, off, from), cnt = __shfl_sync(kAll, n, from);
+        const int row0 = (int)__shfl_sync(kAll, pos, from) & (v.ps - 1) & ~(kTile - 1);
+        uint8_t* base = v.base[w] + (int64_t)un * v.unit[w];
+        uint8_t* code = base + row0 * D + col;
+        float* scale = reinterpret_cast<float*>(base + v.ps * D) + row0 / kTile;
+        const T* src = (const T*)p.src[w] + (r0 + from) * p.stride[w] + (int64_t)head * D + col;
+        uint4 x[IT];
+        uint2 old[IT];
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            const int k = i * RPI + sub;
+            x[i] = make_uint4(0, 0, 0, 0);
+            if (k < cnt) x[i] = *reinterpret_cast<const uint4*>(src + k * p.stride[w]);
+        }
+        int held = kMinPower;
+        if (o > 0) {
+            held = min(max(exponent_of(*scale), kMinPower), kMaxPower);
+#pragma unroll
+            for (int i = 0; i < IT; ++i) {
+                old[i] = make_uint2(0, 0);
+                if (i * RPI + sub < o) old[i] = *reinterpret_cast<const uint2*>(code + (i * RPI + sub) * D);
+            }
+        }
+        constexpr uint32_t inf = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < IT; ++i)
+            m = __vmaxu2(m, __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
+                                     __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu)));
+        m = max(m & 0xffffu, m >> 16);
+        const bool odd = __any_sync(kAll, m >= inf);                 // an infinity or NaN: the block goes by its other values
+        if (odd) {
+            m = 0;
+#pragma unroll
+            for (int i = 0; i < IT; ++i) {
+                const uint32_t y[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const uint32_t a = (y[k / 2] >> (16 * (k & 1))) & 0x7fffu;
+                    m = max(m, a < inf ? a : 0u);
+                }
+            }
+            if (lane == 0) raise_status(v.status, KVQ_PAGED_NONFINITE);
+        }
+        m = __reduce_max_sync(kAll, m);
+        const uint32_t top = __float_as_uint(Two<T>::unpack(m).x);  // of 1.75 x 2^8 = 448: one more above a mantissa of 0.75
+        int e = (int)(top >> 23) - 127 - 8 + ((top & 0x7fffffu) > 0x600000u);
+        e = max(max(e, kMinPower), held);
+        if (lane == 0 && e > kMaxPowerAttn) raise_status(v.status, KVQ_PAGED_RANGE);
+        const float inv = power_of(-e);
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            const int k = i * RPI + sub;
+            float f[8];
+            unpack8<T>(x[i], f);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                if (odd && !isfinite(f[q])) f[q] = __int_as_float(0x7fffffff);
+                f[q] *= inv;
+            }
+            const uint2 c = make_uint2(e4m3_codes(f[0], f[1]) | (e4m3_codes(f[2], f[3]) << 16),
+                                       e4m3_codes(f[4], f[5]) | (e4m3_codes(f[6], f[7]) << 16));
+            if (k < cnt) *reinterpret_cast<uint2*>(code + (o + k) * D) = c;
+        }
+        if (o > 0 && e > held) {
+            const float by = power_of(max(held - e, kMinPower));
+#pragma unroll
+            for (int i = 0; i < IT; ++i) {
+                const uint32_t y[2] = {old[i].x, old[i].y};
+                uint32_t c[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float2 a = __half22float2(h2(e4m3_pair(y[k] & 0xffffu))), d = __half22float2(h2(e4m3_pair(y[k] >> 16)));
+                    c[k] = e4m3_codes(a.x * by, a.y * by) | (e4m3_codes(d.x * by, d.y * by) << 16);
+                }
+                if (i * RPI + sub < o) *reinterpret_cast<uint2*>(code + (i * RPI + sub) * D) = make_uint2(c[0], c[1]);
+            }
+        }
+        if (lane == 0) *scale = power_of(e);
+    }
+}
+
 // ---------------------------------------------------------------------------- read
 // A CTA takes kReadRows output rows: one thread per row finds the row's sequence (binary search over cu) and page, then
 // all threads move the rows' pieces, head by head, so that neighbouring lanes read neighbouring rows of a unit.
@@ -298,14 +432,16 @@ constexpr int kReadRows = 16;
 
 template <typename TO, int FMT, int D> __device__ __forceinline__ void read_rows(const ReadParams& p, int w, const int* s_page, const int* s_row) {
     const PagedView& v = p.v;
-    constexpr bool CODES = FMT == KVQ_Q8_0 || FMT == KVQ_Q4_0, WIDE = std::is_same<TO, float>::value;
-    constexpr int CH = WIDE ? 4 : 8, P = D / CH, RB = FMT == KVQ_Q8_0 ? D : (FMT == KVQ_Q4_0 ? D / 2 : 2 * D);
+    constexpr bool E4 = FMT == KVQ_PAGED_E4M3, BYTES = FMT == KVQ_Q8_0 || E4, CODES = BYTES || FMT == KVQ_Q4_0;
+    constexpr bool WIDE = std::is_same<TO, float>::value;
+    constexpr int CH = WIDE ? 4 : 8, P = D / CH, RB = BYTES ? D : (FMT == KVQ_Q4_0 ? D / 2 : 2 * D);
+    using Scale = typename std::conditional<E4, uint32_t, uint16_t>::type;
     // 16-bit rows out: four pieces (q8_0 rows of 3 sequences: 173 us, with eight 205: fewer warps fit); fp32: eight (123 us, 125)
     constexpr int U = WIDE ? 8 : 4;
     const int row0 = blockIdx.x * kReadRows, n = v.H * kReadRows * P;
     for (int i0 = threadIdx.x; i0 < n; i0 += U * kRowThreads) {
         uint32_t x[U][4];
-        uint16_t d[U];
+        Scale d[U];
         bool live[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -315,8 +451,8 @@ template <typename TO, int FMT, int D> __device__ __forceinline__ void read_rows
             d[u] = 0;
             if (live[u] && s_page[r] >= 0) {
                 const uint8_t* unit = unit_at(v, w, s_page[r], head);
-                const uint8_t* a = unit + s_row[r] * RB + (CODES ? (FMT == KVQ_Q8_0 ? ch : ch / 2) : 2 * ch);
-                constexpr int B = CODES ? (FMT == KVQ_Q8_0 ? CH : CH / 2) : 2 * CH;      // bytes of a piece
+                const uint8_t* a = unit + s_row[r] * RB + (CODES ? (BYTES ? ch : ch / 2) : 2 * ch);
+                constexpr int B = CODES ? (BYTES ? CH : CH / 2) : 2 * CH;                // bytes of a piece
                 if constexpr (B == 16) {
                     const uint4 y = *reinterpret_cast<const uint4*>(a);
                     x[u][0] = y.x;
@@ -332,7 +468,8 @@ template <typename TO, int FMT, int D> __device__ __forceinline__ void read_rows
                 } else {
                     x[u][0] = *reinterpret_cast<const uint16_t*>(a);
                 }
-                if constexpr (CODES) d[u] = reinterpret_cast<const uint16_t*>(unit + v.ps * RB)[s_row[r] * (D / 32) + ch / 32];
+                if constexpr (E4) d[u] = reinterpret_cast<const uint32_t*>(unit + v.ps * RB)[s_row[r] / kTile];
+                else if constexpr (CODES) d[u] = reinterpret_cast<const uint16_t*>(unit + v.ps * RB)[s_row[r] * (D / 32) + ch / 32];
             }
         }
 #pragma unroll
@@ -346,10 +483,15 @@ template <typename TO, int FMT, int D> __device__ __forceinline__ void read_rows
                 continue;
             }
             float f[8];
-            const float scale = __half2float(__ushort_as_half(d[u]));
+            float scale;
+            if constexpr (E4) scale = __uint_as_float(d[u]);
+            else scale = __half2float(__ushort_as_half(d[u]));
 #pragma unroll
             for (int e = 0; e < CH; ++e) {
-                if constexpr (FMT == KVQ_Q8_0) {
+                if constexpr (E4) {
+                    const float2 y = __half22float2(h2(e4m3_pair(x[u][e >> 2] >> (16 * (e >> 1 & 1)) & 0xffffu)));
+                    f[e] = scale * (e & 1 ? y.y : y.x);
+                } else if constexpr (FMT == KVQ_Q8_0) {
                     f[e] = scale * (float)(int8_t)(x[u][e >> 2] >> (8 * (e & 3)));
                 } else if constexpr (FMT == KVQ_Q4_0) {
                     f[e] = scale * (float)((int)((x[u][0] >> (4 * e)) & 15u) - 8);
@@ -421,9 +563,21 @@ template <typename T, int D> int write_d(const WriteParams& p, cudaStream_t s) {
 template <typename T> int write_t(const WriteParams& p, cudaStream_t s) {
     return p.v.D == 64 ? write_d<T, 64>(p, s) : (p.v.D == 128 ? write_d<T, 128>(p, s) : write_d<T, 256>(p, s));
 }
+template <typename T, int D> int append_d(const PagedAppendParams& p, cudaStream_t s) {
+    // 16 rows a CTA where a sequence brings half a block or more, on the mean
+    const int rows = p.n_rows / 8 >= p.n_seq ? kTile : 1;
+    const dim3 grid((unsigned)((p.n_rows + (int64_t)rows - 1) / rows), (unsigned)((2 * p.v.H + kAppendWarps - 1) / kAppendWarps));
+    const auto k = rows == 1 ? paged_append_kernel<T, D, 1> : paged_append_kernel<T, D, kTile>;
+    return (int)launch_k(k, grid, dim3(32 * kAppendWarps), 0, s, true, p);
+}
+template <typename T> int append_t(const PagedAppendParams& p, cudaStream_t s) {
+    return p.v.D == 64 ? append_d<T, 64>(p, s) : (p.v.D == 128 ? append_d<T, 128>(p, s) : append_d<T, 256>(p, s));
+}
 template <typename TO, int D> int read_d(const ReadParams& p, cudaStream_t s) {
+    const dim3 grid((unsigned)((p.n_rows + kReadRows - 1) / kReadRows), p.out[0] && p.out[1] ? 2 : 1);
+    if (p.v.fmt[0] == KVQ_PAGED_E4M3)
+        return (int)launch_k(read_kernel<TO, KVQ_PAGED_E4M3, KVQ_PAGED_E4M3, D>, grid, dim3(kRowThreads), 0, s, true, p);
     return by_formats(p.v, [&](auto k, auto v) {
-        const dim3 grid((unsigned)((p.n_rows + kReadRows - 1) / kReadRows), p.out[0] && p.out[1] ? 2 : 1);
         return (int)launch_k(read_kernel<TO, k.value, v.value, D>, grid, dim3(kRowThreads), 0, s, true, p);
     });
 }
@@ -444,6 +598,10 @@ int launch_norm_rope(const kvq_norm_rope_args& a, int sm_count, void* stream) {
 
 int launch_paged_write(const WriteParams& p, void* stream) {
     return p.dtype == KVQ_F16 ? write_t<__half>(p, (cudaStream_t)stream) : write_t<__nv_bfloat16>(p, (cudaStream_t)stream);
+}
+
+int launch_paged_append(const PagedAppendParams& p, void* stream) {
+    return p.dtype == KVQ_F16 ? append_t<__half>(p, (cudaStream_t)stream) : append_t<__nv_bfloat16>(p, (cudaStream_t)stream);
 }
 
 int launch_paged_read(const ReadParams& p, void* stream) {

@@ -33,7 +33,7 @@ bool geometry(const kvq_paged_config& c, Geometry* g) {
     if (c.n_q_heads % c.n_kv_heads || c.n_q_heads / c.n_kv_heads > kMaxG) return false;
     if (c.page_size < 16 || c.page_size > 256 || (c.page_size & (c.page_size - 1))) return false;
     if ((int64_t)c.n_pages * c.page_size >= (int64_t)1 << 31) return false;
-    const bool k16 = c.k_fmt == KVQ_F16 || c.k_fmt == KVQ_BF16, kq = c.k_fmt == KVQ_Q8_0 || c.k_fmt == KVQ_Q4_0;
+    const bool k16 = c.k_fmt == KVQ_F16 || c.k_fmt == KVQ_BF16, kq = c.k_fmt == KVQ_Q8_0 || c.k_fmt == KVQ_Q4_0 || c.k_fmt == KVQ_PAGED_E4M3;
     if (!k16 && !kq) return false;
     if (c.v_fmt != c.k_fmt && !(c.k_fmt == KVQ_Q8_0 && c.v_fmt == KVQ_Q4_0)) return false;
     if (!(c.softmax_scale >= 0.f) || !std::isfinite(c.softmax_scale)) return false;
@@ -257,6 +257,7 @@ kvq_status kv_paged_write(kvq_paged* h, int32_t layer, int32_t dtype, int32_t n_
     if (st != KVQ_OK) return st;
     if (!dtype16(dtype) || n_tok < 0) return KVQ_EINVAL;
     if (n_tok == 0) return KVQ_OK;
+    if (h->cfg.k_fmt == KVQ_PAGED_E4M3) return KVQ_EUNSUPPORTED;
     const int64_t row = (int64_t)h->cfg.n_kv_heads * h->cfg.head_dim;
     if (!k || !v || !slots || !aligned16(k) || !aligned16(v) || !aligned4(slots)) return KVQ_EINVAL;
     if (!stride_ok(k_stride, row) || !stride_ok(v_stride, row)) return KVQ_EINVAL;
@@ -270,6 +271,36 @@ kvq_status kv_paged_write(kvq_paged* h, int32_t layer, int32_t dtype, int32_t n_
     p.n_tok = n_tok;
     p.dtype = dtype;
     return launched(launch_paged_write(p, stream));
+}
+
+kvq_status kv_paged_append(kvq_paged* h, int32_t layer, int32_t dtype, int32_t n_seq, const int32_t* page_table,
+                           int32_t max_pages, int64_t table_stride, const int32_t* cu_rows, const int32_t* start,
+                           int32_t n_rows, const void* k, int64_t k_stride, const void* v, int64_t v_stride, void* stream) {
+    const kvq_status st = check(h, layer);
+    if (st != KVQ_OK) return st;
+    if (!dtype16(dtype) || n_seq < 0 || n_rows < 0) return KVQ_EINVAL;
+    if (h->cfg.k_fmt != KVQ_PAGED_E4M3) return KVQ_EUNSUPPORTED;
+    if (n_seq == 0 || n_rows == 0) return KVQ_OK;
+    const int64_t row = (int64_t)h->cfg.n_kv_heads * h->cfg.head_dim;
+    if (!k || !v || !page_table || !cu_rows || max_pages <= 0 || table_stride < max_pages) return KVQ_EINVAL;
+    if (!aligned16(k) || !aligned16(v) || !aligned4(page_table) || !aligned4(cu_rows) || !aligned4(start)) return KVQ_EINVAL;
+    if (!stride_ok(k_stride, row) || !stride_ok(v_stride, row)) return KVQ_EINVAL;
+    if (h->cfg.n_kv_heads > 2 * 65535) return KVQ_EUNSUPPORTED;      // grid rows: four (head, K / V) each
+    PagedAppendParams p{};
+    p.v = view(h, layer);
+    p.src[0] = k;
+    p.src[1] = v;
+    p.stride[0] = k_stride;
+    p.stride[1] = v_stride;
+    p.table = page_table;
+    p.cu = cu_rows;
+    p.start = start;
+    p.table_stride = table_stride;
+    p.n_seq = n_seq;
+    p.max_pages = max_pages;
+    p.n_rows = n_rows;
+    p.dtype = dtype;
+    return launched(launch_paged_append(p, stream));
 }
 
 kvq_status kv_paged_read(kvq_paged* h, int32_t layer, int32_t dtype, int32_t n_seq, const int32_t* page_table,
@@ -332,7 +363,8 @@ kvq_status kv_paged_prefill_attn(kvq_paged* h, int32_t layer, int32_t dtype, int
     p.cu = cu_q;
     p.n_rows = n_rows;
     p.max_q = max_q < n_rows ? max_q : n_rows;
-    return launched(launch_paged_prefill(p, &h->maps[2 * (size_t)layer], h->sm_count, stream));
+    const auto launch = p.v.D == 64 ? launch_paged_prefill_64 : (p.v.D == 128 ? launch_paged_prefill_128 : launch_paged_prefill_256);
+    return launched(launch(p, &h->maps[2 * (size_t)layer], h->sm_count, stream));
 }
 
 kvq_status kv_qk_norm_rope(const kvq_norm_rope_args* a, void* stream) {

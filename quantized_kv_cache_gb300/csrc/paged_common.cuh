@@ -75,6 +75,7 @@ __device__ __forceinline__ float tanh_any(float x) {
     return a < 0.25f ? tanh_small(x) : copysignf(t, x);
 }
 
+__device__ __forceinline__ float normal_factor(float f) { return fminf(fmaxf(f, 1.17549435e-38f), 3.40282347e38f); }
 // The score options, in units of log2. A score x = q.k * f, f = (the row's power of two) * scale * log2(e);
 // with a cap, f = .. * scale / softcap and x = softcap * log2(e) * tanh(q.k * f); then the bias.
 struct ScoreRule {
@@ -83,7 +84,7 @@ struct ScoreRule {
     __device__ __forceinline__ bool plain() const { return cap == 0.f && !biased; }
     // kept among fp32's normal numbers: 0 or an infinity times a score of infinity or 0 is no score
     __device__ __forceinline__ float factor(float back) const {
-        return fminf(fmaxf(back * scale * (cap > 0.f ? 1.f / cap : kL2e), 1.17549435e-38f), 3.40282347e38f);
+        return normal_factor(back * scale * (cap > 0.f ? 1.f / cap : kL2e));
     }
     // dist: |distance| in positions; slope_l2: the head's slope * log2(e)
     __device__ __forceinline__ float operator()(float x, int dist, float slope_l2) const {
@@ -112,5 +113,21 @@ template <bool Q8> __device__ __forceinline__ uint32_t cut_scales(uint32_t d) {
     const uint32_t top = Q8 ? kMaxScaleQ8 * 0x10001u : kMaxScaleQ4 * 0x10001u;
     return u32(__hfma2(h2(d), h2(0u), __hmin2(h2(d), h2(top))));
 }
+
+// Two e4m3 codes (the low 16 bits) as fp16 numbers, exactly; a NaN stays one.
+__device__ __forceinline__ uint32_t e4m3_pair(uint32_t c) {
+    uint32_t h;
+    asm("{ .reg .b16 x; cvt.u16.u32 x, %1; cvt.rn.f16x2.e4m3x2 %0, x; }\n" : "=r"(h) : "r"(c));
+    return h;
+}
+// Two numbers as e4m3 codes, nearest even, 448 at most; a NaN stays one.
+__device__ __forceinline__ uint32_t e4m3_codes(float lo, float hi) {
+    uint32_t c;
+    asm("{ .reg .b16 x; cvt.rn.satfinite.e4m3x2.f32 x, %2, %1; cvt.u32.u16 %0, x; }\n" : "=r"(c) : "f"(lo), "f"(hi));
+    return c;
+}
+// 2^e, e from -126 to 127, and the exponent of a power of two among the normal numbers.
+__device__ __forceinline__ float power_of(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+__device__ __forceinline__ int exponent_of(float p) { return (int)((__float_as_uint(p) >> 23) & 255) - 127; }
 }  // namespace
 }  // namespace kvq

@@ -20,7 +20,7 @@
 namespace kvq {
 namespace {
 
-enum { PF_16 = 0, PF_Q8 = 1, PF_Q4 = 2 };   // row encodings: 16-bit values, int8 codes, nibbles
+enum { PF_16 = 0, PF_Q8 = 1, PF_Q4 = 2, PF_E4 = 3 };   // row encodings: 16-bit values, int8 codes, nibbles, e4m3 codes
 
 __device__ __forceinline__ void mma_t(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, __half) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
@@ -59,16 +59,16 @@ __device__ __forceinline__ void byte_pairs(uint32_t r, uint32_t d, uint32_t& o0,
 template <int N> struct Words { uint32_t w[N]; };
 
 template <int D, int PF> struct KGeo {
-    static constexpr int RB = PF == PF_16 ? 2 * D : (PF == PF_Q8 ? D : D / 2);   // row bytes
+    static constexpr int RB = PF == PF_16 ? 2 * D : (PF == PF_Q4 ? D / 2 : D);   // row bytes
     static constexpr int CB = RB / 4 < 16 ? RB / 4 : 16;                          // piece bytes
     static constexpr int NJ = RB / 4 / CB, NW = CB / 4;                           // pieces, words of one
-    static constexpr int CH = PF == PF_16 ? CB / 2 : (PF == PF_Q8 ? CB : CB * 2); // channels of one
+    static constexpr int CH = PF == PF_16 ? CB / 2 : (PF == PF_Q4 ? CB * 2 : CB); // channels of one
 };
 template <int D, int PF> struct VGeo {
     static constexpr int RB = KGeo<D, PF>::RB;
     static constexpr int CB = RB / 8 < 16 ? RB / 8 : 16;
     static constexpr int NJ = RB / 8 / CB, NW = CB / 4;
-    static constexpr int CH = PF == PF_16 ? CB / 2 : (PF == PF_Q8 ? CB : CB * 2);
+    static constexpr int CH = PF == PF_16 ? CB / 2 : (PF == PF_Q4 ? CB * 2 : CB);
 };
 
 // First of the eight consecutive channels that k-steps 2 i and 2 i + 1 of lane t take. Their operand pairs are
@@ -82,7 +82,7 @@ template <int D, int PF> __device__ __forceinline__ int qchan(int i, int t) {
 template <int D, int PF> __device__ __forceinline__ int ochan(int j, int g) { return VGeo<D, PF>::CH * (g + 8 * j); }
 
 // Where a lane finds its pieces and scales in a tile, fixed over the tiles: a tile in shared memory is 16 code rows of RB
-// bytes, then (block formats) the rows' scales. The 16-byte pieces of a 128-byte line are permuted by row so
+// bytes, then (block formats) the rows' scales, or the tile's one scale (e4m3). The 16-byte pieces of a 128-byte line are permuted by row so
 // that the eight lanes of a load phase (K: two rows, four neighbouring pieces; V: rows 0, 2, 4, 6, two
 // neighbouring pieces) hit all banks.
 template <int RB, bool VALUES> __device__ __forceinline__ uint32_t tile_swizzle(uint32_t byte) {
@@ -120,6 +120,13 @@ __device__ __forceinline__ uint32_t ld_half(uint32_t a) {
     return x;
 }
 
+// The scale of an e4m3 tile, cut to what keeps code x scale among fp16's numbers (of Q8_0 / Q4_0 the scales are cut alike).
+template <int D> __device__ __forceinline__ float tile_scale(uint32_t base) {
+    float x;
+    asm volatile("ld.shared.f32 %0, [%1];\n" : "=f"(x) : "r"(base + 16 * D));
+    return fminf(x, (float)(1 << kMaxPowerAttn));
+}
+
 // s[q] += K Q^T of the tile at `base` and query group q.
 template <int D, int PF, int NQ, typename T, typename PLACE>
 __device__ __forceinline__ void tile_scores(uint32_t base, const PLACE& at, const uint32_t (&qf)[D / 16][NQ][2], float (&s)[NQ][4]) {
@@ -139,6 +146,10 @@ __device__ __forceinline__ void tile_scores(uint32_t base, const PLACE& at, cons
         if constexpr (PF == PF_16) {
             step(KS * j, x.w[0], y.w[0], x.w[1], y.w[1]);
             step(KS * j + 1, x.w[2], y.w[2], x.w[3], y.w[3]);
+        } else if constexpr (PF == PF_E4) {                                // codes as they are: the tile's scale goes to the scores
+#pragma unroll
+            for (int i = 0; i < K::NW; ++i)
+                step(KS * j + i, e4m3_pair(x.w[i] & 0xffffu), e4m3_pair(y.w[i] & 0xffffu), e4m3_pair(x.w[i] >> 16), e4m3_pair(y.w[i] >> 16));
         } else {
             const uint32_t d1 = ld_half(sc + K::CH * j / 4), e1 = ld_half(sc + 8 * (D / 16) + K::CH * j / 4);
             const uint32_t d = cut_scales<PF == PF_Q8>(__byte_perm(d1, d1, 0x1010)), e = cut_scales<PF == PF_Q8>(__byte_perm(e1, e1, 0x1010));
@@ -160,7 +171,7 @@ __device__ __forceinline__ void tile_scores(uint32_t base, const PLACE& at, cons
     }
 }
 
-// o += V^T P^T of the tile's 16 positions. With LO, P = p + lo (two bf16 parts).
+// o += V^T P^T of the tile's 16 positions (e4m3: times the tile's scale, in fp32). With LO, P = p + lo (two bf16 parts).
 template <int D, int PF, int NQ, typename T, bool LO, typename PLACE>
 __device__ __forceinline__ void tile_values(uint32_t base, const PLACE& at, const uint32_t (&p)[NQ][2], const uint32_t (&lo)[NQ][2],
                                             float (&o)[D / 16][NQ][4]) {
@@ -168,12 +179,14 @@ __device__ __forceinline__ void tile_values(uint32_t base, const PLACE& at, cons
     static_assert(V::NJ == 1 || V::CB == 16, "pieces j and j + 1 are 128 bytes apart");
     // rows 2t + 8 and 2t + 9: the same permutation (that of 32-byte rows too: two lines on)
     const uint32_t a0 = base + at.v[0], a1 = base + at.v[1], sc = base + at.vs;
+    float scale = 1.f;
+    if constexpr (PF == PF_E4) scale = tile_scale<D>(base);
 #pragma unroll
     for (int j = 0; j < V::NJ; ++j) {
         const Words<V::NW> r0 = ld_words<V::NW>(a0 + 128 * j), r1 = ld_words<V::NW>(a1 + 128 * j);
         const Words<V::NW> r2 = ld_words<V::NW>(a0 + 128 * j + 8 * V::RB), r3 = ld_words<V::NW>(a1 + 128 * j + 8 * V::RB);
         uint32_t d01 = 0, d23 = 0;
-        if constexpr (PF != PF_16) {
+        if constexpr (PF == PF_Q8 || PF == PF_Q4) {
             const uint32_t x = sc + V::CH * j / 2;
             d01 = cut_scales<PF == PF_Q8>(__byte_perm(ld_half(x), ld_half(x + D / 16), 0x5410));
             d23 = cut_scales<PF == PF_Q8>(__byte_perm(ld_half(x + 8 * (D / 16)), ld_half(x + 9 * (D / 16)), 0x5410));
@@ -186,6 +199,13 @@ __device__ __forceinline__ void tile_values(uint32_t base, const PLACE& at, cons
             uint32_t b0[N], b1[N];
             if constexpr (PF == PF_16) {
                 b0[0] = xl; b0[1] = xh; b1[0] = yl; b1[1] = yh;
+            } else if constexpr (PF == PF_E4) {                            // rows 2t, 2t + 1 byte by byte
+                const uint32_t xe = __byte_perm(r0.w[i], r1.w[i], 0x5140), xo = __byte_perm(r0.w[i], r1.w[i], 0x7362);
+                const uint32_t ye = __byte_perm(r2.w[i], r3.w[i], 0x5140), yo = __byte_perm(r2.w[i], r3.w[i], 0x7362);
+                b0[0] = e4m3_pair(xe & 0xffffu); b0[1] = e4m3_pair(xe >> 16);
+                b0[2] = e4m3_pair(xo & 0xffffu); b0[3] = e4m3_pair(xo >> 16);
+                b1[0] = e4m3_pair(ye & 0xffffu); b1[1] = e4m3_pair(ye >> 16);
+                b1[2] = e4m3_pair(yo & 0xffffu); b1[3] = e4m3_pair(yo >> 16);
             } else if constexpr (PF == PF_Q8) {
                 byte_pairs(xl, d01, b0[0], b0[1]);
                 byte_pairs(xh, d01, b0[2], b0[3]);
@@ -203,6 +223,13 @@ __device__ __forceinline__ void tile_values(uint32_t base, const PLACE& at, cons
 #pragma unroll
                 for (int q = 0; q < NQ; ++q) {
                     float (&acc)[4] = o[(V::CH * j + N * i + c) / 2][q];
+                    if constexpr (PF == PF_E4) {
+                        float x[4] = {};
+                        mma_t(x, a, p[q][0], p[q][1], T());
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[e] = fmaf(x[e], scale, acc[e]);
+                        continue;
+                    }
                     mma_t(acc, a, p[q][0], p[q][1], T());
                     if constexpr (LO) mma_t(acc, a, lo[q][0], lo[q][1], T());
                 }
@@ -271,10 +298,13 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
     return d;
 }
 
-template <int D, int PF> constexpr int tile_bytes() { return 16 * KGeo<D, PF>::RB + (PF == PF_16 ? 0 : D); }
+template <int D, int PF> constexpr int tile_bytes() { return 16 * KGeo<D, PF>::RB + (PF == PF_16 ? 0 : (PF == PF_E4 ? 16 : D)); }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory"); }
@@ -298,18 +328,20 @@ __device__ __forceinline__ void copy_tile(uint32_t dst, uint32_t at, const uint8
 #pragma unroll
         for (int i = 0; i < (N + 31) / 32; ++i)
             if (N % 32 == 0 || lane < N) cp_async16(dst + 512 * i + (at ^ (tile_swizzle<RB, VALUES>(512 * i) - 512 * i)), src + 512 * i);
-        if constexpr (PF != PF_16)
+        if constexpr (PF == PF_E4) {
+            if (lane == 0) cp_async4(dst + 16 * RB, unit + ps * RB + off / 4);
+        } else if constexpr (PF != PF_16)
             if (lane < D / 16) cp_async16(dst + 16 * RB + lane * 16, unit + ps * RB + off * (D / 16) + lane * 16);
     } else {
         for (int i = lane; i < tile_bytes<D, PF>() / 16; i += 32) st_zero16(dst + i * 16);
     }
 }
 
-// Zeroes what the rows outside `live` would add (the values of 16-bit rows, the scales of the others): a
+// Zeroes what the rows outside `live` would add (the values of 16-bit rows, e4m3 codes, the scales of the others): a
 // weight of 0 does not keep an infinity or NaN of an unused row out of the product.
 template <int D, int PF> __device__ __forceinline__ void clear_rows(uint32_t base, uint32_t live, int lane) {
     constexpr int RB = KGeo<D, PF>::RB;
-    if constexpr (PF == PF_16) {
+    if constexpr (PF == PF_16 || PF == PF_E4) {
         for (int c = lane; c < RB; c += 32)            // 16 rows x RB / 16 pieces
             if (!((live >> (c / (RB / 16))) & 1)) st_zero16(base + tile_swizzle<RB, true>(c * 16));
     } else {

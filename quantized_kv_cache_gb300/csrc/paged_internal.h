@@ -13,11 +13,19 @@ constexpr int kMaxDecodeCtas = 1024; // bound of a decode launch's CTAs (sizes t
 // fp16's infinity.
 constexpr uint32_t kMaxScaleQ8 = 0x6007, kMaxScaleQ4 = 0x7091;
 
-// Bytes of one code row (D values) and of a row's scales.
-KVQ_HD int paged_row_bytes(int fmt, int D) { return fmt == KVQ_Q8_0 ? D : (fmt == KVQ_Q4_0 ? D / 2 : 2 * D); }
-KVQ_HD int paged_scale_bytes(int fmt, int D) { return (fmt == KVQ_Q8_0 || fmt == KVQ_Q4_0) ? D / 16 : 0; }
+// Exponents of an e4m3 block's power of two: 448 2^120 is above bf16's largest number. The attentions take powers up to 2^7
+// (448 2^7 is an fp16 number, 448 2^8 is none).
+constexpr int kMinPower = -126, kMaxPower = 120, kMaxPowerAttn = 7;
+
+// Bytes of one code row (D values), and of the scales of a unit: a row's by 32 values, or one for a tile of an e4m3 unit (padded to
+// 32 bytes, so that rows and units stay on sectors).
+KVQ_HD int paged_row_bytes(int fmt, int D) { return fmt == KVQ_Q8_0 || fmt == KVQ_PAGED_E4M3 ? D : (fmt == KVQ_Q4_0 ? D / 2 : 2 * D); }
+KVQ_HD int paged_scale_bytes(int fmt, int D, int ps) {
+    if (fmt == KVQ_PAGED_E4M3) return ps / kTile * 4 < 32 ? 32 : ps / kTile * 4;
+    return (fmt == KVQ_Q8_0 || fmt == KVQ_Q4_0) ? ps * (D / 16) : 0;
+}
 KVQ_HD int64_t paged_unit_bytes(int fmt, int D, int ps) {
-    return (int64_t)ps * (paged_row_bytes(fmt, D) + paged_scale_bytes(fmt, D));
+    return (int64_t)ps * paged_row_bytes(fmt, D) + paged_scale_bytes(fmt, D, ps);
 }
 
 // One layer of the pool as the kernels see it.
@@ -35,6 +43,17 @@ struct WriteParams {
     int64_t stride[2];       // elements
     const int32_t* slots;
     int32_t n_tok, dtype;
+};
+
+struct PagedAppendParams {
+    PagedView v;
+    const void* src[2];
+    int64_t stride[2];       // elements
+    const int32_t* table;
+    const int32_t* cu;
+    const int32_t* start;
+    int64_t table_stride;
+    int32_t n_seq, max_pages, n_rows, dtype;
 };
 
 struct ReadParams {
@@ -73,14 +92,18 @@ int resident_ctas(const void* kernel, int threads, int smem, int* ctas);
 int launch_paged_clear_status(uint32_t* status, uint32_t bits);   // on the legacy stream
 int launch_norm_rope(const kvq_norm_rope_args& a, int sm_count, void* stream);
 int launch_paged_write(const WriteParams& p, void* stream);
+int launch_paged_append(const PagedAppendParams& p, void* stream);
 int launch_paged_read(const ReadParams& p, void* stream);
 int launch_paged_decode_64(const PagedAttnParams& p, int sm_count, void* stream);
 int launch_paged_decode_128(const PagedAttnParams& p, int sm_count, void* stream);
 int launch_paged_decode_256(const PagedAttnParams& p, int sm_count, void* stream);
 // maps: two CUtensorMap, the layer's K and V area as [units][page_size][head_dim] of 16-bit values in boxes of
 // prefill_box_rows rows x 64 (16-bit pages; read for no other format)
-int launch_paged_prefill(const PagedAttnParams& p, const void* maps, int sm_count, void* stream);
-int prefill_box_rows(int D, int ps);
+int launch_paged_prefill_64(const PagedAttnParams& p, const void* maps, int sm_count, void* stream);
+int launch_paged_prefill_128(const PagedAttnParams& p, const void* maps, int sm_count, void* stream);
+int launch_paged_prefill_256(const PagedAttnParams& p, const void* maps, int sm_count, void* stream);
+KVQ_HD constexpr int prefill_tile(int D) { return D == 256 ? 64 : 128; }    // positions of a KV tile
+KVQ_HD int prefill_box_rows(int D, int ps) { return ps < prefill_tile(D) ? ps : prefill_tile(D); }
 // A run's partial result of a head: 16 maxima, 16 sums, the outputs.
 KVQ_HD int64_t partial_floats(int G, int D) { return 32 + (int64_t)G * D; }
 // Before the partials: n_seq + 1 int64, the tiles before each sequence.

@@ -24,12 +24,12 @@ _DT_READ[torch.float32] = _lib.PAGED_F32
 
 
 def paged_config(n_layers, n_kv_heads, head_dim, n_q_heads, page_size, n_pages, k_fmt="f16", v_fmt=None, softmax_scale=0.0):
-    """A kvq_paged_config; formats by name ("f16", "bf16", "q8_0", "q4_0"), v_fmt None meaning k_fmt."""
+    """A kvq_paged_config; formats by name ("f16", "bf16", "q8_0", "q4_0", "e4m3"), v_fmt None meaning k_fmt."""
     c = _lib.kvq_paged_config()
     c.n_layers, c.n_kv_heads, c.head_dim, c.n_q_heads = n_layers, n_kv_heads, head_dim, n_q_heads
     c.page_size, c.n_pages = page_size, n_pages
-    c.k_fmt = _lib.FMT_NAMES[k_fmt]
-    c.v_fmt = _lib.FMT_NAMES[k_fmt if v_fmt is None else v_fmt]
+    c.k_fmt = _lib.PAGED_FMT_NAMES[k_fmt]
+    c.v_fmt = _lib.PAGED_FMT_NAMES[k_fmt if v_fmt is None else v_fmt]
     c.softmax_scale = softmax_scale
     return c
 
@@ -147,6 +147,22 @@ class PagedKVCache:
         sp = _ints(slots, "slots", n, self._dev)
         _no_grad(k, v)
         _guarded(self._dev, _lib.kv_paged_write, self.h, layer, dt, n, k.data_ptr(), ks, v.data_ptr(), vs, sp, stream)
+
+    def append(self, layer, k, v, page_table, cu_rows, start=None, stream=0):
+        """Rows cu_rows[b] .. cu_rows[b+1]-1 of k, v ([rows, H, D] fp16 or bf16, token stride free) become positions
+        start[b].. of sequence b in "e4m3" pages, where 16 positions share a scale. cu_rows: int32 [sequences + 1]; start:
+        int32 [sequences] (None: zeros)."""
+        dt, dev = _type_of(k, "k", _DT), self._dev
+        rows, ks = _rows(k, "k", self._H, self._D, dev, k.dtype)
+        nv, vs = _rows(v, "v", self._H, self._D, dev, k.dtype)
+        if nv != rows:
+            _bad("k and v: the same number of tokens is wanted")
+        tp, n, w, ts = self._table(page_table)
+        cp = _ints(cu_rows, "cu_rows", n + 1, dev)
+        sp = None if start is None else _ints(start, "start", n, dev)
+        _no_grad(k, v)
+        _guarded(dev, _lib.kv_paged_append, self.h, layer, dt, n, tp, w, ts, cp, sp, rows, k.data_ptr(), ks, v.data_ptr(), vs,
+                 stream)
 
     def _table(self, table):
         """(address, sequences, entries of a row, row stride) of a page table."""
