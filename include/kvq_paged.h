@@ -155,6 +155,35 @@ kvq_status kv_paged_prefill_attn(kvq_paged* h, int32_t layer, int32_t dtype, int
                                  const int32_t* lens, void* out, const kvq_attn_opts* opts, void* workspace,
                                  size_t ws_bytes, void* stream);
 
+/* Arguments of kv_prompt_attn: packed prompts, sequence b's tokens in rows cu[b] .. cu[b+1] - 1 of q, k, v and out. */
+typedef struct {
+    int32_t dtype;             /* KVQ_F16 or KVQ_BF16: q, k, v, out */
+    int32_t n_seq;             /* up to 65,535 */
+    int32_t n_rows;
+    int32_t max_q;             /* at least the longest prompt; of a longer one only the first max_q tokens are computed */
+    int32_t n_q_heads;         /* a multiple of n_kv_heads, with n_q_heads / n_kv_heads <= 16 */
+    int32_t n_kv_heads;
+    int32_t head_dim;          /* 64, 128 or 256 */
+    float softmax_scale;       /* 0 selects 1/sqrt(head_dim) */
+    const void* q;             /* device [n_rows][n_q_heads][head_dim], stride q_stride */
+    const void* k;             /* device [n_rows][n_kv_heads][head_dim], stride k_stride */
+    const void* v;
+    const int32_t* cu;         /* device [n_seq + 1], non-decreasing */
+    void* out;                 /* device [n_rows][n_q_heads][head_dim], contiguous */
+    int64_t q_stride, k_stride, v_stride;
+} kvq_prompt_args;
+
+/* kv_prompt_attn — causal attention of whole prompts over their own rows: the token at position i of a sequence sees its positions
+ * 0 .. i (options as for the paged calls). No cache is read or needed: before or beside the calls that store k and v, of either
+ * cache. Rows of out and lse outside [cu[0], cu[n_seq]) stay as they are, and so do those of a sequence whose bounds are
+ * no rows of the call. workspace: device, 16-byte aligned, >= kv_prompt_required_bytes for the call; its first 256 bytes
+ * hold a status word (the bits above), which its owner zeroes once and kv_prompt_get_status reads; the rest is written before
+ * it is read. Calls that may overlap need workspaces of their own. The current device's pointers. */
+kvq_status kv_prompt_required_bytes(int64_t n_rows, int32_t n_q_heads, int32_t head_dim, size_t* workspace_bytes);
+kvq_status kv_prompt_attn(const kvq_prompt_args* args, const kvq_attn_opts* opts, void* workspace, size_t ws_bytes, void* stream);
+/* kv_prompt_get_status — as kv_paged_get_status, of the calls with this workspace. */
+kvq_status kv_prompt_get_status(void* workspace, uint32_t* word);
+
 /* Arguments of kv_qk_norm_rope. Outputs may be the inputs (in place, equal strides); otherwise they
  * must not overlap them. The rows of q and k are different rows (slices of one buffer, not the same slice). */
 typedef struct {
@@ -184,6 +213,14 @@ typedef struct {
  * b cos + a sin); fp32 arithmetic, one rounding at the end. The rows of a token whose position is
  * outside [0, max_pos) are set to NaN. Needs no cache handle; the current device's pointers. */
 kvq_status kv_qk_norm_rope(const kvq_norm_rope_args* args, void* stream);
+
+/* kv_qk_norm_rope_axes — kv_qk_norm_rope with positions on 1 to 4 axes (time, height and width of a patch, say): positions
+ * is device int32 [n_axes][n_tok], and frequency i of the rot_dim / 2 turns its pair by the token's position on one of the axes,
+ * sections[a] (host, >= 0, rot_dim / 2 in all) of them by axis a: in runs, axis after axis, or (cyclic != 0) dealt to the axes in
+ * turn until each has its number. One table serves all axes. The rows of a token that has a position outside [0, max_pos) on an
+ * axis with frequencies are set to NaN. rot_dim is above 0. */
+kvq_status kv_qk_norm_rope_axes(const kvq_norm_rope_args* args, int32_t n_axes, const int32_t* sections, int32_t cyclic,
+                                void* stream);
 
 #ifdef __cplusplus
 }

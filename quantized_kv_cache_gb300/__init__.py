@@ -4,7 +4,7 @@ The work is done by ``lib/libkvq.so`` (hand-written CUDA behind the C ABI of
 ``include/kvq.h``); this package only marshals arguments (``_lib``), names the measured
 workloads (``configs``), draws seeded synthetic inputs (``synth``) and wraps device memory
 owned by PyTorch (``KVCache``; the paged cache and what goes with it: ``PagedKVCache``,
-``paged_config``, ``qk_norm_rope``). There is no CPU fallback: without the shared library every call
+``paged_config``, ``qk_norm_rope``, ``prompt_attn``, ``prompt_workspace``, ``prompt_status``). There is no CPU fallback: without the shared library every call
 raises.
 """
 
@@ -16,7 +16,7 @@ from ._lib import (KVQError, kvq_config, kv_bytes_per_token, kv_required_bytes, 
 
 def __getattr__(name):
     # .paged imports torch, which importing this package does not
-    if name in ("PagedKVCache", "paged_config", "qk_norm_rope"):
+    if name in ("PagedKVCache", "paged_config", "prompt_attn", "prompt_status", "prompt_workspace", "qk_norm_rope"):
         from . import paged
         return getattr(paged, name)
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -72,6 +72,12 @@ class kvq_norm_rope_args(ctypes.Structure):
                 [(n, ctypes.c_int64) for n in ("q_stride", "k_stride", "q_out_stride", "k_out_stride")])
 
 
+class kvq_prompt_args(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("dtype", "n_seq", "n_rows", "max_q", "n_q_heads", "n_kv_heads", "head_dim")] +
+                [("softmax_scale", ctypes.c_float)] + [(n, ctypes.c_void_p) for n in ("q", "k", "v", "cu", "out")] +
+                [(n, ctypes.c_int64) for n in ("q_stride", "k_stride", "v_stride")])
+
+
 _lib = None
 
 P = ctypes.c_void_p
@@ -120,6 +126,10 @@ _SIGS = {
     "kv_paged_decode_attn": [P, I32, I32, I32, P, I64, P, I32, I64, P, P, ctypes.POINTER(kvq_attn_opts), P, SZ, P],
     "kv_paged_prefill_attn": [P, I32, I32, I32, I32, I32, P, I64, P, P, I32, I64, P, P, ctypes.POINTER(kvq_attn_opts), P,
                               SZ, P],
+    "kv_prompt_required_bytes": [I64, I32, I32, ctypes.POINTER(SZ)],
+    "kv_prompt_attn": [ctypes.POINTER(kvq_prompt_args), ctypes.POINTER(kvq_attn_opts), P, SZ, P],
+    "kv_prompt_get_status": [P, ctypes.POINTER(ctypes.c_uint32)],
+    "kv_qk_norm_rope_axes": [ctypes.POINTER(kvq_norm_rope_args), I32, ctypes.POINTER(I32), I32, P],
     "kv_qk_norm_rope": [ctypes.POINTER(kvq_norm_rope_args), P],
     "kvq_synth_fill": [P, I64, ctypes.c_int, ctypes.c_int, ctypes.POINTER(ctypes.c_uint64), I64, P, P, P],
 }
@@ -377,6 +387,31 @@ def kv_paged_prefill_attn(h, layer, dtype, n_seq, n_rows, max_q, q_ptr, q_stride
     _check("kv_paged_prefill_attn", load().kv_paged_prefill_attn(h, layer, dtype, n_seq, n_rows, max_q, q_ptr, q_stride,
                                                                  cu_ptr, table_ptr, max_pages, table_stride, lens_ptr,
                                                                  out_ptr, opts, ws_ptr, ws_bytes, stream))
+
+
+def kv_prompt_required_bytes(n_rows, n_q_heads, head_dim):
+    n = SZ()
+    _check("kv_prompt_required_bytes", load().kv_prompt_required_bytes(n_rows, n_q_heads, head_dim, ctypes.byref(n)))
+    return n.value
+
+
+def kv_prompt_attn(args, opts, ws_ptr, ws_bytes, stream=0):
+    """args: a kvq_prompt_args; opts: a kvq_attn_opts or None."""
+    _check("kv_prompt_attn", load().kv_prompt_attn(args, opts, ws_ptr, ws_bytes, stream))
+
+
+def kv_prompt_get_status(ws_ptr):
+    word = ctypes.c_uint32()
+    code = load().kv_prompt_get_status(ws_ptr, ctypes.byref(word))
+    if code not in (0, 5):
+        raise KVQError("kv_prompt_get_status", code)
+    return word.value
+
+
+def kv_qk_norm_rope_axes(args, sections, cyclic, stream=0):
+    """args: a kvq_norm_rope_args; sections: frequencies of each axis."""
+    n = len(sections)
+    _check("kv_qk_norm_rope_axes", load().kv_qk_norm_rope_axes(args, n, (I32 * n)(*sections), cyclic, stream))
 
 
 def kv_qk_norm_rope(args, stream=0):

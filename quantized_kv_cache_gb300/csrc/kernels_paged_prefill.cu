@@ -1,4 +1,4 @@
-// Attention of chunks of new tokens over pages, on the tensor cores (tcgen05).
+// Attention of chunks of new tokens over pages, and of whole prompts over their own rows, on the tensor cores (tcgen05).
 //
 // The rows of a KV head are the chunk's tokens times the G query heads that read it, row r = token r / G,
 // head r % G, so K and V tiles serve all of them. A CTA holds NT tiles of 128 rows (two up to D = 128, one
@@ -56,8 +56,9 @@ struct Chunk {
 __device__ __forceinline__ Chunk chunk_of(const PagedAttnParams& p, int b, bool report) {
     Chunk c;
     const int64_t cap = (int64_t)p.max_pages << p.v.ps_shift;
-    const int len = p.lens[b], c0 = p.cu[b], c1 = p.cu[b + 1];
+    const int c0 = p.cu[b], c1 = p.cu[b + 1];
     const bool bad = c0 < 0 || c1 > p.n_rows || c1 < c0;
+    const int len = p.lens ? p.lens[b] : (bad ? 0 : c1 - c0);       // a prompt holds its own rows
     c.len = len < 0 ? 0 : (len > cap ? (int)cap : len);
     c.row0 = c0;
     c.n = bad ? 0 : c1 - c0;
@@ -276,11 +277,41 @@ __device__ __forceinline__ void apply_rule(uint32_t (&s)[32], const ScoreRule& r
     }
 }
 
+// Whole prompts: the row tiles of all sequences are one line, so that ragged ones leave no block without work. The sequence of
+// tile `slot`, and the tile's number in it (-1: the line is shorter); called by whole warps.
+__device__ __forceinline__ int find_tile(const PagedAttnParams& p, int slot, int tile_rows, bool report, int* tile) {
+    const int lane = threadIdx.x & 31;
+    int before = 0, found = -1;
+    for (int i = 0; i < p.n_seq && (found < 0 || report); i += 32) {
+        const int b = i + lane;
+        int n = 0;
+        if (b < p.n_seq) n = (chunk_of(p, b, report).n * p.G + tile_rows - 1) / tile_rows;
+        int sum = n;
+#pragma unroll
+        for (int s = 1; s < 32; s <<= 1) {
+            const int y = __shfl_up_sync(kAll, sum, s);
+            if (lane >= s) sum += y;
+        }
+        const unsigned m = __ballot_sync(kAll, found < 0 && before + sum > slot);
+        if (m) {
+            const int k = __ffs(m) - 1;
+            found = i + k;
+            *tile = slot - before - __shfl_sync(kAll, sum - n, k);
+        }
+        before += __shfl_sync(kAll, sum, 31);
+    }
+    return found;
+}
+
+// Where K and V rows come from: pages of 16-bit rows (0) or codes (1 int8, 2 nibbles, 3 e4m3), or the prompts' own rows (4).
+constexpr int kRows = 4;
+constexpr bool codes_of(int kf) { return kf > 0 && kf < kRows; }
+
 template <int D, int KF, int VF, typename T, typename TQ>
-__global__ void __launch_bounds__(Geo<D, KF != 0>::threads, 1) prefill_kernel(const __grid_constant__ PagedAttnParams p,
+__global__ void __launch_bounds__(Geo<D, codes_of(KF)>::threads, 1) prefill_kernel(const __grid_constant__ PagedAttnParams p,
                                                                         const __grid_constant__ CUtensorMap k_map,
                                                                         const __grid_constant__ CUtensorMap v_map, int splits) {
-    using GE = Geo<D, KF != 0>;
+    using GE = Geo<D, codes_of(KF)>;
     constexpr int NT = GE::NT, BN = GE::BN;
     constexpr bool BF = std::is_same<T, __nv_bfloat16>::value;
     // Weights are 2^(s - m), m = the largest score when m last moved, less kUp; it moves when a score is more than kLazy
@@ -295,15 +326,20 @@ __global__ void __launch_bounds__(Geo<D, KF != 0>::threads, 1) prefill_kernel(co
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort, s_skip[2];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int h = blockIdx.x, b = blockIdx.z / splits, split = blockIdx.z % splits, G = p.G;
+    const int h = blockIdx.x, split = blockIdx.z % splits, G = p.G;
     const uint32_t full = su32(bars), empty = full + 16, q_full = full + 32, s_full = full + 40, p_full = full + 56,
                    o_done = full + 72;
     grid_dep_wait();
-    const Chunk c = chunk_of(p, b, h == 0 && blockIdx.y == 0 && split == 0 && threadIdx.x == 0);
+    int b = blockIdx.z / splits, tile = blockIdx.y;
+    if constexpr (KF == kRows) {
+        b = find_tile(p, blockIdx.y, GE::rows, h == 0 && blockIdx.y == 0 && split == 0 && warp == 0, &tile);
+        if (b < 0) return;
+    }
+    const Chunk c = chunk_of(p, b, KF != kRows && h == 0 && blockIdx.y == 0 && split == 0 && threadIdx.x == 0);
     // tiles in descending order: the last rows see the most positions and start first
     const int rows = c.n * G, row_tiles = (rows + GE::rows - 1) / GE::rows;
-    if ((int)blockIdx.y >= row_tiles) return;
-    const int r0 = (row_tiles - 1 - (int)blockIdx.y) * GE::rows, r1 = min(rows, r0 + GE::rows);
+    if (tile >= row_tiles) return;
+    const int r0 = (row_tiles - 1 - tile) * GE::rows, r1 = min(rows, r0 + GE::rows);
     const KvTiles<BN> kv(c, c.pos0 + r0 / G, c.pos0 + (r1 - 1) / G, p.window);
     const int i0 = (int)((int64_t)kv.n * split / splits), nt = (int)((int64_t)kv.n * (split + 1) / splits) - i0;
     const int active = r1 - r0 > 128 ? 2 : 1;                  // row tiles that hold rows
@@ -312,7 +348,7 @@ __global__ void __launch_bounds__(Geo<D, KF != 0>::threads, 1) prefill_kernel(co
     if (threadIdx.x == 0) {
         mbar_init(q_full, 128 * active);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(full + 8 * i, 32 * GE::prod);
+            mbar_init(full + 8 * i, KF == kRows ? 32 : 32 * GE::prod);
             mbar_init(empty + 8 * i, 1);
             mbar_init(s_full + 8 * i, 1);
             mbar_init(p_full + 8 * i, 128);
@@ -391,7 +427,24 @@ __global__ void __launch_bounds__(Geo<D, KF != 0>::threads, 1) prefill_kernel(co
             // ------------------------------------------------------------------ K and V tiles
             const int pw = warp - GE::first_prod;               // 8-row blocks pw, pw + prod, ..
             const int32_t* table = p.table + (int64_t)b * p.table_stride;
-            if constexpr (KF == 0) {
+            if constexpr (KF == kRows) {
+                // Boxes of BN rows x 64 channels, one per lane of the first producer. A tile that ends behind the prompt
+                // holds the next one's rows there (behind the last row zeros): no query here sees them.
+                if (pw == 0) {
+                    bool may = true;                                // as for the products
+                    for (int n = 1; n <= 2 * nt; ++n) {             // items as for 16-bit pages below
+                        const int u = n >> 1, w = n & 1 ? 0 : 1, i = w ? u - 1 : u;
+                        const uint32_t bar = full + 8 * (u & 1);
+                        if (w && u >= 2) may &= wait(empty + 8 * (u & 1), ((u >> 1) - 1) & 1);
+                        if (lane == 0 && may) tc_expect(bar, GE::slot);
+                        __syncwarp();
+                        if (lane < D / 64 && may)
+                            tma_load3(ring + (2 * w + (i & 1)) * GE::slot + tile_byte(BN, 0, 64 * lane), w ? &v_map : &k_map, 64 * lane, h,
+                                      c.row0 + kv.at(i0 + i), bar);
+                        if (w == 0 || u == nt) mbar_arrive(bar);    // the last item of the stage
+                    }
+                }
+            } else if constexpr (KF == 0) {
                 // page numbers of a tile's 16-row blocks, one per lane, loaded a tile ahead
                 auto pages_of = [&](int i) {
                     int page = -1;
@@ -793,13 +846,18 @@ template <int D, typename TQ> __global__ void __launch_bounds__(kJT) prefill_joi
 
 template <int D, int KF, int VF, typename T, typename TQ>
 int prefill_run(const PagedAttnParams& p, const CUtensorMap* maps, int sm_count, cudaStream_t s) {
-    using GE = Geo<D, KF != 0>;
+    using GE = Geo<D, codes_of(KF)>;
     const auto k = prefill_kernel<D, KF, VF, T, TQ>;
     int res = 0;
     if (const int e = resident_ctas((const void*)k, GE::threads, GE::smem, &res)) return e;
     const int64_t chunk = (int64_t)p.max_q * p.G;
-    const int splits = prefill_splits((int64_t)p.n_rows * p.G, p.n_seq, p.v.H, GE::rows, sm_count);
-    const dim3 grid(p.v.H, (unsigned)((chunk + GE::rows - 1) / GE::rows), (unsigned)(p.n_seq * splits));
+    int splits = prefill_splits((int64_t)p.n_rows * p.G, p.n_seq, p.v.H, GE::rows, sm_count);
+    dim3 grid(p.v.H, (unsigned)((chunk + GE::rows - 1) / GE::rows), (unsigned)(p.n_seq * splits));
+    if constexpr (KF == kRows) {
+        splits = min(splits, prompt_splits(p.max_q, D));
+        grid.y = (unsigned)prompt_tiles(p.n_rows, p.n_seq, p.G, D);
+        grid.z = splits;
+    }
     cudaError_t e = launch_k(k, grid, dim3(GE::threads), GE::smem, s, true, p, maps[0], maps[1], splits);
     if (e == cudaSuccess && splits > 1) {
         constexpr int R = kJT / (D / 8);
@@ -827,10 +885,15 @@ template <int D> int prefill_d(const PagedAttnParams& p, const CUtensorMap* m, i
 }  // namespace
 
 // One head dimension per compilation of this file (KVQ_D), so that they build side by side.
-#define KVQ_NAME2(d) launch_paged_prefill_##d
-#define KVQ_NAME(d) KVQ_NAME2(d)
-int KVQ_NAME(KVQ_D)(const PagedAttnParams& p, const void* maps, int sms, void* stream) {
+#define KVQ_NAME2(n, d) launch_##n##_##d
+#define KVQ_NAME(n, d) KVQ_NAME2(n, d)
+int KVQ_NAME(paged_prefill, KVQ_D)(const PagedAttnParams& p, const void* maps, int sms, void* stream) {
     return prefill_d<KVQ_D>(p, (const CUtensorMap*)maps, sms, (cudaStream_t)stream);
+}
+int KVQ_NAME(prompt_attn, KVQ_D)(const PagedAttnParams& p, const void* maps, int sms, void* stream) {
+    const CUtensorMap* m = (const CUtensorMap*)maps;
+    return p.dtype == KVQ_F16 ? prefill_run<KVQ_D, kRows, kRows, __half, __half>(p, m, sms, (cudaStream_t)stream)
+                              : prefill_run<KVQ_D, kRows, kRows, __nv_bfloat16, __nv_bfloat16>(p, m, sms, (cudaStream_t)stream);
 }
 
 }  // namespace kvq

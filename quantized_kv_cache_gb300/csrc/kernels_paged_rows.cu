@@ -183,6 +183,180 @@ int norm_rope_t(const kvq_norm_rope_args& a, int sm_count, cudaStream_t s) {
     }
 }
 
+// ---------------------------------------------------------------------------- norm and rotation, positions on several axes
+// A lane holds both values of each of its eight pairs, 16 channels: two pieces of eight, half of the rotated channels apart (or, with
+// pairs (2i, 2i + 1), next to one another), so that no value is fetched from another lane or weighed twice. Its eight
+// cosines and sines come once per token, each from the table's row of its frequency's axis; arithmetic goes two values at a time.
+__device__ __forceinline__ float2 neg2(float2 x) { return make_float2(-x.x, -x.y); }
+template <typename T, int D, bool INTER>
+__global__ void __launch_bounds__(kRowThreads, 2) norm_rope_axes_kernel(const __grid_constant__ kvq_norm_rope_args a,
+                                                                        const __grid_constant__ RopeAxes ax, int heads, int parts) {
+    constexpr int LPR = D / 16, RPW = 32 / LPR, U = 2;           // lanes of a row, rows of a warp, in flight
+    const int lane = threadIdx.x & 31, li = lane % LPR, sub = lane / LPR;
+    grid_dep_wait();
+    const int64_t task = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
+    const int t = (int)(task / parts);
+    if (t >= a.n_tok) return;
+    const int nh = a.n_q_heads + a.n_k_heads;
+    const int h0 = (int)(task % parts) * heads, h1 = min(nh, h0 + heads);
+    const int half = a.rot_dim / 2, np = half / 8;
+    const bool rotated = li < np;
+    // first channels of the lane's two pieces; lanes behind the rotated ones take two pieces side by side
+    const int c0 = INTER || !rotated ? 16 * li : 8 * li, c1 = INTER || !rotated ? c0 + 8 : c0 + half;
+    const auto row_of = [&](int h) {
+        return h < a.n_q_heads ? (const T*)a.q + t * a.q_stride + (int64_t)h * D
+                               : (const T*)a.k + t * a.k_stride + (int64_t)(h - a.n_q_heads) * D;
+    };
+    uint4 ahead[U][2] = {};
+    const auto load_rows = [&](int hb) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int h = hb + u * RPW + sub;
+            if (h >= h1) continue;
+            const T* src = row_of(h);
+            ahead[u][0] = *reinterpret_cast<const uint4*>(src + c0);
+            ahead[u][1] = *reinterpret_cast<const uint4*>(src + c1);
+        }
+    };
+    load_rows(h0);
+    int pos[4] = {};
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if ((ax.used >> i) & 1) {
+            pos[i] = a.positions[(int64_t)i * a.n_tok + t];
+            bad |= pos[i] < 0 || pos[i] >= a.max_pos;
+        }
+    float2 cs[4] = {}, sn[4] = {};                               // of pairs 2 i, 2 i + 1 of the lane's
+    if (rotated && !bad) {
+        const uint32_t of = ax.of8[li];
+        const auto at = [&](int e) {
+            const int x = (of >> (2 * e)) & 3;
+            return a.cos_sin + (int64_t)(x & 2 ? (x & 1 ? pos[3] : pos[2]) : (x & 1 ? pos[1] : pos[0])) * a.rot_dim + 8 * li + e;
+        };
+        if (of == (of & 3) * 0x5555u) {                          // one axis: its row by vectors
+            const float* p = at(0);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float4 c = *reinterpret_cast<const float4*>(p + 4 * i), s = *reinterpret_cast<const float4*>(p + half + 4 * i);
+                cs[2 * i] = make_float2(c.x, c.y);
+                cs[2 * i + 1] = make_float2(c.z, c.w);
+                sn[2 * i] = make_float2(s.x, s.y);
+                sn[2 * i + 1] = make_float2(s.z, s.w);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float *p = at(2 * i), *q = at(2 * i + 1);
+                cs[i] = make_float2(*p, *q);
+                sn[i] = make_float2(p[half], q[half]);
+            }
+        }
+    }
+    float2 w[8];                                                  // the side's weights, channel by channel as the values
+    bool weighed = false;
+    int side = -1;
+    for (int hb = h0; hb < h1; hb += U * RPW) {
+        uint4 x[U][2];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            x[u][0] = ahead[u][0];
+            x[u][1] = ahead[u][1];
+        }
+        load_rows(hb + U * RPW);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int h = hb + u * RPW + sub, now = h < a.n_q_heads ? 0 : 1;
+            float2 y[8];                                          // piece 0: y[0..3], piece 1: y[4..7]
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                y[4 * i] = Two<T>::unpack(x[u][i].x);
+                y[4 * i + 1] = Two<T>::unpack(x[u][i].y);
+                y[4 * i + 2] = Two<T>::unpack(x[u][i].z);
+                y[4 * i + 3] = Two<T>::unpack(x[u][i].w);
+            }
+            float2 s2 = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s2 = __ffma2_rn(y[i], y[i], s2);
+            float ss = s2.x + s2.y;
+#pragma unroll
+            for (int s = 1; s < LPR; s <<= 1) ss += __shfl_xor_sync(kAll, ss, s);
+            if (h >= h1) continue;
+            if (now != side) {
+                side = now;
+                const T* wt = (const T*)(now ? a.k_weight : a.q_weight);
+                weighed = wt != nullptr;
+                if (weighed) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint4 z = *reinterpret_cast<const uint4*>(wt + (i ? c1 : c0));
+                        w[4 * i] = Two<T>::unpack(z.x);
+                        w[4 * i + 1] = Two<T>::unpack(z.y);
+                        w[4 * i + 2] = Two<T>::unpack(z.z);
+                        w[4 * i + 3] = Two<T>::unpack(z.w);
+                    }
+                }
+            }
+            if (weighed) {
+                const float r = rsqrtf(ss * (1.0f / D) + a.eps);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) y[i] = __fmul2_rn(y[i], __fmul2_rn(w[i], make_float2(r, r)));
+            }
+            if (rotated) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    // first and second values of pairs 2 i, 2 i + 1
+                    const float2 p = INTER ? make_float2(y[2 * i].x, y[2 * i + 1].x) : y[i];
+                    const float2 q = INTER ? make_float2(y[2 * i].y, y[2 * i + 1].y) : y[4 + i];
+                    const float2 f = __ffma2_rn(p, cs[i], neg2(__fmul2_rn(q, sn[i]))), g = __ffma2_rn(q, cs[i], __fmul2_rn(p, sn[i]));
+                    if constexpr (INTER) {
+                        y[2 * i] = make_float2(f.x, g.x);
+                        y[2 * i + 1] = make_float2(f.y, g.y);
+                    } else {
+                        y[i] = f;
+                        y[4 + i] = g;
+                    }
+                }
+            }
+            if (bad) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) y[i].x = y[i].y = __int_as_float(0x7fffffff);
+            }
+            T* dst = now ? (T*)a.k_out + t * a.k_out_stride + (int64_t)(h - a.n_q_heads) * D
+                         : (T*)a.q_out + t * a.q_out_stride + (int64_t)h * D;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                *reinterpret_cast<uint4*>(dst + (i ? c1 : c0)) =
+                    make_uint4(Two<T>::pack(y[4 * i].x, y[4 * i].y), Two<T>::pack(y[4 * i + 1].x, y[4 * i + 1].y),
+                               Two<T>::pack(y[4 * i + 2].x, y[4 * i + 2].y), Two<T>::pack(y[4 * i + 3].x, y[4 * i + 3].y));
+        }
+    }
+}
+
+template <typename T, int D>
+int norm_rope_axes_d(const kvq_norm_rope_args& a, const RopeAxes& x, int sm_count, cudaStream_t s) {
+    constexpr int RPW = 512 / D;
+    const int nh = a.n_q_heads + a.n_k_heads;
+    // head rows per warp: all of a token's while that gives every SM 32 warps, fewer below (as for one axis)
+    int heads = (nh + RPW - 1) / RPW * RPW;
+    const int64_t want = (int64_t)sm_count * 32;
+    while (heads > RPW && (int64_t)a.n_tok * ((nh + heads - 1) / heads) < want) heads = (heads / 2 + RPW - 1) / RPW * RPW;
+    const int parts = (nh + heads - 1) / heads;
+    const unsigned grid = (unsigned)(((int64_t)a.n_tok * parts + kRowThreads / 32 - 1) / (kRowThreads / 32));
+    const auto k = a.interleaved ? norm_rope_axes_kernel<T, D, true> : norm_rope_axes_kernel<T, D, false>;
+    return (int)launch_k(k, dim3(grid), dim3(kRowThreads), 0, s, true, a, x, heads, parts);
+}
+
+template <typename T>
+int norm_rope_axes_t(const kvq_norm_rope_args& a, const RopeAxes& x, int sm_count, cudaStream_t s) {
+    switch (a.head_dim) {
+        case 64: return norm_rope_axes_d<T, 64>(a, x, sm_count, s);
+        case 128: return norm_rope_axes_d<T, 128>(a, x, sm_count, s);
+        case 256: return norm_rope_axes_d<T, 256>(a, x, sm_count, s);
+        default: return norm_rope_axes_d<T, 512>(a, x, sm_count, s);
+    }
+}
+
 // ---------------------------------------------------------------------------- write
 // Quantises 16 values; a 32-value block is two neighbouring lanes. The block's largest magnitude is taken on the
 // bits (a NaN compares above infinity, so it reaches the scale). c: the codes as the low bits of 1.5 * 2^23 + q, which
@@ -594,6 +768,11 @@ int launch_paged_clear_status(uint32_t* status, uint32_t bits) {
 int launch_norm_rope(const kvq_norm_rope_args& a, int sm_count, void* stream) {
     return a.dtype == KVQ_F16 ? norm_rope_t<__half>(a, sm_count, (cudaStream_t)stream)
                               : norm_rope_t<__nv_bfloat16>(a, sm_count, (cudaStream_t)stream);
+}
+
+int launch_norm_rope_axes(const kvq_norm_rope_args& a, const RopeAxes& x, int sm_count, void* stream) {
+    return a.dtype == KVQ_F16 ? norm_rope_axes_t<__half>(a, x, sm_count, (cudaStream_t)stream)
+                              : norm_rope_axes_t<__nv_bfloat16>(a, x, sm_count, (cudaStream_t)stream);
 }
 
 int launch_paged_write(const WriteParams& p, void* stream) {

@@ -96,33 +96,75 @@ size_t workspace_floats(const kvq_paged_config& c, int64_t seqs, int64_t rows) {
     return a > b ? a : b;
 }
 
+// The driver's call that encodes a tensor map; null where it is not found.
+using EncodeMap = decltype(&cuTensorMapEncodeTiled);
+EncodeMap encode_map() {
+    static const EncodeMap known = [] {
+        void* fn = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            fn = nullptr;
+        return (EncodeMap)fn;
+    }();
+    return known;
+}
+
+// A map of 16-bit values [dims[2]][dims[1]][dims[0]] (strides in bytes), boxes of 64 x box1 x box2 values in the 128-byte swizzle.
+bool encode16(CUtensorMap* map, int fmt, const void* base, const cuuint64_t (&dims)[3], const cuuint64_t (&strides)[2], cuuint32_t box1,
+              cuuint32_t box2) {
+    const EncodeMap encode = encode_map();
+    const cuuint32_t box[3] = {64, box1, box2}, one[3] = {1, 1, 1};
+    return encode && encode(map, fmt == KVQ_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, (void*)base, dims,
+                            strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // The tensor maps of a 16-bit pool: per layer K, then V, as [units][page_size][head_dim].
 bool make_maps(kvq_paged* h) {
     const kvq_paged_config& c = h->cfg;
     h->maps.resize(2 * (size_t)c.n_layers);
     if (c.k_fmt != KVQ_F16 && c.k_fmt != KVQ_BF16) return true;
-    void* fn = nullptr;
-    cudaDriverEntryPointQueryResult found;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) != cudaSuccess ||
-        found != cudaDriverEntryPointSuccess)
-        return false;
-    const auto encode = (decltype(&cuTensorMapEncodeTiled))fn;
     for (int l = 0; l < c.n_layers; ++l) {
         const PagedView v = view(h, l);
         for (int w = 0; w < 2; ++w) {
             const cuuint64_t dims[3] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.page_size, (cuuint64_t)c.n_pages * c.n_kv_heads};
             const cuuint64_t strides[2] = {(cuuint64_t)c.head_dim * 2, (cuuint64_t)v.unit[w]};
-            const cuuint32_t box[3] = {64, (cuuint32_t)prefill_box_rows(c.head_dim, c.page_size), 1}, one[3] = {1, 1, 1};
-            if (encode(&h->maps[2 * l + w], c.k_fmt == KVQ_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                       3, v.base[w], dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            if (!encode16(&h->maps[2 * l + w], c.k_fmt, v.base[w], dims, strides, (cuuint32_t)prefill_box_rows(c.head_dim, c.page_size), 1))
                 return false;
         }
     }
     return true;
 }
 
+// Waits for all work of the device, reads the status word at `at` and clears the bits read.
+kvq_status read_status(uint32_t* at, uint32_t* word) {
+    // the word of all that was enqueued before, on any stream; then exactly the bits that are reported are taken out, so
+    // that one that a later call sets meanwhile stays for the next reading
+    uint32_t w = 0;
+    if (cudaDeviceSynchronize() != cudaSuccess) return KVQ_ECUDA;
+    if (cudaMemcpy(&w, at, 4, cudaMemcpyDeviceToHost) != cudaSuccess) return KVQ_ECUDA;
+    if (w && (launch_paged_clear_status(at, w) || cudaStreamSynchronize(nullptr) != cudaSuccess)) return KVQ_ECUDA;
+    if (word) *word = w;
+    return w ? KVQ_EDEVICE : KVQ_OK;
+}
+
 kvq_status launched(int e) { return e == 0 ? KVQ_OK : KVQ_ECUDA; }
+
+// The options, checked, of a call over at most `most` positions a sequence.
+bool take_opts(const kvq_attn_opts* opts, int64_t most, PagedAttnParams* p) {
+    if (!opts) return true;
+    if (!(opts->softcap >= 0.f) || !std::isfinite(opts->softcap) || opts->window < 0) return false;
+    if (opts->softcap > 0.f && opts->softcap < 1e-30f) return false;    // its reciprocal has to be finite
+    if (opts->softcap > 2e38f) return false;                            // and its multiple by log2(e)
+    if (!aligned4(opts->slopes) || !aligned4(opts->prefix) || !aligned4(opts->lse)) return false;
+    p->softcap = opts->softcap;
+    p->window = opts->window >= most ? 0 : opts->window;                // a window of all that a sequence can hold hides nothing
+    p->slopes = opts->slopes;
+    p->prefix = opts->prefix;
+    p->lse = opts->lse;
+    return true;
+}
 
 // What the two attention calls share. rows: query rows (decode: n_seq).
 kvq_status attn_params(kvq_paged* h, int layer, int dtype, int n_seq, int64_t rows, const void* q, int64_t q_stride,
@@ -136,18 +178,7 @@ kvq_status attn_params(kvq_paged* h, int layer, int dtype, int n_seq, int64_t ro
     if ((int64_t)max_pages * c.page_size > ((int64_t)1 << 31) - 256) return KVQ_EINVAL;   // the end of a tile behind the last position too is below 2^31
     if (dtype16(c.k_fmt) && dtype != c.k_fmt) return KVQ_EUNSUPPORTED;
     *p = PagedAttnParams{};
-    if (opts) {
-        if (!(opts->softcap >= 0.f) || !std::isfinite(opts->softcap) || opts->window < 0) return KVQ_EINVAL;
-        if (opts->softcap > 0.f && opts->softcap < 1e-30f) return KVQ_EINVAL;    // its reciprocal has to be finite
-        if (opts->softcap > 2e38f) return KVQ_EINVAL;                            // and its multiple by log2(e)
-        if (!aligned4(opts->slopes) || !aligned4(opts->prefix) || !aligned4(opts->lse)) return KVQ_EINVAL;
-        p->softcap = opts->softcap;
-        // a window of all that the table holds hides nothing
-        p->window = opts->window >= (int64_t)max_pages * c.page_size ? 0 : opts->window;
-        p->slopes = opts->slopes;
-        p->prefix = opts->prefix;
-        p->lse = opts->lse;
-    }
+    if (!take_opts(opts, (int64_t)max_pages * c.page_size, p)) return KVQ_EINVAL;
     if (ws_bytes < workspace_floats(c, n_seq, rows) * 4) return KVQ_EINVAL;
     p->v = view(h, layer);
     p->q = q;
@@ -163,6 +194,34 @@ kvq_status attn_params(kvq_paged* h, int layer, int dtype, int n_seq, int64_t ro
     p->G = c.n_q_heads / c.n_kv_heads;
     p->dtype = dtype;
     p->scale = c.softmax_scale > 0.f ? c.softmax_scale : 1.0f / std::sqrt((float)c.head_dim);
+    return KVQ_OK;
+}
+
+// What both norm and rotation calls check; *sms: the device's SMs, 0 where there is nothing to do.
+kvq_status check_norm_rope(const kvq_norm_rope_args* a, int* sms) {
+    *sms = 0;
+    if (!a || !dtype16(a->dtype) || a->n_tok < 0 || a->n_q_heads < 0 || a->n_k_heads < 0) return KVQ_EINVAL;
+    if (a->n_q_heads + (int64_t)a->n_k_heads == 0 || (int64_t)a->n_q_heads + a->n_k_heads > 1 << 20) return KVQ_EINVAL;
+    const int D = a->head_dim, align = D == 512 ? 32 : 16;
+    if (D != 64 && D != 128 && D != 256 && D != 512) return KVQ_EINVAL;
+    if (a->rot_dim < 0 || a->rot_dim > D || a->rot_dim % align) return KVQ_EINVAL;
+    if (!(a->eps >= 0.f) || !std::isfinite(a->eps)) return KVQ_EINVAL;
+    if (a->n_tok == 0) return KVQ_OK;
+    if (a->rot_dim && (!a->cos_sin || !a->positions || a->max_pos <= 0)) return KVQ_EINVAL;
+    if (!aligned16(a->cos_sin) || !aligned4(a->positions)) return KVQ_EINVAL;
+    struct Side { int heads; const void* in; const void* w; const void* out; int64_t si, so; };
+    const Side sides[2] = {{a->n_q_heads, a->q, a->q_weight, a->q_out, a->q_stride, a->q_out_stride},
+                           {a->n_k_heads, a->k, a->k_weight, a->k_out, a->k_stride, a->k_out_stride}};
+    for (const Side& s : sides) {
+        if (!s.heads) continue;
+        const int64_t row = (int64_t)s.heads * D;
+        if (!s.in || !s.out || !aligned16(s.in) || !aligned16(s.out) || !aligned16(s.w)) return KVQ_EINVAL;
+        if (!stride_ok(s.si, row) || !stride_ok(s.so, row)) return KVQ_EINVAL;
+        if (s.in == s.out && s.si != s.so) return KVQ_EINVAL;
+    }
+    int d = 0;
+    if (cudaGetDevice(&d) != cudaSuccess || cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, d) != cudaSuccess)
+        return KVQ_ECUDA;
     return KVQ_OK;
 }
 
@@ -240,15 +299,7 @@ kvq_status kv_paged_destroy(kvq_paged* h) {
 
 kvq_status kv_paged_get_status(kvq_paged* h, uint32_t* word) {
     const kvq_status st = check(h, 0);
-    if (st != KVQ_OK) return st;
-    // the word of all that was enqueued before, on any stream; then exactly the bits that are reported are taken out, so
-    // that one that a later call sets meanwhile stays for the next reading
-    uint32_t w = 0;
-    if (cudaDeviceSynchronize() != cudaSuccess) return KVQ_ECUDA;
-    if (cudaMemcpy(&w, h->pool, 4, cudaMemcpyDeviceToHost) != cudaSuccess) return KVQ_ECUDA;
-    if (w && (launch_paged_clear_status((uint32_t*)h->pool, w) || cudaStreamSynchronize(nullptr) != cudaSuccess)) return KVQ_ECUDA;
-    if (word) *word = w;
-    return w ? KVQ_EDEVICE : KVQ_OK;
+    return st != KVQ_OK ? st : read_status((uint32_t*)h->pool, word);
 }
 
 kvq_status kv_paged_write(kvq_paged* h, int32_t layer, int32_t dtype, int32_t n_tok, const void* k, int64_t k_stride,
@@ -367,30 +418,88 @@ kvq_status kv_paged_prefill_attn(kvq_paged* h, int32_t layer, int32_t dtype, int
     return launched(launch(p, &h->maps[2 * (size_t)layer], h->sm_count, stream));
 }
 
-kvq_status kv_qk_norm_rope(const kvq_norm_rope_args* a, void* stream) {
-    if (!a || !dtype16(a->dtype) || a->n_tok < 0 || a->n_q_heads < 0 || a->n_k_heads < 0) return KVQ_EINVAL;
-    if (a->n_q_heads + (int64_t)a->n_k_heads == 0 || (int64_t)a->n_q_heads + a->n_k_heads > 1 << 20) return KVQ_EINVAL;
-    const int D = a->head_dim, align = D == 512 ? 32 : 16;
-    if (D != 64 && D != 128 && D != 256 && D != 512) return KVQ_EINVAL;
-    if (a->rot_dim < 0 || a->rot_dim > D || a->rot_dim % align) return KVQ_EINVAL;
-    if (!(a->eps >= 0.f) || !std::isfinite(a->eps)) return KVQ_EINVAL;
-    if (a->n_tok == 0) return KVQ_OK;
-    if (a->rot_dim && (!a->cos_sin || !a->positions || a->max_pos <= 0)) return KVQ_EINVAL;
-    if (!aligned16(a->cos_sin) || !aligned4(a->positions)) return KVQ_EINVAL;
-    struct Side { int heads; const void* in; const void* w; const void* out; int64_t si, so; };
-    const Side sides[2] = {{a->n_q_heads, a->q, a->q_weight, a->q_out, a->q_stride, a->q_out_stride},
-                           {a->n_k_heads, a->k, a->k_weight, a->k_out, a->k_stride, a->k_out_stride}};
-    for (const Side& s : sides) {
-        if (!s.heads) continue;
-        const int64_t row = (int64_t)s.heads * D;
-        if (!s.in || !s.out || !aligned16(s.in) || !aligned16(s.out) || !aligned16(s.w)) return KVQ_EINVAL;
-        if (!stride_ok(s.si, row) || !stride_ok(s.so, row)) return KVQ_EINVAL;
-        if (s.in == s.out && s.si != s.so) return KVQ_EINVAL;
-    }
+kvq_status kv_prompt_required_bytes(int64_t n_rows, int32_t n_q_heads, int32_t head_dim, size_t* workspace_bytes) {
+    if (n_rows < 0 || n_rows >= (int64_t)1 << 31 || n_q_heads < 1 || n_q_heads > 1 << 20 || !workspace_bytes) return KVQ_EINVAL;
+    if (head_dim != 64 && head_dim != 128 && head_dim != 256) return KVQ_EINVAL;
+    *workspace_bytes = 256 + 4 * (size_t)paged_prefill_ws_floats(head_dim, n_rows * n_q_heads);
+    return KVQ_OK;
+}
+
+kvq_status kv_prompt_attn(const kvq_prompt_args* a, const kvq_attn_opts* opts, void* workspace, size_t ws_bytes, void* stream) {
+    if (!a || !dtype16(a->dtype) || a->n_seq < 0 || a->n_rows < 0 || a->max_q < 0) return KVQ_EINVAL;
+    const int H = a->n_kv_heads, D = a->head_dim;
+    if (H < 1 || a->n_q_heads < 1 || a->n_q_heads % H || a->n_q_heads / H > kMaxG) return KVQ_EINVAL;
+    if (!(a->softmax_scale >= 0.f) || !std::isfinite(a->softmax_scale)) return KVQ_EINVAL;
+    size_t need = 0;
+    kvq_status st = kv_prompt_required_bytes(a->n_rows, a->n_q_heads, D, &need);
+    if (st != KVQ_OK) return st;
+    if (a->n_seq == 0 || a->n_rows == 0 || a->max_q == 0) return KVQ_OK;
+    if (!a->q || !a->k || !a->v || !a->cu || !a->out || !workspace || ws_bytes < need) return KVQ_EINVAL;
+    if (!aligned16(a->q) || !aligned16(a->k) || !aligned16(a->v) || !aligned16(a->out) || !aligned16(workspace) || !aligned4(a->cu))
+        return KVQ_EINVAL;
+    const int64_t row = (int64_t)H * D, q_row = (int64_t)a->n_q_heads * D;
+    if (!stride_ok(a->q_stride, q_row) || !stride_ok(a->k_stride, row) || !stride_ok(a->v_stride, row)) return KVQ_EINVAL;
+    PagedAttnParams p{};
+    if (!take_opts(opts, a->n_rows, &p)) return KVQ_EINVAL;
+    p.G = a->n_q_heads / H;
+    // grid rows: one per row tile of all prompts, or of the longest one (the join's, smaller); a head's row numbers stay below 2^31
+    if (a->n_seq > 65535 || (int64_t)a->n_rows * kMaxG >= (int64_t)1 << 31 || prompt_tiles(a->n_rows, a->n_seq, p.G, D) > 65535 ||
+        H > 65535 || a->k_stride >= (int64_t)1 << 38 || a->v_stride >= (int64_t)1 << 38)
+        return KVQ_EUNSUPPORTED;
     int d = 0, sms = 0;
     if (cudaGetDevice(&d) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, d) != cudaSuccess)
         return KVQ_ECUDA;
-    return launched(launch_norm_rope(*a, sms, stream));
+    CUtensorMap maps[2];
+    for (int w = 0; w < 2; ++w) {
+        const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)a->n_rows};
+        const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)(w ? a->v_stride : a->k_stride) * 2};
+        if (!encode16(&maps[w], a->dtype, w ? a->v : a->k, dims, strides, 1, (cuuint32_t)prefill_tile(D))) return KVQ_ECUDA;
+    }
+    p.v.status = (uint32_t*)workspace;
+    p.v.H = H;
+    p.v.D = D;
+    p.q = a->q;
+    p.out = a->out;
+    p.cu = a->cu;
+    p.ws = (float*)workspace + 64;
+    p.q_stride = a->q_stride;
+    p.n_seq = a->n_seq;
+    p.max_pages = 0x7fffffff;                                    // no table bounds the positions
+    p.Hq = a->n_q_heads;
+    p.dtype = a->dtype;
+    p.n_rows = a->n_rows;
+    p.max_q = a->max_q < a->n_rows ? a->max_q : a->n_rows;
+    p.scale = a->softmax_scale > 0.f ? a->softmax_scale : 1.0f / std::sqrt((float)D);
+    const auto launch = D == 64 ? launch_prompt_attn_64 : (D == 128 ? launch_prompt_attn_128 : launch_prompt_attn_256);
+    return launched(launch(p, maps, sms, stream));
+}
+
+kvq_status kv_prompt_get_status(void* workspace, uint32_t* word) {
+    if (!workspace || !aligned16(workspace)) return KVQ_EINVAL;
+    return read_status((uint32_t*)workspace, word);
+}
+
+kvq_status kv_qk_norm_rope(const kvq_norm_rope_args* a, void* stream) {
+    int sms;
+    const kvq_status st = check_norm_rope(a, &sms);
+    return st != KVQ_OK || !sms ? st : launched(launch_norm_rope(*a, sms, stream));
+}
+
+kvq_status kv_qk_norm_rope_axes(const kvq_norm_rope_args* a, int32_t n_axes, const int32_t* sections, int32_t cyclic,
+                                void* stream) {
+    if (!a || a->rot_dim <= 0 || !sections || n_axes < 1 || n_axes > 4) return KVQ_EINVAL;
+    int64_t total = 0;
+    for (int i = 0; i < n_axes; ++i) {
+        if (sections[i] < 0) return KVQ_EINVAL;
+        total += sections[i];
+    }
+    if (2 * total != a->rot_dim) return KVQ_EINVAL;
+    int sms;
+    const kvq_status st = check_norm_rope(a, &sms);
+    if (st != KVQ_OK || !sms) return st;
+    RopeAxes x;
+    rope_axes(n_axes, sections, cyclic != 0, &x);
+    return launched(launch_norm_rope_axes(*a, x, sms, stream));
 }
 
 }  // extern "C"

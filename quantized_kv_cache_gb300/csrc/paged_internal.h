@@ -90,7 +90,33 @@ struct PagedAttnParams {
 int resident_ctas(const void* kernel, int threads, int smem, int* ctas);
 
 int launch_paged_clear_status(uint32_t* status, uint32_t bits);   // on the legacy stream
+// The axis of each frequency of a rotation, two bits each, eight to a word; and the axes that have any, by bit.
+struct RopeAxes {
+    uint32_t n, used;
+    uint16_t of8[32];
+};
+// Frequencies in runs of sections[a], or dealt to the axes in turn until each has its number.
+inline void rope_axes(int n_axes, const int32_t* sections, bool cyclic, RopeAxes* x) {
+    *x = RopeAxes{};
+    x->n = (uint32_t)n_axes;
+    int left[4] = {}, total = 0, f = 0;
+    for (int a = 0; a < n_axes; ++a) {
+        left[a] = sections[a];
+        total += sections[a];
+        if (sections[a] > 0) x->used |= 1u << a;
+    }
+    const auto put = [&](int a) { x->of8[f / 8] = (uint16_t)(x->of8[f / 8] | a << 2 * (f % 8)); ++f; --left[a]; };
+    while (f < total)
+        for (int a = 0; a < n_axes; ++a)
+            if (cyclic) {
+                if (left[a] > 0) put(a);
+            } else {
+                while (left[a] > 0) put(a);
+            }
+}
+
 int launch_norm_rope(const kvq_norm_rope_args& a, int sm_count, void* stream);
+int launch_norm_rope_axes(const kvq_norm_rope_args& a, const RopeAxes& x, int sm_count, void* stream);
 int launch_paged_write(const WriteParams& p, void* stream);
 int launch_paged_append(const PagedAppendParams& p, void* stream);
 int launch_paged_read(const ReadParams& p, void* stream);
@@ -102,6 +128,10 @@ int launch_paged_decode_256(const PagedAttnParams& p, int sm_count, void* stream
 int launch_paged_prefill_64(const PagedAttnParams& p, const void* maps, int sm_count, void* stream);
 int launch_paged_prefill_128(const PagedAttnParams& p, const void* maps, int sm_count, void* stream);
 int launch_paged_prefill_256(const PagedAttnParams& p, const void* maps, int sm_count, void* stream);
+// maps: two CUtensorMap, K and V rows as [rows][heads][head_dim] in boxes of prefill_tile rows x 1 x 64
+int launch_prompt_attn_64(const PagedAttnParams& p, const void* maps, int sm_count, void* stream);
+int launch_prompt_attn_128(const PagedAttnParams& p, const void* maps, int sm_count, void* stream);
+int launch_prompt_attn_256(const PagedAttnParams& p, const void* maps, int sm_count, void* stream);
 KVQ_HD constexpr int prefill_tile(int D) { return D == 256 ? 64 : 128; }    // positions of a KV tile
 KVQ_HD int prefill_box_rows(int D, int ps) { return ps < prefill_tile(D) ? ps : prefill_tile(D); }
 // A run's partial result of a head: 16 maxima, 16 sums, the outputs.
@@ -116,6 +146,10 @@ KVQ_HD int prefill_splits(int64_t rows, int n_seq, int H, int tile_rows, int sm_
     const int64_t s = (sm_count < kMaxSms ? sm_count : kMaxSms) / (ctas > 0 ? ctas : 1);
     return (int)(s < 1 ? 1 : (s > kMaxSplits ? kMaxSplits : s));
 }
+// Whole prompts: the row tiles of all of them, at most one part-filled per sequence; and splits that leave each at least four of the
+// position tiles of the longest one's last rows.
+KVQ_HD int64_t prompt_tiles(int64_t n_rows, int64_t n_seq, int G, int D) { return n_rows * G / (D == 256 ? 128 : 256) + n_seq; }
+KVQ_HD int prompt_splits(int max_q, int D) { return 1 + max_q / prefill_tile(D) / 8; }
 // The splits' partials in the workspace: (maximum, sum) of all `pairs` (split, query row, head), then from float
 // split_out_at on their outputs. Those go by 16-byte accesses, and pairs may be odd: rounded up to four floats.
 KVQ_HD int64_t split_out_at(int64_t pairs) { return (2 * pairs + 3) & ~(int64_t)3; }

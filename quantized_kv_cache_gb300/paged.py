@@ -81,6 +81,23 @@ def _no_grad(*tensors):
 # Written tensors: autograd finds out if it had saved one of them.
 _changed = torch.autograd.graph.increment_version
 
+
+def _attn_opts(dev, Hq, n, rows, lse, softcap, window, slopes, prefix):
+    """The kvq_attn_opts of a call over n sequences and `rows` query rows."""
+    sp = pp = lp = None
+    if slopes is not None:
+        if slopes.dtype is not torch.float32 or slopes.get_device() != dev or slopes.shape != (Hq,) or not slopes.is_contiguous():
+            _bad(f"slopes: contiguous fp32 of shape ({Hq},) on cuda:{dev} is wanted")
+        sp = slopes.data_ptr()
+    if prefix is not None:
+        pp = _ints(prefix, "prefix", n, dev)
+    if lse is not None:
+        if lse.dtype is not torch.float32 or lse.get_device() != dev or lse.shape != (rows, Hq) or not lse.is_contiguous():
+            _bad(f"lse: contiguous fp32 of shape ({rows}, {Hq}) on cuda:{dev} is wanted")
+        lp = lse.data_ptr()
+    return ctypes.byref(_lib.kvq_attn_opts(softcap, window, sp, pp, lp))
+
+
 _one_device = None
 
 
@@ -190,20 +207,7 @@ class PagedKVCache:
         _changed([x for x in (k_out, v_out) if x is not None])
 
     def _opts(self, n, rows, lse, softcap, window, slopes, prefix):
-        sp = pp = lp = None
-        if slopes is not None:
-            if (slopes.dtype is not torch.float32 or slopes.get_device() != self._dev or slopes.shape != (self._Hq,) or
-                    not slopes.is_contiguous()):
-                _bad(f"slopes: contiguous fp32 of shape ({self._Hq},) on {self.device} is wanted")
-            sp = slopes.data_ptr()
-        if prefix is not None:
-            pp = _ints(prefix, "prefix", n, self._dev)
-        if lse is not None:
-            if (lse.dtype is not torch.float32 or lse.get_device() != self._dev or lse.shape != (rows, self._Hq) or
-                    not lse.is_contiguous()):
-                _bad(f"lse: contiguous fp32 of shape ({rows}, {self._Hq}) on {self.device} is wanted")
-            lp = lse.data_ptr()
-        return ctypes.byref(_lib.kvq_attn_opts(softcap, window, sp, pp, lp))
+        return _attn_opts(self._dev, self._Hq, n, rows, lse, softcap, window, slopes, prefix)
 
     def _space(self, ws):
         if ws is None:
@@ -247,11 +251,57 @@ class PagedKVCache:
         _changed(out if lse is None else (out, lse))
 
 
+def prompt_workspace(max_rows, n_q_heads, head_dim, device=0):
+    """A workspace of prompt_attn for calls of up to max_rows rows, its status word cleared. Calls that may overlap on the GPU
+    need one each."""
+    dev = torch.device("cuda", device) if isinstance(device, int) else torch.device(device)
+    ws = torch.empty(_lib.kv_prompt_required_bytes(max_rows, n_q_heads, head_dim), dtype=torch.uint8, device=dev)
+    ws[:256] = 0
+    torch.cuda.current_stream(dev).synchronize()      # before a call on any stream
+    return ws
+
+
+def prompt_status(ws):
+    """The status word (bits PAGED_* of ``_lib``) of the calls with this workspace, read when the device has finished all
+    work, and cleared."""
+    return _guarded(ws.get_device(), _lib.kv_prompt_get_status, ws.data_ptr())
+
+
+def prompt_attn(q, k, v, cu, max_q, out, ws, lse=None, softcap=0.0, window=0, slopes=None, prefix=None, softmax_scale=0.0,
+                stream=0):
+    """Causal attention of whole packed prompts over their own rows, without a cache: sequence b's tokens are the rows cu[b] ..
+    cu[b+1]-1 of q ([rows, Hq, D] fp16 or bf16) and k, v ([rows, H, D], all with free token strides). cu: int32
+    [sequences + 1]; max_q: at least the longest prompt (of a longer one only the first max_q tokens are computed); out:
+    [rows, Hq, D], contiguous; ws: from prompt_workspace. Options as for PagedKVCache.prefill_attn."""
+    dt, dev, dtype = _type_of(q, "q", _DT), q.get_device(), q.dtype
+    if q.dim() != 3 or k.dim() != 3 or dev < 0:
+        _bad("q, k: [rows, heads, D] CUDA tensors are wanted")
+    Hq, H, D = q.shape[1], k.shape[1], q.shape[2]
+    rows, qs = _rows(q, "q", Hq, D, dev, dtype)
+    nk, ks = _rows(k, "k", H, D, dev, dtype)
+    nv, vs = _rows(v, "v", H, D, dev, dtype)
+    if nk != rows or nv != rows:
+        _bad("q, k and v: the same number of rows is wanted")
+    if cu.dim() != 1 or cu.shape[0] < 1:
+        _bad("cu: int32 [sequences + 1] is wanted")
+    n = cu.shape[0] - 1
+    cp, op = _ints(cu, "cu", n + 1, dev), _out_rows(out, "out", rows, Hq, D, dev, dtype)
+    o = _attn_opts(dev, Hq, n, rows, lse, softcap, window, slopes, prefix)
+    if ws.get_device() != dev or not ws.is_contiguous():
+        _bad(f"ws: contiguous, on cuda:{dev}")
+    _no_grad(q, k, v, out, slopes)
+    a = _lib.kvq_prompt_args(dt, n, rows, max_q, Hq, H, D, softmax_scale, q.data_ptr(), k.data_ptr(), v.data_ptr(), cp, op, qs, ks, vs)
+    _guarded(dev, _lib.kv_prompt_attn, ctypes.byref(a), o, ws.data_ptr(), ws.numel() * ws.element_size(), stream)
+    _changed(out if lse is None else (out, lse))
+
+
 def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, q_out=None, k_out=None, eps=1e-6, interleaved=False,
-                 stream=0):
+                 stream=0, sections=None, cyclic=False):
     """RMS norm of every head of q [tokens, Hq, D] and k [tokens, H, D] and their rotation by position, in one
     pass; q or k may be None, a weight None leaves its side without the norm. cos_sin: fp32 [positions, rot],
-    cosines then sines (None: no rotation); positions: int32 [tokens]. Outputs default to the inputs (in place)."""
+    cosines then sines (None: no rotation); positions: int32 [tokens]. Outputs default to the inputs (in place).
+    With sections (1 to 4 numbers, rot / 2 in all) positions is int32 [axes, tokens] and frequency i goes by one of the axes:
+    sections[a] of them by axis a, in runs, or with cyclic dealt to the axes in turn until each has its number."""
     x = q if q is not None else k
     if x is None or x.dim() != 3 or not x.is_cuda:
         _bad("q, k: [tokens, heads, D] CUDA tensors are wanted")
@@ -288,10 +338,21 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, q_out=None, k_out
         if positions is None:
             _bad("positions are wanted with cos_sin")
         max_pos, rot = cos_sin.shape
-        cp, pp = cos_sin.data_ptr(), _ints(positions, "positions", n, dev)
+        if sections is None:
+            cp, pp = cos_sin.data_ptr(), _ints(positions, "positions", n, dev)
+        else:
+            if (positions.dtype is not torch.int32 or positions.get_device() != dev or positions.shape != (len(sections), n) or
+                    not positions.is_contiguous()):
+                _bad(f"positions: a contiguous int32 tensor of shape ({len(sections)}, {n}) on cuda:{dev} is wanted")
+            cp, pp = cos_sin.data_ptr(), positions.data_ptr()
+    elif sections is not None:
+        _bad("sections without cos_sin")
     (hq, qp, qw, qo, qs, qos), (hk, kp, kw, ko, ks, kos) = sides
     a = _lib.kvq_norm_rope_args(dt, n, hq, hk, D, rot, 1 if interleaved else 0, max_pos, eps, 0, qp, kp, qw, kw, cp, pp, qo, ko,
                                 qs, ks, qos, kos)
     _no_grad(q, k, q_weight, k_weight, q_out, k_out, cos_sin)
-    _guarded(dev, _lib.kv_qk_norm_rope, ctypes.byref(a), stream)
+    if sections is None:
+        _guarded(dev, _lib.kv_qk_norm_rope, ctypes.byref(a), stream)
+    else:
+        _guarded(dev, _lib.kv_qk_norm_rope_axes, ctypes.byref(a), sections, 1 if cyclic else 0, stream)
     _changed([t if o is None else o for t, o in ((q, q_out), (k, k_out)) if t is not None])
