@@ -45,6 +45,7 @@ enum {
     KVQ_PAGED_BAD_INDEX = 4,    /* a slot or a page number was out of range: a write was skipped, a page read as zeros */
     KVQ_PAGED_BAD_LENGTH = 8,   /* a length, row offset or max_q was out of range: lengths are cut to what the page
                                    table holds, rows beyond the call's buffers or max_q are skipped */
+    KVQ_PAGED_NO_PAGES = 32,    /* kv_pages_extend: fewer free pages than the call needs; it changed nothing */
     KVQ_PAGED_RANGE = 16        /* a quantised block reaches beyond fp16's 65,504: the page holds it and kv_paged_read
                                    gives it, the attentions cut its scale (kv_paged_decode_attn) */
 };
@@ -154,6 +155,51 @@ kvq_status kv_paged_prefill_attn(kvq_paged* h, int32_t layer, int32_t dtype, int
                                  const int32_t* page_table, int32_t max_pages, int64_t table_stride,
                                  const int32_t* lens, void* out, const kvq_attn_opts* opts, void* workspace,
                                  size_t ws_bytes, void* stream);
+
+/* Page tables that the device keeps. A row is a sequence: lens[r] positions in the pages table[r][0] .. (device int32
+ * [rows][max_pages], rows table_stride apart); what stands behind them is not looked at. refs[p] says how many rows hold page p
+ * (device int32 [n_pages]; 0: free), and whoever else keeps a page counts in it too. A new cache's refs and lens are zeros. */
+typedef struct {
+    int32_t rows;
+    int32_t max_pages;
+    int64_t table_stride;
+    int32_t* table;
+    int32_t* lens;
+    int32_t* refs;
+} kvq_page_tables;
+
+/* Sequences forked, made longer, cut and freed, pages copied and moved, in all layers at once. Nothing is read back, so that the
+ * calls can be captured; the same call on the same tables gives the same pages. Calls on the same tables, and calls that read or
+ * write the pages concerned, go on one stream or wait for one another. Workspaces: device, 16-byte aligned,
+ * >= kv_pages_required_bytes, written before they are read, one each for calls that may overlap. */
+kvq_status kv_pages_required_bytes(const kvq_paged_config* cfg, size_t* workspace_bytes);
+
+/* kv_pages_copy — page src[i] to page dst[i], i < n (device int32 [n]), K and V of every layer. A pair with a negative number is
+ * skipped; no page may be a destination twice, nor both a source and a destination. */
+kvq_status kv_pages_copy(kvq_paged* h, int32_t n, const int32_t* src, const int32_t* dst, void* stream);
+
+/* kv_pages_fork — row children[i] becomes what row parents[i] is, i < n <= 65,535 (device int32 [n]): all pages are shared. A negative
+ * child is skipped. A child that holds positions, has come before in the call or is a parent in it is left out
+ * (KVQ_PAGED_BAD_INDEX); several children of one parent are fine. */
+kvq_status kv_pages_fork(kvq_paged* h, const kvq_page_tables* t, int32_t n, const int32_t* parents, const int32_t* children, void* stream);
+
+/* kv_pages_extend — row r will hold add[r] more positions (device int32 [rows], >= 0; 0 leaves a row as it is): lens grows, and
+ * pages for them come from the free ones, lowest first, row after row. A row that would go on in a part-filled page that is held
+ * by others too gets a copy of it instead (of several rows that go on in one page all of whose holders go on, the lowest
+ * keeps it), so that what is then written at the new positions is the row's own. If the free pages do not suffice for the
+ * whole call it changes nothing and sets KVQ_PAGED_NO_PAGES; a row that would outgrow its table, or whose last page is no
+ * page, is left out (KVQ_PAGED_BAD_LENGTH, KVQ_PAGED_BAD_INDEX). */
+kvq_status kv_pages_extend(kvq_paged* h, const kvq_page_tables* t, const int32_t* add, void* workspace, size_t ws_bytes, void* stream);
+
+/* kv_pages_free — row rows[i] is cut to keep[i] positions (keep null: to none), i < n (device int32 [n]): the pages behind them
+ * are given back (held once less), their entries become -1. A negative row is skipped, a row that is shorter stays as it is, one
+ * that comes twice is cut to the lower number. */
+kvq_status kv_pages_free(kvq_paged* h, const kvq_page_tables* t, int32_t n, const int32_t* rows, const int32_t* keep, void* stream);
+
+/* kv_pages_compact — the L pages in use become pages 0 .. L - 1: those behind are moved to the free ones before, both in order, with
+ * their counts, and the rows' entries are renumbered. remap (device int32 [n_pages], written): the new number of each page, -1 for
+ * a free one. */
+kvq_status kv_pages_compact(kvq_paged* h, const kvq_page_tables* t, int32_t* remap, void* workspace, size_t ws_bytes, void* stream);
 
 /* Arguments of kv_prompt_attn: packed prompts, sequence b's tokens in rows cu[b] .. cu[b+1] - 1 of q, k, v and out. */
 typedef struct {

@@ -27,7 +27,7 @@ ENOSPC = 2
 PAGED_F32 = 100
 PAGED_E4M3 = 101
 PAGED_FMT_NAMES = dict(FMT_NAMES, e4m3=PAGED_E4M3)
-PAGED_NONFINITE, PAGED_TIMEOUT, PAGED_BAD_INDEX, PAGED_BAD_LENGTH, PAGED_RANGE = 1, 2, 4, 8, 16
+PAGED_NONFINITE, PAGED_TIMEOUT, PAGED_BAD_INDEX, PAGED_BAD_LENGTH, PAGED_RANGE, PAGED_NO_PAGES = 1, 2, 4, 8, 16, 32
 STATUS = {0: "KVQ_OK", 1: "KVQ_EINVAL", 2: "KVQ_ENOSPC", 3: "KVQ_EUNSUPPORTED", 4: "KVQ_ECUDA", 5: "KVQ_EDEVICE"}
 
 
@@ -70,6 +70,11 @@ class kvq_norm_rope_args(ctypes.Structure):
                 [(n, ctypes.c_void_p) for n in ("q", "k", "q_weight", "k_weight", "cos_sin", "positions", "q_out",
                                                 "k_out")] +
                 [(n, ctypes.c_int64) for n in ("q_stride", "k_stride", "q_out_stride", "k_out_stride")])
+
+
+class kvq_page_tables(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("table_stride", ctypes.c_int64),
+                ("table", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("refs", ctypes.c_void_p)]
 
 
 class kvq_prompt_args(ctypes.Structure):
@@ -126,6 +131,12 @@ _SIGS = {
     "kv_paged_decode_attn": [P, I32, I32, I32, P, I64, P, I32, I64, P, P, ctypes.POINTER(kvq_attn_opts), P, SZ, P],
     "kv_paged_prefill_attn": [P, I32, I32, I32, I32, I32, P, I64, P, P, I32, I64, P, P, ctypes.POINTER(kvq_attn_opts), P,
                               SZ, P],
+    "kv_pages_required_bytes": [ctypes.POINTER(kvq_paged_config), ctypes.POINTER(SZ)],
+    "kv_pages_copy": [P, I32, P, P, P],
+    "kv_pages_fork": [P, ctypes.POINTER(kvq_page_tables), I32, P, P, P],
+    "kv_pages_extend": [P, ctypes.POINTER(kvq_page_tables), P, P, SZ, P],
+    "kv_pages_free": [P, ctypes.POINTER(kvq_page_tables), I32, P, P, P],
+    "kv_pages_compact": [P, ctypes.POINTER(kvq_page_tables), P, P, SZ, P],
     "kv_prompt_required_bytes": [I64, I32, I32, ctypes.POINTER(SZ)],
     "kv_prompt_attn": [ctypes.POINTER(kvq_prompt_args), ctypes.POINTER(kvq_attn_opts), P, SZ, P],
     "kv_prompt_get_status": [P, ctypes.POINTER(ctypes.c_uint32)],
@@ -387,6 +398,33 @@ def kv_paged_prefill_attn(h, layer, dtype, n_seq, n_rows, max_q, q_ptr, q_stride
     _check("kv_paged_prefill_attn", load().kv_paged_prefill_attn(h, layer, dtype, n_seq, n_rows, max_q, q_ptr, q_stride,
                                                                  cu_ptr, table_ptr, max_pages, table_stride, lens_ptr,
                                                                  out_ptr, opts, ws_ptr, ws_bytes, stream))
+
+
+def kv_pages_required_bytes(cfg):
+    n = SZ()
+    _check("kv_pages_required_bytes", load().kv_pages_required_bytes(ctypes.byref(cfg), ctypes.byref(n)))
+    return n.value
+
+
+def kv_pages_copy(h, n, src_ptr, dst_ptr, stream=0):
+    _check("kv_pages_copy", load().kv_pages_copy(h, n, src_ptr, dst_ptr, stream))
+
+
+def kv_pages_fork(h, tables, n, parents_ptr, children_ptr, stream=0):
+    """tables: a kvq_page_tables."""
+    _check("kv_pages_fork", load().kv_pages_fork(h, tables, n, parents_ptr, children_ptr, stream))
+
+
+def kv_pages_extend(h, tables, add_ptr, ws_ptr, ws_bytes, stream=0):
+    _check("kv_pages_extend", load().kv_pages_extend(h, tables, add_ptr, ws_ptr, ws_bytes, stream))
+
+
+def kv_pages_free(h, tables, n, rows_ptr, keep_ptr, stream=0):
+    _check("kv_pages_free", load().kv_pages_free(h, tables, n, rows_ptr, keep_ptr, stream))
+
+
+def kv_pages_compact(h, tables, remap_ptr, ws_ptr, ws_bytes, stream=0):
+    _check("kv_pages_compact", load().kv_pages_compact(h, tables, remap_ptr, ws_ptr, ws_bytes, stream))
 
 
 def kv_prompt_required_bytes(n_rows, n_q_heads, head_dim):

@@ -31,6 +31,7 @@ UNITS = {
     "synth.cu": [],
     "paged_api.cpp": [],
     "kernels_paged_rows.cu": [],
+    "kernels_pages.cu": [],
     "kernels_paged_decode.cu:64": ["-DKVQ_D=64"],
     "kernels_paged_decode.cu:128": ["-DKVQ_D=128"],
     "kernels_paged_decode.cu:256": ["-DKVQ_D=256"],

@@ -197,6 +197,38 @@ kvq_status attn_params(kvq_paged* h, int layer, int dtype, int n_seq, int64_t ro
     return KVQ_OK;
 }
 
+PagesParams pages_params(const kvq_paged* h) {
+    Geometry g;
+    geometry(h->cfg, &g);
+    PagesParams p{};
+    p.v = view(h, 0);
+    p.layer_bytes = g.layer;
+    p.n_layers = h->cfg.n_layers;
+    p.sm_count = h->sm_count;
+    return p;
+}
+
+// What the calls on page tables share.
+kvq_status page_tables(const kvq_paged* h, const kvq_page_tables* t, PagesParams* p) {
+    const kvq_status st = check(h, 0);
+    if (st != KVQ_OK) return st;
+    if (!t || t->rows < 0 || t->max_pages <= 0 || t->table_stride < t->max_pages) return KVQ_EINVAL;
+    if (!t->refs || !aligned4(t->refs) || (t->rows && (!t->table || !t->lens)) || !aligned4(t->table) || !aligned4(t->lens)) return KVQ_EINVAL;
+    if ((int64_t)t->max_pages * h->cfg.page_size >= (int64_t)1 << 31) return KVQ_EINVAL;      // lengths are int32
+    *p = pages_params(h);
+    p->table_stride = t->table_stride;
+    p->table = t->table;
+    p->lens = t->lens;
+    p->refs = t->refs;
+    p->rows = t->rows;
+    p->max_pages = t->max_pages;
+    return KVQ_OK;
+}
+
+bool pages_ws_ok(const kvq_paged* h, const void* ws, size_t bytes) {
+    return ws && aligned16(ws) && bytes >= 4 * (size_t)pages_ws_ints(h->cfg.n_pages);
+}
+
 // What both norm and rotation calls check; *sms: the device's SMs, 0 where there is nothing to do.
 kvq_status check_norm_rope(const kvq_norm_rope_args* a, int* sms) {
     *sms = 0;
@@ -416,6 +448,60 @@ kvq_status kv_paged_prefill_attn(kvq_paged* h, int32_t layer, int32_t dtype, int
     p.max_q = max_q < n_rows ? max_q : n_rows;
     const auto launch = p.v.D == 64 ? launch_paged_prefill_64 : (p.v.D == 128 ? launch_paged_prefill_128 : launch_paged_prefill_256);
     return launched(launch(p, &h->maps[2 * (size_t)layer], h->sm_count, stream));
+}
+
+kvq_status kv_pages_required_bytes(const kvq_paged_config* cfg, size_t* workspace_bytes) {
+    Geometry g;
+    if (!cfg || !workspace_bytes || !geometry(*cfg, &g)) return KVQ_EINVAL;
+    *workspace_bytes = 4 * (size_t)pages_ws_ints(cfg->n_pages);
+    return KVQ_OK;
+}
+
+kvq_status kv_pages_copy(kvq_paged* h, int32_t n, const int32_t* src, const int32_t* dst, void* stream) {
+    const kvq_status st = check(h, 0);
+    if (st != KVQ_OK) return st;
+    if (n < 0) return KVQ_EINVAL;
+    if (n == 0) return KVQ_OK;
+    if (!src || !dst || !aligned4(src) || !aligned4(dst)) return KVQ_EINVAL;
+    return launched(launch_pages_copy(pages_params(h), n, src, dst, stream));
+}
+
+kvq_status kv_pages_fork(kvq_paged* h, const kvq_page_tables* t, int32_t n, const int32_t* parents, const int32_t* children, void* stream) {
+    PagesParams p;
+    const kvq_status st = page_tables(h, t, &p);
+    if (st != KVQ_OK) return st;
+    if (n < 0) return KVQ_EINVAL;
+    if (n == 0) return KVQ_OK;
+    if (!parents || !children || !aligned4(parents) || !aligned4(children)) return KVQ_EINVAL;
+    if (n > 65535) return KVQ_EUNSUPPORTED;
+    return launched(launch_pages_fork(p, n, parents, children, stream));
+}
+
+kvq_status kv_pages_extend(kvq_paged* h, const kvq_page_tables* t, const int32_t* add, void* workspace, size_t ws_bytes, void* stream) {
+    PagesParams p;
+    const kvq_status st = page_tables(h, t, &p);
+    if (st != KVQ_OK) return st;
+    if (p.rows == 0) return KVQ_OK;
+    if (!add || !aligned4(add) || !pages_ws_ok(h, workspace, ws_bytes)) return KVQ_EINVAL;
+    return launched(launch_pages_extend(p, add, (int32_t*)workspace, stream));
+}
+
+kvq_status kv_pages_free(kvq_paged* h, const kvq_page_tables* t, int32_t n, const int32_t* rows, const int32_t* keep, void* stream) {
+    PagesParams p;
+    const kvq_status st = page_tables(h, t, &p);
+    if (st != KVQ_OK) return st;
+    if (n < 0) return KVQ_EINVAL;
+    if (n == 0) return KVQ_OK;
+    if (!rows || !aligned4(rows) || !aligned4(keep)) return KVQ_EINVAL;
+    return launched(launch_pages_free(p, n, rows, keep, stream));
+}
+
+kvq_status kv_pages_compact(kvq_paged* h, const kvq_page_tables* t, int32_t* remap, void* workspace, size_t ws_bytes, void* stream) {
+    PagesParams p;
+    const kvq_status st = page_tables(h, t, &p);
+    if (st != KVQ_OK) return st;
+    if (!remap || !aligned4(remap) || !pages_ws_ok(h, workspace, ws_bytes)) return KVQ_EINVAL;
+    return launched(launch_pages_compact(p, remap, (int32_t*)workspace, stream));
 }
 
 kvq_status kv_prompt_required_bytes(int64_t n_rows, int32_t n_q_heads, int32_t head_dim, size_t* workspace_bytes) {

@@ -85,6 +85,18 @@ struct PagedAttnParams {
     float scale, softcap;
 };
 
+// Page tables on the device, and the whole pool: v is layer 0, layers are layer_bytes apart.
+struct PagesParams {
+    PagedView v;
+    int64_t layer_bytes, table_stride;
+    int32_t* table;
+    int32_t* lens;
+    int32_t* refs;
+    int32_t n_layers, rows, max_pages, sm_count;
+};
+// int32 of workspace: a header, then up to five numbers per page
+KVQ_HD int64_t pages_ws_ints(int64_t n_pages) { return 16 + 5 * n_pages; }
+
 // Resident CTAs per SM of a kernel on the current device; lets it use `smem` bytes of dynamic shared memory.
 // Asked once per kernel and device. Returns a cudaError_t as int.
 int resident_ctas(const void* kernel, int threads, int smem, int* ctas);
@@ -120,6 +132,11 @@ int launch_norm_rope_axes(const kvq_norm_rope_args& a, const RopeAxes& x, int sm
 int launch_paged_write(const WriteParams& p, void* stream);
 int launch_paged_append(const PagedAppendParams& p, void* stream);
 int launch_paged_read(const ReadParams& p, void* stream);
+int launch_pages_copy(const PagesParams& p, int n, const int32_t* src, const int32_t* dst, void* stream);
+int launch_pages_fork(const PagesParams& p, int n, const int32_t* parents, const int32_t* children, void* stream);
+int launch_pages_free(const PagesParams& p, int n, const int32_t* rows, const int32_t* keep, void* stream);
+int launch_pages_extend(const PagesParams& p, const int32_t* add, int32_t* ws, void* stream);
+int launch_pages_compact(const PagesParams& p, int32_t* remap, int32_t* ws, void* stream);
 int launch_paged_decode_64(const PagedAttnParams& p, int sm_count, void* stream);
 int launch_paged_decode_128(const PagedAttnParams& p, int sm_count, void* stream);
 int launch_paged_decode_256(const PagedAttnParams& p, int sm_count, void* stream);

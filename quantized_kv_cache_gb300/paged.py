@@ -131,12 +131,18 @@ class PagedKVCache:
             _bad(f"pool: {self.pool_bytes} contiguous bytes on {self.device} are wanted")
         self.pool = pool
         self.ws = self.new_workspace()
+        self.pages_ws_bytes = _lib.kv_pages_required_bytes(cfg)
+        self.pages_ws = self.new_pages_workspace()
         self._dev, self._H, self._Hq, self._D = device, cfg.n_kv_heads, cfg.n_q_heads, cfg.head_dim
         torch.cuda.current_stream(self.device).synchronize()      # the pool's contents, before the status word is set
         self.h = _guarded(device, _lib.kv_paged_create, cfg, pool.data_ptr(), pool.numel(), device)
 
     def new_workspace(self):
         return torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.device)
+
+    def new_pages_workspace(self):
+        """A workspace of extend and compact, for calls that may overlap with others of them."""
+        return torch.empty(self.pages_ws_bytes, dtype=torch.uint8, device=self.device)
 
     def close(self):
         if self.h is not None:
@@ -249,6 +255,60 @@ class PagedKVCache:
         _guarded(dev, _lib.kv_paged_prefill_attn, self.h, layer, dt, n, rows, max_q, q.data_ptr(), qs, cp, tp, w, ts, lp, op,
                  o, wp, wb, stream)
         _changed(out if lse is None else (out, lse))
+
+
+    def _tables(self, table, lens, refs):
+        tp, n, w, ts = self._table(table)
+        return ctypes.byref(_lib.kvq_page_tables(n, w, ts, tp, _ints(lens, "lens", n, self._dev),
+                                                 _ints(refs, "refs", self.cfg.n_pages, self._dev)))
+
+    def _pages_space(self, ws):
+        if ws is None:
+            return self.pages_ws.data_ptr(), self.pages_ws_bytes
+        if ws.get_device() != self._dev or not ws.is_contiguous():
+            _bad(f"ws: contiguous, on {self.device}")
+        return ws.data_ptr(), ws.numel() * ws.element_size()
+
+    def copy_pages(self, src, dst, stream=0):
+        """Page src[i] to page dst[i], in every layer (int32 [n]; a pair with a negative number is skipped). No page may be a
+        destination twice, nor both a source and a destination."""
+        n = src.numel()
+        sp, dp = _ints(src, "src", n, self._dev), _ints(dst, "dst", n, self._dev)
+        _guarded(self._dev, _lib.kv_pages_copy, self.h, n, sp, dp, stream)
+        _changed(self.pool)
+
+    def fork(self, page_table, lens, refs, parents, children, stream=0):
+        """Row children[i] of the table becomes what row parents[i] is, sharing its pages (int32 [n]; a negative child is
+        skipped). lens: int32 [rows], positions held; refs: int32 [n_pages], how many rows hold each page."""
+        t, n = self._tables(page_table, lens, refs), children.numel()
+        pp, cp = _ints(parents, "parents", n, self._dev), _ints(children, "children", n, self._dev)
+        _guarded(self._dev, _lib.kv_pages_fork, self.h, t, n, pp, cp, stream)
+        _changed((page_table, lens, refs))
+
+    def extend(self, page_table, lens, refs, add, ws=None, stream=0):
+        """Row r will hold add[r] more positions (int32 [rows]): lens grows, free pages are taken, and a part-filled page that
+        others hold too is copied first. With too few free pages nothing changes and the status word says NO_PAGES."""
+        t, ap = self._tables(page_table, lens, refs), _ints(add, "add", lens.shape[0], self._dev)
+        wp, wb = self._pages_space(ws)
+        _guarded(self._dev, _lib.kv_pages_extend, self.h, t, ap, wp, wb, stream)
+        _changed((page_table, lens, refs, self.pool))
+
+    def free(self, page_table, lens, refs, rows, keep=None, stream=0):
+        """Row rows[i] is cut to keep[i] positions (int32 [n]; keep None: to none; a negative row is skipped), and the pages
+        behind them are given back."""
+        t, n = self._tables(page_table, lens, refs), rows.numel()
+        rp = _ints(rows, "rows", n, self._dev)
+        kp = None if keep is None else _ints(keep, "keep", n, self._dev)
+        _guarded(self._dev, _lib.kv_pages_free, self.h, t, n, rp, kp, stream)
+        _changed((page_table, lens, refs))
+
+    def compact(self, page_table, lens, refs, remap, ws=None, stream=0):
+        """The pages in use move to the front of the pool; the table is renumbered, and remap (int32 [n_pages], written) has
+        each page's new number, -1 for a free one."""
+        t, mp = self._tables(page_table, lens, refs), _ints(remap, "remap", self.cfg.n_pages, self._dev)
+        wp, wb = self._pages_space(ws)
+        _guarded(self._dev, _lib.kv_pages_compact, self.h, t, mp, wp, wb, stream)
+        _changed((page_table, refs, remap, self.pool))
 
 
 def prompt_workspace(max_rows, n_q_heads, head_dim, device=0):
