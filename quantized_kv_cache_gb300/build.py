@@ -35,6 +35,9 @@ UNITS = {
     "kernels_paged_decode.cu:64": ["-DKVQ_D=64"],
     "kernels_paged_decode.cu:128": ["-DKVQ_D=128"],
     "kernels_paged_decode.cu:256": ["-DKVQ_D=256"],
+    "kernels_paged_draft.cu:64": ["-DKVQ_D=64"],
+    "kernels_paged_draft.cu:128": ["-DKVQ_D=128"],
+    "kernels_paged_draft.cu:256": ["-DKVQ_D=256"],
     "kernels_paged_prefill.cu:64": ["-DKVQ_D=64"],
     "kernels_paged_prefill.cu:128": ["-DKVQ_D=128"],
     "kernels_paged_prefill.cu:256": ["-DKVQ_D=256"],

@@ -71,7 +71,8 @@ __global__ void __launch_bounds__(kDT, (Ring<D, KF, VF, NQ>::ctas)) decode_kerne
     // fp16 weights are 2^(s - (max - 15)): the largest is 2^15, and those down to 2^-29 of it keep all bits, down to 2^-40 some
     // (at 2^(s - max) what lies 2^-25 below the largest would be lost to the outputs but not to the sums). m is max - kUp
     // everywhere, sums and outputs are in its units; bf16 has the exponents.
-    constexpr float kUp = LO ? 0.f : 15.f;
+    // e4m3: m moves only when a weight would be above 2^15, and then to the largest score less kFirst.
+    constexpr float kUp = LO ? 0.f : 15.f, kFirst = 8.f;
     using R = Ring<D, KF, VF, NQ>;
     extern __shared__ __align__(128) float smem[];               // the rings; [kDW][G][D] outputs at a head's end
     __shared__ float s_m[kDW][16], s_l[kDW][16];
@@ -206,10 +207,12 @@ __global__ void __launch_bounds__(kDT, (Ring<D, KF, VF, NQ>::ctas)) decode_kerne
             for (int e = 0; e < 2; ++e) {
                 const int r = 8 * k + 2 * t + e;
                 f[k][e] = rule.factor(__shfl_sync(kAll, back[k], 4 * (2 * t + e)));
+                if constexpr (KF == PF_E4) f[k][e] = fminf(f[k][e], kMaxFactor);
                 slope[k][e] = p.slopes && r < G ? p.slopes[h * G + r] * kL2e : 0.f;
                 m[k][e] = -INFINITY;
             }
 
+        ValueScale values;
         for (int i = 0; i < nt; ++i) {
             const int p0 = st.tile(i * kDW + i0 + warp) * kTile;
             const uint32_t k_tile = take();
@@ -223,8 +226,7 @@ __global__ void __launch_bounds__(kDT, (Ring<D, KF, VF, NQ>::ctas)) decode_kerne
                 const float d = tile_scale<D>(k_tile);
 #pragma unroll
                 for (int k = 0; k < NQ; ++k) {
-                    // among the normal numbers, as the factor itself (score_rule)
-                    const float f0 = normal_factor(f[k][0] * d), f1 = normal_factor(f[k][1] * d);
+                    const float f0 = f[k][0] * d, f1 = f[k][1] * d;
                     s[k][0] *= f0;
                     s[k][1] *= f1;
                     s[k][2] *= f0;
@@ -249,23 +251,37 @@ __global__ void __launch_bounds__(kDT, (Ring<D, KF, VF, NQ>::ctas)) decode_kerne
                     for (int c = 0; c < 4; ++c)
                         if (!((see >> (g + 8 * (c >> 1))) & 1)) s[k][c] = -INFINITY;
             }
-            float base[NQ][2], a[NQ][2];
-            bool moved = false;
+            float base[NQ][2], a[NQ][2], by = 1.f;
+            bool moved = KF != PF_E4;
+            if constexpr (KF == PF_E4) {                          // one vote says whether the maximum has to move
+#pragma unroll
+                for (int k = 0; k < NQ; ++k)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) moved |= fmaxf(s[k][e], s[k][2 + e]) > m[k][e] + kUp;
+                moved = __any_sync(kAll, moved);
+            }
+            if (moved) {
+                moved = false;
+#pragma unroll
+                for (int k = 0; k < NQ; ++k)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float mx = fmaxf(s[k][e], s[k][2 + e]);
+                        mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 4));
+                        mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 8));
+                        mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 16));
+                        float mn = fmaxf(m[k][e], mx - kUp);
+                        if constexpr (KF == PF_E4) mn = mx > m[k][e] + kUp ? mx - kFirst : m[k][e];
+                        moved |= m[k][e] != mn;
+                        a[k][e] = m[k][e];
+                        m[k][e] = mn;
+                    }
+            }
 #pragma unroll
             for (int k = 0; k < NQ; ++k)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float mx = fmaxf(s[k][e], s[k][2 + e]);
-                    mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 4));
-                    mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 8));
-                    mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 16));
-                    const float mn = fmaxf(m[k][e], mx - kUp);
-                    base[k][e] = mn == -INFINITY ? 0.f : mn;
-                    moved |= m[k][e] != mn;
-                    a[k][e] = m[k][e];
-                    m[k][e] = mn;
-                }
-            if (__any_sync(kAll, moved)) {
+                for (int e = 0; e < 2; ++e) base[k][e] = m[k][e] == -INFINITY ? 0.f : m[k][e];
+            if (KF == PF_E4 ? moved : __any_sync(kAll, moved)) {
 #pragma unroll
                 for (int k = 0; k < NQ; ++k)
 #pragma unroll
@@ -279,6 +295,21 @@ __global__ void __launch_bounds__(kDT, (Ring<D, KF, VF, NQ>::ctas)) decode_kerne
                         }
                     }
             }
+            uint32_t v_tile = k_tile + R::kb;
+            if constexpr (KF == PF_E4) {
+                if constexpr (!R::one) {
+                    v_tile = take();
+                    copy_next();
+                }
+                by = values.take(tile_scale<D>(v_tile), [&](float x) {
+#pragma unroll
+                    for (int d = 0; d < D / 16; ++d)
+#pragma unroll
+                        for (int k = 0; k < NQ; ++k)
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) o[d][k][c] *= x;
+                });
+            }
             uint32_t pb[NQ][2], lo[NQ][2] = {};
 #pragma unroll
             for (int k = 0; k < NQ; ++k)
@@ -287,15 +318,14 @@ __global__ void __launch_bounds__(kDT, (Ring<D, KF, VF, NQ>::ctas)) decode_kerne
                     const float x = ex2(s[k][2 * n] - base[k][0]), y = ex2(s[k][2 * n + 1] - base[k][1]);
                     l[k][0] += x;
                     l[k][1] += y;
-                    const uint32_t w = Two<T>::pack(x, y);
+                    const uint32_t w = KF == PF_E4 ? Two<T>::pack(x * by, y * by) : Two<T>::pack(x, y);
                     pb[k][n] = transpose8(w);
                     if constexpr (LO) {
                         const float2 hi = Two<T>::unpack(w);
                         lo[k][n] = transpose8(Two<T>::pack(x - hi.x, y - hi.y));
                     }
                 }
-            uint32_t v_tile = k_tile + R::kb;
-            if constexpr (!R::one) {
+            if constexpr (!R::one && KF != PF_E4) {
                 v_tile = take();
                 copy_next();
             }
@@ -330,7 +360,8 @@ __global__ void __launch_bounds__(kDT, (Ring<D, KF, VF, NQ>::ctas)) decode_kerne
                 if (r >= G) continue;
                 float mm = -INFINITY;
                 for (int w = 0; w < kDW; ++w) mm = fmaxf(mm, s_m[w][r]);
-                const float a = mm == -INFINITY ? 0.f : ex2(m[k][e] - mm);
+                float a = mm == -INFINITY ? 0.f : ex2(m[k][e] - mm);
+                if constexpr (KF == PF_E4) a *= values.unit;
                 float* dst = smem + ((int64_t)warp * G + r) * D;
                 using V = VGeo<D, VF>;
 #pragma unroll

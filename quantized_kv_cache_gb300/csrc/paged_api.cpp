@@ -92,7 +92,11 @@ PagedView view(const kvq_paged* h, int layer) {
 size_t workspace_floats(const kvq_paged_config& c, int64_t seqs, int64_t rows) {
     const int G = c.n_q_heads / c.n_kv_heads;
     const size_t a = (size_t)(line_floats(seqs) + (kMaxDecodeCtas + seqs * c.n_kv_heads) * partial_floats(G, c.head_dim));
-    const size_t b = (size_t)paged_prefill_ws_floats(c.head_dim, rows * c.n_q_heads);
+    size_t b = (size_t)paged_prefill_ws_floats(c.head_dim, rows * c.n_q_heads);
+    if (c.k_fmt == KVQ_PAGED_E4M3 && rows > 0) {
+        const size_t d = (size_t)paged_draft_ws_floats(c.head_dim, seqs);
+        if (d > b) b = d;
+    }
     return a > b ? a : b;
 }
 
@@ -446,6 +450,10 @@ kvq_status kv_paged_prefill_attn(kvq_paged* h, int32_t layer, int32_t dtype, int
     p.cu = cu_q;
     p.n_rows = n_rows;
     p.max_q = max_q < n_rows ? max_q : n_rows;
+    if (h->cfg.k_fmt == KVQ_PAGED_E4M3 && p.max_q * p.G <= kMaxDraftRows) {
+        const auto few = p.v.D == 64 ? launch_paged_draft_64 : (p.v.D == 128 ? launch_paged_draft_128 : launch_paged_draft_256);
+        return launched(few(p, h->sm_count, stream));
+    }
     const auto launch = p.v.D == 64 ? launch_paged_prefill_64 : (p.v.D == 128 ? launch_paged_prefill_128 : launch_paged_prefill_256);
     return launched(launch(p, &h->maps[2 * (size_t)layer], h->sm_count, stream));
 }

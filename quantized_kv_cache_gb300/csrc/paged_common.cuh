@@ -76,6 +76,7 @@ __device__ __forceinline__ float tanh_any(float x) {
 }
 
 __device__ __forceinline__ float normal_factor(float f) { return fminf(fmaxf(f, 1.17549435e-38f), 3.40282347e38f); }
+constexpr float kMaxFactor = 1.32922800e36f;      // 2^120: times an e4m3 block's power it stays finite
 // The score options, in units of log2. A score x = q.k * f, f = (the row's power of two) * scale * log2(e);
 // with a cap, f = .. * scale / softcap and x = softcap * log2(e) * tanh(q.k * f); then the bias.
 struct ScoreRule {

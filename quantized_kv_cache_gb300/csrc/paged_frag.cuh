@@ -127,6 +127,21 @@ template <int D> __device__ __forceinline__ float tile_scale(uint32_t base) {
     return fminf(x, (float)(1 << kMaxPowerAttn));
 }
 
+// The scales of e4m3 values go to the weights: o is in units of the largest power seen, and a tile's weights are multiplied by its
+// power over that, at most 1: powers of two, no rounding but below fp16's smallest number.
+struct ValueScale {
+    float unit = 0.f, one = 0.f;                 // the unit, and 1 / it
+    // The factor of a tile's weights; move(a) multiplies o by a where the unit grows.
+    template <typename F> __device__ __forceinline__ float take(float scale, const F& move) {
+        if (scale > unit) {
+            one = power_of(-exponent_of(scale));
+            move(unit * one);
+            unit = scale;
+        }
+        return scale * one;
+    }
+};
+
 // s[q] += K Q^T of the tile at `base` and query group q.
 template <int D, int PF, int NQ, typename T, typename PLACE>
 __device__ __forceinline__ void tile_scores(uint32_t base, const PLACE& at, const uint32_t (&qf)[D / 16][NQ][2], float (&s)[NQ][4]) {
@@ -171,7 +186,7 @@ __device__ __forceinline__ void tile_scores(uint32_t base, const PLACE& at, cons
     }
 }
 
-// o += V^T P^T of the tile's 16 positions (e4m3: times the tile's scale, in fp32). With LO, P = p + lo (two bf16 parts).
+// o += V^T P^T of the tile's 16 positions (e4m3: of the codes, see ValueScale). With LO, P = p + lo (two bf16 parts).
 template <int D, int PF, int NQ, typename T, bool LO, typename PLACE>
 __device__ __forceinline__ void tile_values(uint32_t base, const PLACE& at, const uint32_t (&p)[NQ][2], const uint32_t (&lo)[NQ][2],
                                             float (&o)[D / 16][NQ][4]) {
@@ -179,8 +194,6 @@ __device__ __forceinline__ void tile_values(uint32_t base, const PLACE& at, cons
     static_assert(V::NJ == 1 || V::CB == 16, "pieces j and j + 1 are 128 bytes apart");
     // rows 2t + 8 and 2t + 9: the same permutation (that of 32-byte rows too: two lines on)
     const uint32_t a0 = base + at.v[0], a1 = base + at.v[1], sc = base + at.vs;
-    float scale = 1.f;
-    if constexpr (PF == PF_E4) scale = tile_scale<D>(base);
 #pragma unroll
     for (int j = 0; j < V::NJ; ++j) {
         const Words<V::NW> r0 = ld_words<V::NW>(a0 + 128 * j), r1 = ld_words<V::NW>(a1 + 128 * j);
@@ -223,13 +236,6 @@ __device__ __forceinline__ void tile_values(uint32_t base, const PLACE& at, cons
 #pragma unroll
                 for (int q = 0; q < NQ; ++q) {
                     float (&acc)[4] = o[(V::CH * j + N * i + c) / 2][q];
-                    if constexpr (PF == PF_E4) {
-                        float x[4] = {};
-                        mma_t(x, a, p[q][0], p[q][1], T());
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[e] = fmaf(x[e], scale, acc[e]);
-                        continue;
-                    }
                     mma_t(acc, a, p[q][0], p[q][1], T());
                     if constexpr (LO) mma_t(acc, a, lo[q][0], lo[q][1], T());
                 }

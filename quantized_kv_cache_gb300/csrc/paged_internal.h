@@ -142,6 +142,9 @@ int launch_paged_decode_128(const PagedAttnParams& p, int sm_count, void* stream
 int launch_paged_decode_256(const PagedAttnParams& p, int sm_count, void* stream);
 // maps: two CUtensorMap, the layer's K and V area as [units][page_size][head_dim] of 16-bit values in boxes of
 // prefill_box_rows rows x 64 (16-bit pages; read for no other format)
+int launch_paged_draft_64(const PagedAttnParams& p, int sm_count, void* stream);
+int launch_paged_draft_128(const PagedAttnParams& p, int sm_count, void* stream);
+int launch_paged_draft_256(const PagedAttnParams& p, int sm_count, void* stream);
 int launch_paged_prefill_64(const PagedAttnParams& p, const void* maps, int sm_count, void* stream);
 int launch_paged_prefill_128(const PagedAttnParams& p, const void* maps, int sm_count, void* stream);
 int launch_paged_prefill_256(const PagedAttnParams& p, const void* maps, int sm_count, void* stream);
@@ -155,6 +158,14 @@ KVQ_HD int prefill_box_rows(int D, int ps) { return ps < prefill_tile(D) ? ps : 
 KVQ_HD int64_t partial_floats(int G, int D) { return 32 + (int64_t)G * D; }
 // Before the partials: n_seq + 1 int64, the tiles before each sequence.
 KVQ_HD int64_t line_floats(int64_t n_seq) { return (2 * (n_seq + 1) + 3) & ~(int64_t)3; }
+
+// Chunks of a few tokens over e4m3 pages (kernels_paged_draft.cu): rows of a group, the most rows of a KV head that go there, and the
+// floats that the runs leave, two partials each.
+KVQ_HD constexpr int draft_rows(int D) { return D == 256 ? 16 : 32; }
+constexpr int kMaxDraftRows = 64, kMaxDraftCtas = kMaxSms * 2;
+KVQ_HD int64_t paged_draft_ws_floats(int D, int64_t n_seq) {
+    return line_floats(n_seq) + (int64_t)kMaxDraftCtas * 2 * (2 * draft_rows(D) + (int64_t)draft_rows(D) * D);
+}
 
 // A chunk's positions are split when its row tiles alone leave SMs without work: as many splits as leave one CTA per SM.
 constexpr int kMaxSplits = 16;

@@ -356,6 +356,101 @@ def test_chunk_of_drafted_tokens_and_split_positions(D):
     chunk_case("bf16", 1, 4, D, 16, [6000], [40], dict(window=3000))
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("H,G,D,ps,q", [(2, 2, 64, 16, 7), (8, 5, 128, 32, 5), (4, 6, 256, 64, 5), (2, 16, 128, 16, 4), (1, 9, 64, 128, 7),
+                                        (1, 16, 256, 256, 4), (3, 1, 128, 64, 64), (2, 3, 256, 16, 21), (1, 5, 128, 16, 13)])
+def test_few_rows_match_64_bits(dtype, H, G, D, ps, q):
+    """Up to 64 rows a KV head, and one token more than that."""
+    chunk_case(dtype, H, G, D, ps, [q, 1, 1025, 17, 300, q + 1], [q, 1, q, 0, 2, q], {})
+
+
+@pytest.mark.parametrize("opts", OPTS[1:] + [dict(window=1), dict(prefix=60, window=3)])
+@pytest.mark.parametrize("dtype,D,G", [("f16", 128, 4), ("bf16", 64, 12), ("bf16", 256, 3)])
+def test_few_rows_options(opts, dtype, D, G):
+    chunk_case(dtype, 2, G, D, 32, [200, 1, 47, 1500], [5, 1, 4, 3], opts)
+
+
+def test_few_rows_of_many_sequences():
+    """More groups than runs, and one sequence that all runs share; odd gaps of a batch padded with empty sequences."""
+    chunk_case("f16", 4, 4, 128, 16, [3 + (11 * i) % 60 for i in range(200)], [i % 4 for i in range(200)], {}, gap=5)
+    chunk_case("bf16", 1, 8, 128, 64, [40000], [8], {})
+    chunk_case("f16", 1, 4, 256, 64, [30001], [9], dict(slopes=True))
+
+
+@pytest.mark.parametrize("D,tokens", [(64, 6), (128, 6), (256, 3), (128, 40)])
+def test_later_rows_do_not_reach_earlier_queries(D, tokens):
+    """NaN in the keys and values of some of the chunk's own tokens: the rows before them stay within the bound, those from them on are NaN."""
+    for at in ("k", "v"):
+        n = 50 + tokens
+        p = Pages8(2, D, 32, 8, Hq=8, max_seqs=1, max_tokens=tokens)
+        table, ks, vs = e8.fill(p, 0, [n], 5)
+        raw, j = p.host(), n - 2
+        codes, _ = p.unit(raw, 0, 1 if at == "v" else 0, int(table[0, j // 32]), 1)
+        codes[j % 32] = 127
+        codes[j % 32, ::2] = 255
+        p.pool.copy_(torch.from_numpy(raw))
+        q = torch.randn((tokens, 8, D), generator=torch.Generator().manual_seed(1)).half().cuda()
+        out, lse = torch.empty_like(q), torch.empty((tokens, 8), device="cuda")
+        p.cache.prefill_attn(0, q, ints([0, tokens]), tokens, table, ints([n]), out, lse=lse)
+        k = tokens - 2
+        want = pc.attention64(q.double(), ks[0], vs[0], torch.arange(n - tokens, n, device="cuda"), 1 / math.sqrt(D))
+        pc.check_attention(out[:k], lse[:k], tuple(x[:k] for x in want), "f16", 2.0 ** -11, steps_of(n))
+        pc.check_attention(out[:, :4].contiguous(), lse[:, :4], tuple(x[:, :4] for x in want), "f16", 2.0 ** -11, steps_of(n))
+        assert torch.isnan(out[k:, 4:]).all() and (torch.isnan(lse[k:, 4:]).all() if at == "k" else torch.isfinite(lse).all())
+
+
+def test_few_rows_at_negative_positions_and_bad_lengths():
+    p = Pages8(1, 64, 16, 4, Hq=2, max_seqs=2, max_tokens=20)
+    table, ks, vs = e8.fill(p, 0, [10, 30], 1)
+    q = torch.randn((18, 2, 64), device="cuda").half()
+    out, lse = torch.full_like(q, 7.0), torch.full((18, 2), 7.0, device="cuda")
+    p.cache.prefill_attn(0, q, ints([0, 13, 15]), 13, table, ints([10, 30]), out, lse=lse, prefix=ints([4, 0]))
+    assert not out[:3].any() and (lse[:3] == -math.inf).all() and (out[15:] == 7).all()
+    want = pc.attention64(q[:13].double(), ks[0], vs[0], torch.arange(-3, 10, device="cuda"), 1 / 8, prefix=4)
+    pc.check_attention(out[:13], lse[:13], want, "f16", 2.0 ** -11, steps_of(10))
+    p.cache.prefill_attn(0, q, ints([0, 13, 15]), 13, table, ints([0, -1]), out, lse=lse)
+    assert not out[:15].any() and (lse[:15] == -math.inf).all() and p.cache.status() == _lib.PAGED_BAD_LENGTH
+    out.fill_(7.0)
+    p.cache.prefill_attn(0, q, ints([0, 10, 15]), 2, table, ints([10, 30]), out, lse=lse)     # longer than max_q
+    assert p.cache.status() == _lib.PAGED_BAD_LENGTH and (out[2:10] == 7).all() and (out[12:] == 7).all()
+    want = pc.attention64(q[:2].double(), ks[0], vs[0], torch.arange(2, device="cuda"), 1 / 8)
+    pc.check_attention(out[:2], lse[:2], want, "f16", 2.0 ** -11, steps_of(10))
+    for cu in ([0, 13, 19], [-1, 3, 5], [0, 5, 3]):
+        p.cache.prefill_attn(0, q, ints(cu), 13, table, ints([10, 30]), out, lse=lse)
+        assert p.cache.status() == _lib.PAGED_BAD_LENGTH
+    bad = table.clone()
+    bad[1, 0] = 4
+    p.cache.prefill_attn(0, q, ints([0, 5, 10]), 5, bad, ints([10, 30]), out, lse=lse)
+    assert p.cache.status() == _lib.PAGED_BAD_INDEX
+
+
+def test_captured_drafts_follow_their_bounds():
+    p = Pages8(2, 128, 32, 60, Hq=8, max_seqs=3, max_tokens=24, seed=3)
+    table, _, _ = e8.fill(p, 0, [900, 333, 40], 4)
+    cu, lens = ints([0, 5, 10, 15]), ints([900, 333, 40])
+    q = torch.randn((15, 8, 128), generator=torch.Generator().manual_seed(0)).half().cuda()
+    out, lse = torch.empty_like(q), torch.empty((15, 8), device="cuda")
+    g, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+
+    def call(out, lse):
+        p.cache.prefill_attn(0, q, cu, 8, table, lens, out, lse=lse, stream=stream())
+
+    with torch.cuda.stream(side):
+        call(out, lse)
+        side.synchronize()
+        with torch.cuda.graph(g, stream=side):
+            call(out, lse)
+    for i, (c, n) in enumerate((([0, 5, 10, 15], [900, 333, 40]), ([0, 0, 7, 15], [1, 50, 39]), ([0, 1, 2, 2], [800, 333, 40]))):
+        cu.copy_(ints(c))
+        lens.copy_(ints(n))
+        q.copy_(torch.randn(q.shape, generator=torch.Generator().manual_seed(i)))
+        g.replay()
+        want, want_lse = torch.empty_like(out), torch.empty_like(lse)
+        torch.cuda.synchronize()
+        call(want, want_lse)
+        assert torch.equal(out[:c[3]], want[:c[3]]) and torch.equal(lse[:c[3]], want_lse[:c[3]])
+
+
 # ------------------------------------------------------------------------------------------------ together
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 def test_prompt_then_steps(dtype):
