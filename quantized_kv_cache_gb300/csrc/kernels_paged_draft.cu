@@ -78,19 +78,19 @@ __device__ __forceinline__ void draft_scores(uint32_t base, const PLACE& at, uin
         uint32_t f[K::NW][4];
 #pragma unroll
         for (int i = 0; i < K::NW; ++i) {
-            f[i][0] = e4m3_pair(x.w[i] & 0xffffu);
-            f[i][1] = e4m3_pair(y.w[i] & 0xffffu);
-            f[i][2] = e4m3_pair(x.w[i] >> 16);
-            f[i][3] = e4m3_pair(y.w[i] >> 16);
+            e4m3_four(x.w[i], f[i][0], f[i][2]);
+            e4m3_four(y.w[i], f[i][1], f[i][3]);
         }
 #pragma unroll
-        for (int k = 0; k < NQ; ++k)
+        for (int i = 0; i < 2 * KS; ++i) {                        // a block's products wait for one another: the blocks in turn
+            Words<4> z[NQ];
 #pragma unroll
-            for (int i = 0; i < 2 * KS; ++i) {
-                const Words<4> z = ld_words<4>(q + ((k * (D / 32) + 2 * KS * j + i) * 32) * 16);
-                mma_t(s[k], f[2 * i], z.w[0], z.w[1], __half());
-                mma_t(s[k], f[2 * i + 1], z.w[2], z.w[3], __half());
-            }
+            for (int k = 0; k < NQ; ++k) z[k] = ld_words<4>(q + ((k * (D / 32) + 2 * KS * j + i) * 32) * 16);
+#pragma unroll
+            for (int k = 0; k < NQ; ++k) mma_t(s[k], f[2 * i], z[k].w[0], z[k].w[1], __half());
+#pragma unroll
+            for (int k = 0; k < NQ; ++k) mma_t(s[k], f[2 * i + 1], z[k].w[2], z[k].w[3], __half());
+        }
     }
 }
 

@@ -121,10 +121,11 @@ __device__ __forceinline__ uint4 decode_q4(uint32_t c, uint32_t d) {
 // number) and, where `small`, what is left of it.
 __device__ __forceinline__ uint4 decode_e4(uint2 c, uint32_t mul, uint32_t rest, bool small) {
     uint32_t o[4];
+    e4m3_four(c.x, o[0], o[1]);
+    e4m3_four(c.y, o[2], o[3]);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t x = i & 2 ? c.y : c.x;
-        o[i] = u32(__hmul2(h2(e4m3_pair(i & 1 ? x >> 16 : x & 0xffffu)), h2(mul)));
+        o[i] = u32(__hmul2(h2(o[i]), h2(mul)));
         if (small) o[i] = u32(__hmul2(h2(o[i]), h2(rest)));
     }
     return make_uint4(o[0], o[1], o[2], o[3]);
@@ -242,39 +243,71 @@ __device__ __forceinline__ void weights32(const uint32_t (&x)[32], uint64_t f, u
     for (int e = 16 - A; e < 16; ++e) last(e);
 }
 
-// Raw scores of 32 positions from p0 on to scores in units of log2: the cap, then the bias. Two scores an instruction;
-// where all capped ones are below 1/4 of the cap no exponential is taken (the odd series of tanh, five terms).
-__device__ __forceinline__ void apply_rule(uint32_t (&s)[32], const ScoreRule& rule, const RowState& r, int p0) {
-    const float2 f = make_float2(r.f, r.f);
-    float big = 0.f;
+// weights32 with the cap and the bias on the way: scores of 32 positions from p0 on, in units of log2, less the row's maximum (m its
+// negative) as it stands; `hide` takes out what the row does not see. Where all capped scores are below 0.35 of the cap no
+// exponential is taken for them: tanh x = x (1 + q c(q)), q = x^2, with the polynomial of least relative error on that range
+// (2^-24.5). top: the largest score less the maximum.
+template <typename T, typename HIDE>
+__device__ __forceinline__ void rule_weights32(uint32_t (&s)[32], const ScoreRule& rule, const RowState& r, int p0, float m, const HIDE& hide,
+                                               uint32_t* w, uint64_t (&sum)[4], float (&top)[4]) {
+    const float2 f = make_float2(r.f, r.f), back = make_float2(m, m);
+    float2 x[16];
 #pragma unroll
-    for (int e = 0; e < 32; e += 2) {
-        const float2 x = __fmul2_rn(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), f);
-        s[e] = __float_as_uint(x.x);
-        s[e + 1] = __float_as_uint(x.y);
-        big = max3(big, fabsf(x.x), fabsf(x.y));
-    }
+    for (int e = 0; e < 16; ++e) x[e] = make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
     if (rule.cap > 0.f) {
-        if (__all_sync(kAll, big < 0.25f)) {
-            const auto both = [&](float c) { return make_float2(c * rule.cap_l2, c * rule.cap_l2); };
-            const float2 c0 = both(1.f), c1 = both(-0.33333334f), c2 = both(0.13333333f), c3 = both(-0.053968254f), c4 = both(0.021869489f);
+        float big = 0.f;
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-                const float2 x = make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), q = __fmul2_rn(x, x);
-                const float2 y = __fmul2_rn(x, __ffma2_rn(q, __ffma2_rn(q, __ffma2_rn(q, __ffma2_rn(q, c4, c3), c2), c1), c0));
-                s[e] = __float_as_uint(y.x);
-                s[e + 1] = __float_as_uint(y.y);
+        for (int e = 0; e < 16; ++e) {
+            x[e] = __fmul2_rn(x[e], f);
+            big = max3(big, fabsf(x[e].x), fabsf(x[e].y));
+        }
+        const auto both = [&](float c) { return make_float2(c * rule.cap_l2, c * rule.cap_l2); };
+        if (__all_sync(kAll, big < 0.35f)) {
+            const float2 c0 = both(1.f), c1 = both(-0.33332664f), c2 = both(0.13299826f), c3 = both(-0.049148493f);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const float2 q = __fmul2_rn(x[e], x[e]);
+                x[e] = __fmul2_rn(x[e], __ffma2_rn(q, __ffma2_rn(q, __ffma2_rn(q, c3, c2), c1), c0));
             }
         } else {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) s[e] = __float_as_uint(rule.cap_l2 * tanh_any(__uint_as_float(s[e])));
+            for (int e = 0; e < 16; ++e)
+                x[e] = make_float2(rule.cap_l2 * tanh_any(x[e].x), rule.cap_l2 * tanh_any(x[e].y));
         }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[e] = __fmul2_rn(x[e], f);
     }
     if (rule.biased) {
         const float d = (float)(r.pos - p0);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) s[e] = __float_as_uint(__uint_as_float(s[e]) - r.slope * fabsf(d - (float)e));
+        for (int e = 0; e < 16; ++e) {
+            x[e].x = fmaf(-r.slope, fabsf(d - (float)(2 * e)), x[e].x);
+            x[e].y = fmaf(-r.slope, fabsf(d - (float)(2 * e + 1)), x[e].y);
+        }
     }
+    // subtracted by itself: of large scores the rounding of the product would be left where it is fused
+#pragma unroll
+    for (int e = 0; e < 16; ++e) x[e] = __fadd2_rn(x[e], back);
+    hide(x);
+    float v[32] = {};
+    const auto last = [&](int e) {                            // as in weights32
+        if constexpr (std::is_same<T, __half>::value)
+            asm volatile("cvt.rn.f16x2.f32 %0, %1, %2;\n" : "=r"(w[e]) : "f"(v[2 * e + 1]), "f"(v[2 * e]));
+        else
+            asm volatile("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(w[e]) : "f"(v[2 * e + 1]), "f"(v[2 * e]));
+        asm volatile("add.rn.f32x2 %0, %0, %1;\n" : "+l"(sum[e & 3]) : "l"(pair(v[2 * e], v[2 * e + 1])));
+    };
+    constexpr int A = 2;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+        asm volatile("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(v[2 * e]) : "f"(x[e].x));
+        asm volatile("max.f32 %0, %0, %1, %2;\n" : "+f"(top[e & 3]) : "f"(x[e].x), "f"(x[e].y));
+        asm volatile("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(v[2 * e + 1]) : "f"(x[e].y));
+        if (e >= A) last(e - A);
+    }
+#pragma unroll
+    for (int e = 16 - A; e < 16; ++e) last(e);
 }
 
 // Whole prompts: the row tiles of all sequences are one line, so that ragged ones leave no block without work. The sequence of
@@ -307,7 +340,7 @@ __device__ __forceinline__ int find_tile(const PagedAttnParams& p, int slot, int
 constexpr int kRows = 4;
 constexpr bool codes_of(int kf) { return kf > 0 && kf < kRows; }
 
-template <int D, int KF, int VF, typename T, typename TQ>
+template <int D, int KF, int VF, typename T, typename TQ, bool RULE>      // RULE: scores go through a cap or a bias
 __global__ void __launch_bounds__(Geo<D, codes_of(KF)>::threads, 1) prefill_kernel(const __grid_constant__ PagedAttnParams p,
                                                                         const __grid_constant__ CUtensorMap k_map,
                                                                         const __grid_constant__ CUtensorMap v_map, int splits) {
@@ -514,35 +547,36 @@ __global__ void __launch_bounds__(Geo<D, codes_of(KF)>::threads, 1) prefill_kern
                 // numbers are loaded a stage before they are looked at (item by item, with the number checked at once,
                 // an item's loads took 1,500 cycles and the 6 prompts above 336 us, against 321 at that time).
                 constexpr int per = D / 16, step = 32 * GE::prod / per, E = (BN + step - 1) / step;   // rows apart, of a thread
-                const int id = 32 * pw + lane, row0 = id / per, ch = id % per * 16;
+                // eight lanes take four pieces of two neighbouring rows: their stores hit all banks
+                constexpr int nb = D / 64;
+                const int row0 = pw * (32 / per) + ((lane >> 2) & 1) + 2 * (lane / 8 / nb), ch = 64 * (lane / 8 % nb) + 16 * (lane & 3);
                 struct Codes {
                     uint4 c[E];
-                    uint32_t d[E];
-                } kc, vc;
+                    uint32_t d[E], held;                                // by bit: the row holds a position
+                };
                 const auto load = [&](auto fmt, int w, int tile, int units, Codes& x) {   // units: of the tile's 16-row blocks, by lane
                     constexpr bool E4 = decltype(fmt)::value == 3, Q8 = decltype(fmt)::value == 1 || E4;   // a byte a value
                     constexpr int RB = Q8 ? D : D / 2;
                     const uint8_t* base_w = w ? p.v.base[1] : p.v.base[0];
                     const uint32_t unit = (uint32_t)(w ? p.v.unit[1] : p.v.unit[0]);
                     const int p0 = kv.at(i0 + tile), live = c.len - p0;
+                    // Loaded whether the row holds a position or not (of page 0 where there is no page): a load behind a branch
+                    // goes to its place by a move, which waits for it.
+                    x.held = 0;
 #pragma unroll
                     for (int e = 0; e < E; ++e) {
-                        const int r = row0 + e * step, un = __shfl_sync(kAll, units, (r >> 4) & (BN / 16 - 1));
-                        x.c[e] = make_uint4(0, 0, 0, 0);
-                        x.d[e] = 0;
-                        if (r < BN && un >= 0 && r < live) {
-                            const int row = (p0 + r) & (p.v.ps - 1);
-                            const uint8_t* a = base_w + (uint64_t)(uint32_t)un * unit;
-                            if constexpr (E4) x.d[e] = *reinterpret_cast<const uint32_t*>(a + p.v.ps * RB + row / kTile * 4);
-                            else x.d[e] = *reinterpret_cast<const uint16_t*>(a + (p.v.ps * RB + row * (D / 16) + ch / 32 * 2));
-                            a += row * RB + (Q8 ? ch : ch / 2);
-                            if constexpr (Q8) {
-                                x.c[e] = *reinterpret_cast<const uint4*>(a);
-                            } else {
-                                const uint2 y = *reinterpret_cast<const uint2*>(a);
-                                x.c[e].x = y.x;
-                                x.c[e].y = y.y;
-                            }
+                        const int r = min(row0 + e * step, BN - 1), un = __shfl_sync(kAll, units, r >> 4), row = (p0 + r) & (p.v.ps - 1);
+                        if (un >= 0 && r < live) x.held |= 1u << e;
+                        const uint8_t* a = base_w + (uint64_t)(uint32_t)max(un, 0) * unit;
+                        if constexpr (E4) x.d[e] = *reinterpret_cast<const uint32_t*>(a + p.v.ps * RB + row / kTile * 4);
+                        else x.d[e] = *reinterpret_cast<const uint16_t*>(a + (p.v.ps * RB + row * (D / 16) + ch / 32 * 2));
+                        a += row * RB + (Q8 ? ch : ch / 2);
+                        if constexpr (Q8) {
+                            x.c[e] = *reinterpret_cast<const uint4*>(a);
+                        } else {
+                            const uint2 y = *reinterpret_cast<const uint2*>(a);
+                            x.c[e].x = y.x;
+                            x.c[e].y = y.y;
                         }
                     }
                 };
@@ -552,16 +586,17 @@ __global__ void __launch_bounds__(Geo<D, codes_of(KF)>::threads, 1) prefill_kern
                     for (int e = 0; e < E; ++e) {
                         const int r = row0 + e * step;
                         if (r >= BN) continue;
+                        const bool held = (x.held >> e) & 1;
                         if constexpr (decltype(fmt)::value == 3) {
-                            const float d = fminf(__uint_as_float(x.d[e]), (float)(1 << kMaxPowerAttn)), mul = fmaxf(d, power_of(-13));
+                            const float d = fminf(__uint_as_float(held ? x.d[e] : 0u), (float)(1 << kMaxPowerAttn)), mul = fmaxf(d, power_of(-13));
                             const bool small = mul > d;
                             const uint32_t dd = Two<__half>::pack(mul, mul), rest = Two<__half>::pack(d * 8192.f, d * 8192.f);
-                            const uint4 y = x.c[e];
+                            const uint4 y = held ? x.c[e] : make_uint4(0, 0, 0, 0);
                             st_shared16(dst + tile_byte(BN, r, ch), decode_e4(make_uint2(y.x, y.y), dd, rest, small));
                             st_shared16(dst + tile_byte(BN, r, ch + 8), decode_e4(make_uint2(y.z, y.w), dd, rest, small));
                             continue;
                         }
-                        const uint32_t dd = cut_scales<Q8>(x.d[e] | (x.d[e] << 16));
+                        const uint32_t dd = held ? cut_scales<Q8>(x.d[e] | (x.d[e] << 16)) : 0u;
                         const uint4 y = x.c[e];
                         st_shared16(dst + tile_byte(BN, r, ch), Q8 ? decode_q8(make_uint2(y.x, y.y), dd) : decode_q4(y.x, dd));
                         st_shared16(dst + tile_byte(BN, r, ch + 8), Q8 ? decode_q8(make_uint2(y.z, y.w), dd) : decode_q4(y.y, dd));
@@ -579,25 +614,36 @@ __global__ void __launch_bounds__(Geo<D, codes_of(KF)>::threads, 1) prefill_kern
                     raise_status(p.v.status, KVQ_PAGED_BAD_INDEX);
                     return -1;
                 };
-                int page = table_of(0), units = -1;
-                if (nt > 0) {
-                    units = units_of(page);
-                    load(kf, 0, 0, units, kc);
-                }
-                page = table_of(1);
-#pragma unroll 1
-                for (int u = 0; u <= nt && nt > 0; ++u) {
-                    if (u >= 2) wait(empty + 8 * (u & 1), ((u >> 1) - 1) & 1);
-                    if (u > 0) store(vf, ring + (2 + ((u - 1) & 1)) * GE::slot, vc);
-                    if (u < nt) store(kf, ring + (u & 1) * GE::slot, kc);
+                const auto await_stage = [&](int u) { if (u >= 2) wait(empty + 8 * (u & 1), ((u >> 1) - 1) & 1); };
+                const auto stage_full = [&](int u) {
                     fence_async_smem();
                     mbar_arrive(full + 8 * (u & 1));
-                    if (u < nt) load(vf, 1, u, units, vc);
-                    if (u + 1 < nt) {
+                };
+                // Stage u takes V of tile u - 1 and K of tile u; the next one's loads are issued behind it, without a branch (behind one
+                // the loads' places are moved about, which waits for them), and the next page numbers are looked at before any of
+                // them (a wait for these behind them would be one for those too).
+                if (nt > 0) {
+                    Codes kc, vc;
+                    int units = units_of(table_of(0)), page = table_of(1);
+                    load(kf, 0, 0, units, kc);
+                    store(kf, ring, kc);
+                    stage_full(0);
+#pragma unroll 1
+                    for (int u = 1; u < nt; ++u) {
+                        const int old = units;
                         units = units_of(page);
-                        page = table_of(u + 2);
-                        load(kf, 0, u + 1, units, kc);
+                        page = table_of(u + 1);
+                        load(vf, 1, u - 1, old, vc);
+                        load(kf, 0, u, units, kc);
+                        await_stage(u);
+                        store(vf, ring + (2 + ((u - 1) & 1)) * GE::slot, vc);
+                        store(kf, ring + (u & 1) * GE::slot, kc);
+                        stage_full(u);
                     }
+                    load(vf, 1, nt - 1, units, vc);
+                    await_stage(nt);
+                    store(vf, ring + (2 + ((nt - 1) & 1)) * GE::slot, vc);
+                    stage_full(nt);
                 }
             }
         }
@@ -607,14 +653,13 @@ __global__ void __launch_bounds__(Geo<D, codes_of(KF)>::threads, 1) prefill_kern
         const int t = warp >> 2, in = threadIdx.x & 127, row = r0 + 128 * t + in;
         const bool alive = row < r1;
         const ScoreRule rule = score_rule(p);
-        const bool plain = rule.plain();
         RowState rs;
         const int64_t at = (int64_t)(c.row0 + (alive ? row / G : 0)) * p.Hq + h * G + (alive ? row % G : 0);
         rs.pos = alive ? c.pos0 + row / G : -1;
         rs.lo = p.window > 0 && rs.pos >= p.window ? rs.pos - p.window + 1 : 0;
         rs.hi = min(rs.pos, c.len - 1);
         rs.pre = rs.pos >= 0 ? c.pre : 0;
-        rs.slope = plain || !p.slopes || !alive ? 0.f : p.slopes[h * G + row % G] * kL2e;
+        rs.slope = !RULE || !p.slopes || !alive ? 0.f : p.slopes[h * G + row % G] * kL2e;
         rs.f = rule.factor(1.f);
         float m = -INFINITY, l = 0.f;
         if (t < active) {
@@ -667,40 +712,40 @@ __global__ void __launch_bounds__(Geo<D, codes_of(KF)>::threads, 1) prefill_kern
                 const bool whole = p0 + BN <= c.pre ? first >= 0
                                                     : p0 + BN - 1 <= first && p0 + BN <= c.len &&
                                                           (p.window <= 0 || p0 >= last - p.window + 1);
-                const float f = plain ? rs.f : 1.f;
                 uint32_t sr[2][32], pr[BN / 64][32];
                 float mx = -INFINITY, sum = 0.f;
-                // scores that the options or the visibility change go back to S first
-                if (!plain || !whole) {
+                const auto hide = [&](int k, const auto& put) {           // put(e): position 32 k + e of the tile is not seen
+                    const int hi = rs.hi - p0 - 32 * k, lo = rs.lo - p0 - 32 * k, pre = rs.pre - p0 - 32 * k;
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (!((e <= hi && e >= lo) || e < pre)) put(e);
+                };
+                // scores that the visibility changes go back to S first (with options they are changed on their way to the weights)
+                if (!RULE && !whole) {
                     tmem_ld32(s_addr, sr[0]);
 #pragma unroll
                     for (int k = 0; k < BN / 32; ++k) {
                         uint32_t(&x)[32] = sr[k & 1];
                         tmem_wait_ld(x);
                         if (k + 1 < BN / 32) tmem_ld32(s_addr + 32 * (k + 1), sr[(k + 1) & 1]);
-                        if (!plain) apply_rule(x, rule, rs, p0 + 32 * k);
-                        if (!whole) {
-                            const int hi = rs.hi - p0 - 32 * k, lo = rs.lo - p0 - 32 * k, pre = rs.pre - p0 - 32 * k;
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (!((e <= hi && e >= lo) || e < pre)) x[e] = 0xff800000u;
-                        }
+                        hide(k, [&](int e) { x[e] = 0xff800000u; });
                         tmem_st32(s_addr + 32 * k, x);
                     }
                     tmem_wait_st();
                 }
-                if constexpr (NT == 1) {
-                    // S runs ahead of the values here: those of tile i - 1 are done before this tile's weights go out
-                    // (with two row tiles, S of tile i was issued after them)
-                    if (i > 0) {
-                        wait(o_done, (i - 1) & 1);
-                        tc_fence_after();
-                    }
-                }
+                // With one row tile S runs ahead of the values: those of tile i - 1 are done before O is touched and before this
+                // tile's weights go out (with two row tiles, S of tile i was issued after them).
+                bool o_free = NT == 2 || i == 0;
+                const auto await_o = [&]() {
+                    if (o_free) return;
+                    wait(o_done, (i - 1) & 1);
+                    tc_fence_after();
+                    o_free = true;
+                };
                 // The weights are formed with the maximum as it stands while the tile's own is found; only where that
                 // is more than kLazy above (and for the first tile) the maximum moves and the weights are formed again.
                 for (bool last_try = false;; last_try = true) {
-                    const float2 f2 = make_float2(f, f), mb = m == -INFINITY ? make_float2(0.f, 0.f) : make_float2(-m, -m);
+                    const float2 f2 = make_float2(rs.f, rs.f), mb = m == -INFINITY ? make_float2(0.f, 0.f) : make_float2(-m, -m);
                     uint64_t s2[4] = {};
                     float y[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
                     tmem_ld32(s_addr, sr[0]);
@@ -709,20 +754,27 @@ __global__ void __launch_bounds__(Geo<D, codes_of(KF)>::threads, 1) prefill_kern
                         uint32_t(&x)[32] = sr[k & 1];
                         tmem_wait_ld(x);
                         if (k + 1 < BN / 32) tmem_ld32(s_addr + 32 * (k + 1), sr[(k + 1) & 1]);
-                        weights32<T>(x, pair(f2.x, f2.y), pair(mb.x, mb.y), &pr[k / 2][16 * (k & 1)], s2, y);
+                        if constexpr (RULE)
+                            rule_weights32<T>(x, rule, rs, p0 + 32 * k, mb.x, [&](float2 (&z)[16]) {
+                                if (!whole) hide(k, [&](int e) { (e & 1 ? z[e / 2].y : z[e / 2].x) = -INFINITY; });
+                            }, &pr[k / 2][16 * (k & 1)], s2, y);
+                        else
+                            weights32<T>(x, pair(f2.x, f2.y), pair(mb.x, mb.y), &pr[k / 2][16 * (k & 1)], s2, y);
                     }
                     {
                         const float2 a = unpair(s2[0]), b = unpair(s2[1]), c2 = unpair(s2[2]), d = unpair(s2[3]);
                         sum = ((a.x + a.y) + (b.x + b.y)) + ((c2.x + c2.y) + (d.x + d.y));
                     }
                     if (last_try) break;
-                    mx = max3(fmaxf(y[0], y[1]), y[2], y[3]) * f - kUp;
+                    mx = max3(fmaxf(y[0], y[1]), y[2], y[3]);
+                    mx = (RULE ? mx - mb.x : mx * rs.f) - kUp;
                     const bool grow = mx > m + kLazy || (m == -INFINITY && mx > -INFINITY);
                     if (!__any_sync(kAll, grow)) break;
                     const float a = grow ? ex2(m - mx) : 1.f;
                     if (grow) m = mx;
                     l *= a;
                     if (i > 0) {
+                        await_o();
 #pragma unroll 1
                         for (int d = 0; d < D; d += 32) {
                             tmem_ld32(o_addr + d, sr[0]);
@@ -734,6 +786,7 @@ __global__ void __launch_bounds__(Geo<D, codes_of(KF)>::threads, 1) prefill_kern
                     }
                 }
                 l += sum;
+                await_o();
 #pragma unroll
                 for (int k = 0; k < BN / 64; ++k) tmem_st32(s_addr + 32 * k, pr[k]);
                 tmem_wait_st();
@@ -847,7 +900,7 @@ template <int D, typename TQ> __global__ void __launch_bounds__(kJT) prefill_joi
 template <int D, int KF, int VF, typename T, typename TQ>
 int prefill_run(const PagedAttnParams& p, const CUtensorMap* maps, int sm_count, cudaStream_t s) {
     using GE = Geo<D, codes_of(KF)>;
-    const auto k = prefill_kernel<D, KF, VF, T, TQ>;
+    const auto k = p.softcap > 0.f || p.slopes ? prefill_kernel<D, KF, VF, T, TQ, true> : prefill_kernel<D, KF, VF, T, TQ, false>;
     int res = 0;
     if (const int e = resident_ctas((const void*)k, GE::threads, GE::smem, &res)) return e;
     const int64_t chunk = (int64_t)p.max_q * p.G;

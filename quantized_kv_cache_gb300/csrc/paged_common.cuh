@@ -121,6 +121,10 @@ __device__ __forceinline__ uint32_t e4m3_pair(uint32_t c) {
     asm("{ .reg .b16 x; cvt.u16.u32 x, %1; cvt.rn.f16x2.e4m3x2 %0, x; }\n" : "=r"(h) : "r"(c));
     return h;
 }
+// Four codes: the lower two, the upper two.
+__device__ __forceinline__ void e4m3_four(uint32_t c, uint32_t& lo, uint32_t& hi) {
+    asm("{ .reg .b16 x, y; mov.b32 {x, y}, %2; cvt.rn.f16x2.e4m3x2 %0, x; cvt.rn.f16x2.e4m3x2 %1, y; }\n" : "=r"(lo), "=r"(hi) : "r"(c));
+}
 // Two numbers as e4m3 codes, nearest even, 448 at most; a NaN stays one.
 __device__ __forceinline__ uint32_t e4m3_codes(float lo, float hi) {
     uint32_t c;

@@ -153,6 +153,7 @@ __device__ __forceinline__ void tile_scores(uint32_t base, const PLACE& at, cons
 #pragma unroll
         for (int q = 0; q < NQ; ++q) mma_t(s[q], a, qf[ks][q][0], qf[ks][q][1], T());
     };
+    float odds[NQ][4] = {};      // e4m3: two sums in turn, as one product waits for the other
 #pragma unroll
     for (int j = 0; j < K::NJ; ++j) {
         const uint32_t a = (j & 1 ? odd : even) + j / 2 * 128;
@@ -163,8 +164,13 @@ __device__ __forceinline__ void tile_scores(uint32_t base, const PLACE& at, cons
             step(KS * j + 1, x.w[2], y.w[2], x.w[3], y.w[3]);
         } else if constexpr (PF == PF_E4) {                                // codes as they are: the tile's scale goes to the scores
 #pragma unroll
-            for (int i = 0; i < K::NW; ++i)
-                step(KS * j + i, e4m3_pair(x.w[i] & 0xffffu), e4m3_pair(y.w[i] & 0xffffu), e4m3_pair(x.w[i] >> 16), e4m3_pair(y.w[i] >> 16));
+            for (int i = 0; i < K::NW; ++i) {
+                uint32_t a[4];
+                e4m3_four(x.w[i], a[0], a[2]);
+                e4m3_four(y.w[i], a[1], a[3]);
+#pragma unroll
+                for (int q = 0; q < NQ; ++q) mma_t(i & 1 ? odds[q] : s[q], a, qf[KS * j + i][q][0], qf[KS * j + i][q][1], T());
+            }
         } else {
             const uint32_t d1 = ld_half(sc + K::CH * j / 4), e1 = ld_half(sc + 8 * (D / 16) + K::CH * j / 4);
             const uint32_t d = cut_scales<PF == PF_Q8>(__byte_perm(d1, d1, 0x1010)), e = cut_scales<PF == PF_Q8>(__byte_perm(e1, e1, 0x1010));
@@ -183,6 +189,12 @@ __device__ __forceinline__ void tile_scores(uint32_t base, const PLACE& at, cons
                 }
             }
         }
+    }
+    if constexpr (PF == PF_E4) {
+#pragma unroll
+        for (int q = 0; q < NQ; ++q)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) s[q][c] += odds[q][c];
     }
 }
 
@@ -215,10 +227,10 @@ __device__ __forceinline__ void tile_values(uint32_t base, const PLACE& at, cons
             } else if constexpr (PF == PF_E4) {                            // rows 2t, 2t + 1 byte by byte
                 const uint32_t xe = __byte_perm(r0.w[i], r1.w[i], 0x5140), xo = __byte_perm(r0.w[i], r1.w[i], 0x7362);
                 const uint32_t ye = __byte_perm(r2.w[i], r3.w[i], 0x5140), yo = __byte_perm(r2.w[i], r3.w[i], 0x7362);
-                b0[0] = e4m3_pair(xe & 0xffffu); b0[1] = e4m3_pair(xe >> 16);
-                b0[2] = e4m3_pair(xo & 0xffffu); b0[3] = e4m3_pair(xo >> 16);
-                b1[0] = e4m3_pair(ye & 0xffffu); b1[1] = e4m3_pair(ye >> 16);
-                b1[2] = e4m3_pair(yo & 0xffffu); b1[3] = e4m3_pair(yo >> 16);
+                e4m3_four(xe, b0[0], b0[1]);
+                e4m3_four(xo, b0[2], b0[3]);
+                e4m3_four(ye, b1[0], b1[1]);
+                e4m3_four(yo, b1[2], b1[3]);
             } else if constexpr (PF == PF_Q8) {
                 byte_pairs(xl, d01, b0[0], b0[1]);
                 byte_pairs(xh, d01, b0[2], b0[3]);
