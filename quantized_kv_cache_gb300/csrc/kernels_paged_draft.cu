@@ -458,7 +458,7 @@ template <int D, typename TQ> __global__ void __launch_bounds__(kMT) draft_merge
     constexpr int RP = DGeo<D>::RP, PF = part_floats<D>(), C = D / 32;                  // channels of a lane
     grid_dep_wait();
     const int64_t* line = (const int64_t*)p.ws;
-    const int id = blockIdx.x, H = p.v.H, G = p.G, lane = threadIdx.x & 31, r = blockIdx.y * 8 + (threadIdx.x >> 5);
+    const int id = blockIdx.x, G = p.G, lane = threadIdx.x & 31, r = blockIdx.y * 8 + (threadIdx.x >> 5);
     const int64_t total = line[p.n_seq], U = run_tiles(total, p.n_cta), at = (int64_t)id * U;
     if (id == 0 || at >= total) return;
     int b = 0, hi = p.n_seq - 1;                         // the last sequence that starts at or before the run

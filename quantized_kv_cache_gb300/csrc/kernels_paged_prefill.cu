@@ -243,6 +243,47 @@ __device__ __forceinline__ void weights32(const uint32_t (&x)[32], uint64_t f, u
     for (int e = 16 - A; e < 16; ++e) last(e);
 }
 
+// The exponentials of 16 pairs, packed, added to the sums; their largest arguments.
+template <typename T>
+__device__ __forceinline__ void exps32(const float2 (&x)[16], uint32_t* w, uint64_t (&sum)[4], float (&top)[4]) {
+    float v[32] = {};
+    const auto last = [&](int e) {                            // as in weights32
+        if constexpr (std::is_same<T, __half>::value)
+            asm volatile("cvt.rn.f16x2.f32 %0, %1, %2;\n" : "=r"(w[e]) : "f"(v[2 * e + 1]), "f"(v[2 * e]));
+        else
+            asm volatile("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(w[e]) : "f"(v[2 * e + 1]), "f"(v[2 * e]));
+        asm volatile("add.rn.f32x2 %0, %0, %1;\n" : "+l"(sum[e & 3]) : "l"(pair(v[2 * e], v[2 * e + 1])));
+    };
+    constexpr int A = 2;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+        asm volatile("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(v[2 * e]) : "f"(x[e].x));
+        asm volatile("max.f32 %0, %0, %1, %2;\n" : "+f"(top[e & 3]) : "f"(x[e].x), "f"(x[e].y));
+        asm volatile("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(v[2 * e + 1]) : "f"(x[e].y));
+        if (e >= A) last(e - A);
+    }
+#pragma unroll
+    for (int e = 16 - A; e < 16; ++e) last(e);
+}
+
+// weights32 with a cap alone, straight through: y = cap tanh(s f) = s (a0 + a1 s^2 + a2 s^4 + a3 s^6) for |s f| < 0.35 (a: of the
+// polynomial below, with f and the cap in it). What is beyond that shows in `big`, the largest |s|. No branch parts the products from
+// the exponentials, so that they share the time: with the vote of rule_weights32 between them 5 chunks up to 1,501 tokens at 6,000 positions, 40 heads on 8 x 128 (bf16 pages, a cap of 30), took 684 us where this takes 502.
+template <typename T>
+__device__ __forceinline__ void cap_weights32(const uint32_t (&s)[32], const float (&a)[4], float m, uint32_t* w, uint64_t (&sum)[4],
+                                              float (&top)[4], float& big) {
+    const auto both = [](float c) { return make_float2(c, c); };
+    float2 x[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+        const float2 r = make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), q = __fmul2_rn(r, r);
+        const float2 y = __fmul2_rn(r, __ffma2_rn(q, __ffma2_rn(q, __ffma2_rn(q, both(a[3]), both(a[2])), both(a[1])), both(a[0])));
+        big = max3(big, fabsf(r.x), fabsf(r.y));
+        x[e] = __fadd2_rn(y, both(m));                        // by itself, as below
+    }
+    exps32<T>(x, w, sum, top);
+}
+
 // weights32 with the cap and the bias on the way: scores of 32 positions from p0 on, in units of log2, less the row's maximum (m its
 // negative) as it stands; `hide` takes out what the row does not see. Where all capped scores are below 0.35 of the cap no
 // exponential is taken for them: tanh x = x (1 + q c(q)), q = x^2, with the polynomial of least relative error on that range
@@ -290,24 +331,7 @@ __device__ __forceinline__ void rule_weights32(uint32_t (&s)[32], const ScoreRul
 #pragma unroll
     for (int e = 0; e < 16; ++e) x[e] = __fadd2_rn(x[e], back);
     hide(x);
-    float v[32] = {};
-    const auto last = [&](int e) {                            // as in weights32
-        if constexpr (std::is_same<T, __half>::value)
-            asm volatile("cvt.rn.f16x2.f32 %0, %1, %2;\n" : "=r"(w[e]) : "f"(v[2 * e + 1]), "f"(v[2 * e]));
-        else
-            asm volatile("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(w[e]) : "f"(v[2 * e + 1]), "f"(v[2 * e]));
-        asm volatile("add.rn.f32x2 %0, %0, %1;\n" : "+l"(sum[e & 3]) : "l"(pair(v[2 * e], v[2 * e + 1])));
-    };
-    constexpr int A = 2;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-        asm volatile("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(v[2 * e]) : "f"(x[e].x));
-        asm volatile("max.f32 %0, %0, %1, %2;\n" : "+f"(top[e & 3]) : "f"(x[e].x), "f"(x[e].y));
-        asm volatile("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(v[2 * e + 1]) : "f"(x[e].y));
-        if (e >= A) last(e - A);
-    }
-#pragma unroll
-    for (int e = 16 - A; e < 16; ++e) last(e);
+    exps32<T>(x, w, sum, top);
 }
 
 // Whole prompts: the row tiles of all sequences are one line, so that ragged ones leave no block without work. The sequence of
@@ -678,7 +702,9 @@ __global__ void __launch_bounds__(Geo<D, codes_of(KF)>::threads, 1) prefill_kern
                     }
                 const int ex = (int)((__float_as_uint(a) >> 23) & 255) - 127;
                 if (a > 0.f && ex < 128) {
-                    const int sh = min(14 - ex, 100);                // from -113 on
+                    // the largest magnitude to [2^14, 2^15): from -113 on; where scores are capped to [2^4, 2^5), for which the powers of
+                    // their factor stay numbers (cap_weights32; what that costs is 2^-29 of the largest)
+                    const int sh = min((RULE ? 4 : 14) - ex, 100);
                     up = __uint_as_float((uint32_t)(127 + sh) << 23);
                     rs.f = rule.factor(__uint_as_float((uint32_t)(127 - sh) << 23));
                 }
@@ -702,6 +728,11 @@ __global__ void __launch_bounds__(Geo<D, codes_of(KF)>::threads, 1) prefill_kern
             mbar_arrive(q_full);
 
             const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16), o_addr = lanes + GE::o_col(t);
+            // the polynomial of cap_weights32, where f^7 and the cap leave its coefficients among the normal numbers
+            const float f2 = rs.f * rs.f, cap[4] = {rs.f * rule.cap_l2, -0.33332664f * f2 * rs.f * rule.cap_l2,
+                                                    0.13299826f * f2 * f2 * rs.f * rule.cap_l2, -0.049148493f * f2 * f2 * f2 * rs.f * rule.cap_l2};
+            const bool cap_alone = RULE && __all_sync(kAll, rule.cap >= 1.f && rule.cap <= 1e6f && !rule.biased && rs.f >= 7.6e-6f && rs.f <= 16.f);
+            int wide = 0;                                         // tiles for which scores beyond the polynomial are expected
             // positions of the row tile's first and last rows: what decides whether a KV tile is seen whole
             const int first = c.pos0 + (r0 + 128 * t) / G, last = c.pos0 + (min(r1, r0 + 128 * t + 128) - 1) / G;
             for (int i = 0; i < nt; ++i) {
@@ -744,32 +775,47 @@ __global__ void __launch_bounds__(Geo<D, codes_of(KF)>::threads, 1) prefill_kern
                 };
                 // The weights are formed with the maximum as it stands while the tile's own is found; only where that
                 // is more than kLazy above (and for the first tile) the maximum moves and the weights are formed again.
-                for (bool last_try = false;; last_try = true) {
+                bool lean = RULE && cap_alone && whole && wide == 0;
+                if (wide > 0) --wide;
+                for (bool last_try = false;;) {
                     const float2 f2 = make_float2(rs.f, rs.f), mb = m == -INFINITY ? make_float2(0.f, 0.f) : make_float2(-m, -m);
                     uint64_t s2[4] = {};
-                    float y[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    float y[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, big = 0.f;
                     tmem_ld32(s_addr, sr[0]);
+                    const auto each32 = [&](const auto& use) {            // use(scores, number) of every 32, the next on their way
 #pragma unroll
-                    for (int k = 0; k < BN / 32; ++k) {
-                        uint32_t(&x)[32] = sr[k & 1];
-                        tmem_wait_ld(x);
-                        if (k + 1 < BN / 32) tmem_ld32(s_addr + 32 * (k + 1), sr[(k + 1) & 1]);
-                        if constexpr (RULE)
+                        for (int k = 0; k < BN / 32; ++k) {
+                            uint32_t(&x)[32] = sr[k & 1];
+                            tmem_wait_ld(x);
+                            if (k + 1 < BN / 32) tmem_ld32(s_addr + 32 * (k + 1), sr[(k + 1) & 1]);
+                            use(x, k);
+                        }
+                    };
+                    if constexpr (!RULE)
+                        each32([&](uint32_t (&x)[32], int k) { weights32<T>(x, pair(f2.x, f2.y), pair(mb.x, mb.y), &pr[k / 2][16 * (k & 1)], s2, y); });
+                    else if (lean)
+                        each32([&](uint32_t (&x)[32], int k) { cap_weights32<T>(x, cap, mb.x, &pr[k / 2][16 * (k & 1)], s2, y, big); });
+                    else
+                        each32([&](uint32_t (&x)[32], int k) {
                             rule_weights32<T>(x, rule, rs, p0 + 32 * k, mb.x, [&](float2 (&z)[16]) {
                                 if (!whole) hide(k, [&](int e) { (e & 1 ? z[e / 2].y : z[e / 2].x) = -INFINITY; });
                             }, &pr[k / 2][16 * (k & 1)], s2, y);
-                        else
-                            weights32<T>(x, pair(f2.x, f2.y), pair(mb.x, mb.y), &pr[k / 2][16 * (k & 1)], s2, y);
-                    }
+                        });
                     {
                         const float2 a = unpair(s2[0]), b = unpair(s2[1]), c2 = unpair(s2[2]), d = unpair(s2[3]);
                         sum = ((a.x + a.y) + (b.x + b.y)) + ((c2.x + c2.y) + (d.x + d.y));
+                    }
+                    if (RULE && lean && __any_sync(kAll, !(big * rs.f < 0.35f))) {
+                        lean = false;                             // some score is beyond the polynomial: this tile again, and the next
+                        wide = 8;                                 // ones the other way
+                        continue;
                     }
                     if (last_try) break;
                     mx = max3(fmaxf(y[0], y[1]), y[2], y[3]);
                     mx = (RULE ? mx - mb.x : mx * rs.f) - kUp;
                     const bool grow = mx > m + kLazy || (m == -INFINITY && mx > -INFINITY);
                     if (!__any_sync(kAll, grow)) break;
+                    last_try = true;
                     const float a = grow ? ex2(m - mx) : 1.f;
                     if (grow) m = mx;
                     l *= a;
