@@ -18,7 +18,8 @@ def __getattr__(name):
     # .paged imports torch, which importing this package does not
     if name in ("PagedKVCache", "paged_config", "prompt_attn", "prompt_status", "prompt_workspace", "qk_norm_rope"):
         from . import paged
-        return getattr(paged, name)
+        globals()[name] = found = getattr(paged, name)       # asked for once
+        return found
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 

@@ -1,10 +1,11 @@
 // Chunks of a few tokens over e4m3 pages (drafted tokens looked at by the target): attention with few rows for each KV head, split over
 // positions and joined.
 //
-// A head has tokens x G query rows here, up to 32 of which (16 at D = 256) are a group. As in decode, the 16-position tiles of all
+// A head has tokens x G query rows here, up to 16 or 32 of which are a group. As in decode, the 16-position tiles of all
 // (sequence, KV head, group) are one line that is cut into equal runs, one per CTA, on the device; a CTA's four warps take the tiles
-// of a run in turn through rings of their own, positions or channels on M of mma.sync, the group's rows on N in blocks of eight.
-// The rows' fragments wait in shared memory (one copy for the four warps) and a decoded piece of K serves them all; the outputs stay in registers.
+// of a run in turn, positions or channels on M of mma.sync, the group's rows on N in blocks of eight, two blocks a warp: by
+// themselves (groups of 16), or two warps on one tile (groups of 32: with four blocks a warp, 253 registers and two warps a
+// scheduler, a tile was one long wait). The rows' fragments wait in shared memory, one copy for the four warps; the outputs stay in registers.
 // A run writes a group that it holds whole and leaves (m, l, o) of the at most two that its ends cut, which the merge kernel
 // joins. Rows see different positions: where a tile is not seen whole by all of them the scores are hidden row by row, and rows
 // of V that hold a NaN are added to the rows that see them and taken out before the product.
@@ -55,16 +56,21 @@ __device__ __forceinline__ int64_t run_tiles(int64_t total, int n_cta) {
     return u < kMinTiles ? kMinTiles : u;
 }
 
-template <int D> struct DGeo {
-    static constexpr int NQ = D == 256 ? 2 : 4, RP = 8 * NQ;     // blocks of eight rows, rows of a group
+template <int D, int NQ, int SPLIT> struct DGeo {                 // blocks of eight rows of a warp; warps on one tile
+    static constexpr int RP = 8 * NQ * SPLIT, W = kDW / SPLIT;    // rows of a group; tiles in hand at a time
+    static constexpr int ctas = draft_ctas(D, NQ);                // per SM
     static constexpr int tile = tile_bytes<D, PF_E4>(), slot = 2 * tile, q_bytes = RP * D * 2;
-    static constexpr int fit = (110 * 1024 - q_bytes) / kDW / slot, NS = fit > 8 ? 8 : fit;
-    static constexpr int join = kDW * RP * D * 4;                 // the warps' outputs at a group's end
-    static constexpr int rings = NS * slot * kDW > join ? NS * slot * kDW : join;
-    static constexpr int smem = q_bytes + rings;
+    static constexpr int fit = ((226 / ctas - 3) * 1024 - q_bytes) / W / slot, NS = fit > 8 ? 8 : fit;
+    static constexpr int join = W * RP * D * 4;                   // the outputs at a group's end
+    static constexpr int rings = NS * slot * W > join ? NS * slot * W : join;
+    static constexpr int smem = q_bytes + rings, part = 2 * RP + RP * D;
     static_assert(NS >= 3, "tiles in flight beside the one in use");
 };
-template <int D> constexpr int part_floats() { return 2 * DGeo<D>::RP + DGeo<D>::RP * D; }
+// The warps on one tile wait for one another.
+template <int SPLIT> __device__ __forceinline__ void sync_tile(int stream) {
+    if constexpr (SPLIT == 1) __syncwarp();
+    else asm volatile("barrier.cta.sync %0, %1;\n" ::"r"(1 + stream), "n"(32 * SPLIT) : "memory");
+}
 
 // s[q] += K Q^T: a piece of K decoded, then all blocks of rows from their fragments at `q`.
 template <int D, int NQ, typename PLACE>
@@ -94,17 +100,18 @@ __device__ __forceinline__ void draft_scores(uint32_t base, const PLACE& at, uin
     }
 }
 
-template <int D, typename TQ>
-__global__ void __launch_bounds__(kDT, 2) draft_kernel(PagedAttnParams p) {
-    using GE = DGeo<D>;
-    constexpr int NQ = GE::NQ, RP = GE::RP;
-    extern __shared__ __align__(128) float smem[];                // fragments of the rows; the rings, or [kDW][RP][D] outputs
-    __shared__ float s_m[kDW][RP], s_l[kDW][RP], s_f[RP];
+template <int D, int NQ, int SPLIT, typename TQ>
+__global__ void __launch_bounds__(kDT, draft_ctas(D, NQ)) draft_kernel(PagedAttnParams p) {
+    using GE = DGeo<D, NQ, SPLIT>;
+    constexpr int RP = GE::RP, W = GE::W;
+    extern __shared__ __align__(128) float smem[];                // fragments of the rows; the rings, or [W][RP][D] outputs
+    __shared__ float s_m[W][RP], s_l[W][RP], s_f[RP];
     __shared__ int64_t red[kDW];
     __shared__ int s_b, s_h, s_i;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int H = p.v.H, G = p.G;
-    const uint32_t q_at = (uint32_t)__cvta_generic_to_shared(smem), ring = q_at + GE::q_bytes + warp * GE::NS * GE::slot;
+    const int stream = warp / SPLIT, half = warp % SPLIT, block0 = half * NQ;     // the warp's tiles; its rows' first block
+    const uint32_t q_at = (uint32_t)__cvta_generic_to_shared(smem), ring = q_at + GE::q_bytes + stream * GE::NS * GE::slot;
     float* s_out = smem + GE::q_bytes / 4;
     grid_dep_wait();
 
@@ -181,14 +188,14 @@ __global__ void __launch_bounds__(kDT, 2) draft_kernel(PagedAttnParams p) {
         const int h = hg / st.groups, base_row = hg % st.groups * RP, rows = min(RP, st.n * G - base_row);
         const int i1 = (int)min((int64_t)st.tiles, i0 + left);
         left -= i1 - i0;
-        const int nt = (i1 - i0 - warp + kDW - 1) / kDW;          // this warp's tiles
-        // the copies run ahead, K and V of a tile in one slot
+        const int nt = (i1 - i0 - stream + W - 1) / W;            // this warp's tiles
+        // the copies run ahead, K and V of a tile in one slot (of two warps one brings K, the other V)
         int pages = 0, unit_page = 0, unit_off = 0, put = 0, item = 0;
         auto copy_next = [&]() {
             if (item < nt) {
                 const uint32_t dst = ring + put * GE::slot;
                 if ((item & 31) == 0) {                           // the next 32 tiles' page numbers, one per lane
-                    const int k = min(item + lane, nt - 1) * kDW + i0 + warp;
+                    const int k = min(item + lane, nt - 1) * W + i0 + stream;
                     pages = p.table[b * p.table_stride + ((st.tile(k) * kTile) >> p.v.ps_shift)];
                     if (pages < 0 || pages >= p.v.n_pages) {
                         raise_status(p.v.status, KVQ_PAGED_BAD_INDEX);
@@ -198,12 +205,12 @@ __global__ void __launch_bounds__(kDT, 2) draft_kernel(PagedAttnParams p) {
                     }
                 }
                 unit_page = __shfl_sync(kAll, pages, item & 31);
-                unit_off = (st.tile(item * kDW + i0 + warp) * kTile) & (p.v.ps - 1);
+                unit_off = (st.tile(item * W + i0 + stream) * kTile) & (p.v.ps - 1);
                 const auto unit = [&](int w) -> const uint8_t* {
                     return unit_page < 0 ? nullptr : p.v.base[w] + (uint64_t)(uint32_t)unit_page * (uint32_t)p.v.unit[w];
                 };
-                copy_tile<D, PF_E4, false>(dst, k_at, unit(0), p.v.ps, unit_off, lane);
-                copy_tile<D, PF_E4, true>(dst + GE::tile, v_at, unit(1), p.v.ps, unit_off, lane);
+                if (half == 0) copy_tile<D, PF_E4, false>(dst, k_at, unit(0), p.v.ps, unit_off, lane);
+                if (half == SPLIT - 1) copy_tile<D, PF_E4, true>(dst + GE::tile, v_at, unit(1), p.v.ps, unit_off, lane);
             }
             cp_commit();
             ++item;
@@ -213,7 +220,7 @@ __global__ void __launch_bounds__(kDT, 2) draft_kernel(PagedAttnParams p) {
         for (int i = 0; i < GE::NS - 1; ++i) copy_next();
 
         // the rows' fragments, a block of eight rows a warp
-        for (int k = warp; k < NQ; k += kDW) {
+        for (int k = warp; k < RP / 8; k += kDW) {
             uint32_t qf[D / 16][1][2];
             float back[1];
             load_queries<D, PF_E4, 1, __half, TQ>(
@@ -237,23 +244,24 @@ __global__ void __launch_bounds__(kDT, 2) draft_kernel(PagedAttnParams p) {
         for (int k = 0; k < NQ; ++k)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                f[k][e] = s_f[8 * k + 2 * t + e];
+                f[k][e] = s_f[8 * (block0 + k) + 2 * t + e];
                 m[k][e] = -INFINITY;
             }
         // position of a row of the group (rows behind the last one: the last token's)
+        const auto row_at = [&](int k, int e) { return 8 * (block0 + k) + 2 * t + e; };
         const auto pos_of = [&](int r) { return st.first + min(base_row + r, st.n * G - 1) / G; };
         const int lo_last = p.window > 0 && st.last >= p.window ? st.last - p.window + 1 : 0;
         ValueScale values;
         int get = 0;
         for (int i = 0; i < nt; ++i) {
-            const int p0 = st.tile(i * kDW + i0 + warp) * kTile;
+            const int p0 = st.tile(i * W + i0 + stream) * kTile;
             cp_wait<GE::NS - 2>();
-            __syncwarp();
+            sync_tile<SPLIT>(stream);                             // the tile has landed, and the one before it is done with
             const uint32_t k_tile = ring + get * GE::slot, v_tile = k_tile + GE::tile;
             get = get + 1 == GE::NS ? 0 : get + 1;
             copy_next();
             float s[NQ][4] = {};                                  // (position g, g + 8) x (row 2t, 2t + 1)
-            draft_scores<D, NQ>(k_tile, place, q_at + lane * 16, s);
+            draft_scores<D, NQ>(k_tile, place, q_at + (block0 * D + lane) * 16, s);
             const bool all = st.first >= 0 && (p0 + kTile <= st.pre || (p0 + kTile - 1 <= st.first && p0 >= lo_last));
             const float d = tile_scale<D>(k_tile);
 #pragma unroll
@@ -269,7 +277,7 @@ __global__ void __launch_bounds__(kDT, 2) draft_kernel(PagedAttnParams p) {
                 for (int k = 0; k < NQ; ++k)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const int r = 8 * k + 2 * t + e, x = pos_of(r);
+                        const int r = row_at(k, e), x = pos_of(r);
                         const float slope = p.slopes && r < rows ? p.slopes[h * G + (base_row + r) % G] * kL2e : 0.f;
                         s[k][e] = rule(s[k][e], abs(x - p0 - g), slope);
                         s[k][2 + e] = rule(s[k][2 + e], abs(x - p0 - g - 8), slope);
@@ -280,7 +288,7 @@ __global__ void __launch_bounds__(kDT, 2) draft_kernel(PagedAttnParams p) {
                 for (int k = 0; k < NQ; ++k)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const int x = pos_of(8 * k + 2 * t + e);
+                        const int x = pos_of(row_at(k, e));
                         if (!sees(x, p0 + g)) s[k][e] = -INFINITY;
                         if (!sees(x, p0 + g + 8)) s[k][2 + e] = -INFINITY;
                     }
@@ -364,7 +372,7 @@ __global__ void __launch_bounds__(kDT, 2) draft_kernel(PagedAttnParams p) {
                             for (int k = 0; k < NQ; ++k)
 #pragma unroll
                                 for (int e = 0; e < 2; ++e)
-                                    if (sees(pos_of(8 * k + 2 * t + e), p0 + j)) {
+                                    if (sees(pos_of(row_at(k, e)), p0 + j)) {
                                         float (&acc)[4] = o[(V::CH * jj + c) / 2][k];
                                         acc[e] = fmaf(w[k][e], y.x, acc[e]);
                                         acc[2 + e] = fmaf(w[k][e], y.y, acc[2 + e]);
@@ -372,9 +380,11 @@ __global__ void __launch_bounds__(kDT, 2) draft_kernel(PagedAttnParams p) {
                         }
                     }
                 }
-                __syncwarp();
-                clear_rows<D, PF_E4>(v_tile, ~bad, lane);
-                __syncwarp();
+                if (bad) {
+                    sync_tile<SPLIT>(stream);
+                    clear_rows<D, PF_E4>(v_tile, ~bad, lane);
+                    sync_tile<SPLIT>(stream);
+                }
             }
             tile_values<D, PF_E4, NQ, __half, false>(v_tile, place, pb, lo, o);
         }
@@ -390,8 +400,8 @@ __global__ void __launch_bounds__(kDT, 2) draft_kernel(PagedAttnParams p) {
                 l[k][e] += __shfl_xor_sync(kAll, l[k][e], 8);
                 l[k][e] += __shfl_xor_sync(kAll, l[k][e], 16);
                 if (g == 0) {
-                    s_m[warp][8 * k + 2 * t + e] = m[k][e];
-                    s_l[warp][8 * k + 2 * t + e] = l[k][e];
+                    s_m[stream][row_at(k, e)] = m[k][e];
+                    s_l[stream][row_at(k, e)] = l[k][e];
                 }
             }
         __syncthreads();
@@ -399,11 +409,11 @@ __global__ void __launch_bounds__(kDT, 2) draft_kernel(PagedAttnParams p) {
         for (int k = 0; k < NQ; ++k)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int r = 8 * k + 2 * t + e;
+                const int r = row_at(k, e);
                 float mm = -INFINITY;
-                for (int w = 0; w < kDW; ++w) mm = fmaxf(mm, s_m[w][r]);
+                for (int w = 0; w < W; ++w) mm = fmaxf(mm, s_m[w][r]);
                 const float a = (mm == -INFINITY ? 0.f : ex2(m[k][e] - mm)) * values.unit;
-                float* dst = s_out + (warp * RP + r) * D;
+                float* dst = s_out + (stream * RP + r) * D;
                 using V = VGeo<D, PF_E4>;
 #pragma unroll
                 for (int j = 0; j < V::NJ; ++j)
@@ -413,19 +423,19 @@ __global__ void __launch_bounds__(kDT, 2) draft_kernel(PagedAttnParams p) {
         __syncthreads();
         const bool whole = i0 == 0 && i1 == st.tiles;
         // a run leaves at most two partials: of a group that it goes on with, and of one that it begins
-        float* part = p.ws + line_floats(p.n_seq) + ((int64_t)blockIdx.x * 2 + (i0 == 0)) * part_floats<D>();
+        float* part = p.ws + line_floats(p.n_seq) + ((int64_t)blockIdx.x * 2 + (i0 == 0)) * GE::part;
         for (int e = threadIdx.x; e < rows * D / 2; e += kDT) {
             const int r = 2 * e / D;
             float x = 0.f, y = 0.f;
-            for (int w = 0; w < kDW; ++w) {
+            for (int w = 0; w < W; ++w) {
                 const float2 z = *reinterpret_cast<const float2*>(s_out + w * RP * D + 2 * e);
                 x += z.x;
                 y += z.y;
             }
             if (whole) {
                 float mm = -INFINITY, ll = 0.f;
-                for (int w = 0; w < kDW; ++w) mm = fmaxf(mm, s_m[w][r]);
-                for (int w = 0; w < kDW; ++w) ll += s_l[w][r] * (mm == -INFINITY ? 0.f : ex2(s_m[w][r] - mm));
+                for (int w = 0; w < W; ++w) mm = fmaxf(mm, s_m[w][r]);
+                for (int w = 0; w < W; ++w) ll += s_l[w][r] * (mm == -INFINITY ? 0.f : ex2(s_m[w][r] - mm));
                 const float inv = inverse_sum(ll);
                 const int z = base_row + r, tok = z / G;
                 const int64_t at = (int64_t)(st.row0 + tok) * p.Hq + h * G + z - tok * G;
@@ -437,8 +447,8 @@ __global__ void __launch_bounds__(kDT, 2) draft_kernel(PagedAttnParams p) {
         if (threadIdx.x < rows) {
             const int r = threadIdx.x;
             float mm = -INFINITY, ll = 0.f;
-            for (int w = 0; w < kDW; ++w) mm = fmaxf(mm, s_m[w][r]);
-            for (int w = 0; w < kDW; ++w) ll += s_l[w][r] * (mm == -INFINITY ? 0.f : ex2(s_m[w][r] - mm));
+            for (int w = 0; w < W; ++w) mm = fmaxf(mm, s_m[w][r]);
+            for (int w = 0; w < W; ++w) ll += s_l[w][r] * (mm == -INFINITY ? 0.f : ex2(s_m[w][r] - mm));
             if (!whole) {
                 part[r] = mm;
                 part[RP + r] = ll;
@@ -454,8 +464,8 @@ __global__ void __launch_bounds__(kDT, 2) draft_kernel(PagedAttnParams p) {
 // Joins the partials of the groups that runs share: a block per run and eight rows of a group. At most one group is cut by the start of
 // a run, and its first cut joins it: a warp a row.
 constexpr int kMT = 256;
-template <int D, typename TQ> __global__ void __launch_bounds__(kMT) draft_merge_kernel(PagedAttnParams p) {
-    constexpr int RP = DGeo<D>::RP, PF = part_floats<D>(), C = D / 32;                  // channels of a lane
+template <int D, int RP, typename TQ> __global__ void __launch_bounds__(kMT) draft_merge_kernel(PagedAttnParams p) {
+    constexpr int PF = 2 * RP + RP * D, C = D / 32;      // floats of a partial, channels of a lane
     grid_dep_wait();
     const int64_t* line = (const int64_t*)p.ws;
     const int id = blockIdx.x, G = p.G, lane = threadIdx.x & 31, r = blockIdx.y * 8 + (threadIdx.x >> 5);
@@ -502,15 +512,23 @@ template <int D, typename TQ> __global__ void __launch_bounds__(kMT) draft_merge
     if (p.lse && lane == 0) p.lse[to] = log_sum(m, l);
 }
 
-template <int D, typename TQ> int draft_run(const PagedAttnParams& p, int sm_count, cudaStream_t s) {
+template <int D, int NQ, int SPLIT, typename TQ> int draft_run(const PagedAttnParams& p, int sm_count, cudaStream_t s) {
     PagedAttnParams a = p;
-    const auto k = draft_kernel<D, TQ>;
+    using GE = DGeo<D, NQ, SPLIT>;
+    static_assert(GE::part * GE::ctas <= draft_part_floats(D), "the workspace's");
+    const auto k = draft_kernel<D, NQ, SPLIT, TQ>;
     int res = 0;
-    if (const int e = resident_ctas((const void*)k, kDT, DGeo<D>::smem, &res)) return e;
-    a.n_cta = min(kMaxDraftCtas, sm_count * res);
-    cudaError_t e = launch_k(k, dim3(a.n_cta), dim3(kDT), DGeo<D>::smem, s, true, a);
-    if (e == cudaSuccess) e = launch_k(draft_merge_kernel<D, TQ>, dim3((unsigned)a.n_cta, DGeo<D>::RP / 8), dim3(kMT), 0, s, true, a);
+    if (const int e = resident_ctas((const void*)k, kDT, GE::smem, &res)) return e;
+    a.n_cta = min(kMaxSms * GE::ctas, sm_count * res);
+    cudaError_t e = launch_k(k, dim3(a.n_cta), dim3(kDT), GE::smem, s, true, a);
+    if (e == cudaSuccess) e = launch_k(draft_merge_kernel<D, GE::RP, TQ>, dim3((unsigned)a.n_cta, GE::RP / 8), dim3(kMT), 0, s, true, a);
     return (int)e;
+}
+template <int D, typename TQ> int draft_rows_run(const PagedAttnParams& p, int sm_count, cudaStream_t s) {
+    const int rows = p.max_q * p.G;
+    if (rows <= 16) return draft_run<D, 2, 1, TQ>(p, sm_count, s);
+    if constexpr (D == 256) return draft_run<D, 2, 2, TQ>(p, sm_count, s);
+    else return rows <= 32 ? draft_run<D, 4, 1, TQ>(p, sm_count, s) : draft_run<D, 4, 2, TQ>(p, sm_count, s);
 }
 
 }  // namespace
@@ -519,9 +537,8 @@ template <int D, typename TQ> int draft_run(const PagedAttnParams& p, int sm_cou
 #define KVQ_NAME2(d) launch_paged_draft_##d
 #define KVQ_NAME(d) KVQ_NAME2(d)
 int KVQ_NAME(KVQ_D)(const PagedAttnParams& p, int sms, void* stream) {
-    static_assert(DGeo<KVQ_D>::RP == draft_rows(KVQ_D), "the workspace's");
-    return p.dtype == KVQ_F16 ? draft_run<KVQ_D, __half>(p, sms, (cudaStream_t)stream)
-                              : draft_run<KVQ_D, __nv_bfloat16>(p, sms, (cudaStream_t)stream);
+    return p.dtype == KVQ_F16 ? draft_rows_run<KVQ_D, __half>(p, sms, (cudaStream_t)stream)
+                              : draft_rows_run<KVQ_D, __nv_bfloat16>(p, sms, (cudaStream_t)stream);
 }
 
 }  // namespace kvq

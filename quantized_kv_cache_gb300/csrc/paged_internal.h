@@ -159,13 +159,13 @@ KVQ_HD int64_t partial_floats(int G, int D) { return 32 + (int64_t)G * D; }
 // Before the partials: n_seq + 1 int64, the tiles before each sequence.
 KVQ_HD int64_t line_floats(int64_t n_seq) { return (2 * (n_seq + 1) + 3) & ~(int64_t)3; }
 
-// Chunks of a few tokens over e4m3 pages (kernels_paged_draft.cu): rows of a group, the most rows of a KV head that go there, and the
-// floats that the runs leave, two partials each.
-KVQ_HD constexpr int draft_rows(int D) { return D == 256 ? 16 : 32; }
-constexpr int kMaxDraftRows = 64, kMaxDraftCtas = kMaxSms * 2;
-KVQ_HD int64_t paged_draft_ws_floats(int D, int64_t n_seq) {
-    return line_floats(n_seq) + (int64_t)kMaxDraftCtas * 2 * (2 * draft_rows(D) + (int64_t)draft_rows(D) * D);
-}
+// Chunks of a few tokens over e4m3 pages (kernels_paged_draft.cu): the most rows of a KV head that go there, CTAs per SM (nq: blocks of
+// eight rows of a warp), the floats of the partial results (maxima, sums, outputs) that the CTAs of an SM leave, each once: 64 rows
+// of two CTAs, at D = 256 32 of two; and of all runs, two partials each.
+constexpr int kMaxDraftRows = 64;
+KVQ_HD constexpr int draft_ctas(int D, int nq) { return nq == 4 || D == 256 ? 2 : (D == 128 ? 3 : 4); }
+KVQ_HD constexpr int draft_part_floats(int D) { return D == 256 ? 2 * (64 + 32 * D) : 2 * (128 + 64 * D); }
+KVQ_HD int64_t paged_draft_ws_floats(int D, int64_t n_seq) { return line_floats(n_seq) + (int64_t)kMaxSms * 2 * draft_part_floats(D); }
 
 // A chunk's positions are split when its row tiles alone leave SMs without work: as many splits as leave one CTA per SM.
 constexpr int kMaxSplits = 16;
