@@ -466,11 +466,11 @@ template <typename T, int KF, int VF, int D> __global__ void __launch_bounds__(k
 // ---------------------------------------------------------------------------- append
 // e4m3 blocks: 16 positions of a head under one power of two. A warp takes a whole block (one head of K or V), all its new rows
 // in registers: their largest magnitude on the bits, the power, the codes. Rows that were there are rounded to the new power
-// where it grew; their codes are loaded beside the new rows, before that is known (a decode step is one such load after the other).
+// where it grew; in a decode step (one such load after the other) their codes are loaded beside the new rows, before that is known.
 // No two warps touch the same bytes, and no order of anything matters.
 //
-// The warps find their blocks from the rows: a row that begins a block, or its sequence's rows, leads one. With R = 16 a CTA looks at
-// 16 rows, of which one leads where sequences bring many; with R = 1 (a decode step) a CTA takes one row's block.
+// The warps find their blocks from the rows: a row that begins a block, or its sequence's rows, leads one. With R = 32 a CTA looks at
+// 32 rows, of which two lead where sequences bring many; with R = 1 (a decode step) a CTA takes one row's block.
 constexpr int kAppendWarps = 4;
 template <typename T, int D, int R> __global__ void __launch_bounds__(32 * kAppendWarps) paged_append_kernel(PagedAppendParams p) {
     const PagedView& v = p.v;
@@ -522,7 +522,7 @@ template <typename T, int D, int R> __global__ void __launch_bounds__(32 * kAppe
         float* scale = reinterpret_cast<float*>(base + v.ps * D) + row0 / kTile;
         const T* src = (const T*)p.src[w] + (r0 + from) * p.stride[w] + (int64_t)head * D + col;
         uint4 x[IT];
-        uint2 old[IT];
+        uint2 old[R == 1 ? IT : 1];
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
             const int k = i * RPI + sub;
@@ -532,10 +532,12 @@ template <typename T, int D, int R> __global__ void __launch_bounds__(32 * kAppe
         int held = kMinPower;
         if (o > 0) {
             held = min(max(exponent_of(*scale), kMinPower), kMaxPower);
+            if constexpr (R == 1) {
 #pragma unroll
-            for (int i = 0; i < IT; ++i) {
-                old[i] = make_uint2(0, 0);
-                if (i * RPI + sub < o) old[i] = *reinterpret_cast<const uint2*>(code + (i * RPI + sub) * D);
+                for (int i = 0; i < IT; ++i) {
+                    old[i] = make_uint2(0, 0);
+                    if (i * RPI + sub < o) old[i] = *reinterpret_cast<const uint2*>(code + (i * RPI + sub) * D);
+                }
             }
         }
         constexpr uint32_t inf = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
@@ -581,9 +583,10 @@ template <typename T, int D, int R> __global__ void __launch_bounds__(32 * kAppe
         }
         if (o > 0 && e > held) {
             const float by = power_of(max(held - e, kMinPower));
-#pragma unroll
+#pragma unroll(R == 1 ? IT : 1)
             for (int i = 0; i < IT; ++i) {
-                const uint32_t y[2] = {old[i].x, old[i].y};
+                if (R > 1 && i * RPI + sub < o) old[0] = *reinterpret_cast<const uint2*>(code + (i * RPI + sub) * D);
+                const uint32_t y[2] = {old[R == 1 ? i : 0].x, old[R == 1 ? i : 0].y};
                 uint32_t c[2];
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
@@ -738,10 +741,10 @@ template <typename T> int write_t(const WriteParams& p, cudaStream_t s) {
     return p.v.D == 64 ? write_d<T, 64>(p, s) : (p.v.D == 128 ? write_d<T, 128>(p, s) : write_d<T, 256>(p, s));
 }
 template <typename T, int D> int append_d(const PagedAppendParams& p, cudaStream_t s) {
-    // 16 rows a CTA where a sequence brings half a block or more, on the mean
-    const int rows = p.n_rows / 8 >= p.n_seq ? kTile : 1;
+    // 32 rows a CTA where a sequence brings half a block or more, on the mean
+    const int rows = p.n_rows / 8 >= p.n_seq ? 32 : 1;
     const dim3 grid((unsigned)((p.n_rows + (int64_t)rows - 1) / rows), (unsigned)((2 * p.v.H + kAppendWarps - 1) / kAppendWarps));
-    const auto k = rows == 1 ? paged_append_kernel<T, D, 1> : paged_append_kernel<T, D, kTile>;
+    const auto k = rows == 1 ? paged_append_kernel<T, D, 1> : paged_append_kernel<T, D, 32>;
     return (int)launch_k(k, grid, dim3(32 * kAppendWarps), 0, s, true, p);
 }
 template <typename T> int append_t(const PagedAppendParams& p, cudaStream_t s) {
