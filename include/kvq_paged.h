@@ -45,9 +45,9 @@ enum {
     KVQ_PAGED_BAD_INDEX = 4,    /* a slot or a page number was out of range: a write was skipped, a page read as zeros */
     KVQ_PAGED_BAD_LENGTH = 8,   /* a length, row offset or max_q was out of range: lengths are cut to what the page
                                    table holds, rows beyond the call's buffers or max_q are skipped */
-    KVQ_PAGED_NO_PAGES = 32,    /* kv_pages_extend: fewer free pages than the call needs; it changed nothing */
-    KVQ_PAGED_RANGE = 16        /* a quantised block reaches beyond fp16's 65,504: the page holds it and kv_paged_read
+    KVQ_PAGED_RANGE = 16,       /* a quantised block reaches beyond fp16's 65,504: the page holds it and kv_paged_read
                                    gives it, the attentions cut its scale (kv_paged_decode_attn) */
+    KVQ_PAGED_NO_PAGES = 32     /* kv_pages_extend: fewer free pages than the call needs; it changed nothing */
 };
 
 typedef struct {
@@ -135,7 +135,8 @@ kvq_status kv_paged_read(kvq_paged* h, int32_t layer, int32_t dtype, int32_t n_s
  * 16-bit pages take queries of their own type; rows of Q8_0 / Q4_0 pages enter as code x scale
  * rounded to fp16, with queries of either type. Scales above 515.5 (Q8_0) or 9352 (Q4_0) are taken as
  * these, as code x scale would be no fp16 number (their write has set KVQ_PAGED_RANGE). KVQ_PAGED_E4M3 rows likewise, with
- * scales up to 2^7 (here code x scale is not rounded; a chunk takes it as an fp16 number, which it is from 2^-15 on). lens[b] = 0 gives
+ * scales up to 2^7 (a chunk of more than 64 rows a KV head takes code x scale as an fp16 number, which it is from scales of 2^-15
+ * on; decode and smaller chunks do not round it). lens[b] = 0 gives
  * zeros. max_pages x page_size is at most 2^31 - 256. workspace: device, 16-byte aligned,
  * >= kv_paged_required_bytes for n_seq; written before it is read. */
 kvq_status kv_paged_decode_attn(kvq_paged* h, int32_t layer, int32_t dtype, int32_t n_seq, const void* q,
@@ -221,7 +222,7 @@ typedef struct {
 
 /* kv_prompt_attn — causal attention of whole prompts over their own rows: the token at position i of a sequence sees its positions
  * 0 .. i (options as for the paged calls). No cache is read or needed: before or beside the calls that store k and v, of either
- * cache. Rows of out and lse outside [cu[0], cu[n_seq]) stay as they are, and so do those of a sequence whose bounds are
+ * cache. out overlaps none of q, k and v. Rows of out and lse outside [cu[0], cu[n_seq]) stay as they are, and so do those of a sequence whose bounds are
  * no rows of the call. workspace: device, 16-byte aligned, >= kv_prompt_required_bytes for the call; its first 256 bytes
  * hold a status word (the bits above), which its owner zeroes once and kv_prompt_get_status reads; the rest is written before
  * it is read. Calls that may overlap need workspaces of their own. The current device's pointers. */

@@ -522,7 +522,7 @@ template <typename T, int D, int R> __global__ void __launch_bounds__(32 * kAppe
         float* scale = reinterpret_cast<float*>(base + v.ps * D) + row0 / kTile;
         const T* src = (const T*)p.src[w] + (r0 + from) * p.stride[w] + (int64_t)head * D + col;
         uint4 x[IT];
-        uint2 old[R == 1 ? IT : 1];
+        uint2 old[R == 1 ? IT : 1] = {};
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
             const int k = i * RPI + sub;
@@ -534,10 +534,8 @@ template <typename T, int D, int R> __global__ void __launch_bounds__(32 * kAppe
             held = min(max(exponent_of(*scale), kMinPower), kMaxPower);
             if constexpr (R == 1) {
 #pragma unroll
-                for (int i = 0; i < IT; ++i) {
-                    old[i] = make_uint2(0, 0);
+                for (int i = 0; i < IT; ++i)
                     if (i * RPI + sub < o) old[i] = *reinterpret_cast<const uint2*>(code + (i * RPI + sub) * D);
-                }
             }
         }
         constexpr uint32_t inf = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;

@@ -533,6 +533,11 @@ kvq_status kv_prompt_attn(const kvq_prompt_args* a, const kvq_attn_opts* opts, v
         return KVQ_EINVAL;
     const int64_t row = (int64_t)H * D, q_row = (int64_t)a->n_q_heads * D;
     if (!stride_ok(a->q_stride, q_row) || !stride_ok(a->k_stride, row) || !stride_ok(a->v_stride, row)) return KVQ_EINVAL;
+    const auto covers = [&](const void* x, int64_t stride, int64_t cols) {      // does a tensor share bytes with out?
+        const uintptr_t lo = (uintptr_t)x, hi = lo + 2 * (uintptr_t)((a->n_rows - 1) * stride + cols), out = (uintptr_t)a->out;
+        return lo < out + 2 * (uintptr_t)(a->n_rows * q_row) && out < hi;
+    };
+    if (covers(a->q, a->q_stride, q_row) || covers(a->k, a->k_stride, row) || covers(a->v, a->v_stride, row)) return KVQ_EINVAL;
     PagedAttnParams p{};
     if (!take_opts(opts, a->n_rows, &p)) return KVQ_EINVAL;
     p.G = a->n_q_heads / H;

@@ -332,7 +332,7 @@ def prompt_attn(q, k, v, cu, max_q, out, ws, lse=None, softcap=0.0, window=0, sl
     """Causal attention of whole packed prompts over their own rows, without a cache: sequence b's tokens are the rows cu[b] ..
     cu[b+1]-1 of q ([rows, Hq, D] fp16 or bf16) and k, v ([rows, H, D], all with free token strides). cu: int32
     [sequences + 1]; max_q: at least the longest prompt (of a longer one only the first max_q tokens are computed); out:
-    [rows, Hq, D], contiguous; ws: from prompt_workspace. Options as for PagedKVCache.prefill_attn."""
+    [rows, Hq, D], contiguous, none of the others' memory; ws: from prompt_workspace. Options as for PagedKVCache.prefill_attn."""
     dt, dev, dtype = _type_of(q, "q", _DT), q.get_device(), q.dtype
     if q.dim() != 3 or k.dim() != 3 or dev < 0:
         _bad("q, k: [rows, heads, D] CUDA tensors are wanted")

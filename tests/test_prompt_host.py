@@ -20,8 +20,8 @@ def lib():
 
 def prompt(**kw):
     a = _lib.kvq_prompt_args()
-    base = dict(dtype=_lib.F16, n_seq=2, n_rows=100, max_q=60, n_q_heads=8, n_kv_heads=2, head_dim=128, softmax_scale=0.0, q=4096,
-                k=8192, v=16384, cu=4096, out=32768, q_stride=1024, k_stride=256, v_stride=256)
+    base = dict(dtype=_lib.F16, n_seq=2, n_rows=100, max_q=60, n_q_heads=8, n_kv_heads=2, head_dim=128, softmax_scale=0.0, q=1 << 50,
+                k=1 << 51, v=1 << 52, cu=4096, out=4096, q_stride=1024, k_stride=256, v_stride=256)
     base.update(kw)
     for k, v in base.items():
         setattr(a, k, v)
@@ -32,6 +32,7 @@ def prompt(**kw):
                                 dict(n_kv_heads=0), dict(n_kv_heads=3), dict(n_q_heads=34, q_stride=8192), dict(head_dim=96), dict(head_dim=512),
                                 dict(softmax_scale=-1.0), dict(softmax_scale=float("nan")), dict(q=None), dict(k=None), dict(v=None),
                                 dict(cu=None), dict(out=None), dict(q=4104), dict(k=8200), dict(v=16388), dict(out=32770), dict(cu=4098),
+                                dict(q=4096), dict(k=4096 + 2 * 100 * 1024 - 16), dict(v=4096 - 16), dict(out=(1 << 50) + 2 * (99 * 1024 + 1024) - 16),
                                 dict(q_stride=1000), dict(k_stride=248), dict(v_stride=257)])
 def test_prompt_refusals(kw):
     """Refused on the host: the pointers here are never followed."""
