@@ -12,6 +12,11 @@
 // quantised ones (131,072 positions, 8 x 128, q8_0 / q4_0: 59 us, 54%; issue slots 65% busy, two thirds of the 566
 // instructions of a tile in the two products' decoding). Groups of 16, two query tiles a warp: 16 sequences up to 32,768 on
 // 2 x 128, fp16 94 us (65%), q8_0 / q4_0 68 us (37%).
+//
+// e4m3 pages (24 ragged sequences up to 50,001, 8 x 128: 236 us, 81%): a code becomes fp16 by one conversion for two, and the scales,
+// one for a tile, go to the scores and to the weights, 320 instructions a tile. What is left is latency (four warps a scheduler,
+// issue slots 39-42% busy) and SMs that end before others (a tenth of the time: with six times as many runs 235 us against 252 there,
+// but one sequence of 131,072 106 us against 78). Three CTAs an SM 260 us, five 270.
 #include "device_common.cuh"
 #include "paged_frag.cuh"
 

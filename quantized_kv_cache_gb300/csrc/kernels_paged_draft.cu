@@ -1,17 +1,21 @@
 // Chunks of a few tokens over e4m3 pages (drafted tokens looked at by the target): attention with few rows for each KV head, split over
 // positions and joined.
 //
-// A head has tokens x G query rows here, up to 16 or 32 of which are a group. As in decode, the 16-position tiles of all
+// A head has tokens x G query rows here, up to 16, 32 or 64 of which are a group. As in decode, the 16-position tiles of all
 // (sequence, KV head, group) are one line that is cut into equal runs, one per CTA, on the device; a CTA's four warps take the tiles
-// of a run in turn, positions or channels on M of mma.sync, the group's rows on N in blocks of eight, two blocks a warp: by
-// themselves (groups of 16), or two warps on one tile (groups of 32: with four blocks a warp, 253 registers and two warps a
-// scheduler, a tile was one long wait). The rows' fragments wait in shared memory, one copy for the four warps; the outputs stay in registers.
+// of a run in turn, positions or channels on M of mma.sync, the group's rows on N in blocks of eight, two or four blocks a warp, and
+// where those are not enough two warps on one tile. The rows' fragments wait in shared memory, one copy for the four warps; the outputs
+// stay in registers.
 // A run writes a group that it holds whole and leaves (m, l, o) of the at most two that its ends cut, which the merge kernel
 // joins. Rows see different positions: where a tile is not seen whole by all of them the scores are hidden row by row, and rows
 // of V that hold a NaN are added to the rows that see them and taken out before the product.
 //
 // On the tensor cores of the chunk kernel a tile of 128 rows would be a fifth full, and its softmax a chain of one
-// tile after the other: 20 sequences of five tokens up to 16,001 positions, 40 heads on 8 x 128: 606 us there.
+// tile after the other: 20 sequences of five tokens up to 16,001 positions, 40 heads on 8 x 128 (25 rows a KV head): 606 us there,
+// 139 us here (HBM's floor 64). Bound by latency: a tile of 16 positions takes a warp 590 instructions, the matrix pipe 540 of
+// a scheduler's 1,550 cycles, and two warps a scheduler do not fill the waits between them. Other forms of the same batch: up to 16
+// rows 113 us (two blocks of rows, three CTAs an SM; with four blocks 147); 25 rows as two warps on a tile 151; 60 rows 242; 4 x 256, 30
+// rows 152 (as two groups 172). The scores of the next tile formed beside the values of this one: 149, the registers spill.
 #include "device_common.cuh"
 #include "paged_frag.cuh"
 

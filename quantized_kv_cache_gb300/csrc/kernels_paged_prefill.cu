@@ -8,7 +8,8 @@
 //    the 128-byte-swizzled layout both products read: K with the summed axis contiguous, V with its other
 //    axis contiguous. 16-bit pages come by tensor-map copies, one lane per page and 64 channels (16-byte
 //    copies by the threads took 1,550 of the 2,400 cycles of a tile); a tile that ends behind the last position
-//    is copied by the threads, zeros in place of the rows behind it. Quantised rows are decoded on the way;
+//    is copied by the threads, zeros in place of the rows behind it. Quantised rows are decoded on the way. Prompts' own rows come
+//    by tensor-map copies alone;
 //  - one warp issues the products: S = Q K^T into tensor memory, and O += P V with P read from tensor memory;
 //  - one thread per row does the softmax: S from tensor memory to registers, maximum, exponentials, P back
 //    over S. The running maximum moves only when it grows by more than 2^4 (bf16 pages: 2^8), so that O is
@@ -16,11 +17,14 @@
 // With two row tiles, the products of one run while the other's softmax does; with one, S of the next
 // tile is computed meanwhile (two S buffers).
 //
-// 4,096 tokens at 8,192 positions, 40 heads on 8 x 128, bf16: 414 us, 1,240 TFLOP/s (64% of the measured matrix rate).
-// A row tile's turn is a chain: softmax 1,000 cycles, products 1,130 (1,024 at the peak), barriers and wake-ups 850;
-// the other tile's turn fills most of the rest. Over codes at D = 256 (6 prompts, cap, window, prefix: 332 us) the
-// decoding warps bind: every 128 rows decode their positions anew. 16-bit pages at D = 256 (4,096 tokens at 8,192, 24 heads
-// on 4): 627 us, 51%, the scores of 64 positions taking as long as those of 128 would; D = 64 (40 heads on 8): 336 us, 40%.
+// 4,096 tokens at 8,192 positions, 40 heads on 8 x 128, bf16: 412 us, 1,250 TFLOP/s (65% of the measured matrix rate); 9 packed
+// prompts up to 8,191 tokens, their own rows: 2,614 us, 1,258 TFLOP/s. A row tile's turn is a chain: softmax 1,000 cycles, products
+// 1,130 (1,024 at the peak), barriers and wake-ups 850; the other tile's turn fills most of the rest. 16-bit pages at D = 256
+// (4,096 tokens at 8,192, 24 heads on 4): 620 us, 52%, the scores of 64 positions taking as long as those of 128 would; D = 64 (40
+// heads on 8): 340 us, 39%. Over codes every row tile (two up to D = 128) decodes its positions anew: the 4,096 tokens take 483 us
+// (q8_0) and 490 us (e4m3) at D = 128, 760 and 858 us at D = 256, where a tile of 64 positions is 2,700 cycles, its decoding 1,700 of
+// them beside the chain. Capped scores cost the products of a polynomial (packed multiply-adds take two cycles): 5 chunks up to
+// 1,501 tokens at 6,000, cap 30, 797 us over e4m3 pages of 4 x 256 (without the cap 700).
 #include <cuda.h>
 #include "stream_common.cuh"
 #include "paged_common.cuh"
