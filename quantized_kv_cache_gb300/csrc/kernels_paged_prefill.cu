@@ -22,9 +22,9 @@
 // 1,130 (1,024 at the peak), barriers and wake-ups 850; the other tile's turn fills most of the rest. 16-bit pages at D = 256
 // (4,096 tokens at 8,192, 24 heads on 4): 620 us, 52%, the scores of 64 positions taking as long as those of 128 would; D = 64 (40
 // heads on 8): 340 us, 39%. Over codes every row tile (two up to D = 128) decodes its positions anew: the 4,096 tokens take 483 us
-// (q8_0) and 490 us (e4m3) at D = 128, 760 and 858 us at D = 256, where a tile of 64 positions is 2,700 cycles, its decoding 1,700 of
+// (q8_0) and 487 us (e4m3) at D = 128, 739 and 786 us at D = 256, where a tile of 64 positions is 2,600 cycles, its decoding 1,700 of
 // them beside the chain. Capped scores cost the products of a polynomial (packed multiply-adds take two cycles): 5 chunks up to
-// 1,501 tokens at 6,000, cap 30, 797 us over e4m3 pages of 4 x 256 (without the cap 700).
+// 1,501 tokens at 6,000, cap 30, 750 us over e4m3 pages of 4 x 256 (without the cap 655).
 #include <cuda.h>
 #include "stream_common.cuh"
 #include "paged_common.cuh"
@@ -41,9 +41,10 @@ template <int D, bool CODES> struct Geo {
     static constexpr int mma_warp = 4 * NT, first_prod = mma_warp + 1, prod = CODES ? 15 - mma_warp : 3;
     static constexpr int threads = 32 * (first_prod + prod);
     // registers (0: not moved): what the block is launched with, 384 x 168 or 512 x 128, is shared out between the softmax's
-    // 128 NT threads and the others
-    static constexpr int soft_regs = NT == 2 ? (CODES ? 168 : 208) : (CODES ? 200 : 0);
-    static constexpr int other_regs = NT == 2 ? 88 : (CODES ? 104 : 0);
+    // 128 NT threads and the others. Codes (5 chunks up to 1,501 tokens at 6,000 positions): at D = 256 152 and 120 (200 and 104, the decoding spilling: e4m3 700 us
+    // against 655), at D = 128 168 and 88 (152 and 104: 473 against 434; 144 and 112: 442)
+    static constexpr int soft_regs = NT == 2 ? (CODES ? 168 : 208) : (CODES ? 152 : 0);
+    static constexpr int other_regs = NT == 2 ? 88 : (CODES ? 120 : 0);
     static constexpr int q_bytes = 128 * D * 2;              // of a row tile
     static constexpr int slot = BN * D * 2;
     static constexpr int smem = 1024 + NT * q_bytes + 4 * slot;

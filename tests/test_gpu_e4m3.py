@@ -351,6 +351,20 @@ def test_chunk_options(opts, dtype, D, G):
 
 
 @pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("cap,q_scale", [(30.0, 1.0), (50.0, 3.0), (30.0, 20.0), (1.0, 1e-3)])
+def test_chunk_caps_near_and_far(D, cap, q_scale):
+    chunk_case("bf16", 2, 4, D, 32, [900, 333], [200, 333], dict(softcap=cap), q_scale=q_scale)
+    chunk_case("f16", 1, 3, D, 64, [600], [150], dict(softcap=cap), q_scale=q_scale)
+
+
+def test_more_heads_than_runs():
+    """Decode and few rows of 700 sequences: more heads than a launch has CTAs, the joins by runs."""
+    lens = [1 + (37 * i) % 90 for i in range(700)]
+    decode_case("f16", 2, 4, 128, 16, lens, {})
+    chunk_case("bf16", 2, 4, 64, 16, [n + 3 for n in lens], [1 + i % 3 for i in range(700)], {})
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
 def test_chunk_of_drafted_tokens_and_split_positions(D):
     chunk_case("f16", 8, 5, D, 32, [3000, 700, 3, 5], [5, 5, 3, 1], {})
     chunk_case("bf16", 1, 4, D, 16, [6000], [40], dict(window=3000))

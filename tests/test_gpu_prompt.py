@@ -261,3 +261,20 @@ def test_refusals():
             f()
         assert e.value.code == code
     assert prompt_status(ws) == 0
+
+
+@pytest.mark.parametrize("dtype,D,G", [("f16", 128, 4), ("bf16", 64, 3), ("bf16", 256, 2), ("bf16", 128, 5)])
+@pytest.mark.parametrize("cap,q_scale", [(30.0, 1.0), (50.0, 3.0), (30.0, 12.0), (1.0, 1.0), (1e6, 1.0), (0.9, 0.5)])
+def test_caps_near_and_far(dtype, D, G, cap, q_scale):
+    """Scores well inside the cap, beyond it in some tiles, far beyond it in all, and caps at the ends of what the short way takes."""
+    case(dtype, 2, G, D, [700, 130], dict(softcap=cap), q_scale=q_scale)
+
+
+def test_caps_that_some_rows_reach():
+    """Every 50th query is long: tiles in which few rows go beyond the polynomial's range, and tiles behind them."""
+    q, k, v = rows_of(900, 4, 2, 128, "bf16", 3)
+    q[::50] *= 40
+    out, lse, ws = torch.empty((900, 4, 128), dtype=torch.bfloat16, device="cuda"), torch.empty((900, 4), device="cuda"), prompt_workspace(900, 4, 128)
+    prompt_attn(q, k, v, ints([0, 900]), 900, out, ws, lse=lse, softcap=20.0)
+    check(q, k, v, [0], [900], out, lse, dict(softcap=20.0), "bf16")
+    assert prompt_status(ws) == 0
