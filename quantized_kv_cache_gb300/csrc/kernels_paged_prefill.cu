@@ -273,20 +273,46 @@ __device__ __forceinline__ void exps32(const float2 (&x)[16], uint32_t* w, uint6
 
 // weights32 with a cap alone, straight through: y = cap tanh(s f) = s (a0 + a1 s^2 + a2 s^4 + a3 s^6) for |s f| < 0.35 (a: of the
 // polynomial below, with f and the cap in it). What is beyond that shows in `big`, the largest |s|. No branch parts the products from
-// the exponentials, so that they share the time: with the vote of rule_weights32 between them 5 chunks up to 1,501 tokens at 6,000 positions, 40 heads on 8 x 128 (bf16 pages, a cap of 30), took 684 us where this takes 502.
+// the exponentials, and they are written in the order in which they should issue, as in weights32: a pair's six products one step apart
+// from the next pair's, so that none waits for the one before it. 5 chunks up to 1,501 tokens at 6,000 positions, 40 heads on 8 x 128,
+// a cap of 30, 16-bit pages: 500 us, with rule_weights32 for every tile 684, without the cap 367. Over codes the registers bind (168 a
+// softmax thread, where scores and weights of a tile are 128): 766 us, without the cap 434.
 template <typename T>
-__device__ __forceinline__ void cap_weights32(const uint32_t (&s)[32], const float (&a)[4], float m, uint32_t* w, uint64_t (&sum)[4],
+__device__ __forceinline__ void cap_weights32(const uint32_t (&s)[32], const uint64_t (&a)[4], uint64_t m, uint32_t* w, uint64_t (&sum)[4],
                                               float (&top)[4], float& big) {
-    const auto both = [](float c) { return make_float2(c, c); };
-    float2 x[16];
+    uint64_t q[16], p[16];
+    float v[32];
+    const auto both = [&](int e) { return (uint64_t)s[2 * e] | ((uint64_t)s[2 * e + 1] << 32); };
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-        const float2 r = make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), q = __fmul2_rn(r, r);
-        const float2 y = __fmul2_rn(r, __ffma2_rn(q, __ffma2_rn(q, __ffma2_rn(q, both(a[3]), both(a[2])), both(a[1])), both(a[0])));
-        big = max3(big, fabsf(r.x), fabsf(r.y));
-        x[e] = __fadd2_rn(y, both(m));                        // by itself, as below
+    for (int n = -6; n < 18; ++n) {
+        const auto at = [&](int e) { return e >= 0 && e < 16; };
+        float2 y = make_float2(0.f, 0.f);
+        if (at(n)) {
+            y = unpair(p[n]);
+            asm volatile("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(v[2 * n]) : "f"(y.x));
+        }
+        if (at(n + 6)) asm volatile("mul.rn.f32x2 %0, %1, %1;\n" : "=l"(q[n + 6]) : "l"(both(n + 6)));
+        if (at(n + 5)) asm volatile("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(p[n + 5]) : "l"(q[n + 5]), "l"(a[3]), "l"(a[2]));
+        if (at(n + 6))
+            asm volatile("{ .reg .f32 x, y; abs.f32 x, %1; abs.f32 y, %2; max.f32 %0, %0, x, y; }\n"
+                         : "+f"(big) : "f"(__uint_as_float(s[2 * (n + 6)])), "f"(__uint_as_float(s[2 * (n + 6) + 1])));
+        if (at(n + 4)) asm volatile("fma.rn.f32x2 %0, %1, %0, %2;\n" : "+l"(p[n + 4]) : "l"(q[n + 4]), "l"(a[1]));
+        if (at(n + 3)) asm volatile("fma.rn.f32x2 %0, %1, %0, %2;\n" : "+l"(p[n + 3]) : "l"(q[n + 3]), "l"(a[0]));
+        if (at(n)) {
+            asm volatile("max.f32 %0, %0, %1, %2;\n" : "+f"(top[n & 3]) : "f"(y.x), "f"(y.y));
+            asm volatile("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(v[2 * n + 1]) : "f"(y.y));
+        }
+        if (at(n + 2)) asm volatile("mul.rn.f32x2 %0, %0, %1;\n" : "+l"(p[n + 2]) : "l"(both(n + 2)));
+        if (at(n + 1)) asm volatile("add.rn.f32x2 %0, %0, %1;\n" : "+l"(p[n + 1]) : "l"(m));       // by itself, as below
+        if (at(n - 2)) {
+            const int e = n - 2;
+            if constexpr (std::is_same<T, __half>::value)
+                asm volatile("cvt.rn.f16x2.f32 %0, %1, %2;\n" : "=r"(w[e]) : "f"(v[2 * e + 1]), "f"(v[2 * e]));
+            else
+                asm volatile("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(w[e]) : "f"(v[2 * e + 1]), "f"(v[2 * e]));
+            asm volatile("add.rn.f32x2 %0, %0, %1;\n" : "+l"(sum[e & 3]) : "l"(pair(v[2 * e], v[2 * e + 1])));
+        }
     }
-    exps32<T>(x, w, sum, top);
 }
 
 // weights32 with the cap and the bias on the way: scores of 32 positions from p0 on, in units of log2, less the row's maximum (m its
@@ -734,8 +760,9 @@ __global__ void __launch_bounds__(Geo<D, codes_of(KF)>::threads, 1) prefill_kern
 
             const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16), o_addr = lanes + GE::o_col(t);
             // the polynomial of cap_weights32, where f^7 and the cap leave its coefficients among the normal numbers
-            const float f2 = rs.f * rs.f, cap[4] = {rs.f * rule.cap_l2, -0.33332664f * f2 * rs.f * rule.cap_l2,
-                                                    0.13299826f * f2 * f2 * rs.f * rule.cap_l2, -0.049148493f * f2 * f2 * f2 * rs.f * rule.cap_l2};
+            const float f2 = rs.f * rs.f, a0 = rs.f * rule.cap_l2;
+            const auto both = [](float c) { return pair(c, c); };
+            const uint64_t cap[4] = {both(a0), both(-0.33332664f * f2 * a0), both(0.13299826f * f2 * f2 * a0), both(-0.049148493f * f2 * f2 * f2 * a0)};
             const bool cap_alone = RULE && __all_sync(kAll, rule.cap >= 1.f && rule.cap <= 1e6f && !rule.biased && rs.f >= 7.6e-6f && rs.f <= 16.f);
             int wide = 0;                                         // tiles for which scores beyond the polynomial are expected
             // positions of the row tile's first and last rows: what decides whether a KV tile is seen whole
@@ -799,7 +826,7 @@ __global__ void __launch_bounds__(Geo<D, codes_of(KF)>::threads, 1) prefill_kern
                     if constexpr (!RULE)
                         each32([&](uint32_t (&x)[32], int k) { weights32<T>(x, pair(f2.x, f2.y), pair(mb.x, mb.y), &pr[k / 2][16 * (k & 1)], s2, y); });
                     else if (lean)
-                        each32([&](uint32_t (&x)[32], int k) { cap_weights32<T>(x, cap, mb.x, &pr[k / 2][16 * (k & 1)], s2, y, big); });
+                        each32([&](uint32_t (&x)[32], int k) { cap_weights32<T>(x, cap, pair(mb.x, mb.y), &pr[k / 2][16 * (k & 1)], s2, y, big); });
                     else
                         each32([&](uint32_t (&x)[32], int k) {
                             rule_weights32<T>(x, rule, rs, p0 + 32 * k, mb.x, [&](float2 (&z)[16]) {
