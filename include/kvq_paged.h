@@ -188,7 +188,7 @@ kvq_status kv_pages_fork(kvq_paged* h, const kvq_page_tables* t, int32_t n, cons
  * pages for them come from the free ones, lowest first, row after row. A row that would go on in a part-filled page that is held
  * by others too gets a copy of it instead (of several rows that go on in one page all of whose holders go on, the lowest
  * keeps it), so that what is then written at the new positions is the row's own. If the free pages do not suffice for the
- * whole call it changes nothing and sets KVQ_PAGED_NO_PAGES; a row that would outgrow its table, or whose last page is no
+ * whole call it changes nothing and sets KVQ_PAGED_NO_PAGES (lens stays; rows must not be written behind it then); a row that would outgrow its table, or whose last page is no
  * page, is left out (KVQ_PAGED_BAD_LENGTH, KVQ_PAGED_BAD_INDEX). */
 kvq_status kv_pages_extend(kvq_paged* h, const kvq_page_tables* t, const int32_t* add, void* workspace, size_t ws_bytes, void* stream);
 

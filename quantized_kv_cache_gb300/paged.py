@@ -287,7 +287,8 @@ class PagedKVCache:
 
     def extend(self, page_table, lens, refs, add, ws=None, stream=0):
         """Row r will hold add[r] more positions (int32 [rows]): lens grows, free pages are taken, and a part-filled page that
-        others hold too is copied first. With too few free pages nothing changes and the status word says NO_PAGES."""
+        others hold too is copied first. With too few free pages nothing changes and the status word says NO_PAGES; nothing
+        must be written behind lens then."""
         t, ap = self._tables(page_table, lens, refs), _ints(add, "add", lens.shape[0], self._dev)
         wp, wb = self._pages_space(ws)
         _guarded(self._dev, _lib.kv_pages_extend, self.h, t, ap, wp, wb, stream)
