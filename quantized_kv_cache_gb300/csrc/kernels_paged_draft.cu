@@ -15,7 +15,7 @@
 // 139 us here (HBM's floor 64). Bound by latency: a tile of 16 positions takes a warp 590 instructions, the matrix pipe 540 of
 // a scheduler's 1,550 cycles, and two warps a scheduler do not fill the waits between them. Other forms of the same batch: up to 16
 // rows 113 us (two blocks of rows, three CTAs an SM; with four blocks 147); 25 rows as two warps on a tile 151; 60 rows 242; 4 x 256, 30
-// rows 152 (as two groups 172). The scores of the next tile formed beside the values of this one: 149, the registers spill.
+// rows 152 (as two groups 172). The scores of the next tile formed beside the values of this one: 143-149, the registers spill.
 #include "device_common.cuh"
 #include "paged_frag.cuh"
 

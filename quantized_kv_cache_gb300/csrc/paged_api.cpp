@@ -100,7 +100,7 @@ size_t workspace_floats(const kvq_paged_config& c, int64_t seqs, int64_t rows) {
     return a > b ? a : b;
 }
 
-// The driver's call that encodes a tensor map; null where it is not found.
+// The call of CUDA's driver that encodes a tensor map; null where it is not found.
 using EncodeMap = decltype(&cuTensorMapEncodeTiled);
 EncodeMap encode_map() {
     static const EncodeMap known = [] {
