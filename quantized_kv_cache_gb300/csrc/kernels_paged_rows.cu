@@ -742,8 +742,9 @@ template <typename T> int write_t(const WriteParams& p, cudaStream_t s) {
     return p.v.D == 64 ? write_d<T, 64>(p, s) : (p.v.D == 128 ? write_d<T, 128>(p, s) : write_d<T, 256>(p, s));
 }
 template <typename T, int D> int append_d(const PagedAppendParams& p, cudaStream_t s) {
-    // 32 rows a CTA where a sequence brings half a block or more, on the mean
-    const int rows = p.n_rows / 8 >= p.n_seq ? 32 : 1;
+    // 32 rows a CTA where there are many and a sequence brings four or more, on the mean (a row a CTA against 32, in us: 32
+    // sequences of 16 rows 10 / 12, of 64 14 / 12; 512 sequences of one 16 / 51, of four 25 / 23, of eight 35 / 18)
+    const int rows = p.n_rows >= 2048 && p.n_rows / 4 >= p.n_seq ? 32 : 1;
     const dim3 grid((unsigned)((p.n_rows + (int64_t)rows - 1) / rows), (unsigned)((2 * p.v.H + kAppendWarps - 1) / kAppendWarps));
     const auto k = rows == 1 ? paged_append_kernel<T, D, 1> : paged_append_kernel<T, D, 32>;
     return (int)launch_k(k, grid, dim3(32 * kAppendWarps), 0, s, true, p);
