@@ -174,10 +174,11 @@ KVQ_HD int prefill_splits(int64_t rows, int n_seq, int H, int tile_rows, int sm_
     const int64_t s = (sm_count < kMaxSms ? sm_count : kMaxSms) / (ctas > 0 ? ctas : 1);
     return (int)(s < 1 ? 1 : (s > kMaxSplits ? kMaxSplits : s));
 }
-// Whole prompts: the row tiles of all of them, at most one part-filled per sequence; and splits that leave each at least four of the
-// position tiles of the longest one's last rows.
+// Whole prompts: the row tiles of all of them, at most one part-filled per sequence; and splits that leave each some four of the
+// position tiles of the longest one's last rows (333 tokens, 4 heads on 2 x 128: unsplit 20 us, two 25; 1,024 tokens of one head unsplit 31,
+// four 27, eight 25; 8,191 unsplit 113, four 49, more 49).
 KVQ_HD int64_t prompt_tiles(int64_t n_rows, int64_t n_seq, int G, int D) { return n_rows * G / (D == 256 ? 128 : 256) + n_seq; }
-KVQ_HD int prompt_splits(int max_q, int D) { return 1 + max_q / prefill_tile(D) / 8; }
+KVQ_HD int prompt_splits(int max_q, int D) { return 1 + max_q / prefill_tile(D) / 4; }
 // The splits' partials in the workspace: (maximum, sum) of all `pairs` (split, query row, head), then from float
 // split_out_at on their outputs. Those go by 16-byte accesses, and pairs may be odd: rounded up to four floats.
 KVQ_HD int64_t split_out_at(int64_t pairs) { return (2 * pairs + 3) & ~(int64_t)3; }
