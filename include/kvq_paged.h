@@ -135,8 +135,8 @@ kvq_status kv_paged_read(kvq_paged* h, int32_t layer, int32_t dtype, int32_t n_s
  * 16-bit pages take queries of their own type; rows of Q8_0 / Q4_0 pages enter as code x scale
  * rounded to fp16, with queries of either type. Scales above 515.5 (Q8_0) or 9352 (Q4_0) are taken as
  * these, as code x scale would be no fp16 number (their write has set KVQ_PAGED_RANGE). KVQ_PAGED_E4M3 rows likewise, with
- * scales up to 2^7 (a chunk of more than 64 rows a KV head takes code x scale as an fp16 number, which it is from scales of 2^-15
- * on; decode and smaller chunks do not round it). lens[b] = 0 gives
+ * scales up to 2^7 (a chunk may take code x scale as an fp16 number, which it is from scales of 2^-15 on; decode does not round
+ * it). lens[b] = 0 gives
  * zeros. max_pages x page_size is at most 2^31 - 256. workspace: device, 16-byte aligned,
  * >= kv_paged_required_bytes for n_seq; written before it is read. */
 kvq_status kv_paged_decode_attn(kvq_paged* h, int32_t layer, int32_t dtype, int32_t n_seq, const void* q,

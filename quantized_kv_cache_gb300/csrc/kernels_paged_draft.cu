@@ -11,10 +11,10 @@
 // of V that hold a NaN are added to the rows that see them and taken out before the product.
 //
 // On the tensor cores of the chunk kernel a tile of 128 rows would be a fifth full, and its softmax a chain of one
-// tile after the other: 20 sequences of five tokens up to 16,001 positions, 40 heads on 8 x 128 (25 rows a KV head): 606 us there,
-// 139 us here (HBM's floor 64). Bound by latency: a tile of 16 positions takes a warp 590 instructions, the matrix pipe 540 of
+// tile after the other: 20 sequences of 12 tokens up to 16,001 positions, 40 heads on 8 x 128 (60 rows a KV head): 293 us there,
+// 242 here, and of five tokens (25 rows) 139 (HBM's floor 64). Where little is held that kernel is the faster one (draft_better). Bound by latency: a tile of 16 positions takes a warp 590 instructions, the matrix pipe 540 of
 // a scheduler's 1,550 cycles, and two warps a scheduler do not fill the waits between them. Other forms of the same batch: up to 16
-// rows 113 us (two blocks of rows, three CTAs an SM; with four blocks 147); 25 rows as two warps on a tile 151; 60 rows 242; 4 x 256, 30
+// rows 113 us (two blocks of rows, three CTAs an SM; with four blocks 147); 25 rows as two warps on a tile 151; 4 x 256, 30
 // rows 152 (as two groups 172). The scores of the next tile formed beside the values of this one: 143-149, the registers spill.
 #include "device_common.cuh"
 #include "paged_frag.cuh"

@@ -450,7 +450,7 @@ kvq_status kv_paged_prefill_attn(kvq_paged* h, int32_t layer, int32_t dtype, int
     p.cu = cu_q;
     p.n_rows = n_rows;
     p.max_q = max_q < n_rows ? max_q : n_rows;
-    if (h->cfg.k_fmt == KVQ_PAGED_E4M3 && p.max_q * p.G <= kMaxDraftRows) {
+    if (h->cfg.k_fmt == KVQ_PAGED_E4M3 && draft_better((int64_t)p.max_q * p.G, n_seq, p.v.H, (int64_t)max_pages * h->cfg.page_size)) {
         const auto few = p.v.D == 64 ? launch_paged_draft_64 : (p.v.D == 128 ? launch_paged_draft_128 : launch_paged_draft_256);
         return launched(few(p, h->sm_count, stream));
     }

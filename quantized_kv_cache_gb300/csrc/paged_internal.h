@@ -159,13 +159,20 @@ KVQ_HD int64_t partial_floats(int G, int D) { return 32 + (int64_t)G * D; }
 // Before the partials: n_seq + 1 int64, the tiles before each sequence.
 KVQ_HD int64_t line_floats(int64_t n_seq) { return (2 * (n_seq + 1) + 3) & ~(int64_t)3; }
 
-// Chunks of a few tokens over e4m3 pages (kernels_paged_draft.cu): the most rows of a KV head that go there, CTAs per SM (nq: blocks of
-// eight rows of a warp), the floats of the partial results (maxima, sums, outputs) that the CTAs of an SM leave, each once: 64 rows
-// of two CTAs, at D = 256 32 of two; and of all runs, two partials each.
-constexpr int kMaxDraftRows = 64;
+// Chunks of a few tokens over e4m3 pages (kernels_paged_draft.cu): CTAs per SM (nq: blocks of eight rows of a warp), the floats of the
+// partial results (maxima, sums, outputs) that the CTAs of an SM leave, each once: 64 rows of two CTAs, at D = 256 32 of two; and of all
+// runs, two partials each.
 KVQ_HD constexpr int draft_ctas(int D, int nq) { return nq == 4 || D == 256 ? 2 : (D == 128 ? 3 : 4); }
 KVQ_HD constexpr int draft_part_floats(int D) { return D == 256 ? 2 * (64 + 32 * D) : 2 * (128 + 64 * D); }
 KVQ_HD int64_t paged_draft_ws_floats(int D, int64_t n_seq) { return line_floats(n_seq) + (int64_t)kMaxSms * 2 * draft_part_floats(D); }
+// Whether a chunk goes there: up to 64 rows a KV head, over as many positions of heads as make its even split worth more than the
+// chunk kernel's tensor cores and split positions (their lengths are on the device: as many as the table holds). Of 40 heads on 8 x 128, us,
+// chunk kernel / few-row kernel, 15 rows: 2 sequences up to 8,000 24 / 26, 4 36 / 30, 8 up to 2,000 23 / 23, 16 34 / 28 and up to 32,000
+// 472 / 167; 30 rows: 4 up to 8,000 37 / 39, 8 70 / 54, 16 up to 2,000 34 / 37; one up to 32,000 39 / 36 and 41 / 44. D = 64 and 256
+// cross at the same products. 60 rows (two warps of 32 on a tile): 16 up to 8,000 126 / 125, 20 up to 16,001 293 / 242.
+KVQ_HD bool draft_better(int64_t rows, int64_t n_seq, int64_t H, int64_t positions) {
+    return rows <= 64 && n_seq * H * positions >= (rows <= 16 ? 160000 : rows <= 32 ? 270000 : 1100000);
+}
 
 // A chunk's positions are split when its row tiles alone leave SMs without work: as many splits as leave one CTA per SM.
 constexpr int kMaxSplits = 16;

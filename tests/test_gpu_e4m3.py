@@ -320,10 +320,15 @@ def test_nan_codes_that_a_query_sees_give_nan():
 
 
 # ------------------------------------------------------------------------------------------------ chunk
-def chunk_case(dtype, H, G, D, ps, lens, qlens, opts, seed=0, q_scale=1.0, scale=1.0, gap=3):
+def wide(H, ps, n_seq):
+    """Table entries behind the pages, so that a chunk of few rows goes where few rows go (by what the table could hold)."""
+    return 1100000 // (H * ps * n_seq) + 1
+
+
+def chunk_case(dtype, H, G, D, ps, lens, qlens, opts, seed=0, q_scale=1.0, scale=1.0, gap=3, spare=1):
     T = sum(qlens) + 2 * gap
     p = Pages8(H, D, ps, sum(-(-n // ps) for n in lens) + 1, Hq=H * G, max_seqs=len(lens), max_tokens=T, seed=seed)
-    table, ks, vs = e8.fill(p, 0, lens, seed, dtype, scale)
+    table, ks, vs = e8.fill(p, 0, lens, seed, dtype, scale, spare)
     wide = torch.randn((T, H * G + 2 * H, D), generator=torch.Generator(device="cuda").manual_seed(seed + 1), device="cuda")
     q = (q_scale * wide).to(DT[dtype])[:, :H * G]
     out = torch.full((T, H * G, D), 7.0, dtype=DT[dtype], device="cuda")
@@ -361,7 +366,7 @@ def test_more_heads_than_runs():
     """Decode and few rows of 700 sequences: more heads than a launch has CTAs, the joins by runs."""
     lens = [1 + (37 * i) % 90 for i in range(700)]
     decode_case("f16", 2, 4, 128, 16, lens, {})
-    chunk_case("bf16", 2, 4, 64, 16, [n + 3 for n in lens], [1 + i % 3 for i in range(700)], {})
+    chunk_case("bf16", 2, 4, 64, 16, [n + 3 for n in lens], [1 + i % 3 for i in range(700)], {}, spare=wide(2, 16, 700))
 
 
 @pytest.mark.parametrize("D", [64, 128, 256])
@@ -374,21 +379,23 @@ def test_chunk_of_drafted_tokens_and_split_positions(D):
 @pytest.mark.parametrize("H,G,D,ps,q", [(2, 2, 64, 16, 7), (8, 5, 128, 32, 5), (4, 6, 256, 64, 5), (2, 16, 128, 16, 4), (1, 9, 64, 128, 7),
                                         (1, 16, 256, 256, 4), (3, 1, 128, 64, 64), (2, 3, 256, 16, 21), (1, 5, 128, 16, 13)])
 def test_few_rows_match_64_bits(dtype, H, G, D, ps, q):
-    """Up to 64 rows a KV head, and one token more than that."""
-    chunk_case(dtype, H, G, D, ps, [q, 1, 1025, 17, 300, q + 1], [q, 1, q, 0, 2, q], {})
+    """Up to 64 rows a KV head, and one token more than that, over tables that hold little and much."""
+    for spare in (1, wide(H, ps, 6)):
+        chunk_case(dtype, H, G, D, ps, [q, 1, 1025, 17, 300, q + 1], [q, 1, q, 0, 2, q], {}, spare=spare)
 
 
 @pytest.mark.parametrize("opts", OPTS[1:] + [dict(window=1), dict(prefix=60, window=3)])
 @pytest.mark.parametrize("dtype,D,G", [("f16", 128, 4), ("bf16", 64, 12), ("bf16", 256, 3)])
 def test_few_rows_options(opts, dtype, D, G):
-    chunk_case(dtype, 2, G, D, 32, [200, 1, 47, 1500], [5, 1, 4, 3], opts)
+    for spare in (1, wide(2, 32, 4)):
+        chunk_case(dtype, 2, G, D, 32, [200, 1, 47, 1500], [5, 1, 4, 3], opts, spare=spare)
 
 
 def test_few_rows_of_many_sequences():
     """More groups than runs, and one sequence that all runs share; odd gaps of a batch padded with empty sequences."""
-    chunk_case("f16", 4, 4, 128, 16, [3 + (11 * i) % 60 for i in range(200)], [i % 4 for i in range(200)], {}, gap=5)
-    chunk_case("bf16", 1, 8, 128, 64, [40000], [8], {})
-    chunk_case("f16", 1, 4, 256, 64, [30001], [9], dict(slopes=True))
+    chunk_case("f16", 4, 4, 128, 16, [3 + (11 * i) % 60 for i in range(200)], [i % 4 for i in range(200)], {}, gap=5, spare=wide(4, 16, 200))
+    chunk_case("bf16", 1, 8, 128, 64, [40000], [8], {}, spare=wide(1, 64, 1))
+    chunk_case("f16", 1, 4, 256, 64, [30001], [9], dict(slopes=True), spare=wide(1, 64, 1))
 
 
 @pytest.mark.parametrize("D,tokens", [(64, 6), (128, 6), (256, 3), (128, 40)])
@@ -397,7 +404,7 @@ def test_later_rows_do_not_reach_earlier_queries(D, tokens):
     for at in ("k", "v"):
         n = 50 + tokens
         p = Pages8(2, D, 32, 8, Hq=8, max_seqs=1, max_tokens=tokens)
-        table, ks, vs = e8.fill(p, 0, [n], 5)
+        table, ks, vs = e8.fill(p, 0, [n], 5, spare=wide(2, 32, 1))
         raw, j = p.host(), n - 2
         codes, _ = p.unit(raw, 0, 1 if at == "v" else 0, int(table[0, j // 32]), 1)
         codes[j % 32] = 127
@@ -415,7 +422,7 @@ def test_later_rows_do_not_reach_earlier_queries(D, tokens):
 
 def test_few_rows_at_negative_positions_and_bad_lengths():
     p = Pages8(1, 64, 16, 4, Hq=2, max_seqs=2, max_tokens=20)
-    table, ks, vs = e8.fill(p, 0, [10, 30], 1)
+    table, ks, vs = e8.fill(p, 0, [10, 30], 1, spare=wide(1, 16, 2))
     q = torch.randn((18, 2, 64), device="cuda").half()
     out, lse = torch.full_like(q, 7.0), torch.full((18, 2), 7.0, device="cuda")
     p.cache.prefill_attn(0, q, ints([0, 13, 15]), 13, table, ints([10, 30]), out, lse=lse, prefix=ints([4, 0]))
@@ -440,7 +447,7 @@ def test_few_rows_at_negative_positions_and_bad_lengths():
 
 def test_captured_drafts_follow_their_bounds():
     p = Pages8(2, 128, 32, 60, Hq=8, max_seqs=3, max_tokens=24, seed=3)
-    table, _, _ = e8.fill(p, 0, [900, 333, 40], 4)
+    table, _, _ = e8.fill(p, 0, [900, 333, 40], 4, spare=wide(2, 32, 3))
     cu, lens = ints([0, 5, 10, 15]), ints([900, 333, 40])
     q = torch.randn((15, 8, 128), generator=torch.Generator().manual_seed(0)).half().cuda()
     out, lse = torch.empty_like(q), torch.empty((15, 8), device="cuda")
