@@ -391,20 +391,23 @@ def test_few_rows_options(opts, dtype, D, G):
         chunk_case(dtype, 2, G, D, 32, [200, 1, 47, 1500], [5, 1, 4, 3], opts, spare=spare)
 
 
-def test_few_rows_of_many_sequences():
+@pytest.mark.parametrize("much", [False, True])
+def test_few_rows_of_many_sequences(much):
     """More groups than runs, and one sequence that all runs share; odd gaps of a batch padded with empty sequences."""
-    chunk_case("f16", 4, 4, 128, 16, [3 + (11 * i) % 60 for i in range(200)], [i % 4 for i in range(200)], {}, gap=5, spare=wide(4, 16, 200))
-    chunk_case("bf16", 1, 8, 128, 64, [40000], [8], {}, spare=wide(1, 64, 1))
-    chunk_case("f16", 1, 4, 256, 64, [30001], [9], dict(slopes=True), spare=wide(1, 64, 1))
+    many = [i % 4 for i in range(200)]
+    chunk_case("f16", 4, 4, 128, 16, [3 + (11 * i) % 60 for i in range(200)], many, {}, gap=5, spare=wide(4, 16, 200) if much else 1)
+    chunk_case("bf16", 1, 8, 128, 64, [40000], [8], {}, spare=wide(1, 64, 1) if much else 1)
+    chunk_case("f16", 1, 4, 256, 64, [30001], [9], dict(slopes=True), spare=wide(1, 64, 1) if much else 1)
 
 
+@pytest.mark.parametrize("much", [False, True])
 @pytest.mark.parametrize("D,tokens", [(64, 6), (128, 6), (256, 3), (128, 40)])
-def test_later_rows_do_not_reach_earlier_queries(D, tokens):
+def test_later_rows_do_not_reach_earlier_queries(D, tokens, much):
     """NaN in the keys and values of some of the chunk's own tokens: the rows before them stay within the bound, those from them on are NaN."""
     for at in ("k", "v"):
         n = 50 + tokens
         p = Pages8(2, D, 32, 8, Hq=8, max_seqs=1, max_tokens=tokens)
-        table, ks, vs = e8.fill(p, 0, [n], 5, spare=wide(2, 32, 1))
+        table, ks, vs = e8.fill(p, 0, [n], 5, spare=wide(2, 32, 1) if much else 1)
         raw, j = p.host(), n - 2
         codes, _ = p.unit(raw, 0, 1 if at == "v" else 0, int(table[0, j // 32]), 1)
         codes[j % 32] = 127
@@ -420,9 +423,10 @@ def test_later_rows_do_not_reach_earlier_queries(D, tokens):
         assert torch.isnan(out[k:, 4:]).all() and (torch.isnan(lse[k:, 4:]).all() if at == "k" else torch.isfinite(lse).all())
 
 
-def test_few_rows_at_negative_positions_and_bad_lengths():
+@pytest.mark.parametrize("much", [False, True])
+def test_few_rows_at_negative_positions_and_bad_lengths(much):
     p = Pages8(1, 64, 16, 4, Hq=2, max_seqs=2, max_tokens=20)
-    table, ks, vs = e8.fill(p, 0, [10, 30], 1, spare=wide(1, 16, 2))
+    table, ks, vs = e8.fill(p, 0, [10, 30], 1, spare=wide(1, 16, 2) if much else 1)
     q = torch.randn((18, 2, 64), device="cuda").half()
     out, lse = torch.full_like(q, 7.0), torch.full((18, 2), 7.0, device="cuda")
     p.cache.prefill_attn(0, q, ints([0, 13, 15]), 13, table, ints([10, 30]), out, lse=lse, prefix=ints([4, 0]))
@@ -445,9 +449,10 @@ def test_few_rows_at_negative_positions_and_bad_lengths():
     assert p.cache.status() == _lib.PAGED_BAD_INDEX
 
 
-def test_captured_drafts_follow_their_bounds():
+@pytest.mark.parametrize("much", [False, True])
+def test_captured_drafts_follow_their_bounds(much):
     p = Pages8(2, 128, 32, 60, Hq=8, max_seqs=3, max_tokens=24, seed=3)
-    table, _, _ = e8.fill(p, 0, [900, 333, 40], 4, spare=wide(2, 32, 3))
+    table, _, _ = e8.fill(p, 0, [900, 333, 40], 4, spare=wide(2, 32, 3) if much else 1)
     cu, lens = ints([0, 5, 10, 15]), ints([900, 333, 40])
     q = torch.randn((15, 8, 128), generator=torch.Generator().manual_seed(0)).half().cuda()
     out, lse = torch.empty_like(q), torch.empty((15, 8), device="cuda")
